@@ -20,6 +20,8 @@ __all__ = [
     "streamkl_fwd_scaled", "streamkl_fwd_splitk_scaled", "streamkl_bwd_scaled",
     "streamkl_fwd_gqa", "streamkl_fwd_splitk_gqa", "streamkl_bwd_gqa", "streamkl_bwd_both",
     "streamkl_bwd_workspace_bytes", "streamkl_bwd_gqa_ws",
+    "AttnSide", "streamkl_fwd_mod", "streamkl_fwd_mod_workspace_bytes", "streamkl_bwd_mod",
+    "streamkl_bwd_mod_workspace_bytes",
     "status_string", "STREAMKL_STATIC_WORKSPACE_BYTES",
     "streamkl_get_device_status", "streamkl_probe_ex2", "streamkl_selftest_wait_timeout",
     "streamkl_selftest_turn_timeout",
@@ -44,6 +46,24 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+
+_LL = ctypes.c_longlong
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("data", _P), ("stride_b", _LL), ("stride_h", _LL), ("stride_n", _LL)]
+
+
+class _Side(ctypes.Structure):
+    _fields_ = [("q", _View), ("k", _View), ("d", _I), ("HK", _I), ("scale", _F), ("softcap", _F), ("slopes", _P),
+                ("table", _P), ("num_buckets", _I), ("max_distance", _I), ("bidirectional", _I)]
+
+
+class _Visible(ctypes.Structure):
+    _fields_ = [("causal", _I), ("prefix", _P), ("doc_q", _P), ("doc_k", _P)]
+
+
+_SP, _VP, _VISP = ctypes.POINTER(_Side), ctypes.POINTER(_View), ctypes.POINTER(_Visible)
 
 _SIGS = {
     "streamkl_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _P]),
@@ -70,6 +90,10 @@ _SIGS = {
     "streamkl_bwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
     "streamkl_bwd_gqa_ws": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _F, _I, _P, _P, _P, _P, _I,
                                  _I, _P, _P, _P, _SZ, _P]),
+    "streamkl_fwd_mod_workspace_bytes": (_SZ, [_SP, _SP, _VISP, _I, _I, _I, _I, _I]),
+    "streamkl_fwd_mod": (_I, [_SP, _SP, _VISP, _I, _I, _I, _I, _I, _P, _SZ, _P, _P, _P, _P]),
+    "streamkl_bwd_mod_workspace_bytes": (_SZ, [_SP, _SP, _VISP, _I, _I, _I, _I, _I, _I, _I]),
+    "streamkl_bwd_mod": (_I, [_SP, _SP, _VISP, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _VP, _VP, _P, _P, _SZ, _P]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
     "streamkl_get_device_status": (_I, []),
     "streamkl_probe_ex2": (_I, [_P, _I, _I, _P]),
@@ -393,6 +417,159 @@ def streamkl_bwd_both(q1, k1, q2, k2, scale1, scale2, causal, kl, lse1, lse2, dk
                                    dk2.data_ptr(), _stream(stream)),
            "streamkl_bwd_both")
     return dq1, dk1, dq2, dk2
+
+
+def _view(t):
+    return _View(t.data_ptr(), *t.stride()[:3])
+
+
+class AttnSide:
+    """One attention distribution over modified scores (see the header):
+    q [B, H, NQ, d] and k [B, HK, NK, d] bf16 (any strides that are multiples
+    of 8 with a dense last dimension, a transposed [B, N, H, d] for one),
+    scale, an optional softcap, and either slopes [H] or a learned table
+    [H, num_buckets] (fp32, contiguous) with max_distance and bidirectional.
+
+    Holds references to its tensors, no copies; may be used for any number of
+    calls while they keep their memory.
+    """
+
+    def __init__(self, q, k, scale, softcap=0.0, slopes=None, table=None, max_distance=128, bidirectional=False):
+        for name, t in (("q", q), ("k", k)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+                raise TypeError(f"{name} must be a CUDA bf16 tensor")
+            if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+                raise ValueError(f"{name} must be a [B, heads, N, d] tensor whose last dimension is dense")
+        B, H, _, d = q.shape
+        if k.shape[0] != B or k.shape[3] != d:
+            raise ValueError("inconsistent shapes: want q [B,H,NQ,d] and k [B,HK,NK,d]")
+        for name, t, ok in (("slopes", slopes, slopes is None or tuple(slopes.shape) == (H,)),
+                            ("table", table, table is None or (table.dim() == 2 and table.shape[0] == H))):
+            if t is None:
+                continue
+            if t.dtype != torch.float32 or t.device != q.device or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous fp32 tensor on {q.device}")
+            if not ok:
+                raise ValueError(f"{name} must have one row for each of the {H} heads, not {tuple(t.shape)}")
+        if k.device != q.device:
+            raise ValueError("q and k must be on the same device")
+        self.q, self.k, self.slopes, self.table = q, k, slopes, table
+        self.num_buckets = 0 if table is None else table.shape[1]
+        self._c = _Side(_view(q), _view(k), d, k.shape[1], float(scale), float(softcap),
+                        None if slopes is None else slopes.data_ptr(), None if table is None else table.data_ptr(),
+                        self.num_buckets, int(max_distance), int(bool(bidirectional)))
+
+
+def _mod_call(p1, p2, causal, prefix, doc_q, doc_k):
+    """(B, H, NQ, NK, streamkl_visible) of a call, its shapes and devices checked."""
+    q, k = p1.q, p1.k
+    B, H, NQ, _ = q.shape
+    NK = k.shape[2]
+    if p2.q.shape[:3] != q.shape[:3] or p2.k.shape[2] != NK:
+        raise ValueError("both sides must have the same B, H, NQ and NK")
+    if p2.q.device != q.device:
+        raise ValueError("both sides must be on the same device")
+    for name, t, shape in (("prefix", prefix, (B,)), ("doc_q", doc_q, (B, NQ)), ("doc_k", doc_k, (B, NK))):
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or t.device != q.device or not t.is_contiguous() or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {q.device}")
+    return B, H, NQ, NK, _Visible(int(bool(causal)), *(None if t is None else t.data_ptr()
+                                                        for t in (prefix, doc_q, doc_k)))
+
+
+def _mod_workspace(workspace, need, device, stream):
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def _grad_out(t, shape, device, name):
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or t.device != device or \
+            (t.shape[3] > 1 and t.stride(3) != 1):
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on {device} with a dense last dimension")
+    return t
+
+
+def _new_on(stream, *pairs):
+    """Tensors made by this call (old one None) are used on `stream` too."""
+    if stream is not None:
+        for old, new in pairs:
+            if old is None and new is not None:
+                new.record_stream(stream)
+
+
+def streamkl_fwd_mod_workspace_bytes(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, num_splits=0):
+    B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
+    return int(lib().streamkl_fwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(num_splits)))
+
+
+def streamkl_fwd_mod(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, num_splits=0, workspace=None, kl=None,
+                     lse1=None, lse2=None, stream=None):
+    """Per-row KL(P1 || P2), LSE1, LSE2 (fp32 [B, H, NQ]) of two AttnSides,
+    over the keys that causal, prefix [B] (int32, with causal) and the
+    document ids doc_q [B, NQ], doc_k [B, NK] (int32, negative: padding) leave
+    visible; rows that see none get KL 0 and LSE -inf.  num_splits 0: the
+    library's choice."""
+    B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
+    dev = p1.q.device
+    with torch.cuda.device(dev):
+        need = int(lib().streamkl_fwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(num_splits)))
+        workspace = _mod_workspace(workspace, need, dev, stream)
+        given = (kl, lse1, lse2)
+        out = tuple(_out(t, (B, H, NQ), dev, name) for t, name in zip(given, ("kl", "lse1", "lse2")))
+        _new_on(stream, *zip(given, out))
+        _check(lib().streamkl_fwd_mod(p1._c, p2._c, vis, B, H, NQ, NK, int(num_splits), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), out[0].data_ptr(),
+                                      out[1].data_ptr(), out[2].data_ptr(), _stream(stream)),
+               "streamkl_fwd_mod")
+    return out
+
+
+def streamkl_bwd_mod_workspace_bytes(p1, p2, mode=STREAMKL_GRAD_P2, causal=False, prefix=None, doc_q=None, doc_k=None,
+                                     deterministic=False, table_grad=True):
+    B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
+    return int(lib().streamkl_bwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(mode),
+                                                      int(bool(deterministic)), int(bool(table_grad))))
+
+
+def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=False, prefix=None, doc_q=None,
+                     doc_k=None, deterministic=False, table_grad=True, dq=None, dk=None, dtable=None, workspace=None,
+                     stream=None):
+    """(dq, dk, dtable) for the side `mode` selects: bf16 gradients of its q
+    and k, and fp32 of its table (None when it has none or table_grad is
+    False).  kl, lse1, lse2 come from streamkl_fwd_mod over the same arguments."""
+    B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
+    g = p2 if mode == STREAMKL_GRAD_P2 else p1
+    dev = g.q.device
+    for name, t in (("kl", kl), ("lse1", lse1), ("lse2", lse2), ("dkl", dkl)):
+        _out(t, (B, H, NQ), dev, name)
+    want_table = g.table is not None and (table_grad or dtable is not None)
+    if dtable is not None and g.table is None:
+        raise ValueError("dtable given for a side without a table")
+    with torch.cuda.device(dev):
+        need = int(lib().streamkl_bwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(mode),
+                                                          int(bool(deterministic)), int(want_table)))
+        workspace = _mod_workspace(workspace, need, dev, stream)
+        given = (dq, dk, dtable)
+        dq = _grad_out(dq, g.q.shape, dev, "dq")
+        dk = _grad_out(dk, g.k.shape, dev, "dk")
+        if want_table:
+            dtable = _out(dtable, (H, g.num_buckets), dev, "dtable")
+        _new_on(stream, *zip(given, (dq, dk, dtable)))
+        _check(lib().streamkl_bwd_mod(p1._c, p2._c, vis, B, H, NQ, NK, kl.data_ptr(), lse1.data_ptr(),
+                                      lse2.data_ptr(), dkl.data_ptr(), int(mode), int(bool(deterministic)),
+                                      _view(dq), _view(dk), dtable.data_ptr() if want_table else None,
+                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                      _stream(stream)),
+               "streamkl_bwd_mod")
+    return dq, dk, dtable if want_table else None
 
 
 def streamkl_get_device_status():

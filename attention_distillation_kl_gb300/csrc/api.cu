@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include "host.cuh"
 #include "kernels.cuh"
 #include "streamkl.h"
 
@@ -164,6 +165,15 @@ int head_group_for(int BH, double bytes_per_head) {
 }
 
 }  // namespace
+
+namespace skl {
+
+int* status_word() { return status_ptr(); }
+int check_device() { return device_ok(); }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode_fn(); }
+int l2_head_group(int BH, double bytes_per_head) { return head_group_for(BH, bytes_per_head); }
+
+}  // namespace skl
 
 extern "C" {
 

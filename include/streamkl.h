@@ -265,6 +265,95 @@ int streamkl_bwd_both(const void* q1, const void* k1, const void* q2, const void
                       const float* dkl, int deterministic, float* dq1, float* dk1, float* dq2,
                       float* dk2, streamkl_stream_t stream);
 
+/*
+ * Attention KL over modified scores: the distributions of models that cap
+ * their scores, bias them by distance, or attend within packed documents or
+ * to a prefix.  (Not on the pages; the same divergence of two softmaxes, of
+ * other scores.)  With r = j - i - (NK - NQ), the key's position relative to
+ * the query's, each side's score is
+ *   S_ij = Y_ij + bias_h(r),   Y = softcap * tanh(scale * q.k / softcap),
+ *                              or scale * q.k with softcap = 0
+ *   bias_h(r) = -slopes[h] * |r|                  (slopes given)
+ *             = table[h][bucket(r)]               (table given)
+ *             = 0                                 (neither)
+ * and key j is visible to query i, for both sides alike, iff
+ *   (causal = 0, or r <= 0, or j < prefix[b])  and
+ *   (no ids, or doc_q[b][i] == doc_k[b][j] >= 0).
+ *
+ * bucket(r): with bidirectional = 0, n = num_buckets and d = max(-r, 0); with
+ *   bidirectional = 1, n = num_buckets / 2, d = |r|, and n is added where
+ *   r > 0.  With e = n / 2 (rounded down): d for d < e, else
+ *   min(n - 1, e + floor((n - e) ln(d / e) / ln(max_distance / e))).
+ */
+typedef struct streamkl_view { /* bf16 [B][heads][N][d]; strides in elements, the last dimension dense */
+  void* data;                  /* 16-byte aligned */
+  long long stride_b, stride_h, stride_n; /* multiples of 8, positive; not read where the dimension's size is 1 */
+} streamkl_view;
+
+typedef struct streamkl_side { /* one attention distribution */
+  streamkl_view q;             /* [B][H][NQ][d] */
+  streamkl_view k;             /* [B][HK][NK][d]; query head h reads key head h / (H / HK) */
+  int d;                       /* a multiple of 16 from 16 to 128 */
+  int HK;                      /* divides H */
+  float scale;                 /* 0 < scale <= 1e4 */
+  float softcap;               /* 0, or 1e-3 .. 1e6 */
+  const float* slopes;         /* device [H], finite, or null */
+  const float* table;          /* device [H][num_buckets] or null (not with slopes); an entry of the type's
+                                  lowest value masks its keys (anything beyond +-6.9e29 counts as that) */
+  int num_buckets;             /* with a table: 2 .. 64 (bidirectional: even, at least 4) */
+  int max_distance;            /* with a table: above e, at most 4096 */
+  int bidirectional;           /* 0 or 1 */
+} streamkl_side;
+
+typedef struct streamkl_visible {
+  int causal;        /* 0 or 1; bottom-right aligned.  NQ > NK is allowed: the first rows see nothing */
+  const int* prefix; /* device [B] or null; only with causal = 1.  Clamped to 0 .. NK */
+  const int* doc_q;  /* device [B][NQ] document ids or null; a negative id matches nothing (padding) */
+  const int* doc_k;  /* device [B][NK]; given exactly when doc_q is */
+} streamkl_visible;
+
+/*
+ * Forward: kl, lse1, lse2 (fp32 [B, H, NQ], contiguous).  A row that sees no
+ * key gets KL 0 and LSE -inf, and so does one whose every score on either
+ * side is below -6.9e5, which only a bias meant as a mask brings about.  What
+ * masked positions hold does not matter, NaN and infinities included.  num_splits as in streamkl_fwd_splitk, or 0
+ * for the library's choice (the same for the same sizes; ids are not
+ * counted).  workspace: device memory, 16-byte aligned, of at least
+ * streamkl_fwd_mod_workspace_bytes(...) bytes with the same arguments, owned
+ * by the caller, contents overwritten; may be null when that is 0.  Calls
+ * that may overlap on the GPU (graphs captured from them included) must not
+ * share one.  The query of bytes reads no device pointer, only which of
+ * them are null; it returns 0 for arguments the call would reject.
+ * Empty problems: B*H*NQ == 0 is a no-op; NK == 0 with rows is INVALID_ARG.
+ */
+size_t streamkl_fwd_mod_workspace_bytes(const streamkl_side* p1, const streamkl_side* p2,
+                                        const streamkl_visible* vis, int B, int H, int NQ, int NK, int num_splits);
+int streamkl_fwd_mod(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis, int B, int H,
+                     int NQ, int NK, int num_splits, void* workspace, size_t workspace_bytes, float* kl, float* lse1,
+                     float* lse2, streamkl_stream_t stream);
+
+/*
+ * Backward: the gradient of sum_i dkl_i KL_i for the side `mode` selects,
+ * from a forward over the same arguments.  dq [B][H][NQ][d] and
+ * dk [B][HK][NK][d] of that side are bf16 (the type of q and k), summed in
+ * fp32 and rounded once; they are fully overwritten.  dtable (fp32
+ * [H][num_buckets], contiguous, or null): the gradient of that side's table,
+ * in fp32 and added in a fixed order; INVALID_ARG when the side has none.
+ * Rows that see no key, and positions whose id is negative, get zeros and
+ * contribute none, whatever q, k and dkl hold there.  Other masked positions
+ * must hold finite values.  deterministic = 1: dq and dk bitwise
+ * reproducible (streamkl_bwd_gqa says how); dtable always is.  workspace as
+ * above, with streamkl_bwd_mod_workspace_bytes (table_grad: whether dtable
+ * is given).  With no query rows dk and dtable become zeros.
+ */
+size_t streamkl_bwd_mod_workspace_bytes(const streamkl_side* p1, const streamkl_side* p2,
+                                        const streamkl_visible* vis, int B, int H, int NQ, int NK, int mode,
+                                        int deterministic, int table_grad);
+int streamkl_bwd_mod(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis, int B, int H,
+                     int NQ, int NK, const float* kl, const float* lse1, const float* lse2, const float* dkl, int mode,
+                     int deterministic, const streamkl_view* dq, const streamkl_view* dk, float* dtable,
+                     void* workspace, size_t workspace_bytes, streamkl_stream_t stream);
+
 /* Static, NUL-terminated description of a status value. */
 const char* streamkl_status_string(int status);
 
