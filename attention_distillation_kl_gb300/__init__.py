@@ -9,6 +9,7 @@ Functions mirror the C ABI in ``include/streamkl.h`` and keep its names.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -420,7 +421,8 @@ def streamkl_bwd_both(q1, k1, q2, k2, scale1, scale2, causal, kl, lse1, lse2, dk
 
 
 def _view(t):
-    return _View(t.data_ptr(), *t.stride()[:3])
+    b, h, n, _ = t.stride()
+    return _View(t.data_ptr(), b, h, n)
 
 
 class AttnSide:
@@ -454,6 +456,7 @@ class AttnSide:
         if k.device != q.device:
             raise ValueError("q and k must be on the same device")
         self.q, self.k, self.slopes, self.table = q, k, slopes, table
+        self.device, self.rows, self.keys = q.device, tuple(q.shape[:3]), k.shape[2]
         self.num_buckets = 0 if table is None else table.shape[1]
         self._c = _Side(_view(q), _view(k), d, k.shape[1], float(scale), float(softcap),
                         None if slopes is None else slopes.data_ptr(), None if table is None else table.data_ptr(),
@@ -462,30 +465,67 @@ class AttnSide:
 
 def _mod_call(p1, p2, causal, prefix, doc_q, doc_k):
     """(B, H, NQ, NK, streamkl_visible) of a call, its shapes and devices checked."""
-    q, k = p1.q, p1.k
-    B, H, NQ, _ = q.shape
-    NK = k.shape[2]
-    if p2.q.shape[:3] != q.shape[:3] or p2.k.shape[2] != NK:
+    B, H, NQ = p1.rows
+    NK = p1.keys
+    if p2.rows != p1.rows or p2.keys != NK:
         raise ValueError("both sides must have the same B, H, NQ and NK")
-    if p2.q.device != q.device:
+    if p2.device != p1.device:
         raise ValueError("both sides must be on the same device")
+    if prefix is None and doc_q is None and doc_k is None:
+        return B, H, NQ, NK, _Visible(1 if causal else 0)
     for name, t, shape in (("prefix", prefix, (B,)), ("doc_q", doc_q, (B, NQ)), ("doc_k", doc_k, (B, NK))):
         if t is None:
             continue
-        if t.dtype != torch.int32 or t.device != q.device or not t.is_contiguous() or tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {q.device}")
-    return B, H, NQ, NK, _Visible(int(bool(causal)), *(None if t is None else t.data_ptr()
+        if t.dtype != torch.int32 or t.device != p1.device or not t.is_contiguous() or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {p1.device}")
+    return B, H, NQ, NK, _Visible(1 if causal else 0, *(None if t is None else t.data_ptr()
                                                         for t in (prefix, doc_q, doc_k)))
 
 
 def _mod_workspace(workspace, need, device, stream):
+    """(address, bytes, tensor to keep) of the workspace; torch's own when the caller gives none."""
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if stream is not None:
             workspace.record_stream(stream)
-    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+    elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _mod_rows(given, names, shape, device, stream):
+    """Per-row outputs, those given checked; the others made here, used on `stream` too."""
+    if given[0] is given[1] is given[2] is None and shape[0] * shape[1] * shape[2] % 4 == 0:
+        out = torch.empty((3,) + shape, dtype=torch.float32, device=device)  # each stays 16-byte aligned
+        if stream is not None:
+            out.record_stream(stream)
+        return out.unbind(0)
+    out = tuple(_out(t, shape, device, name) for t, name in zip(given, names))
+    _new_on(stream, *zip(given, out))
+    return out
+
+
+# The current stream's handle without a Stream object around it, where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _mod_stream(stream, device):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(stream)
+
+
+def _on_device(fn):
+    """Runs fn with the first side's device current (the library launches there)."""
+    @functools.wraps(fn)
+    def wrapped(p1, *a, **k):
+        if p1.device.index == torch.cuda.current_device():
+            return fn(p1, *a, **k)
+        with torch.cuda.device(p1.device):
+            return fn(p1, *a, **k)
+    return wrapped
 
 
 def _grad_out(t, shape, device, name):
@@ -505,11 +545,14 @@ def _new_on(stream, *pairs):
                 new.record_stream(stream)
 
 
+@_on_device
 def streamkl_fwd_mod_workspace_bytes(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, num_splits=0):
+    """Workspace bytes streamkl_fwd_mod needs for these arguments."""
     B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
     return int(lib().streamkl_fwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(num_splits)))
 
 
+@_on_device
 def streamkl_fwd_mod(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, num_splits=0, workspace=None, kl=None,
                      lse1=None, lse2=None, stream=None):
     """Per-row KL(P1 || P2), LSE1, LSE2 (fp32 [B, H, NQ]) of two AttnSides,
@@ -518,27 +561,26 @@ def streamkl_fwd_mod(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, 
     visible; rows that see none get KL 0 and LSE -inf.  num_splits 0: the
     library's choice."""
     B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
-    dev = p1.q.device
-    with torch.cuda.device(dev):
-        need = int(lib().streamkl_fwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(num_splits)))
-        workspace = _mod_workspace(workspace, need, dev, stream)
-        given = (kl, lse1, lse2)
-        out = tuple(_out(t, (B, H, NQ), dev, name) for t, name in zip(given, ("kl", "lse1", "lse2")))
-        _new_on(stream, *zip(given, out))
-        _check(lib().streamkl_fwd_mod(p1._c, p2._c, vis, B, H, NQ, NK, int(num_splits), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), out[0].data_ptr(),
-                                      out[1].data_ptr(), out[2].data_ptr(), _stream(stream)),
-               "streamkl_fwd_mod")
-    return out
+    dev, num_splits, c = p1.device, int(num_splits), lib()
+    need = c.streamkl_fwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, num_splits)
+    ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
+    kl, lse1, lse2 = _mod_rows((kl, lse1, lse2), ("kl", "lse1", "lse2"), (B, H, NQ), dev, stream)
+    _check(c.streamkl_fwd_mod(p1._c, p2._c, vis, B, H, NQ, NK, num_splits, ws, ws_bytes, kl.data_ptr(),
+                              lse1.data_ptr(), lse2.data_ptr(), _mod_stream(stream, dev)),
+           "streamkl_fwd_mod")
+    return kl, lse1, lse2
 
 
+@_on_device
 def streamkl_bwd_mod_workspace_bytes(p1, p2, mode=STREAMKL_GRAD_P2, causal=False, prefix=None, doc_q=None, doc_k=None,
                                      deterministic=False, table_grad=True):
+    """Workspace bytes streamkl_bwd_mod needs for these arguments."""
     B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
     return int(lib().streamkl_bwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(mode),
                                                       int(bool(deterministic)), int(bool(table_grad))))
 
 
+@_on_device
 def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=False, prefix=None, doc_q=None,
                      doc_k=None, deterministic=False, table_grad=True, dq=None, dk=None, dtable=None, workspace=None,
                      stream=None):
@@ -547,28 +589,27 @@ def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=
     False).  kl, lse1, lse2 come from streamkl_fwd_mod over the same arguments."""
     B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
     g = p2 if mode == STREAMKL_GRAD_P2 else p1
-    dev = g.q.device
+    dev, c = g.device, lib()
     for name, t in (("kl", kl), ("lse1", lse1), ("lse2", lse2), ("dkl", dkl)):
+        if t is None:
+            raise ValueError(f"{name} is missing")
         _out(t, (B, H, NQ), dev, name)
-    want_table = g.table is not None and (table_grad or dtable is not None)
     if dtable is not None and g.table is None:
         raise ValueError("dtable given for a side without a table")
-    with torch.cuda.device(dev):
-        need = int(lib().streamkl_bwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(mode),
-                                                          int(bool(deterministic)), int(want_table)))
-        workspace = _mod_workspace(workspace, need, dev, stream)
-        given = (dq, dk, dtable)
-        dq = _grad_out(dq, g.q.shape, dev, "dq")
-        dk = _grad_out(dk, g.k.shape, dev, "dk")
-        if want_table:
-            dtable = _out(dtable, (H, g.num_buckets), dev, "dtable")
-        _new_on(stream, *zip(given, (dq, dk, dtable)))
-        _check(lib().streamkl_bwd_mod(p1._c, p2._c, vis, B, H, NQ, NK, kl.data_ptr(), lse1.data_ptr(),
-                                      lse2.data_ptr(), dkl.data_ptr(), int(mode), int(bool(deterministic)),
-                                      _view(dq), _view(dk), dtable.data_ptr() if want_table else None,
-                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                      _stream(stream)),
-               "streamkl_bwd_mod")
+    want_table = g.table is not None and (table_grad or dtable is not None)
+    det = int(bool(deterministic))
+    need = c.streamkl_bwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(mode), det, int(want_table))
+    ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
+    given = (dq, dk, dtable)
+    dq = _grad_out(dq, g.q.shape, dev, "dq")
+    dk = _grad_out(dk, g.k.shape, dev, "dk")
+    if want_table:
+        dtable = _out(dtable, (H, g.num_buckets), dev, "dtable")
+    _new_on(stream, *zip(given, (dq, dk, dtable)))
+    _check(c.streamkl_bwd_mod(p1._c, p2._c, vis, B, H, NQ, NK, kl.data_ptr(), lse1.data_ptr(), lse2.data_ptr(),
+                              dkl.data_ptr(), int(mode), det, _view(dq), _view(dk),
+                              dtable.data_ptr() if want_table else None, ws, ws_bytes, _mod_stream(stream, dev)),
+           "streamkl_bwd_mod")
     return dq, dk, dtable if want_table else None
 
 

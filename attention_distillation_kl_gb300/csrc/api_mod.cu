@@ -72,27 +72,27 @@ int check_call(const streamkl_side* p1, const streamkl_side* p2, const streamkl_
   return STREAMKL_OK;
 }
 
-// A strided [B][heads][n][d] bf16 tensor: boxes of 64 elements x 128 rows,
+// A strided [B][heads][n][d] bf16 tensor: boxes of 64 elements x box_rows,
 // 128-byte swizzle; rows past n and columns past d read as zeros.
-bool map_bf16(CUtensorMap* m, const streamkl_view& v, int B, int heads, int n, int d) {
+bool map_bf16(CUtensorMap* m, const streamkl_view& v, int B, int heads, int n, int d, int box_rows = kTile) {
   auto fn = skl::tensor_map_encoder();
   if (fn == nullptr) return false;
   auto bytes = [&](long long s, int size) { return cuuint64_t(size <= 1 ? ((d + 7) / 8 * 16) : s * 2); };
   cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(n), cuuint64_t(heads), cuuint64_t(B)};
   cuuint64_t strides[3] = {bytes(v.stride_n, n), bytes(v.stride_h, heads), bytes(v.stride_b, B)};
-  cuuint32_t box[4] = {64u, cuuint32_t(kTile), 1, 1};
+  cuuint32_t box[4] = {64u, cuuint32_t(box_rows), 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(v.data), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The fp32 dQ of the workspace: boxes of 32 x 32, 128-byte swizzle.
-bool map_dq(CUtensorMap* m, float* p, int BH, int NQ, int pitch) {
+// Gradients in the workspace, [heads][n][pitch] fp32: boxes of 32 x 32, 128-byte swizzle.
+bool map_f32(CUtensorMap* m, float* p, int heads, int n, int pitch) {
   auto fn = skl::tensor_map_encoder();
   if (fn == nullptr) return false;
-  cuuint64_t dims[3] = {cuuint64_t(pitch), cuuint64_t(NQ), cuuint64_t(BH)};
-  cuuint64_t strides[2] = {cuuint64_t(pitch) * 4, cuuint64_t(NQ) * pitch * 4};
+  cuuint64_t dims[3] = {cuuint64_t(pitch), cuuint64_t(n), cuuint64_t(heads)};
+  cuuint64_t strides[2] = {cuuint64_t(pitch) * 4, cuuint64_t(n) * pitch * 4};
   cuuint32_t box[3] = {32, 32, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -100,9 +100,10 @@ bool map_dq(CUtensorMap* m, float* p, int BH, int NQ, int pitch) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_maps(skl::ModMaps* m, const streamkl_side& p1, const streamkl_side& p2, int B, int H, int NQ, int NK) {
-  return map_bf16(&m->q1, p1.q, B, H, NQ, p1.d) && map_bf16(&m->k1, p1.k, B, p1.HK, NK, p1.d) &&
-         map_bf16(&m->q2, p2.q, B, H, NQ, p2.d) && map_bf16(&m->k2, p2.k, B, p2.HK, NK, p2.d);
+bool make_maps(skl::ModMaps* m, const streamkl_side& p1, const streamkl_side& p2, int B, int H, int NQ, int NK,
+               int q_rows = kTile) {
+  return map_bf16(&m->q1, p1.q, B, H, NQ, p1.d, q_rows) && map_bf16(&m->k1, p1.k, B, p1.HK, NK, p1.d) &&
+         map_bf16(&m->q2, p2.q, B, H, NQ, p2.d, q_rows) && map_bf16(&m->k2, p2.k, B, p2.HK, NK, p2.d);
 }
 
 // Bytes handed out of a workspace, 16-byte aligned; with a null base it only counts.
@@ -116,6 +117,18 @@ struct Carver {
     return p;
   }
 };
+
+// A direction's first distance of each bucket: one distance each up to half
+// of them, then steps of the logarithm up to max_distance.  In 64 bits; a
+// border that is a whole number (the logarithm's steps meet one whenever the
+// ratio is a power) must not round up past itself.
+void bucket_borders(skl::ModPrepArgs::Table& t) {
+  const int n = t.both ? t.num_buckets / 2 : t.num_buckets, e = n / 2;
+  t.per_side = n;
+  for (int i = 0; i < n; ++i)
+    t.first[i] = i <= e ? i
+                        : int(std::ceil(e * std::pow(double(t.max_distance) / e, double(i - e) / (n - e)) * (1.0 - 1e-12)));
+}
 
 // The part of the workspace that both calls use: ids and lookup rows.
 void take_prep(Carver& c, skl::ModPrepArgs& a, const streamkl_side* const p[2], const streamkl_visible& vis, int B, int H, int NQ,
@@ -138,6 +151,7 @@ void take_prep(Carver& c, skl::ModPrepArgs& a, const streamkl_side* const p[2], 
     a.t[i].num_buckets = p[i]->num_buckets;
     a.t[i].max_distance = p[i]->max_distance;
     a.t[i].both = p[i]->bidirectional;
+    if (c.base != nullptr) bucket_borders(a.t[i]);
     a.t[i].near = c.take<float>(size_t(H) * skl::near_len(p[i]->max_distance));
     if (i == table_grad_side) a.t[i].bmap = c.take<int>(skl::near_len(p[i]->max_distance));
   }
@@ -193,10 +207,45 @@ FwdPlan fwd_plan(const streamkl_side* p1, const streamkl_side* p2, const streamk
   return f;
 }
 
-// 0 splits: the library's advice (ids are not looked at: they live on the device).
-int resolve_splits(int splits, int B, int H, int NQ, int NK, int causal) {
+// Query heads that share a key head on both sides also share a 128-row tile
+// when their rows fit: K is then read once for all of them.  As many as a
+// power of two allows; 32 heads on 8 key heads x 16 rows x 32768 keys,
+// d = 128: 121 us without, 53 with (19 splits of 4 heads each).
+int pack_shift(int H, int HK1, int HK2, int NQ) {
+  int s = 0;
+  while (s < 3 && (H / HK1) % (2 << s) == 0 && (H / HK2) % (2 << s) == 0 && NQ <= (kTile >> (s + 1))) ++s;
+  return s;
+}
+
+// The library's choice of key splits for `tiles_q` query tiles in all: with s
+// splits a launch takes ceil(CTAs / SMs) rounds of (key tiles / s + kFixed),
+// in units of one key tile of one CTA, plus the merge.  (Ids are not looked
+// at: they live on the device.)
+int resolve_splits(int splits, long long tiles_q, double rows, int NK) {
   if (splits != 0) return splits;
-  return std::max(1, streamkl_suggest_splits(B, H, std::min(NQ, NK), NK, causal));
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return 1;
+  const double ctas = double(tiles_q);
+  const int longest = tiles(NK);
+  if (ctas >= 2.0 * sms || longest < 4) return 1;  // rounds of whole rows
+  constexpr double kFixed = 3.0, kMerge = 4.0, kMergeRowsPerTile = 2.0e5;
+  int best = 1;
+  double best_t = std::ceil(ctas / sms) * (longest + kFixed);
+  for (int s = 2; s <= longest / 2 && s <= 1024; ++s) {
+    const double t = std::ceil(ctas * s / sms) * ((longest + s - 1) / s + kFixed) + kMerge + rows * s / kMergeRowsPerTile;
+    if (t < 0.98 * best_t) {
+      best = s;
+      best_t = t;
+    }
+  }
+  return best;
+}
+
+int fwd_splits(int splits, const streamkl_side& p1, const streamkl_side& p2, int B, int H, int NQ, int NK) {
+  const int shift = pack_shift(H, p1.HK, p2.HK, NQ);
+  return resolve_splits(splits, (long long)B * (H >> shift) * tiles(NQ), double(B) * H * NQ, NK);
 }
 
 struct BwdPlan {
@@ -205,7 +254,6 @@ struct BwdPlan {
   float* dk32 = nullptr;
   float* dtab = nullptr;
   unsigned* words = nullptr;  // kmax per key head, ticket, abort, turns
-  size_t dq_count = 0, dk_count = 0, word_count = 0;
   size_t bytes = 0;
   int pitch = 0;
 };
@@ -218,17 +266,17 @@ BwdPlan bwd_plan(const streamkl_side* p1, const streamkl_side* p2, const streamk
   const int gs = mode == STREAMKL_GRAD_P2 ? 1 : 0;
   const streamkl_side& g = *p[gs];
   f.pitch = (g.d + 31) / 32 * 32;
-  f.dq_count = size_t(B) * H * NQ * f.pitch;
-  f.dq32 = c.take<float>(f.dq_count);
-  if (g.HK != H) {
-    f.dk_count = size_t(B) * g.HK * NK * f.pitch;
-    f.dk32 = c.take<float>(f.dk_count);
-  }
+  // what starts at zero comes first, in one piece
+  f.dq32 = c.take<float>(size_t(B) * H * NQ * f.pitch);
+  const bool shared = g.HK != H;
+  if (deterministic)
+    f.words = c.take<unsigned>(size_t(B) * g.HK + (shared ? 2 + size_t(B) * g.HK * tiles(NK) : 0));
+  const size_t dk_count = size_t(B) * g.HK * NK * f.pitch;
+  if (shared && !deterministic) f.dk32 = c.take<float>(dk_count);
+  f.prep.zero = static_cast<uint4*>(ws);
+  f.prep.zero_words = c.used / 16;
+  if (shared && deterministic) f.dk32 = c.take<float>(dk_count);
   if (table) f.dtab = c.take<float>(size_t(B) * H * tiles(NK) * 8 * skl::kMaxBuckets);
-  if (deterministic) {
-    f.word_count = size_t(B) * g.HK + (g.HK != H ? 2 + size_t(B) * g.HK * tiles(NK) : 0);
-    f.words = c.take<unsigned>(f.word_count);
-  }
   take_prep(c, f.prep, p, vis, B, H, NQ, NK, table ? gs : -1);
   f.bytes = c.used;
   return f;
@@ -245,7 +293,7 @@ size_t streamkl_fwd_mod_workspace_bytes(const streamkl_side* p1, const streamkl_
   bool empty = false;
   if (check_call(p1, p2, vis, B, H, NQ, NK, false, &empty) != STREAMKL_OK || empty) return 0;
   if (num_splits < 0 || num_splits > 1024) return 0;
-  return fwd_plan(p1, p2, *vis, B, H, NQ, NK, resolve_splits(num_splits, B, H, NQ, NK, vis->causal), nullptr).bytes;
+  return fwd_plan(p1, p2, *vis, B, H, NQ, NK, fwd_splits(num_splits, *p1, *p2, B, H, NQ, NK), nullptr).bytes;
 }
 
 int streamkl_fwd_mod(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis, int B, int H, int NQ,
@@ -257,12 +305,13 @@ int streamkl_fwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
   if (num_splits < 0 || num_splits > 1024) return STREAMKL_INVALID_ARG;
   if (empty) return STREAMKL_OK;
   if (!kl || !lse1 || !lse2 || !aligned16(kl) || !aligned16(lse1) || !aligned16(lse2)) return STREAMKL_INVALID_ARG;
-  const int splits = resolve_splits(num_splits, B, H, NQ, NK, vis->causal);
+  const int splits = fwd_splits(num_splits, *p1, *p2, B, H, NQ, NK);
   const FwdPlan f = fwd_plan(p1, p2, *vis, B, H, NQ, NK, splits, workspace);
   if (f.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < f.bytes)) return STREAMKL_INVALID_ARG;
   if ((s = skl::check_device()) != STREAMKL_OK) return s;
   skl::ModMaps m{};
-  if (!make_maps(&m, *p1, *p2, B, H, NQ, NK)) return STREAMKL_CUDA_ERROR;
+  const int shift = pack_shift(H, p1->HK, p2->HK, NQ);
+  if (!make_maps(&m, *p1, *p2, B, H, NQ, NK, kTile >> shift)) return STREAMKL_CUDA_ERROR;
   int* st = skl::status_word();
   if (!st) return STREAMKL_CUDA_ERROR;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
@@ -283,8 +332,11 @@ int streamkl_fwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
   a.lse2 = lse2;
   a.partial = f.partial;
   a.status = st;
-  a.head_group = skl::l2_head_group(B * H, 2.0 * NK * (p1->d + p2->d));
-  if (skl::launch_fwd_mod(m, tile_width(p1->d), tile_width(p2->d), a, cs) != 0) return STREAMKL_CUDA_ERROR;
+  a.pack_shift = shift;
+  a.head_group = skl::l2_head_group(B * (H >> shift), 2.0 * NK * (p1->d + p2->d));
+  const int t2 = tile_width(p2->d);
+  if ((tile_width(p1->d) == 64 ? skl::launch_fwd_mod_64(m, t2, a, cs) : skl::launch_fwd_mod_128(m, t2, a, cs)) != 0)
+    return STREAMKL_CUDA_ERROR;
   if (splits == 1) return STREAMKL_OK;
   return as_status(skl::launch_mod_reduce(f.partial, B * H * NQ, splits, kl, lse1, lse2, cs));
 }
@@ -318,8 +370,10 @@ int streamkl_bwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
       return STREAMKL_CUDA_ERROR;
     if (B == 0 || H == 0 || NK == 0) return STREAMKL_OK;
     if (dk == nullptr || !view_ok(*dk, B, g.HK, NK)) return STREAMKL_INVALID_ARG;
-    return as_status(skl::launch_mod_convert(nullptr, B, g.HK, NK, g.d, 0, dk->data, B > 1 ? dk->stride_b : 0,
-                                             g.HK > 1 ? dk->stride_h : 0, NK > 1 ? dk->stride_n : 0, cs));
+    skl::ModFinishArgs fin{};
+    fin.rows[0] = {nullptr, B * g.HK, g.HK, NK, g.d, 0, static_cast<__nv_bfloat16*>(dk->data), B > 1 ? dk->stride_b : 0,
+                   g.HK > 1 ? dk->stride_h : 0, NK > 1 ? dk->stride_n : 0};
+    return as_status(skl::launch_mod_finish(fin, cs));
   }
   if (!kl || !lse1 || !lse2 || !dkl || !aligned16(kl) || !aligned16(lse1) || !aligned16(lse2) || !aligned16(dkl))
     return STREAMKL_INVALID_ARG;
@@ -329,7 +383,9 @@ int streamkl_bwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
   if (!workspace || !aligned16(workspace) || workspace_bytes < f.bytes) return STREAMKL_INVALID_ARG;
   if ((s = skl::check_device()) != STREAMKL_OK) return s;
   skl::ModMaps m{};
-  if (!make_maps(&m, *p1, *p2, B, H, NQ, NK) || !map_dq(&m.dq, f.dq32, B * H, NQ, f.pitch)) return STREAMKL_CUDA_ERROR;
+  if (!make_maps(&m, *p1, *p2, B, H, NQ, NK) || !map_f32(&m.dq, f.dq32, B * H, NQ, f.pitch))
+    return STREAMKL_CUDA_ERROR;
+  if (f.dk32 != nullptr && !map_f32(&m.dk, f.dk32, B * g.HK, NK, f.pitch)) return STREAMKL_CUDA_ERROR;
   int* st = skl::status_word();
   if (!st) return STREAMKL_CUDA_ERROR;
   skl::ModBwdArgs a{};
@@ -359,11 +415,8 @@ int streamkl_bwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
   a.dtab = f.dtab;
   a.status = st;
   a.head_group = skl::l2_head_group(B * H, 2.0 * NQ * (p1->d + p2->d) + 4.0 * NQ * f.pitch);
-  if (cudaMemsetAsync(f.dq32, 0, f.dq_count * 4, cs) != cudaSuccess) return STREAMKL_CUDA_ERROR;
-  if (f.dk32 != nullptr && !deterministic && cudaMemsetAsync(f.dk32, 0, f.dk_count * 4, cs) != cudaSuccess)
-    return STREAMKL_CUDA_ERROR;
+  if (skl::launch_mod_prep(f.prep, cs) != 0) return STREAMKL_CUDA_ERROR;
   if (deterministic) {
-    if (cudaMemsetAsync(f.words, 0, f.word_count * 4, cs) != cudaSuccess) return STREAMKL_CUDA_ERROR;
     if (skl::launch_kmax_strided(g.k.data, B, g.HK, NK, g.d, B > 1 ? g.k.stride_b : 0, g.HK > 1 ? g.k.stride_h : 0,
                                  NK > 1 ? g.k.stride_n : 0, f.words, cs) != 0)
       return STREAMKL_CUDA_ERROR;
@@ -377,20 +430,22 @@ int streamkl_bwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
       a.head_group = 1;
     }
   }
-  if (skl::launch_mod_prep(f.prep, cs) != 0) return STREAMKL_CUDA_ERROR;
   const int t1 = tile_width(p1->d), t2 = tile_width(p2->d);
   if ((mode == STREAMKL_GRAD_P2 ? skl::launch_bwd_mod_p2(m, t1, t2, a, cs) : skl::launch_bwd_mod_p1(m, t1, t2, a, cs)) != 0)
     return STREAMKL_CUDA_ERROR;
-  if (skl::launch_mod_convert(f.dq32, B, H, NQ, g.d, f.pitch, dq->data, B > 1 ? dq->stride_b : 0,
-                              H > 1 ? dq->stride_h : 0, NQ > 1 ? dq->stride_n : 0, cs) != 0)
-    return STREAMKL_CUDA_ERROR;
-  if (f.dk32 != nullptr &&
-      skl::launch_mod_convert(f.dk32, B, g.HK, NK, g.d, f.pitch, dk->data, a.dk_sb, a.dk_sh, a.dk_sn, cs) != 0)
-    return STREAMKL_CUDA_ERROR;
-  if (dtable != nullptr &&
-      skl::launch_mod_table_reduce(f.dtab, B, H, tiles(NK), g.num_buckets, dtable, cs) != 0)
-    return STREAMKL_CUDA_ERROR;
-  return STREAMKL_OK;
+  skl::ModFinishArgs fin{};
+  fin.rows[0] = {f.dq32, B * H, H, NQ, g.d, f.pitch, static_cast<__nv_bfloat16*>(dq->data), B > 1 ? dq->stride_b : 0,
+                 H > 1 ? dq->stride_h : 0, NQ > 1 ? dq->stride_n : 0};
+  if (f.dk32 != nullptr)
+    fin.rows[1] = {f.dk32, B * g.HK, g.HK, NK, g.d, f.pitch, static_cast<__nv_bfloat16*>(dk->data), a.dk_sb, a.dk_sh,
+                   a.dk_sn};
+  fin.dtab = f.dtab;
+  fin.B = B;
+  fin.H = H;
+  fin.nkt = tiles(NK);
+  fin.num_buckets = g.num_buckets;
+  fin.dtable = dtable;
+  return as_status(skl::launch_mod_finish(fin, cs));
 }
 
 }  // extern "C"

@@ -41,7 +41,8 @@ struct ModBwdLayout : BwdLayout<D1, D2, MODE> {
   static constexpr uint32_t oReady = Base::kBytes;  // barrier: K rows that match nothing are zeroed
   static constexpr uint32_t oRange = oReady + 8;    // first and last query tile with a shared id
   static constexpr uint32_t oBias = oRange + 8;     // HeadBias of the other side and of the gradient side
-  static constexpr uint32_t kAlloc = (oBias + 2 * sizeof(HeadBias) + 15) / 16 * 16 + 1024;
+  static constexpr uint32_t oNear = (oBias + 2 * sizeof(HeadBias) + 15) / 16 * 16;  // lookup rows, where they fit
+  static constexpr uint32_t kAlloc = oNear + 1024;
   static_assert(oReady % 8 == 0, "barriers are 8-byte aligned");
   static_assert(kAlloc <= 232448, "over the 227 KB shared memory limit");
 };
@@ -109,10 +110,13 @@ __device__ __forceinline__ void dx_chunk(const uint64_t (&yg)[8], const uint64_t
   const uint64_t CG = f2(p.cmul, p.cmul), W = f2(p.w, p.w), WO = f2(p.wo, p.wo), SG = f2(p.sg, p.sg),
                  CF = f2(p.capf, p.capf);
   uint64_t T = f2(0.f, 0.f);
+  Quad q{};
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
+    if (k % 2 == 0) q = bias_quad<HOW>(bias, 2 * k);
+    const uint64_t B2 = k % 2 == 0 ? q.lo : q.hi;
     uint64_t Y = yg[k];
-    const uint64_t EG = CAP ? f2_add(Y, bias_pair<HOW>(bias, 2 * k)) : f2_fma(Y, CG, bias_pair<HOW>(bias, 2 * k));
+    const uint64_t EG = CAP ? f2_add(Y, B2) : f2_fma(Y, CG, B2);
     float a, b, c, d;
     f2_split(EG, a, b);
     uint64_t D;
@@ -202,7 +206,8 @@ template <int D1, int D2, int MODE, bool CAP, int BIAS>
 __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
     bwd_mod_kernel(const __grid_constant__ CUtensorMap tq1, const __grid_constant__ CUtensorMap tk1,
                    const __grid_constant__ CUtensorMap tq2, const __grid_constant__ CUtensorMap tk2,
-                   const __grid_constant__ CUtensorMap tdq, const __grid_constant__ ModBwdArgs a) {
+                   const __grid_constant__ CUtensorMap tdq, const __grid_constant__ CUtensorMap tdk,
+                   const __grid_constant__ ModBwdArgs a) {
   using L = ModBwdLayout<D1, D2, MODE>;
   constexpr int DG = L::DG, DO = L::DO;
   constexpr bool kP2 = MODE == STREAMKL_GRAD_P2;
@@ -274,6 +279,13 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
     HeadBias* hb = reinterpret_cast<HeadBias*>(smem + L::oBias);
     if (threadIdx.x == 0) hb[0] = head_bias(kP2 ? a.s1 : a.s2, h);
     if (threadIdx.x == 32) hb[1] = head_bias(kP2 ? a.s2 : a.s1, h);
+    if (a.near_smem) {
+      float* rows = reinterpret_cast<float*>(smem + L::oNear);
+      __syncthreads();
+      near_to_smem(hb, 2, rows);
+      __syncthreads();
+      if (threadIdx.x == 0) near_in_smem(hb, 2, rows);
+    }
     if (!ids) __syncthreads();
   }
   if (ids) {
@@ -595,6 +607,23 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
       const float sgs = kP2 ? a.s2.scale : a.s1.scale;
       const float kmax = fixed ? __uint_as_float(a.kmax[bh / gg] << 16) : 0.f;
       float dkl_nx = 0.f, kl_nx = 0.f;
+      // row `lane` of 32 rows x 32 columns, reduce-added at (x, y, z)
+      auto push_box = [&](const CUtensorMap* map, const uint32_t (&v)[32], int x, int y, int z) {
+        const uint32_t box = stage + (nred % kDqBoxes) * kDqBoxBytes;
+        if (!SKL_CHECK(a.status, box + kDqBoxBytes <= sb + L::oBar)) return;
+        if (lane == 0) bulk_wait_read_le<kDqBoxes - 1>();  // the box used kDqBoxes reduces ago has been read
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          st_shared_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_reduce_add_3d(map, box, x, y, z);
+          bulk_commit();
+        }
+        ++nred;
+      };
       auto load_row = [&](int i) {
         const int qi = (qt_lo + i) * kTile + row;
         dkl_nx = kl_nx = 0.f;
@@ -622,25 +651,10 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
         const uint64_t ME = f2(me, me);
         if (i + 1 < n) load_row(i + 1);
         uint32_t v[kChunks][32];
+        // nothing to add past the row length or past NQ, and then no box is
+        // touched (the box count must match the committed reduce groups)
         auto put_box = [&](int c0) {
-          // nothing to add past the row length or past NQ, and then no box is
-          // touched (the box count must match the committed reduce groups)
-          if (c0 * 32 >= a.pitch || r0 >= a.NQ) return;
-          const uint32_t box = stage + (nred % kDqBoxes) * kDqBoxBytes;
-          if (!SKL_CHECK(a.status, box + kDqBoxBytes <= sb + L::oBar)) return;
-          if (lane == 0) bulk_wait_read_le<kDqBoxes - 1>();  // the box used kDqBoxes reduces ago has been read
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            st_shared_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4), v[c0][4 * c], v[c0][4 * c + 1],
-                         v[c0][4 * c + 2], v[c0][4 * c + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_reduce_add_3d(&tdq, box, c0 * 32, r0, bh);
-            bulk_commit();
-          }
-          ++nred;
+          if (c0 * 32 < a.pitch && r0 < a.NQ) push_box(&tdq, v[c0], c0 * 32, r0, bh);
         };
         if constexpr (kChunks == 4) {
           tmem_ld2x32(t_dq + lane_off, t_dq + lane_off + 32, v[0], v[1]);
@@ -660,10 +674,22 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
           put_box(c);
         }
       }
+      // dK of a key head that other CTAs add to as well, any order: the same boxes
+      if (a.dk32 != nullptr && a.dk_turns == nullptr && n > 0 && mbar_wait_warp(bar(L::B_DKFULL), 0, ctl)) {
+        tc_fence_after();
+        const int r0 = k0 + w4 * 32;
+#pragma unroll 1
+        for (int ch = 0; ch < kChunks; ++ch) {
+          if (ch * 32 >= a.pitch || r0 >= a.NK) break;
+          uint32_t v[32];
+          tmem_ld32(t_dk + lane_off + ch * 32, v);
+          push_box(&tdk, v, ch * 32, r0, bh / gg);
+        }
+      }
       if (lane == 0) bulk_wait_all();  // every reduce has landed before the CTA exits
     }
-    // dK: bf16 where this CTA owns it, else fp32 into the workspace (added
-    // with atomics, or, deterministic, in head order)
+    // dK otherwise: bf16 where this CTA owns it, or, deterministic with
+    // shared key heads, fp32 into the workspace in head order
     const int kj = k0 + row;
     const int hk = bh / gg;
     float* dst32 = a.dk32 + (size_t(hk) * a.NK + kj) * a.pitch;
@@ -702,14 +728,14 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
         }
       }
     };
-    if (a.dk_turns == nullptr) {
+    if (a.dk32 == nullptr) {
       if (n > 0 && mbar_wait_warp(bar(L::B_DKFULL), 0, ctl)) {
         tc_fence_after();
-        write_dk(gg == 1 ? kDkStore : kDkAtomic, false);
-      } else if (n == 0 && a.dk32 == nullptr) {
+        write_dk(kDkStore, false);
+      } else if (n == 0) {
         write_dk(kDkStore, true);  // no query row sees this key tile
       }
-    } else {
+    } else if (a.dk_turns != nullptr) {
       // deterministic, grouped key heads: head m of a group waits until the
       // (key head, key tile) count reads m, then stores (m = 0) or adds
       const int member = bh % gg;
@@ -749,10 +775,14 @@ template <int D1, int D2, int MODE, bool CAP, int BIAS>
 int launch_bwd_mod_k(const ModMaps& m, const ModBwdArgs& a, cudaStream_t st) {
   using L = ModBwdLayout<D1, D2, MODE>;
   auto kern = bwd_mod_kernel<D1, D2, MODE, CAP, BIAS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  ModBwdArgs b = a;
+  const size_t near = BIAS != kNoBias ? near_smem_bytes(a.s1, a.s2, 1) : 0;
+  b.near_smem = near > 0 && L::kAlloc + near <= 232448;
+  const int bytes = int(L::kAlloc + (b.near_smem ? near : 0));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   dim3 grid((a.NK + kTile - 1) / kTile, a.B * a.H);
-  kern<<<grid, L::kThreads, L::kAlloc, st>>>(m.q1, m.k1, m.q2, m.k2, m.dq, a);
+  kern<<<grid, L::kThreads, bytes, st>>>(m.q1, m.k1, m.q2, m.k2, m.dq, m.dk, b);
   return cudaGetLastError();
 }
 

@@ -1,6 +1,5 @@
 // Forward over modified scores (see mod_common.cuh): KL, LSE1, LSE2 per query
-// row in one pass over the visible key tiles, plus the small kernels around
-// it (lookup rows of learned tables, id ranges of tiles, key-split merge).
+// row in one pass over the visible key tiles, and the merge of key splits.
 //
 // The pipeline is the plain forward's (fwd_kernel.cuh): one CTA per 128-row
 // query tile; a TMA warp streams K1_j, K2_j through a ring; the MMA warp
@@ -28,6 +27,8 @@
 // anyway.  With ids, the tiles outside the first and last that share an id
 // with the query tile are never loaded, and tiles whose ids are all the same
 // take no mask.
+#pragma once
+
 #include <climits>
 
 #include "mod_common.cuh"
@@ -55,12 +56,18 @@ struct ModFwdLayout {
   static constexpr int kNumBars = 1 + 2 * kStages + 4 + 1;
   static constexpr uint32_t oMisc = oBar + kNumBars * 8;  // tmem base, abort flag
   static constexpr uint32_t oRange = oMisc + 8;           // first and last key tile with a shared id
-  static constexpr uint32_t oBias = (oRange + 8 + 15) / 16 * 16;  // HeadBias of both sides
-  static constexpr uint32_t oMerge = oBias + (2 * sizeof(HeadBias) + 15) / 16 * 16;
-  static constexpr uint32_t kAlloc = oMerge + (kWGs - 1) * kTile * 5 * 4 + 1024;
+  static constexpr uint32_t oBias = (oRange + 8 + 15) / 16 * 16;  // HeadBias of both sides, of up to 8 heads
+  static constexpr uint32_t oMerge = oBias + 16 * sizeof(HeadBias);
+  static_assert(sizeof(HeadBias) % 16 == 0, "what follows stays aligned");
+  static constexpr uint32_t oNear = oMerge + (kWGs - 1) * kTile * 5 * 4;  // lookup rows, where they fit
+  static constexpr uint32_t kAlloc = oNear + 1024;
   static_assert(kStages >= 2, "shared memory ring needs two stages");
+  static_assert(kCols == 32, "one word of visible bits for each row and tile");
   static_assert(kAlloc <= 232448, "over the 227 KB shared memory limit");
 };
+
+// The biases a kernel knows: none, slopes only, tables too.
+enum { kNone = 0, kLinear = 1, kAny = 2 };
 
 constexpr float kLow = -1.0e6f;
 
@@ -118,30 +125,46 @@ __device__ __forceinline__ void move_refs(ModStats& st, float m1, float m2) {
   st.m2 = m2;
 }
 
-// A chunk with masked columns (those not in bits), the first of a row, or
-// one above its references (r1, r2: what its scores are relative to): the
-// references move to its visible maxima where the row has seen nothing or
-// these are above.  What a masked column holds does not matter.
+constexpr float kGone = -3.0e38f;  // 2^ that is 0 against any reference, and differences of it are 0
+
 template <int N>
-__device__ __forceinline__ void fold_chunk(ModStats& st, uint64_t (&e1)[N], uint64_t (&e2)[N], float r1, float r2,
-                                           uint32_t bits) {
-  if (bits == 0u) return;
-  constexpr float kGone = -3.0e38f;  // 2^ that is 0 against any reference, and differences of it are 0
-  float t1 = -INFINITY, t2 = -INFINITY;
+__device__ __forceinline__ void mask_products(uint32_t (&x1)[N], uint32_t (&x2)[N], uint32_t bits) {
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (!((bits >> k) & 1u)) x1[k] = x2[k] = 0u;
+}
+template <int N>
+__device__ __forceinline__ void mask_scores(uint64_t (&e1)[N], uint64_t (&e2)[N], uint32_t bits) {
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const bool va = (bits >> (2 * k)) & 1u, vb = (bits >> (2 * k + 1)) & 1u;
     float a, b, c, d;
     f2_split(e1[k], a, b);
     f2_split(e2[k], c, d);
-    a = va ? a : kGone;
-    b = vb ? b : kGone;
-    c = va ? c : kGone;
-    d = vb ? d : kGone;
+    e1[k] = f2(va ? a : kGone, vb ? b : kGone);
+    e2[k] = f2(va ? c : kGone, vb ? d : kGone);
+  }
+}
+
+// A chunk with masked columns (those not in bits), the first of a row, or
+// one above its references (r1, r2: what its scores are relative to): the
+// references move to its visible maxima where the row has seen nothing or
+// these are above.  What a masked column holds does not matter.
+template <bool MASK, int N>
+__device__ __forceinline__ void fold_chunk(ModStats& st, uint64_t (&e1)[N], uint64_t (&e2)[N], float r1, float r2,
+                                           uint32_t bits) {
+  if (MASK) {
+    if (bits == 0u) return;
+    mask_scores(e1, e2, bits);
+  }
+  float t1 = -INFINITY, t2 = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    float a, b, c, d;
+    f2_split(e1[k], a, b);
+    f2_split(e2[k], c, d);
     t1 = max3(t1, a, b);
     t2 = max3(t2, c, d);
-    e1[k] = f2(a, b);
-    e2[k] = f2(c, d);
   }
   float m1 = rintf(t1) + r1, m2 = rintf(t2) + r2;
   if (st.l1 == 0.f) {
@@ -163,32 +186,40 @@ __device__ __forceinline__ void fold_chunk(ModStats& st, uint64_t (&e1)[N], uint
   add_chunk(st, sum2(s.l1a, s.l1b), sum2(s.l2a, s.l2b), sum2(s.aa, s.ab));
 }
 
-// The whole of it for the 16 columns at ts.  Called by whole warps.
-template <bool CAP1, bool CAP2, bool BIASED>
-__device__ __forceinline__ void fold_tmem(ModStats& st, uint32_t ts, const ModFwdArgs& a, const SideRegs& p1,
-                                          const SideRegs& p2, const HeadBias* hb, const TileBias& tb1,
-                                          const TileBias& tb2, int r0, uint32_t bits) {
-  const float ref1 = chunk_ref(st.m1), ref2 = chunk_ref(st.m2);
-  RowBias rb1{0.f, 0.f, -ref1, -ref1, nullptr}, rb2{0.f, 0.f, -ref2, -ref2, nullptr};
-  if (BIASED) {
-    rb1 = row_bias(hb[0], tb1, r0, -ref1);
-    rb2 = row_bias(hb[1], tb2, r0, -ref2);
+// The whole of it for the row's kCols columns at ts, 16 at a time (they leave
+// the most registers free).  MASK = false: every column is visible.  Called
+// by whole warps.
+template <int kCols, bool CAP1, bool CAP2, int KIND, bool MASK>
+__device__ __forceinline__ void fold_tile(ModStats& st, uint32_t ts, const ModFwdArgs& a, const SideRegs& p1,
+                                          const SideRegs& p2, const HeadBias* hb, int rmin, int r0, uint32_t bits) {
+  constexpr bool kBiased = KIND != kNone;
+  TileBias tb1{kZero, 0.f, 0.f}, tb2 = tb1;
+  if (kBiased) {
+    tb1 = tile_bias(hb[0], rmin, rmin + 2 * kTile - 2);
+    tb2 = tile_bias(hb[1], rmin, rmin + 2 * kTile - 2);
   }
-  uint32_t x1[16], x2[16];
-  uint64_t e1[8], e2[8];
-  tmem_ld2x16(ts, ts + 128, x1, x2);
-  if (CAP1 || CAP2) {  // a masked product must not choose the path below
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (!((bits >> k) & 1u)) x1[k] = x2[k] = 0u;
+#pragma unroll 1
+  for (int c = 0; c < kCols; c += 16, bits >>= 16) {
+    const uint32_t part = MASK ? bits & 0xffffu : 0xffffu;
+    const float ref1 = chunk_ref(st.m1), ref2 = chunk_ref(st.m2);
+    RowBias rb1{0.f, 0.f, -ref1, -ref1, nullptr}, rb2{0.f, 0.f, -ref2, -ref2, nullptr};
+    if (kBiased) {
+      rb1 = row_bias(hb[0], tb1, r0 + c, -ref1);
+      rb2 = row_bias(hb[1], tb2, r0 + c, -ref2);
+    }
+    uint32_t x1[16], x2[16];
+    uint64_t e1[8], e2[8];
+    tmem_ld2x16(ts + c, ts + c + 128, x1, x2);
+    if (MASK && (CAP1 || CAP2)) mask_products(x1, x2, part);  // a masked product must not choose the path below
+    const float z1 = scores<CAP1, kBiased>(x1, e1, p1, tb1.how, rb1);
+    const float z2 = scores<CAP2, kBiased>(x2, e2, p2, tb2.how, rb2);
+    if ((CAP1 || CAP2) && __any_sync(0xffffffffu, z1 > a.s1.zmax || z2 > a.s2.zmax)) {  // beyond half of a cap
+      tmem_ld2x16(ts + c, ts + c + 128, x1, x2);
+      scores_any<CAP1, kBiased>(x1, e1, a.s1, tb1.how, rb1);
+      scores_any<CAP2, kBiased>(x2, e2, a.s2, tb2.how, rb2);
+    }
+    fold_chunk<MASK>(st, e1, e2, ref1, ref2, part);
   }
-  const float z1 = scores<CAP1, BIASED>(x1, e1, p1, tb1.how, rb1), z2 = scores<CAP2, BIASED>(x2, e2, p2, tb2.how, rb2);
-  if ((CAP1 || CAP2) && __any_sync(0xffffffffu, z1 > a.s1.zmax || z2 > a.s2.zmax)) {  // a score beyond half of its cap
-    tmem_ld2x16(ts, ts + 128, x1, x2);
-    scores_any<CAP1, BIASED>(x1, e1, a.s1, tb1.how, rb1);
-    scores_any<CAP2, BIASED>(x2, e2, a.s2, tb2.how, rb2);
-  }
-  fold_chunk(st, e1, e2, ref1, ref2, bits);
 }
 
 // Adds another part of the row; both have seen a key.
@@ -208,14 +239,13 @@ __device__ __forceinline__ void write_row(const ModStats& st, float* kl, float* 
   *kl = seen ? fmaf(kLn2, st.acc / st.l1, logf(st.l2 / st.l1)) : 0.f;
 }
 
-// The row's kCols columns of a tile with every column visible, 16 at a time
-// against the references as they stand.  Returns false with the state
+// The row's kCols columns of a tile, 16 at a time, against the references as
+// they stand; MASK: only the columns in bits.  Returns false with the state
 // untouched where that is not exact: the row has no usable reference, a sum
 // reached 2^64 or a score is beyond half of its cap.
-template <int kCols, bool CAP1, bool CAP2, bool BIASED>
+template <int kCols, bool CAP1, bool CAP2, int HOW1, int HOW2, bool MASK>
 __device__ __forceinline__ bool add_tile(ModStats& st, uint32_t ts, const SideRegs& s1, const SideRegs& s2, float zmax1,
-                                         float zmax2, RowBias rb1, RowBias rb2) {
-  constexpr int kHow = BIASED ? kFlat : kZero;
+                                         float zmax2, RowBias rb1, RowBias rb2, uint32_t bits) {
   ChunkSums s{};
   float z1 = 0.f, z2 = 0.f;
 #pragma unroll
@@ -223,12 +253,12 @@ __device__ __forceinline__ bool add_tile(ModStats& st, uint32_t ts, const SideRe
     uint32_t x1[16], x2[16];
     uint64_t e1[8], e2[8];
     tmem_ld2x16(ts + c, ts + c + 128, x1, x2);
-    z1 = fmaxf(z1, scores_how<CAP1, kHow>(x1, e1, s1, rb1));
-    z2 = fmaxf(z2, scores_how<CAP2, kHow>(x2, e2, s2, rb2));
-    if (BIASED) {
-      rb1 = further(rb1, 16);
-      rb2 = further(rb2, 16);
-    }
+    if (MASK && (CAP1 || CAP2)) mask_products(x1, x2, bits >> c);
+    z1 = fmaxf(z1, scores_how<CAP1, HOW1>(x1, e1, s1, rb1));
+    z2 = fmaxf(z2, scores_how<CAP2, HOW2>(x2, e2, s2, rb2));
+    if (HOW1 != kZero) rb1 = further(rb1, 16);
+    if (HOW2 != kZero) rb2 = further(rb2, 16);
+    if (MASK) mask_scores(e1, e2, bits >> c);
     sums_all(e1, e2, s);
   }
   const float l1 = sum2(s.l1a, s.l1b), l2 = sum2(s.l2a, s.l2b);
@@ -236,12 +266,28 @@ __device__ __forceinline__ bool add_tile(ModStats& st, uint32_t ts, const SideRe
   ok = ok && l1 < 18446744073709551616.f && l2 < 18446744073709551616.f;  // 2^64
   if (CAP1) ok = ok && z1 <= zmax1;
   if (CAP2) ok = ok && z2 <= zmax2;
+  if (MASK) ok = ok || bits == 0u;
   ok = __all_sync(0xffffffffu, ok);
-  if (ok) add_chunk(st, l1, l2, sum2(s.aa, s.ab));
+  if (ok && (!MASK || bits != 0u)) add_chunk(st, l1, l2, sum2(s.aa, s.ab));
   return ok;
 }
 
-template <int D1, int D2, bool CAP1, bool CAP2, bool BIASED>
+// The same by the tile's kinds of bias (neither kFold).
+template <int kCols, bool CAP1, bool CAP2, int KIND, bool MASK>
+__device__ __forceinline__ bool add_tile_how(ModStats& st, uint32_t ts, const SideRegs& s1, const SideRegs& s2,
+                                             float zmax1, float zmax2, int how1, int how2, const RowBias& rb1,
+                                             const RowBias& rb2, uint32_t bits) {
+  if (KIND == kNone) return add_tile<kCols, CAP1, CAP2, kZero, kZero, MASK>(st, ts, s1, s2, zmax1, zmax2, rb1, rb2, bits);
+  if (KIND == kLinear) return add_tile<kCols, CAP1, CAP2, kFlat, kFlat, MASK>(st, ts, s1, s2, zmax1, zmax2, rb1, rb2, bits);
+  if (how1 != kLook)
+    return how2 != kLook ? add_tile<kCols, CAP1, CAP2, kFlat, kFlat, MASK>(st, ts, s1, s2, zmax1, zmax2, rb1, rb2, bits)
+                         : add_tile<kCols, CAP1, CAP2, kFlat, kLook, MASK>(st, ts, s1, s2, zmax1, zmax2, rb1, rb2, bits);
+  return how2 != kLook ? add_tile<kCols, CAP1, CAP2, kLook, kFlat, MASK>(st, ts, s1, s2, zmax1, zmax2, rb1, rb2, bits)
+                       : add_tile<kCols, CAP1, CAP2, kLook, kLook, MASK>(st, ts, s1, s2, zmax1, zmax2, rb1, rb2, bits);
+}
+
+// MASKED: some tile besides a row's first may need a mask (ids, a prefix).
+template <int D1, int D2, bool CAP1, bool CAP2, int KIND, bool MASKED>
 __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
     fwd_mod_kernel(const __grid_constant__ CUtensorMap tq1, const __grid_constant__ CUtensorMap tk1,
                    const __grid_constant__ CUtensorMap tq2, const __grid_constant__ CUtensorMap tk2,
@@ -256,9 +302,13 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   const int nqt = (a.NQ + kTile - 1) / kTile, nkt_rows = (a.NK + kTile - 1) / kTile;
-  int bh, t;
-  grouped_unit(int(blockIdx.y) * int(gridDim.x) + int(blockIdx.x), a.B * a.H, nqt, a.head_group, bh, t);
+  // a unit is a query tile of one head, or the rows of 2^pack_shift heads
+  int unit, t;
+  grouped_unit(int(blockIdx.y) * int(gridDim.x) + int(blockIdx.x), a.B * (a.H >> a.pack_shift), nqt, a.head_group,
+               unit, t);
+  const int bh = unit << a.pack_shift;  // the (first) head
   const int b = bh / a.H, h = bh - b * a.H;
+  const int pack_rows = kTile >> a.pack_shift;
   const int qt = a.vis.causal ? (nqt - 1 - t) : t;  // longest rows first
   const int split = blockIdx.z;
   const int q0 = qt * kTile;
@@ -293,9 +343,16 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
     range[1] = -1;
     fence_barrier_init();
   }
-  HeadBias* hb = reinterpret_cast<HeadBias*>(smem + L::oBias);
-  if (threadIdx.x == 32) hb[0] = head_bias(a.s1, h);
-  if (threadIdx.x == 64) hb[1] = head_bias(a.s2, h);
+  HeadBias* hbs = reinterpret_cast<HeadBias*>(smem + L::oBias);  // two for each head
+  if (KIND != kNone && threadIdx.x < (2u << a.pack_shift))
+    hbs[threadIdx.x] = head_bias(threadIdx.x & 1 ? a.s2 : a.s1, h + int(threadIdx.x >> 1));
+  float* near_rows = reinterpret_cast<float*>(smem + L::oNear);
+  if (KIND == kAny && a.near_smem) {
+    __syncthreads();
+    near_to_smem(hbs, 2 << a.pack_shift, near_rows);
+    __syncthreads();
+    if (threadIdx.x == 0) near_in_smem(hbs, 2 << a.pack_shift, near_rows);
+  }
   if (warp == L::kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -341,8 +398,10 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
       tma_prefetch_desc(&tq2);
       tma_prefetch_desc(&tk2);
       mbar_arrive_expect_tx(bar_q, L::kQ1 + L::kQ2);
-      load_tile<T1>(sb + L::oQ1, &tq1, bar_q, q0, h, b);
-      load_tile<T2>(sb + L::oQ2, &tq2, bar_q, q0, h, b);
+      for (int s = 0; s < (1 << a.pack_shift); ++s) {
+        load_tile<T1>(sb + L::oQ1 + s * pack_rows * T1::kRowBytes, &tq1, bar_q, q0, h + s, b);
+        load_tile<T2>(sb + L::oQ2 + s * pack_rows * T2::kRowBytes, &tq2, bar_q, q0, h + s, b);
+      }
       int issued = 0;
       for (int j = 0; j < nkt; ++j) {
         const int s = j % L::kStages;
@@ -398,48 +457,84 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
     // ---------------------------------------------------------------- statistics
     const int wg = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
-    const int grow = q0 + row;
+    const int slot = row / pack_rows;      // the row's head is h + slot
+    const int grow = q0 + row - slot * pack_rows;  // its query
+    const HeadBias* hb = hbs + 2 * slot;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const int col = wg * L::kCols;
-    const bool ids = a.vis.ids_q != nullptr;
+    const bool ids = MASKED && a.vis.ids_q != nullptr;
     const int id = ids ? a.vis.ids_q[size_t(b) * nqt * kTile + grow] : 0;
     const SideRegs p1 = side_regs<CAP1>(a.s1), p2 = side_regs<CAP2>(a.s2);
+    const bool idle = __all_sync(0xffffffffu, grow >= a.NQ);  // this warp's rows are all past NQ
     ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < nkt; ++j) {
+    // The first tiles, general and masked: the last keys, the diagonal, and
+    // at least one, which gives the row its references.  (With ids or a
+    // prefix any tile may need a mask.)
+    int npeel = 1;
+    if (!MASKED) {
+      int full = a.NK / kTile;
+      if (a.vis.causal) full = min(full, max(q0 + off + 1, 0) / kTile);
+      npeel = max(1, kt_hi - full);
+    }
+    npeel = min(npeel, nkt);
+    for (int j = 0; j < npeel; ++j) {
+      const int i = j & 1;
+      const int kt = kt_hi - 1 - j, k0 = kt * kTile;
+      const bool same = !MASKED || !ids || tiles_same(tq, a.vis.tiles_k[size_t(b) * nkt_rows + kt]);
+      const uint32_t bits = visible_bits<32>(grow, k0 + col, off, a.NK, a.vis.causal, prefix, id,
+                                             same ? nullptr : a.vis.ids_k + size_t(b) * nkt_rows * kTile + k0 + col);
+      if (!mbar_wait_warp(bar_sfull(i), (j >> 1) & 1, ctl)) break;
+      tc_fence_after();
+      if (!idle)
+        fold_tile<L::kCols, CAP1, CAP2, KIND, true>(st, tmem + lane_off + uint32_t(i * 256 + col), a, p1, p2, hb,
+                                                    k0 - (q0 + kTile - 1 + off), k0 + col - (grow + off), bits);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_sempty(i));
+    }
+    // the id range of the tile after this one is fetched a tile ahead
+    auto range_of = [&](int kt) { return ids ? a.vis.tiles_k[size_t(b) * nkt_rows + max(kt, 0)] : int4{0, 0, 1, 0}; };
+    int4 tk = range_of(kt_hi - 1 - npeel);
+    for (int j = npeel; j < nkt; ++j) {
       const int i = j & 1;
       const int kt = kt_hi - 1 - j, k0 = kt * kTile;
       // the tile's relative positions: key k0 + c against query q0 + r
       const int rmin = k0 - (q0 + kTile - 1 + off);
       const int r0 = k0 + col - (grow + off);
-      const bool same = !ids || tiles_same(tq, a.vis.tiles_k[size_t(b) * nkt_rows + kt]);
-      const bool need_mask = (k0 + kTile > a.NK) || !same ||
-                             (a.vis.causal && rmin + 2 * kTile - 2 > 0 && k0 + kTile > prefix);
       const uint32_t ts = tmem + lane_off + uint32_t(i * 256 + col);
-      TileBias tb1{kZero, 0.f, 0.f}, tb2 = tb1;
-      if (BIASED) {
-        tb1 = tile_bias(hb[0], rmin, rmin + 2 * kTile - 2);
-        tb2 = tile_bias(hb[1], rmin, rmin + 2 * kTile - 2);
+      bool need_mask = false;
+      uint32_t bits = 0xffffffffu;
+      if (MASKED) {
+        const bool same = !ids || tiles_same(tq, tk);
+        tk = range_of(kt - 1);
+        need_mask = (k0 + kTile > a.NK) || !same || (a.vis.causal && rmin + 2 * kTile - 2 > 0 && k0 + kTile > prefix);
+        if (need_mask)
+          bits = visible_bits<32>(grow, k0 + col, off, a.NK, a.vis.causal, prefix, id,
+                                  same ? nullptr : a.vis.ids_k + size_t(b) * nkt_rows * kTile + k0 + col);
       }
-      bool general = need_mask || j == 0 || tb1.how > kFlat || tb2.how > kFlat;
+      RowBias rb1{0.f, 0.f, -st.m1, -st.m1, nullptr}, rb2{0.f, 0.f, -st.m2, -st.m2, nullptr};
+      int how1 = kZero, how2 = kZero;
+      if (KIND != kNone) {
+        const TileBias tb1 = tile_bias(hb[0], rmin, rmin + 2 * kTile - 2);
+        const TileBias tb2 = tile_bias(hb[1], rmin, rmin + 2 * kTile - 2);
+        how1 = tb1.how;
+        how2 = tb2.how;
+        rb1 = row_bias(hb[0], tb1, r0, -st.m1);
+        rb2 = row_bias(hb[1], tb2, r0, -st.m2);
+      }
       if (!mbar_wait_warp(bar_sfull(i), (j >> 1) & 1, ctl)) break;
       tc_fence_after();
-      if (!general) {
-        RowBias rb1{0.f, 0.f, -st.m1, -st.m1, nullptr}, rb2{0.f, 0.f, -st.m2, -st.m2, nullptr};
-        if (BIASED) {
-          rb1 = row_bias(hb[0], tb1, r0, -st.m1);
-          rb2 = row_bias(hb[1], tb2, r0, -st.m2);
+      if (!idle) {
+        bool ok = KIND == kNone || (how1 != kFold && how2 != kFold);
+        if (ok) {
+          if (MASKED && need_mask)
+            ok = add_tile_how<L::kCols, CAP1, CAP2, KIND, true>(st, ts, p1, p2, a.s1.zmax, a.s2.zmax, how1, how2, rb1,
+                                                                rb2, bits);
+          else
+            ok = add_tile_how<L::kCols, CAP1, CAP2, KIND, false>(st, ts, p1, p2, a.s1.zmax, a.s2.zmax, how1, how2, rb1,
+                                                                 rb2, bits);
         }
-        general = !add_tile<L::kCols, CAP1, CAP2, BIASED>(st, ts, p1, p2, a.s1.zmax, a.s2.zmax, rb1, rb2);
-      }
-      if (general) {
-#pragma unroll 1
-        for (int c = 0; c < L::kCols; c += 16) {
-          uint32_t bits = 0xffffu;
-          if (need_mask)
-            bits = visible_bits<16>(grow, k0 + col + c, off, a.NK, a.vis.causal, prefix, id,
-                                    same ? nullptr : a.vis.ids_k + size_t(b) * nkt_rows * kTile + k0 + col + c);
-          fold_tmem<CAP1, CAP2, BIASED>(st, ts + c, a, p1, p2, hb, tb1, tb2, r0 + c, bits);
-        }
+        if (!ok) fold_tile<L::kCols, CAP1, CAP2, KIND, MASKED>(st, ts, a, p1, p2, hb, rmin, r0, bits);
       }
       tc_fence_before();
       __syncwarp();
@@ -466,7 +561,7 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
         else merge_stats(st, other);
       }
       const size_t rows = size_t(a.B) * a.H * a.NQ;
-      const size_t idx = size_t(bh) * a.NQ + grow;
+      const size_t idx = size_t(bh + slot) * a.NQ + grow;
       if (!SKL_CHECK(a.status, idx < rows && split < a.num_splits)) {
         // (debug build) out-of-range row or split: nothing is written
       } else if (a.partial != nullptr) {
@@ -490,139 +585,46 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
   }
 }
 
-// Merges the key splits of every row.
-__global__ void __launch_bounds__(256) mod_reduce_kernel(const float* __restrict__ part, int rows, int num_splits,
-                                                         float* __restrict__ kl, float* __restrict__ lse1,
-                                                         float* __restrict__ lse2) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= rows) return;
-  const size_t R = size_t(rows);
-  ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < num_splits; ++s) {
-    const float* p = part + size_t(s) * 5 * R + i;
-    const ModStats o{p[0], p[R], p[2 * R], p[3 * R], p[4 * R]};
-    if (o.l1 == 0.f) continue;
-    if (st.l1 == 0.f) st = o;
-    else merge_stats(st, o);
-  }
-  write_row(st, kl + i, lse1 + i, lse2 + i);
-}
-
-// The bucket of relative position r: half of the buckets for each direction
-// where both count; the near half of a direction's buckets one distance each,
-// the rest in steps of the logarithm up to max_distance.  In 64 bits, with a
-// margin far below the smallest step, so that distances at a border (whole
-// numbers) fall on its far side whatever the logarithm's last bit says.
-__device__ int bucket_of(int r, int num_buckets, int max_distance, int both) {
-  const int n = both ? num_buckets / 2 : num_buckets;
-  const int base = both && r > 0 ? n : 0;
-  const int d = both ? abs(r) : max(-r, 0);
-  const int e = n / 2;
-  if (d < e) return base + d;
-  if (d >= max_distance) return base + n - 1;
-  const int f = e + int(floor((n - e) * log(double(d) / e) / log(double(max_distance) / e) + 1e-9));
-  return base + min(n - 1, f);
-}
-
-// Before the main launch.  blockIdx.y = 0, 1: lookup row of that side's table,
-// base 2, one block column per 256 positions; y = 2: ids of query tiles, y = 3: of key tiles
-// (padded to whole tiles; one warp per tile finds min, max, uniform).
-__global__ void __launch_bounds__(256) mod_prep_kernel(const __grid_constant__ ModPrepArgs a) {
-  const int part = blockIdx.y;
-  if (part < 2) {
-    const ModPrepArgs::Table t = a.t[part];
-    if (t.table == nullptr) return;
-    const int len = near_len(t.max_distance);
-    const int p = blockIdx.x * 256 + threadIdx.x;
-    if (p >= len) return;
-    const int k = bucket_of(p - t.max_distance - kNearPad, t.num_buckets, t.max_distance, t.both);
-    if (t.bmap != nullptr) t.bmap[p] = k;
-    for (int h = 0; h < a.H; ++h) {
-      // a table's lowest values act as a mask: kept finite in base 2
-      const float v = t.table[size_t(h) * t.num_buckets + k] * kLog2e;
-      t.near[size_t(h) * len + p] = v < kNegBig ? kNegBig : (v > -kNegBig ? -kNegBig : v);
-    }
-    return;
-  }
-  const bool q = part == 2;
-  const int* src = q ? a.doc_q : a.doc_k;
-  if (src == nullptr) return;
-  const int n = q ? a.NQ : a.NK, tiles = (n + kTile - 1) / kTile;
-  const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (unit >= a.B * tiles) return;
-  const int b = unit / tiles, tile = unit - b * tiles;
-  int lo = INT_MAX, hi = -1, all = 1;
-  int* dst = (q ? a.ids_q : a.ids_k) + (size_t(b) * tiles + tile) * kTile;
-  for (int e = lane; e < kTile; e += 32) {
-    const int i = tile * kTile + e;
-    const int id = i < n ? src[size_t(b) * n + i] : -1;
-    dst[e] = id >= 0 ? id : (q ? -2 : -1);
-    if (id >= 0) {
-      lo = min(lo, id);
-      hi = max(hi, id);
-    } else if (i < n) {
-      all = 0;
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    all &= __shfl_xor_sync(0xffffffffu, all, o);
-  }
-  if (lane == 0) (q ? a.tiles_q : a.tiles_k)[size_t(b) * tiles + tile] = make_int4(lo, hi, all && lo == hi, 0);
-}
-
-template <int D1, int D2, bool CAP1, bool CAP2, bool BIASED>
+template <int D1, int D2, bool CAP1, bool CAP2, int KIND, bool MASKED>
 int launch_fwd_mod_k(const ModMaps& m, const ModFwdArgs& a, cudaStream_t st) {
   using L = ModFwdLayout<D1, D2>;
-  auto kern = fwd_mod_kernel<D1, D2, CAP1, CAP2, BIASED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  auto kern = fwd_mod_kernel<D1, D2, CAP1, CAP2, KIND, MASKED>;
+  ModFwdArgs b = a;
+  const size_t near = KIND == kAny ? near_smem_bytes(a.s1, a.s2, 1 << a.pack_shift) : 0;
+  b.near_smem = near > 0 && L::kAlloc + near <= 232448;
+  const int bytes = int(L::kAlloc + (b.near_smem ? near : 0));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  dim3 grid((a.NQ + kTile - 1) / kTile, a.B * a.H, a.num_splits);
-  kern<<<grid, L::kThreads, L::kAlloc, st>>>(m.q1, m.k1, m.q2, m.k2, a);
+  dim3 grid((a.NQ + kTile - 1) / kTile, a.B * (a.H >> a.pack_shift), a.num_splits);
+  kern<<<grid, L::kThreads, bytes, st>>>(m.q1, m.k1, m.q2, m.k2, b);
   return cudaGetLastError();
 }
 
 // One kernel for each set of modifications: what a side does not have must
-// not cost the loop registers (held for a cap that is not there, they made
-// it spill, 20 % of the time without modifications).
+// not cost the loop over full tiles registers or instructions (with 16 + 2
+// warps a thread has 96).  At 8K x 32 heads, d = 128, causal, one kernel that
+// branched took 635 us without modifications and 962 with both sides capped;
+// these take 474 and 798 (the plain forward 460).
+template <int D1, int D2, bool CAP1, bool CAP2>
+int launch_fwd_mod_c(const ModMaps& m, const ModFwdArgs& a, cudaStream_t st) {
+  const bool masked = a.vis.ids_q != nullptr || a.vis.prefix != nullptr;
+  if (a.s1.kind == kBiasTable || a.s2.kind == kBiasTable)
+    return masked ? launch_fwd_mod_k<D1, D2, CAP1, CAP2, kAny, true>(m, a, st)
+                  : launch_fwd_mod_k<D1, D2, CAP1, CAP2, kAny, false>(m, a, st);
+  if (a.s1.kind == kBiasSlopes || a.s2.kind == kBiasSlopes)
+    return masked ? launch_fwd_mod_k<D1, D2, CAP1, CAP2, kLinear, true>(m, a, st)
+                  : launch_fwd_mod_k<D1, D2, CAP1, CAP2, kLinear, false>(m, a, st);
+  return masked ? launch_fwd_mod_k<D1, D2, CAP1, CAP2, kNone, true>(m, a, st)
+                : launch_fwd_mod_k<D1, D2, CAP1, CAP2, kNone, false>(m, a, st);
+}
+
 template <int D1, int D2>
 int launch_fwd_mod_t(const ModMaps& m, const ModFwdArgs& a, cudaStream_t st) {
-  const bool biased = a.s1.kind != kBiasNone || a.s2.kind != kBiasNone;
   const bool c1 = a.s1.carg != 0.f, c2 = a.s2.carg != 0.f;
-  if (biased) {
-    if (c1) return c2 ? launch_fwd_mod_k<D1, D2, true, true, true>(m, a, st) : launch_fwd_mod_k<D1, D2, true, false, true>(m, a, st);
-    return c2 ? launch_fwd_mod_k<D1, D2, false, true, true>(m, a, st) : launch_fwd_mod_k<D1, D2, false, false, true>(m, a, st);
-  }
-  if (c1) return c2 ? launch_fwd_mod_k<D1, D2, true, true, false>(m, a, st) : launch_fwd_mod_k<D1, D2, true, false, false>(m, a, st);
-  return c2 ? launch_fwd_mod_k<D1, D2, false, true, false>(m, a, st) : launch_fwd_mod_k<D1, D2, false, false, false>(m, a, st);
+  if (c1) return c2 ? launch_fwd_mod_c<D1, D2, true, true>(m, a, st) : launch_fwd_mod_c<D1, D2, true, false>(m, a, st);
+  return c2 ? launch_fwd_mod_c<D1, D2, false, true>(m, a, st) : launch_fwd_mod_c<D1, D2, false, false>(m, a, st);
 }
 
 }  // namespace
-
-int launch_fwd_mod(const ModMaps& m, int d1, int d2, const ModFwdArgs& a, cudaStream_t st) {
-  if (d1 == 64) return d2 == 64 ? launch_fwd_mod_t<64, 64>(m, a, st) : launch_fwd_mod_t<64, 128>(m, a, st);
-  return d2 == 64 ? launch_fwd_mod_t<128, 64>(m, a, st) : launch_fwd_mod_t<128, 128>(m, a, st);
-}
-
-int launch_mod_reduce(const float* part, int rows, int num_splits, float* kl, float* lse1, float* lse2,
-                      cudaStream_t st) {
-  mod_reduce_kernel<<<(rows + 255) / 256, 256, 0, st>>>(part, rows, num_splits, kl, lse1, lse2);
-  return cudaGetLastError();
-}
-
-int launch_mod_prep(const ModPrepArgs& a, cudaStream_t st) {
-  int blocks = 0;
-  for (const auto& t : a.t)
-    if (t.table != nullptr) blocks = max(blocks, (near_len(t.max_distance) + 255) / 256);
-  if (a.doc_q != nullptr) {
-    const int nq = a.B * ((a.NQ + kTile - 1) / kTile), nk = a.B * ((a.NK + kTile - 1) / kTile);
-    blocks = max(blocks, (max(nq, nk) + 7) / 8);
-  }
-  if (blocks == 0) return cudaSuccess;
-  mod_prep_kernel<<<dim3(blocks, a.doc_q != nullptr ? 4 : 2), 256, 0, st>>>(a);
-  return cudaGetLastError();
-}
 
 }  // namespace skl

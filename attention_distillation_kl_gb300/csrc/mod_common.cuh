@@ -8,6 +8,8 @@
 // The kernels work in base 2: e = S log2 e.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -48,8 +50,10 @@ struct ModVis {
 };
 
 struct ModMaps {
-  CUtensorMap q1, k1, q2, k2;  // 4-D (d, N, heads, B) bf16, boxes of 64 x 128 x 1 x 1, 128-byte swizzle
+  // 4-D (d, N, heads, B) bf16, boxes of 64 x 128 x 1 x 1 (q with packed heads: 128 >> pack_shift rows), 128-byte swizzle
+  CUtensorMap q1, k1, q2, k2;
   CUtensorMap dq;              // [BH][NQ][pitch] fp32, boxes of 32 x 32, 128-byte swizzle (backward)
+  CUtensorMap dk;              // [B HK_g][NK][pitch] fp32, the same (shared key heads)
 };
 
 struct ModFwdArgs {
@@ -63,6 +67,8 @@ struct ModFwdArgs {
   float* partial;  // [num_splits][5][B H NQ] or null
   int* status;
   int head_group;
+  int near_smem;   // lookup rows are copied to shared memory
+  int pack_shift;  // 2^pack_shift query heads share a 128-row tile (few rows), 128 >> pack_shift rows each
 };
 
 struct ModBwdArgs {
@@ -79,6 +85,7 @@ struct ModBwdArgs {
   float* dk32;         // [B HK_g][NK][pitch]: dK of shared key heads (zeroed), null when each has one query head
   void* dk;            // bf16 dK (element strides below), written directly when dk32 is null
   long long dk_sb, dk_sh, dk_sn;
+  int near_smem;       // as ModFwdArgs
   int reach;           // of the gradient side's table (table gradient)
   const int* bmap;     // [near_len(reach)]: bucket of r = index - reach - kNearPad
   float* dtab;         // [BH][nkt][8][kMaxBuckets] partial sums of dS by bucket, or null
@@ -91,8 +98,12 @@ struct ModBwdArgs {
   int head_group;
 };
 
+// Work before the main launch, in one kernel: a region of the workspace
+// zeroed, ids padded and their tiles' ranges found, lookup rows filled.
 struct ModPrepArgs {
   int B, H, NQ, NK;
+  uint4* zero;
+  size_t zero_words;  // 16-byte words
   const int* doc_q;
   const int* doc_k;
   int* ids_q;
@@ -102,22 +113,36 @@ struct ModPrepArgs {
   struct Table {
     const float* table;  // [H][num_buckets] or null
     int num_buckets, max_distance, both;
+    int per_side;            // buckets of a direction
+    int first[kMaxBuckets];  // a direction's first distance of each
     float* near;
     int* bmap;  // or null
   } t[2];
 };
 
+// Work after the backward's main launch, in one kernel: fp32 rows rounded to
+// bf16 (null source: zeros), and the warps' bucket sums added up.
+struct ModFinishArgs {
+  struct Rows {
+    const float* src;  // [B per_batch][n][pitch]
+    int heads, per_batch, n, d, pitch;
+    __nv_bfloat16* dst;  // strides in elements; null: nothing to do
+    long long sb, sh, sn;
+  } rows[2];
+  const float* dtab;
+  int B, H, nkt, num_buckets;
+  float* dtable;  // or null
+};
+
 int launch_mod_prep(const ModPrepArgs& a, cudaStream_t st);
-int launch_fwd_mod(const ModMaps& m, int d1, int d2, const ModFwdArgs& a, cudaStream_t st);
+// d1, d2: tile widths, 64 or 128
+int launch_fwd_mod_64(const ModMaps& m, int d2, const ModFwdArgs& a, cudaStream_t st);
+int launch_fwd_mod_128(const ModMaps& m, int d2, const ModFwdArgs& a, cudaStream_t st);
 int launch_mod_reduce(const float* part, int rows, int num_splits, float* kl, float* lse1, float* lse2,
                       cudaStream_t st);
 int launch_bwd_mod_p2(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cudaStream_t st);
 int launch_bwd_mod_p1(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cudaStream_t st);
-// fp32 rows [heads][n][pitch] (null: zeros) to bf16 with strides; heads = B * per_batch
-int launch_mod_convert(const float* src, int B, int per_batch, int n, int d, int pitch, void* dst, long long sb,
-                       long long sh, long long sn, cudaStream_t st);
-int launch_mod_table_reduce(const float* dtab, int B, int H, int nkt, int num_buckets, float* dtable,
-                            cudaStream_t st);
+int launch_mod_finish(const ModFinishArgs& a, cudaStream_t st);
 int launch_kmax_strided(const void* k, int B, int per_batch, int n, int d, long long sb, long long sh, long long sn,
                         unsigned* kmax, cudaStream_t st);
 
@@ -167,7 +192,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // scores costs six packed operations: x^2, four steps, and one that also
 // adds the bias.  The FMA pipe bounds it: folding the coefficients and the
 // reference of the softmax took the forward at 8K x 32 heads, d = 128, both
-// sides capped, from 1105 us to MEASURED_FOLD us.
+// sides capped, from 1105 us to 798 us.
 constexpr float kTanhMax = 0.5f;
 __host__ __device__ constexpr float tanh_p(int k) {
   return k == 0 ? 1.0f : k == 1 ? -0.33333069f : k == 2 ? 0.13324779f : k == 3 ? -0.052986074f : 0.017135005f;
@@ -221,20 +246,44 @@ enum { kZero = 0, kFlat = 1, kFold = 2, kLook = 3 };
 struct HeadBias {  // of one head, base 2
   int kind, reach;
   float slope;
-  const float* near;  // at r = 0
   float left, right;  // the table's value far to the left and to the right
+  const float* near;  // its lookup row (shared memory where there is room)
 };
 
 __device__ __forceinline__ HeadBias head_bias(const ModSide& s, int h) {
-  HeadBias b{s.kind, s.reach, 0.f, nullptr, 0.f, 0.f};
+  HeadBias b{s.kind, s.reach, 0.f, 0.f, 0.f, nullptr};
   if (s.kind == kBiasSlopes) b.slope = s.slopes[h] * kLog2e;
   if (s.kind == kBiasTable) {
-    const float* row = s.near + size_t(h) * near_len(s.reach);
-    b.near = row + s.reach + kNearPad;
-    b.left = row[0];
-    b.right = row[near_len(s.reach) - 1];
+    b.near = s.near + size_t(h) * near_len(s.reach);
+    b.left = b.near[0];
+    b.right = b.near[near_len(s.reach) - 1];
   }
   return b;
+}
+
+// Copies the lookup rows of `count` HeadBias into shared memory at dst, one
+// after the other, by the whole block; a __syncthreads before and after.
+__device__ __forceinline__ void near_to_smem(HeadBias* hb, int count, float* dst) {
+  for (int i = 0; i < count; ++i) {
+    if (hb[i].kind != kBiasTable) continue;
+    const int len = near_len(hb[i].reach);
+    for (int p = threadIdx.x; p < len; p += blockDim.x) dst[p] = hb[i].near[p];
+    dst += len;
+  }
+}
+// Then, by one thread: where they are.
+__device__ __forceinline__ void near_in_smem(HeadBias* hb, int count, const float* src) {
+  for (int i = 0; i < count; ++i) {
+    if (hb[i].kind != kBiasTable) continue;
+    hb[i].near = src;
+    src += near_len(hb[i].reach);
+  }
+}
+__host__ __device__ inline size_t near_smem_bytes(const ModSide& s1, const ModSide& s2, int heads) {
+  size_t n = 0;
+  if (s1.kind == kBiasTable) n += near_len(s1.reach);
+  if (s2.kind == kBiasTable) n += near_len(s2.reach);
+  return n * heads * 4;
 }
 
 struct TileBias {
@@ -257,28 +306,41 @@ __device__ __forceinline__ TileBias tile_bias(const HeadBias& b, int rmin, int r
   return t;
 }
 
-// The bias of 32 columns of a row, plus `add`: rf = float(r) of column 0,
-// near0 = near + r of column 0.
+// The bias of neighbouring columns of a row, plus `add`: rf = float(r) of
+// column 0; near0: column 0's entry (kLook).
 struct RowBias {
   float rf, step, first, add;  // first = base + step rf + add
   const float* near0;
 };
 __device__ __forceinline__ RowBias row_bias(const HeadBias& b, const TileBias& t, int r0, float add) {
   const float rf = float(r0);
-  return RowBias{rf, t.step, fmaf(t.step, rf, t.base) + add, add, b.near + r0};
+  return RowBias{rf, t.step, fmaf(t.step, rf, t.base) + add, add, b.near + (r0 + b.reach + kNearPad)};
 }
 // The same n columns further on.
 __device__ __forceinline__ RowBias further(const RowBias& b, int n) {
   return RowBias{b.rf + float(n), b.step, fmaf(b.step, float(n), b.first), b.add, b.near0 + n};
 }
-// Columns k and k + 1.
+// Columns k to k + 3 as two pairs.
+struct Quad {
+  uint64_t lo, hi;
+};
 template <int HOW>
-__device__ __forceinline__ uint64_t bias_pair(const RowBias& b, int k) {
-  if (HOW == kFlat) return f2_fma(f2(b.step, b.step), f2(float(k), float(k + 1)), f2(b.first, b.first));
-  if (HOW == kFold)
-    return f2(fmaf(-b.step, fabsf(b.rf + float(k)), b.add), fmaf(-b.step, fabsf(b.rf + float(k + 1)), b.add));
-  if (HOW == kLook) return f2_add(f2(__ldg(b.near0 + k), __ldg(b.near0 + k + 1)), f2(b.add, b.add));
-  return f2(b.add, b.add);
+__device__ __forceinline__ Quad bias_quad(const RowBias& b, int k) {
+  if (HOW == kFlat) {
+    const uint64_t S = f2(b.step, b.step), F = f2(b.first, b.first);
+    return Quad{f2_fma(S, f2(float(k), float(k + 1)), F), f2_fma(S, f2(float(k + 2), float(k + 3)), F)};
+  }
+  if (HOW == kFold) {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fmaf(-b.step, fabsf(b.rf + float(k + i)), b.add);
+    return Quad{f2(v[0], v[1]), f2(v[2], v[3])};
+  }
+  if (HOW == kLook) {
+    const uint64_t A = f2(b.add, b.add);
+    return Quad{f2_add(f2(b.near0[k], b.near0[k + 1]), A), f2_add(f2(b.near0[k + 2], b.near0[k + 3]), A)};
+  }
+  return Quad{f2(b.add, b.add), f2(b.add, b.add)};
 }
 
 // Base-2 score + bias + add of N columns of a row, as pairs; returns the
@@ -291,18 +353,23 @@ __device__ __forceinline__ float scores_how(const uint32_t (&x)[N], uint64_t (&e
                                             const RowBias& b) {
   float za = 0.f, zb = 0.f;
 #pragma unroll
-  for (int k = 0; k < N; k += 2) {
+  for (int k = 0; k < N; k += 4) {
+    const Quad q = bias_quad<HOW>(b, k);
     const uint64_t X = f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-    uint64_t M = s.p[0];
+    const uint64_t Y = f2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+    uint64_t M = s.p[0], L = s.p[0];
     if (CAP) {
-      const uint64_t Z = f2_mul(X, X);
+      const uint64_t Z = f2_mul(X, X), W = f2_mul(Y, Y);
       float u, v;
       f2_split(Z, u, v);
-      if (k & 2) zb = max3(zb, u, v);
-      else za = max3(za, u, v);
+      za = max3(za, u, v);
+      f2_split(W, u, v);
+      zb = max3(zb, u, v);
       M = cap_poly(s, Z);
+      L = cap_poly(s, W);
     }
-    e[k / 2] = f2_fma(X, M, bias_pair<HOW>(b, k));
+    e[k / 2] = f2_fma(X, M, q.lo);
+    e[k / 2 + 1] = f2_fma(Y, L, q.hi);
   }
   return fmaxf(za, zb);
 }
@@ -320,7 +387,7 @@ __device__ __forceinline__ float scores(const uint32_t (&x)[N], uint64_t (&e)[N 
 __device__ __forceinline__ float bias_one(const RowBias& b, int how, int k) {
   if (how == kFlat) return fmaf(b.step, float(k), b.first);
   if (how == kFold) return fmaf(-b.step, fabsf(b.rf + float(k)), b.add);
-  if (how == kLook) return __ldg(b.near0 + k) + b.add;
+  if (how == kLook) return b.near0[k] + b.add;
   return b.add;
 }
 

@@ -137,6 +137,10 @@ CASES = {
     "odd buckets": dict(bias2="one way", nb=7, maxd=11, NQ=200, NK=200, bias1="one way"),
     "grouped": dict(H=4, HK1=2, HK2=1, cap1=30.0, NQ=140, NK=260),
     "grouped table": dict(H=6, HK1=3, HK2=2, bias1="one way", bias2="one way", NQ=140, NK=140, B=2),
+    "few rows of shared heads": dict(H=16, HK1=2, HK2=1, NQ=16, NK=400, cap1=30.0, bias2="one way", B=2),
+    "one row of shared heads": dict(H=8, HK1=2, HK2=2, NQ=1, NK=700, bias1="slopes", bias2="slopes", d1=128),
+    "33 rows of shared heads": dict(H=4, HK1=1, HK2=1, NQ=33, NK=300, causal=False, bias1="both ways", bias2="slopes"),
+    "17 rows of packed shared heads": dict(H=8, HK1=2, HK2=1, NQ=17, NK=260, docs="shuffled", cap2=30.0, B=2),
     "narrow heads": dict(d1=16, d2=48, cap1=30.0, cap2=30.0),
     "padded heads": dict(d1=80, d2=112, bias2="one way"),
     "wide and narrow": dict(d1=128, d2=32, cap2=10.0),
@@ -166,7 +170,7 @@ def test_against_the_definition(name):
 
 
 @pytest.mark.parametrize("splits", [1, 2, 3, 7, 64, 0])
-@pytest.mark.parametrize("name", ["one row", "slopes", "shuffled ids", "prefix over many tiles", "nothing shared",
+@pytest.mark.parametrize("name", ["one row", "few rows of shared heads", "slopes", "shuffled ids", "prefix over many tiles", "nothing shared",
                                   "more rows than keys"])
 def test_key_splits(name, splits):
     dev, kw, where, p = problem(seed=3, **CASES[name])
