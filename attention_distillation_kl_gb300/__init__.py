@@ -497,12 +497,9 @@ def _mod_workspace(workspace, need, device, stream):
 
 def _mod_rows(given, names, shape, device, stream):
     """Per-row outputs, those given checked; the others made here, used on `stream` too."""
-    if given[0] is given[1] is given[2] is None and shape[0] * shape[1] * shape[2] % 4 == 0:
-        out = torch.empty((3,) + shape, dtype=torch.float32, device=device)  # each stays 16-byte aligned
-        if stream is not None:
-            out.record_stream(stream)
-        return out.unbind(0)
-    out = tuple(_out(t, shape, device, name) for t, name in zip(given, names))
+    if given[0] is given[1] is given[2] is None and stream is None:
+        return [torch.empty(shape, dtype=torch.float32, device=device) for _ in names]
+    out = [_out(t, shape, device, name) for t, name in zip(given, names)]
     _new_on(stream, *zip(given, out))
     return out
 

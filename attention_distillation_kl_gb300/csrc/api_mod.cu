@@ -273,10 +273,10 @@ BwdPlan bwd_plan(const streamkl_side* p1, const streamkl_side* p2, const streamk
     f.words = c.take<unsigned>(size_t(B) * g.HK + (shared ? 2 + size_t(B) * g.HK * tiles(NK) : 0));
   const size_t dk_count = size_t(B) * g.HK * NK * f.pitch;
   if (shared && !deterministic) f.dk32 = c.take<float>(dk_count);
+  if (table) f.dtab = c.take<float>(size_t(B) * H * tiles(NK) * 8 * skl::kMaxBuckets);
   f.prep.zero = static_cast<uint4*>(ws);
   f.prep.zero_words = c.used / 16;
   if (shared && deterministic) f.dk32 = c.take<float>(dk_count);
-  if (table) f.dtab = c.take<float>(size_t(B) * H * tiles(NK) * 8 * skl::kMaxBuckets);
   take_prep(c, f.prep, p, vis, B, H, NQ, NK, table ? gs : -1);
   f.bytes = c.used;
   return f;
@@ -418,7 +418,7 @@ int streamkl_bwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
   if (skl::launch_mod_prep(f.prep, cs) != 0) return STREAMKL_CUDA_ERROR;
   if (deterministic) {
     if (skl::launch_kmax_strided(g.k.data, B, g.HK, NK, g.d, B > 1 ? g.k.stride_b : 0, g.HK > 1 ? g.k.stride_h : 0,
-                                 NK > 1 ? g.k.stride_n : 0, f.words, cs) != 0)
+                                 NK > 1 ? g.k.stride_n : 0, f.prep.ids_k, f.words, cs) != 0)
       return STREAMKL_CUDA_ERROR;
     a.dq_fixed = 1;
     a.kmax = f.words;

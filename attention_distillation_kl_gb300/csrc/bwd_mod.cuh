@@ -21,9 +21,9 @@
 // relative position is constant on diagonals, so 32 steps of "shift by one
 // lane, add the next column" leave every diagonal's sum in a lane (those that
 // leave lane 31 early move to a second register); the sums of a bucket are
-// neighbours, joined by a segmented scan, and go to the lane that keeps the
-// bucket.  Tiles beyond the table's reach add to one bucket as a whole.  Each
-// warp writes its buckets once, and a last kernel adds them in a fixed order.
+// neighbours, joined by a segmented scan (add_to_buckets).  Tiles beyond the
+// table's reach add to one bucket as a whole.  Each warp has its own sums, in
+// the workspace, and a last kernel adds them in a fixed order.
 #pragma once
 
 #include <climits>
@@ -59,14 +59,13 @@ __device__ __forceinline__ void zero_row(uint32_t base, int row) {
       st_shared_zero16(base + c * T::kBlockBytes + row * T::kRowBytes + p);
 }
 
-// Sums of one warp's dS by bucket: lane l keeps buckets l and l + 32.
-struct BucketSums {
-  float lo, hi;
-};
-
-// Adds v of each lane to bucket k of each lane (k < 0: nothing).  Equal
-// buckets are neighbours.
-__device__ __forceinline__ void add_to_buckets(BucketSums& s, float v, int k, int lane) {
+// Adds v of each lane to this warp's sum of bucket k of each lane (k < 0:
+// nothing).  Equal buckets are neighbours: a segmented scan joins them, and
+// the last of each adds to memory.  Only this warp adds to these sums, and
+// the warp barrier orders one call's additions before the next one's, so the
+// order is fixed.  (Passing each bucket to a lane that keeps it took 32 rounds
+// near the diagonal: 198 us at 4096 x 16 heads, d = 64, 194 us so.)
+__device__ __forceinline__ void add_to_buckets(float* sums, float v, int k, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const float pv = __shfl_up_sync(0xffffffffu, v, o);
@@ -74,17 +73,8 @@ __device__ __forceinline__ void add_to_buckets(BucketSums& s, float v, int k, in
     if (lane >= o && pk == k) v += pv;
   }
   const int nk = __shfl_down_sync(0xffffffffu, k, 1);
-  uint32_t last = __ballot_sync(0xffffffffu, k >= 0 && (lane == 31 || nk != k));
-  while (last != 0) {
-    const int src = __ffs(int(last)) - 1;
-    last &= last - 1;
-    const float t = __shfl_sync(0xffffffffu, v, src);
-    const int b = __shfl_sync(0xffffffffu, k, src);
-    if (lane == (b & 31)) {
-      if (b < 32) s.lo += t;
-      else s.hi += t;
-    }
-  }
+  __syncwarp();
+  if (k >= 0 && (lane == 31 || nk != k)) atomicAdd(sums + k, v);
 }
 
 constexpr float kUnseen = -3.0e38f;
@@ -160,7 +150,8 @@ __device__ __forceinline__ void dx_chunk(const uint64_t (&yg)[8], const uint64_t
 
 // 16 columns of both sides from TMEM to what dx_chunk takes.  MASK: masked
 // products become zeros first (they must not choose the path of the cap).
-template <bool CAP, bool BIASED, bool MASK>
+// HOW: the other side's bias where MASK is false (else how_o says).
+template <bool CAP, bool BIASED, bool MASK, int HOW>
 __device__ __forceinline__ void load_scores(uint32_t tg, uint32_t to, uint64_t (&yg)[8], uint64_t (&eo)[8],
                                             const ModSide& sg, const ModSide& so, const SideRegs& pg,
                                             const SideRegs& po, int how_o, const RowBias& rbo, uint32_t bits) {
@@ -177,7 +168,7 @@ __device__ __forceinline__ void load_scores(uint32_t tg, uint32_t to, uint64_t (
   load();
   float zo;
   if (MASK) zo = scores<CAP, BIASED>(xo, eo, po, how_o, rbo);
-  else zo = scores_how<CAP, BIASED ? kFlat : kZero>(xo, eo, po, rbo);
+  else zo = scores_how<CAP, HOW>(xo, eo, po, rbo);
   if (CAP) {
     const float zg = scores_how<true, kZero>(xg, yg, pg, none);
     if (__any_sync(0xffffffffu, zo > so.zmax || zg > sg.zmax)) {  // a score beyond half of its cap
@@ -196,6 +187,11 @@ __device__ __forceinline__ float lse_factor(float lse, float neg) {
   const float lost = fmaf(-lse, kLog2e, -neg) - lse * 1.925963033500e-8f;  // log2 e beyond fp32
   return fmaf(lost, kLn2, 1.f);
 }
+
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
 
 // What a launch needs of the dX arithmetic: no bias, some bias, the gradient
 // of the gradient side's table.
@@ -469,7 +465,7 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
       }
     };
     const float capf = sg.carg != 0.f ? -sg.scale / (sg.cmul * sg.cmul) : 0.f;
-    BucketSums bs{0.f, 0.f};
+    float* sums = TAB ? a.dtab + ((size_t(bh) * nkt + kt) * 8 + warp) * kMaxBuckets : nullptr;
     float left = 0.f, right = 0.f;  // this thread's dS beyond the table's reach
     float ng, no, w, wo;
     if (n > 0) params(0, ng, no, w, wo);
@@ -501,24 +497,52 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::B_SFREE));
       };
-      if (!need_mask && tbo.how <= kFlat && tbg.how <= kFlat) {
-        // every column visible, plain biases: dX in registers, so that the
-        // products of the previous tile may still read its dX
+      // the sums over diagonals of a 32 x 32 block that begins at this row
+      // group's column col: lane l holds diagonal 31 - l in acc, -1 - l in
+      // done; diagonal d is relative position d + rd
+      auto diagonals = [&](int col, float acc, float done) {
+        const int rd = k0 + wg * 64 + col - (q0 + (warp & 3) * 32 + off);
+        const int* bm = a.bmap + a.reach + kNearPad + rd;
+        add_to_buckets(sums, acc, __ldg(bm + 31 - lane), lane);
+        add_to_buckets(sums, done, lane < 31 ? __ldg(bm - 1 - lane) : -1, lane);
+      };
+      if (!need_mask && tbo.how != kFold && tbg.how != kFold) {
+        // every column visible: dX in registers, so that the products of the
+        // previous tile may still read its dX
         uint32_t dsr[32];
-        float total = 0.f, unused = 0.f;
+        float total = 0.f, acc = 0.f, done = 0.f;
+        auto tile = [&](auto how_o, auto how_g) {
+          constexpr int kHowO = decltype(how_o)::value, kHowG = decltype(how_g)::value;
+          constexpr int kTab = TAB ? (kHowG == kLook ? 2 : 1) : 0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint64_t yg[8], eo[8];
-          load_scores<CAP, BIAS != kNoBias, false>(tg + 16 * c, to + 16 * c, yg, eo, sg, so, pg, po, kFlat, rbo, 0u);
-          if (c == 3) release_s();
-          dx_chunk<MODE, CAP, BIAS == kNoBias ? kZero : kFlat, TAB ? 1 : 0, false>(yg, eo, p, rbg, 0u, lane, dsr + 8 * c,
-                                                                                   total, unused, unused);
-          if (BIAS != kNoBias) {
-            rbo = further(rbo, 16);
-            rbg = further(rbg, 16);
+          for (int c = 0; c < 4; ++c) {
+            uint64_t yg[8], eo[8];
+            load_scores<CAP, BIAS != kNoBias, false, kHowO>(tg + 16 * c, to + 16 * c, yg, eo, sg, so, pg, po, kHowO,
+                                                            rbo, 0u);
+            if (c == 3) release_s();
+            dx_chunk<MODE, CAP, kHowG, kTab, false>(yg, eo, p, rbg, 0u, lane, dsr + 8 * c, total, acc, done);
+            if (kTab == 2 && (c & 1)) {
+              diagonals(16 * (c - 1), acc, done);
+              acc = done = 0.f;
+            }
+            if (BIAS != kNoBias) {
+              rbo = further(rbo, 16);
+              rbg = further(rbg, 16);
+            }
+          }
+        };
+        if constexpr (BIAS == kNoBias) {
+          tile(Int<kZero>{}, Int<kZero>{});
+        } else {
+          if (tbg.how == kLook) {
+            if (tbo.how == kLook) tile(Int<kLook>{}, Int<kLook>{});
+            else tile(Int<kFlat>{}, Int<kLook>{});
+          } else {
+            if (tbo.how == kLook) tile(Int<kLook>{}, Int<kFlat>{});
+            else tile(Int<kFlat>{}, Int<kFlat>{});
           }
         }
-        if (TAB) (rmax <= -a.reach ? left : right) += total;
+        if (TAB && tbg.how != kLook) (rmax <= -a.reach ? left : right) += total;
         if (!mbar_wait_warp(bar(L::B_DSEMPTY), (i & 1) ^ 1, ctl)) break;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -538,7 +562,7 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
                        : visible_bits<16>(qi, k0 + wg * 64 + 16 * c, off, a.NK, a.vis.causal, prefix, id,
                                           same ? nullptr : a.vis.ids_k + size_t(b) * nkt * kTile + k0 + wg * 64 + 16 * c);
           uint64_t yg[8], eo[8];
-          load_scores<CAP, BIAS != kNoBias, true>(tg + 16 * c, to + 16 * c, yg, eo, sg, so, pg, po, tbo.how, rbo, bits);
+          load_scores<CAP, BIAS != kNoBias, true, kZero>(tg + 16 * c, to + 16 * c, yg, eo, sg, so, pg, po, tbo.how, rbo, bits);
           if (c == 3) release_s();
           uint32_t o[8];
           if constexpr (BIAS == kNoBias) {
@@ -547,12 +571,7 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
             if (tbg.how == kLook) dx_chunk<MODE, CAP, kLook, 2, true>(yg, eo, p, rbg, bits, lane, o, total, acc, done);
             else dx_chunk<MODE, CAP, kFlat, 1, true>(yg, eo, p, rbg, bits, lane, o, total, acc, done);
             if (tbg.how == kLook && (c & 1)) {
-              // lane l: diagonal 31 - l in acc, -1 - l in done; diagonal d of
-              // this block is relative position d + rd
-              const int rd = k0 + wg * 64 + 16 * (c - 1) - (q0 + (warp & 3) * 32 + off);
-              const int* bm = a.bmap + a.reach + kNearPad + rd;
-              add_to_buckets(bs, acc, __ldg(bm + 31 - lane), lane);
-              add_to_buckets(bs, done, lane < 31 ? __ldg(bm - 1 - lane) : -1, lane);
+              diagonals(16 * (c - 1), acc, done);
               acc = done = 0.f;
             }
           } else {
@@ -583,12 +602,10 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
         left += __shfl_xor_sync(0xffffffffu, left, o);
         right += __shfl_xor_sync(0xffffffffu, right, o);
       }
-      const int kl_ = a.bmap[0], kr = a.bmap[near_len(a.reach) - 1];
-      if (lane == (kl_ & 31)) (kl_ < 32 ? bs.lo : bs.hi) += left;
-      if (lane == (kr & 31)) (kr < 32 ? bs.lo : bs.hi) += right;
-      float* o = a.dtab + ((size_t(bh) * nkt + kt) * 8 + warp) * kMaxBuckets;
-      o[lane] = bs.lo;
-      o[lane + 32] = bs.hi;
+      __syncwarp();
+      if (lane == 0) atomicAdd(sums + a.bmap[0], left);
+      __syncwarp();
+      if (lane == 0) atomicAdd(sums + a.bmap[near_len(a.reach) - 1], right);
     }
   } else {
     // ---------------------------------------------------------------- dQ / dK epilogue
@@ -779,7 +796,8 @@ int launch_bwd_mod_k(const ModMaps& m, const ModBwdArgs& a, cudaStream_t st) {
   const size_t near = BIAS != kNoBias ? near_smem_bytes(a.s1, a.s2, 1) : 0;
   b.near_smem = near > 0 && L::kAlloc + near <= 232448;
   const int bytes = int(L::kAlloc + (b.near_smem ? near : 0));
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // (always the most a block may have: threads that launch at once would set each other's size)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
   if (e != cudaSuccess) return e;
   dim3 grid((a.NK + kTile - 1) / kTile, a.B * a.H);
   kern<<<grid, L::kThreads, bytes, st>>>(m.q1, m.k1, m.q2, m.k2, m.dq, m.dk, b);

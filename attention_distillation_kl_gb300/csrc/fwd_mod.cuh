@@ -593,7 +593,8 @@ int launch_fwd_mod_k(const ModMaps& m, const ModFwdArgs& a, cudaStream_t st) {
   const size_t near = KIND == kAny ? near_smem_bytes(a.s1, a.s2, 1 << a.pack_shift) : 0;
   b.near_smem = near > 0 && L::kAlloc + near <= 232448;
   const int bytes = int(L::kAlloc + (b.near_smem ? near : 0));
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // (always the most a block may have: threads that launch at once would set each other's size)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
   if (e != cudaSuccess) return e;
   dim3 grid((a.NQ + kTile - 1) / kTile, a.B * (a.H >> a.pack_shift), a.num_splits);
   kern<<<grid, L::kThreads, bytes, st>>>(m.q1, m.k1, m.q2, m.k2, b);

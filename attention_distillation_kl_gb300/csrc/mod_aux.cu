@@ -135,9 +135,11 @@ __global__ void __launch_bounds__(kAuxThreads) mod_finish_kernel(const __grid_co
     a.dtable[size_t(h) * a.num_buckets + k] = (part[0][k] + part[1][k]) + (part[2][k] + part[3][k]);
 }
 
-// kmax of a strided K (see kmax_kernel in dq_fixed.cu).
+// kmax of a strided K (see kmax_kernel in dq_fixed.cu); keys whose id matches
+// nothing may hold anything and do not count.
 __global__ void __launch_bounds__(256) mod_kmax_kernel(const __nv_bfloat16* __restrict__ k, int per_batch, int n, int d,
-                                                       long long sb, long long sh, long long sn, unsigned* kmax) {
+                                                       long long sb, long long sh, long long sn, const int* ids, int ids_stride,
+                                                       unsigned* kmax) {
   const int b = blockIdx.y / per_batch, h = blockIdx.y - b * per_batch;
   const __nv_bfloat16* p = k + b * sb + h * sh;
   const int per_row = d / 8;
@@ -145,6 +147,7 @@ __global__ void __launch_bounds__(256) mod_kmax_kernel(const __nv_bfloat16* __re
   uint32_t m = 0;
   for (long long u = blockIdx.x * 256ll + threadIdx.x; u < total; u += gridDim.x * 256ll) {
     const long long i = u / per_row;
+    if (ids != nullptr && ids[size_t(b) * ids_stride + i] < 0) continue;
     const uint4 w = *reinterpret_cast<const uint4*>(p + i * sn + (u - i * per_row) * 8);
     const uint32_t x = max(max(w.x & 0x7fffu, (w.x >> 16) & 0x7fffu), max(w.y & 0x7fffu, (w.y >> 16) & 0x7fffu));
     const uint32_t y = max(max(w.z & 0x7fffu, (w.z >> 16) & 0x7fffu), max(w.w & 0x7fffu, (w.w >> 16) & 0x7fffu));
@@ -187,10 +190,11 @@ int launch_mod_finish(const ModFinishArgs& a, cudaStream_t st) {
 }
 
 int launch_kmax_strided(const void* k, int B, int per_batch, int n, int d, long long sb, long long sh, long long sn,
-                        unsigned* kmax, cudaStream_t st) {
+                        const int* ids, unsigned* kmax, cudaStream_t st) {
   const int heads = B * per_batch;
   dim3 grid(unsigned((loop_blocks((long long)n * (d / 8)) + heads - 1) / heads), unsigned(heads));
-  mod_kmax_kernel<<<grid, kAuxThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(k), per_batch, n, d, sb, sh, sn, kmax);
+  mod_kmax_kernel<<<grid, kAuxThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(k), per_batch, n, d, sb, sh, sn, ids,
+                                               (n + kTile - 1) / kTile * kTile, kmax);
   return cudaGetLastError();
 }
 

@@ -88,7 +88,7 @@ struct ModBwdArgs {
   int near_smem;       // as ModFwdArgs
   int reach;           // of the gradient side's table (table gradient)
   const int* bmap;     // [near_len(reach)]: bucket of r = index - reach - kNearPad
-  float* dtab;         // [BH][nkt][8][kMaxBuckets] partial sums of dS by bucket, or null
+  float* dtab;         // [BH][nkt][8][kMaxBuckets], zeroed: each warp's sums of dS by bucket, or null
   int* status;
   int dq_fixed;        // deterministic: dQ contributions on their row's grid (dq_fixed_exp)
   const unsigned* kmax;
@@ -143,8 +143,9 @@ int launch_mod_reduce(const float* part, int rows, int num_splits, float* kl, fl
 int launch_bwd_mod_p2(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cudaStream_t st);
 int launch_bwd_mod_p1(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cudaStream_t st);
 int launch_mod_finish(const ModFinishArgs& a, cudaStream_t st);
+// ids: of the keys, padded to whole tiles (ModVis::ids_k), or null
 int launch_kmax_strided(const void* k, int B, int per_batch, int n, int d, long long sb, long long sh, long long sn,
-                        unsigned* kmax, cudaStream_t st);
+                        const int* ids, unsigned* kmax, cudaStream_t st);
 
 // ------------------------------------------------------------------ device
 

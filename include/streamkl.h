@@ -339,6 +339,7 @@ int streamkl_fwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
  * fp32 and rounded once; they are fully overwritten.  dtable (fp32
  * [H][num_buckets], contiguous, or null): the gradient of that side's table,
  * in fp32 and added in a fixed order; INVALID_ARG when the side has none.
+ * No output may overlap an input or another output.
  * Rows that see no key, and positions whose id is negative, get zeros and
  * contribute none, whatever q, k and dkl hold there.  Other masked positions
  * must hold finite values.  deterministic = 1: dq and dk bitwise

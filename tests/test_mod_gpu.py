@@ -258,12 +258,14 @@ def test_padded_positions_may_hold_anything(junk):
     rows = skl.streamkl_fwd_mod(p1, p2, **where)
     for a, b in zip(rows, clean):
         assert torch.equal(a, b)
-    for mode in "12":
+    for mode, det in (("1", False), ("2", False), ("1", True), ("2", True)):
         dkl = torch.ones_like(rows[0])
         dkl.transpose(1, 2)[pad] = junk
         got = skl.streamkl_bwd_mod(p1, p2, *rows, dkl, skl.STREAMKL_GRAD_P1 if mode == "1" else skl.STREAMKL_GRAD_P2,
-                                   **where)
-        want = ref.backward(p, *(f64(t) for t in rows), np.ones(rows[0].shape), mode)
+                                   **where, deterministic=det)
+        want = list(ref.backward(p, *(f64(t) for t in rows), np.ones(rows[0].shape), mode))
+        if det:
+            want[3] = want[3] + (1 + ref.BF16) * ref.grid_error(p, f64(rows[0]), np.ones(rows[0].shape), mode)
         for g, w, b, what in zip(got, want[:3], want[3:], ("dq", "dk", "dtable")):
             if w is not None:
                 within(g, w, b, what)
@@ -444,3 +446,70 @@ def test_a_distillation_step():
     kw["2"]["table"].sub_(got[2])
     p["q2"], p["table2"] = f64(dev["q2"]), f64(kw["2"]["table"])
     check_forward(p1, p2, where, p)
+
+
+@pytest.mark.parametrize("name", ["grouped table", "shuffled ids", "one row of shared heads", "table both ways", "padded heads",
+                                  "prefix over many tiles"])
+def test_debug_build_checks_pass_and_match(name):
+    """The build whose kernels check their indexes: no check fails, same results."""
+    import os
+    path = os.path.join(os.path.dirname(skl.library_path), "libstreamkl_debug.so")
+    if not os.path.exists(path):
+        pytest.fail("libstreamkl_debug.so was not built")
+    dev, kw, where, p = problem(seed=21, **CASES[name])
+    p1, p2 = sides(dev, kw)
+
+    def calls():
+        rows = tuple(skl.streamkl_fwd_mod(p1, p2, **where, num_splits=2))
+        out = rows
+        for mode in (skl.STREAMKL_GRAD_P1, skl.STREAMKL_GRAD_P2):
+            out = out + skl.streamkl_bwd_mod(p1, p2, *rows, torch.ones_like(rows[0]), mode, **where, deterministic=True)
+        torch.cuda.synchronize()
+        return out
+
+    want = calls()
+    saved = skl._lib, skl.library_path
+    skl._lib, skl.library_path = None, path
+    try:
+        assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
+        got = calls()
+        assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
+    finally:
+        skl._lib, skl.library_path = saved
+    assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_threads_at_once():
+    """Host threads that launch the same kernels with lookup rows of different
+    lengths, each on its own stream."""
+    import threading
+    work = []
+    for seed, maxd in ((22, 20), (23, 900)):
+        dev, kw, where, p = problem(seed=seed, NQ=260, NK=260, bias1="one way", bias2="one way", maxd=maxd)
+        p1, p2 = sides(dev, kw)
+        rows = skl.streamkl_fwd_mod(p1, p2, **where)
+        want = [t.clone() for t in list(rows) + list(skl.streamkl_bwd_mod(p1, p2, *rows, torch.ones_like(rows[0]), **where,
+                                                                          deterministic=True))]
+        work.append((p1, p2, where, want))
+    torch.cuda.synchronize()
+    bad = []
+
+    def go(p1, p2, where, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(40):
+                    rows = skl.streamkl_fwd_mod(p1, p2, **where)
+                    got = list(rows) + list(skl.streamkl_bwd_mod(p1, p2, *rows, torch.ones_like(rows[0]), **where,
+                                                                 deterministic=True))
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    bad.append("results differ")
+        except Exception as e:  # noqa: BLE001
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=go, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not bad and skl.streamkl_get_device_status() == skl.STREAMKL_OK
