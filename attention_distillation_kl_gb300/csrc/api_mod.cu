@@ -152,7 +152,7 @@ void take_prep(Carver& c, skl::ModPrepArgs& a, const streamkl_side* const p[2], 
     a.t[i].max_distance = p[i]->max_distance;
     a.t[i].both = p[i]->bidirectional;
     if (c.base != nullptr) bucket_borders(a.t[i]);
-    a.t[i].near = c.take<float>(size_t(H) * skl::near_len(p[i]->max_distance));
+    a.t[i].near = c.take<float>(size_t(H) * skl::near_row(p[i]->max_distance));
     if (i == table_grad_side) a.t[i].bmap = c.take<int>(skl::near_len(p[i]->max_distance));
   }
 }

@@ -40,7 +40,7 @@ struct ModBwdLayout : BwdLayout<D1, D2, MODE> {
   using Base = BwdLayout<D1, D2, MODE>;
   static constexpr uint32_t oReady = Base::kBytes;  // barrier: K rows that match nothing are zeroed
   static constexpr uint32_t oRange = oReady + 8;    // first and last query tile with a shared id
-  static constexpr uint32_t oBias = oRange + 8;     // HeadBias of the other side and of the gradient side
+  static constexpr uint32_t oBias = (oRange + 8 + 15) / 16 * 16;  // HeadBias of the other side and of the gradient side
   static constexpr uint32_t oNear = (oBias + 2 * sizeof(HeadBias) + 15) / 16 * 16;  // lookup rows, where they fit
   static constexpr uint32_t kAlloc = oNear + 1024;
   static_assert(oReady % 8 == 0, "barriers are 8-byte aligned");
@@ -184,8 +184,7 @@ __device__ __forceinline__ void load_scores(uint32_t tg, uint32_t to, uint64_t (
 
 // The part of -lse log2 e that its rounding to fp32 loses, as a factor of 2^e.
 __device__ __forceinline__ float lse_factor(float lse, float neg) {
-  const float lost = fmaf(-lse, kLog2e, -neg) - lse * 1.925963033500e-8f;  // log2 e beyond fp32
-  return fmaf(lost, kLn2, 1.f);
+  return fmaf(fmaf(-lse, kLog2e, -neg) - lse * kLog2eLo, kLn2, 1.f);
 }
 
 template <int V>
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
     for (int i = 0; i < n; ++i) {
       const int q0 = (qt_lo + i) * kTile;
       const int qi = q0 + row;
-      const DsParams p{sg.cmul, sg.scale, capf, w, wo};
+      DsParams p{sg.cmul, sg.scale, capf, w, wo};
       const float cng = ng, cno = no;
       if (i + 1 < n) params(i + 1, ng, no, w, wo);  // used next tile: the loads overlap this one
       const int rmin = k0 - (q0 + kTile - 1 + off), rmax = rmin + 2 * kTile - 2;
@@ -487,6 +486,10 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
         tbg = tile_bias(hb[1], rmin, rmax);
         rbo = row_bias(hb[0], tbo, r0, cno);
         rbg = row_bias(hb[1], tbg, r0, cng);
+        if (TAB && kP2) {  // as the roundings of -LSE, see params
+          p.w *= fmaf(flat_lost(hb[1], tbg, rbg, rmax), kLn2, 1.f);
+          p.wo *= fmaf(flat_lost(hb[0], tbo, rbo, rmax), kLn2, 1.f);
+        }
       }
       const uint32_t tg = (kP2 ? t_s2 : t_s1) + lane_off + wg * 64, to = (kP2 ? t_s1 : t_s2) + lane_off + wg * 64;
       const uint32_t row_addr = sb + L::oDS + wg * (kTile * 128) + (row >> 3) * 1024 + (row & 7) * 128;

@@ -49,8 +49,11 @@ __global__ void __launch_bounds__(kAuxThreads) mod_prep_kernel(const __grid_cons
       if (t.bmap != nullptr) t.bmap[p] = k;
       for (int h = 0; h < a.H; ++h) {
         // a table's lowest values act as a mask: kept finite in base 2
-        const float v = t.table[size_t(h) * t.num_buckets + k] * kLog2e;
-        t.near[size_t(h) * len + p] = v < kNegBig ? kNegBig : (v > -kNegBig ? -kNegBig : v);
+        const float w = t.table[size_t(h) * t.num_buckets + k], v = w * kLog2e;
+        float* row = t.near + size_t(h) * near_row(t.max_distance);
+        row[p] = v < kNegBig ? kNegBig : (v > -kNegBig ? -kNegBig : v);
+        if (p == 0 || p == len - 1)
+          row[p == 0 ? len : len + 1] = fabsf(w) < 1.0e6f ? fmaf(w, kLog2e, -v) + w * kLog2eLo : 0.f;
       }
       return;
     }

@@ -19,12 +19,16 @@ namespace skl {
 // a lookup row that reaches kNearPad past the last distance whose bucket can
 // differ serves every tile that touches such a distance without a clamp.
 constexpr int kNearPad = 256;
+constexpr float kLog2eLo = 1.925963033500e-8f;  // log2 e beyond kLog2e
 constexpr int kMaxBuckets = 64;
 constexpr int kMaxDistance = 4096;
 
 enum { kBiasNone = 0, kBiasSlopes = 1, kBiasTable = 2 };
 
 __host__ __device__ inline int near_len(int reach) { return 2 * (reach + kNearPad) + 1; }
+// A head's row in memory: those, then what the rounding of the first and the
+// last of them to fp32 lost.
+__host__ __device__ inline int near_row(int reach) { return near_len(reach) + 2; }
 
 struct ModSide {
   float scale;          // s
@@ -35,7 +39,7 @@ struct ModSide {
   int kind;             // kBiasNone, kBiasSlopes, kBiasTable
   int reach;            // table: buckets do not change beyond |r| = reach
   const float* slopes;  // [H]
-  const float* near;    // [H][near_len(reach)]: bias log2 e at r = index - reach - kNearPad
+  const float* near;    // [H][near_row(reach)]: bias log2 e at r = index - reach - kNearPad
 };
 
 struct ModVis {
@@ -244,20 +248,24 @@ __device__ __forceinline__ float cap_any(float x, float cmul, float carg) {
 // kLook: near[r] (a table within its reach); kZero: none.
 enum { kZero = 0, kFlat = 1, kFold = 2, kLook = 3 };
 
-struct HeadBias {  // of one head, base 2
+struct alignas(16) HeadBias {  // of one head, base 2
   int kind, reach;
   float slope;
-  float left, right;  // the table's value far to the left and to the right
+  float left, right;        // the table's value far to the left and to the right
+  float left_lo, right_lo;  // and what its rounding lost
   const float* near;  // its lookup row (shared memory where there is room)
 };
 
 __device__ __forceinline__ HeadBias head_bias(const ModSide& s, int h) {
-  HeadBias b{s.kind, s.reach, 0.f, 0.f, 0.f, nullptr};
+  HeadBias b{s.kind, s.reach, 0.f, 0.f, 0.f, 0.f, 0.f, nullptr};
   if (s.kind == kBiasSlopes) b.slope = s.slopes[h] * kLog2e;
   if (s.kind == kBiasTable) {
-    b.near = s.near + size_t(h) * near_len(s.reach);
+    const int len = near_len(s.reach);
+    b.near = s.near + size_t(h) * near_row(s.reach);
     b.left = b.near[0];
-    b.right = b.near[near_len(s.reach) - 1];
+    b.right = b.near[len - 1];
+    b.left_lo = b.near[len];
+    b.right_lo = b.near[len + 1];
   }
   return b;
 }
@@ -316,6 +324,12 @@ struct RowBias {
 __device__ __forceinline__ RowBias row_bias(const HeadBias& b, const TileBias& t, int r0, float add) {
   const float rf = float(r0);
   return RowBias{rf, t.step, fmaf(t.step, rf, t.base) + add, add, b.near + (r0 + b.reach + kNearPad)};
+}
+// What `first` of a flat table's row lost to rounding, in base 2.
+__device__ __forceinline__ float flat_lost(const HeadBias& b, const TileBias& t, const RowBias& r, int rmax) {
+  if (b.kind != kBiasTable || t.how != kFlat) return 0.f;
+  const float x = r.first - t.base;
+  return (t.base - (r.first - x)) + (r.add - x) + (rmax <= -b.reach ? b.left_lo : b.right_lo);
 }
 // The same n columns further on.
 __device__ __forceinline__ RowBias further(const RowBias& b, int n) {

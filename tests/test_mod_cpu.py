@@ -124,8 +124,8 @@ def test_workspace_bytes(L):
     assert f(side(), side(), seen(), 1, 2, 128, 128, 1) == 0
     assert f(side(softcap=50.0), side(slopes=A), seen(1, A), 1, 2, 128, 128, 1) == 0
     assert f(side(), side(), seen(), 1, 2, 100, 300, 3) == 5 * 4 * 3 * 2 * 100
-    # a lookup row per head over 2 (128 + 256) + 1 positions
-    assert f(side(**TABLE), side(), seen(), 1, 2, 128, 128, 1) == -(-2 * 769 * 4 // 16) * 16
+    # a lookup row per head over 2 (128 + 256) + 1 positions, and two more
+    assert f(side(**TABLE), side(), seen(), 1, 2, 128, 128, 1) == -(-2 * 771 * 4 // 16) * 16
     ids = f(side(), side(), seen(0, None, A, A), 3, 2, 130, 130, 1)
     assert ids == 2 * 3 * 256 * 4 + 2 * 3 * 2 * 16
     assert f(side(scale=0.0), side(), seen(), 1, 2, 128, 128, 1) == 0
