@@ -437,28 +437,30 @@ class AttnSide:
     """
 
     def __init__(self, q, k, scale, softcap=0.0, slopes=None, table=None, max_distance=128, bidirectional=False):
-        for name, t in (("q", q), ("k", k)):
+        for t in (q, k):
             if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
-                raise TypeError(f"{name} must be a CUDA bf16 tensor")
+                raise TypeError("q and k must be CUDA bf16 tensors")
             if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
-                raise ValueError(f"{name} must be a [B, heads, N, d] tensor whose last dimension is dense")
-        B, H, _, d = q.shape
-        if k.shape[0] != B or k.shape[3] != d:
+                raise ValueError("q and k must be [B, heads, N, d] tensors whose last dimension is dense")
+        B, H, NQ, d = q.shape
+        Bk, HK, NK, dk = k.shape
+        device = q.device
+        if Bk != B or dk != d:
             raise ValueError("inconsistent shapes: want q [B,H,NQ,d] and k [B,HK,NK,d]")
-        for name, t, ok in (("slopes", slopes, slopes is None or tuple(slopes.shape) == (H,)),
-                            ("table", table, table is None or (table.dim() == 2 and table.shape[0] == H))):
-            if t is None:
-                continue
-            if t.dtype != torch.float32 or t.device != q.device or not t.is_contiguous():
-                raise TypeError(f"{name} must be a contiguous fp32 tensor on {q.device}")
-            if not ok:
-                raise ValueError(f"{name} must have one row for each of the {H} heads, not {tuple(t.shape)}")
-        if k.device != q.device:
+        if k.device != device:
             raise ValueError("q and k must be on the same device")
+        if slopes is not None or table is not None:
+            for name, t in (("slopes", slopes), ("table", table)):
+                if t is not None and (t.dtype != torch.float32 or t.device != device or not t.is_contiguous()):
+                    raise TypeError(f"{name} must be a contiguous fp32 tensor on {device}")
+            if slopes is not None and tuple(slopes.shape) != (H,):
+                raise ValueError(f"slopes must have one value for each of the {H} heads")
+            if table is not None and (table.dim() != 2 or table.shape[0] != H):
+                raise ValueError(f"table must have one row for each of the {H} heads")
         self.q, self.k, self.slopes, self.table = q, k, slopes, table
-        self.device, self.rows, self.keys = q.device, tuple(q.shape[:3]), k.shape[2]
+        self.device, self.rows, self.keys = device, (B, H, NQ), NK
         self.num_buckets = 0 if table is None else table.shape[1]
-        self._c = _Side(_view(q), _view(k), d, k.shape[1], float(scale), float(softcap),
+        self._c = _Side(_view(q), _view(k), d, HK, scale, softcap,
                         None if slopes is None else slopes.data_ptr(), None if table is None else table.data_ptr(),
                         self.num_buckets, int(max_distance), int(bool(bidirectional)))
 

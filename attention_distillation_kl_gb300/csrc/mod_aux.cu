@@ -23,7 +23,7 @@ __device__ __forceinline__ int bucket_of(int r, const ModPrepArgs::Table& t) {
 }
 
 // Blocks of one launch by part: zeroing, then the tables' lookup rows (256
-// positions a block), then the tiles of ids (8 warps, one tile each).
+// positions of a head a block), then the tiles of ids (8 warps, one tile each).
 struct PrepBlocks {
   int zero, table[2], q, k;
   __host__ __device__ int total() const { return zero + table[0] + table[1] + q + k; }
@@ -42,19 +42,17 @@ __global__ void __launch_bounds__(kAuxThreads) mod_prep_kernel(const __grid_cons
   for (int s = 0; s < 2; ++s) {
     if (blk < pb.table[s]) {
       const ModPrepArgs::Table& t = a.t[s];
-      const int len = near_len(t.max_distance);
-      const int p = blk * kAuxThreads + threadIdx.x;
+      const int len = near_len(t.max_distance), chunks = (len + kAuxThreads - 1) / kAuxThreads;
+      const int h = blk / chunks, p = (blk - h * chunks) * kAuxThreads + threadIdx.x;
       if (p >= len) return;
       const int k = bucket_of(p - t.max_distance - kNearPad, t);
-      if (t.bmap != nullptr) t.bmap[p] = k;
-      for (int h = 0; h < a.H; ++h) {
-        // a table's lowest values act as a mask: kept finite in base 2
-        const float w = t.table[size_t(h) * t.num_buckets + k], v = w * kLog2e;
-        float* row = t.near + size_t(h) * near_row(t.max_distance);
-        row[p] = v < kNegBig ? kNegBig : (v > -kNegBig ? -kNegBig : v);
-        if (p == 0 || p == len - 1)
-          row[p == 0 ? len : len + 1] = fabsf(w) < 1.0e6f ? fmaf(w, kLog2e, -v) + w * kLog2eLo : 0.f;
-      }
+      if (t.bmap != nullptr && h == 0) t.bmap[p] = k;
+      // a table's lowest values act as a mask: kept finite in base 2
+      const float w = t.table[size_t(h) * t.num_buckets + k], v = w * kLog2e;
+      float* row = t.near + size_t(h) * near_row(t.max_distance);
+      row[p] = v < kNegBig ? kNegBig : (v > -kNegBig ? -kNegBig : v);
+      if (p == 0 || p == len - 1)
+        row[p == 0 ? len : len + 1] = fabsf(w) < 1.0e6f ? fmaf(w, kLog2e, -v) + w * kLog2eLo : 0.f;
       return;
     }
     blk -= pb.table[s];
@@ -130,6 +128,7 @@ __global__ void __launch_bounds__(kAuxThreads) mod_finish_kernel(const __grid_co
   float sum = 0.f;
   for (int b = 0; b < a.B; ++b) {
     const float* p = a.dtab + (size_t(b) * a.H + h) * a.nkt * 8 * kMaxBuckets;
+#pragma unroll 8
     for (int u = g; u < a.nkt * 8; u += 4) sum += p[size_t(u) * kMaxBuckets + k];
   }
   part[g][k] = sum;
@@ -171,7 +170,7 @@ int launch_mod_prep(const ModPrepArgs& a, cudaStream_t st) {
   PrepBlocks pb{};
   if (a.zero_words > 0) pb.zero = loop_blocks((long long)a.zero_words);
   for (int s = 0; s < 2; ++s)
-    if (a.t[s].table != nullptr) pb.table[s] = (near_len(a.t[s].max_distance) + kAuxThreads - 1) / kAuxThreads;
+    if (a.t[s].table != nullptr) pb.table[s] = a.H * ((near_len(a.t[s].max_distance) + kAuxThreads - 1) / kAuxThreads);
   if (a.doc_q != nullptr) {
     pb.q = (a.B * ((a.NQ + kTile - 1) / kTile) + 7) / 8;
     pb.k = (a.B * ((a.NK + kTile - 1) / kTile) + 7) / 8;
