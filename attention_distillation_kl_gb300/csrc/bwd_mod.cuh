@@ -247,6 +247,13 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
     range[0] = INT_MAX;
     range[1] = -1;
     fence_barrier_init();
+    // K at once: it does not wait for the rest of the block's start
+    int u_bh, u_kt;
+    grouped_unit(*unit_slot, a.B * a.H, int(gridDim.x), a.head_group, u_bh, u_kt);
+    const int u_b = u_bh / a.H, u_h = u_bh - u_b * a.H;
+    mbar_arrive_expect_tx(bar(L::B_KFULL), L::kK1 + L::kK2);
+    load_tile<T1>(sb + L::oK1, &tk1, bar(L::B_KFULL), u_kt * kTile, u_h / a.g1, u_b);
+    load_tile<T2>(sb + L::oK2, &tk2, bar(L::B_KFULL), u_kt * kTile, u_h / a.g2, u_b);
   }
   if (warp == 13) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -306,13 +313,6 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
   if (warp == 12) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0 && n > 0) {
-      tma_prefetch_desc(&tq1);
-      tma_prefetch_desc(&tk1);
-      tma_prefetch_desc(&tq2);
-      tma_prefetch_desc(&tk2);
-      mbar_arrive_expect_tx(bar(L::B_KFULL), L::kK1 + L::kK2);
-      load_tile<T1>(sb + L::oK1, &tk1, bar(L::B_KFULL), k0, h / a.g1, b);
-      load_tile<T2>(sb + L::oK2, &tk2, bar(L::B_KFULL), k0, h / a.g2, b);
       int issued = 0;
       for (int i = 0; i < n; ++i) {
         const int q0 = (qt_lo + i) * kTile;
@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
           mbar_drain(bar(L::B_QGFULL0 + i % L::kQgBufs), (i / L::kQgBufs) & 1, lim);
       }
     }
+    if (lane == 0 && n <= 0) mbar_drain(bar(L::B_KFULL), 0, 200000000ull);  // no product to wait for it
   } else if (warp == 13) {
     // ---------------------------------------------------------------- S issuer
     if (lane == 0) {

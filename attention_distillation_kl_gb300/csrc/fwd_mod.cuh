@@ -342,6 +342,12 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
     range[0] = INT_MAX;
     range[1] = -1;
     fence_barrier_init();
+    // Q at once: it does not wait for the rest of the block's start
+    mbar_arrive_expect_tx(bar_q, L::kQ1 + L::kQ2);
+    for (int s = 0; s < (1 << a.pack_shift); ++s) {
+      load_tile<T1>(sb + L::oQ1 + s * pack_rows * T1::kRowBytes, &tq1, bar_q, q0, h + s, b);
+      load_tile<T2>(sb + L::oQ2 + s * pack_rows * T2::kRowBytes, &tq2, bar_q, q0, h + s, b);
+    }
   }
   HeadBias* hbs = reinterpret_cast<HeadBias*>(smem + L::oBias);  // two for each head
   if (KIND != kNone && threadIdx.x < (2u << a.pack_shift))
@@ -393,15 +399,6 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
   if (warp == L::kProdWarp) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0 && nkt > 0) {
-      tma_prefetch_desc(&tq1);
-      tma_prefetch_desc(&tk1);
-      tma_prefetch_desc(&tq2);
-      tma_prefetch_desc(&tk2);
-      mbar_arrive_expect_tx(bar_q, L::kQ1 + L::kQ2);
-      for (int s = 0; s < (1 << a.pack_shift); ++s) {
-        load_tile<T1>(sb + L::oQ1 + s * pack_rows * T1::kRowBytes, &tq1, bar_q, q0, h + s, b);
-        load_tile<T2>(sb + L::oQ2 + s * pack_rows * T2::kRowBytes, &tq2, bar_q, q0, h + s, b);
-      }
       int issued = 0;
       for (int j = 0; j < nkt; ++j) {
         const int s = j % L::kStages;
@@ -423,6 +420,7 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
           mbar_drain(bar_kfull(j % L::kStages), (j / L::kStages) & 1, 200000000ull);
       }
     }
+    if (lane == 0 && nkt <= 0) mbar_drain(bar_q, 0, 200000000ull);  // no tile to wait for it
   } else if (warp == L::kMmaWarp) {
     // ---------------------------------------------------------------- MMA issuer
     // (the whole warp runs the loop; the elected lane issues)
