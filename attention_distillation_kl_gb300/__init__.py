@@ -460,7 +460,7 @@ class AttnSide:
         self.q, self.k, self.slopes, self.table = q, k, slopes, table
         self.device, self.rows, self.keys = device, (B, H, NQ), NK
         self.num_buckets = 0 if table is None else table.shape[1]
-        self._c = _Side(_view(q), _view(k), d, HK, scale, softcap,
+        self._c = _Side(_view(q), _view(k), d, HK, float(scale), float(softcap),
                         None if slopes is None else slopes.data_ptr(), None if table is None else table.data_ptr(),
                         self.num_buckets, int(max_distance), int(bool(bidirectional)))
 

@@ -231,9 +231,11 @@ __device__ __forceinline__ void merge_stats(ModStats& st, ModStats o) {
 }
 
 // The row's results.  A row that saw no key, or whose every score is so low
-// on one side that only a mask can have meant it: KL 0, LSE -inf.
+// on one side that only a mask can have meant it: KL 0, LSE -inf.  (A row of
+// NaNs has no maximum either: its sums say so.)
 __device__ __forceinline__ void write_row(const ModStats& st, float* kl, float* lse1, float* lse2) {
-  const bool seen = st.l1 != 0.f && !(st.m1 < kLow) && !(st.m2 < kLow);
+  const bool low = st.m1 < kLow || st.m2 < kLow;
+  const bool seen = st.l1 != 0.f && (!low || st.l1 != st.l1 || st.l2 != st.l2);
   *lse1 = seen ? fmaf(st.m1, kLn2, logf(st.l1)) : -INFINITY;
   *lse2 = seen ? fmaf(st.m2, kLn2, logf(st.l2)) : -INFINITY;
   *kl = seen ? fmaf(kLn2, st.acc / st.l1, logf(st.l2 / st.l1)) : 0.f;

@@ -297,7 +297,7 @@ typedef struct streamkl_side { /* one attention distribution */
   int HK;                      /* divides H */
   float scale;                 /* 0 < scale <= 1e4 */
   float softcap;               /* 0, or 1e-3 .. 1e6 */
-  const float* slopes;         /* device [H], finite, or null */
+  const float* slopes;         /* device [H], or null; each times the largest distance below 1e30 */
   const float* table;          /* device [H][num_buckets] or null (not with slopes); an entry of the type's
                                   lowest value masks its keys (anything beyond +-6.9e29 counts as that) */
   int num_buckets;             /* with a table: 2 .. 64 (bidirectional: even, at least 4) */

@@ -284,6 +284,22 @@ def test_nan_in_a_masked_future_key_does_not_reach_the_forward():
         assert torch.all(torch.isnan(a[:, :, 150:]))
 
 
+@pytest.mark.parametrize("where_nan", ["q1", "q2"])
+def test_a_query_of_nans_gives_nan(where_nan):
+    """Not the values of a row that sees nothing.  The other rows of its warp
+    take the general path too, so they keep to the definition, not to the bits."""
+    dev, kw, where, p = problem(seed=15, NQ=200, NK=200, cap1=30.0, bias2="one way")
+    p1, p2 = sides(dev, kw)
+    want = ref.forward(p)
+    dev[where_nan][:, :, 140] = float("nan")
+    got = skl.streamkl_fwd_mod(p1, p2, **where)
+    keep = np.arange(200) != 140
+    for i, (a, w, e) in enumerate(zip(got, want[:3], want[3:])):
+        within(f64(a)[:, :, keep], w[:, :, keep], e[:, :, keep], ("KL", "LSE1", "LSE2")[i])
+        if i == 0 or where_nan == f"q{i}":
+            assert torch.all(torch.isnan(a[:, :, 140]))
+
+
 def test_empty_rows_and_no_rows():
     dev, kw, where, p = problem(seed=10, docs="apart", causal=False, bias2="one way", H=4, HK2=2)
     p1, p2 = sides(dev, kw)
