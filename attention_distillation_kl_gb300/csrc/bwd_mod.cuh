@@ -83,7 +83,8 @@ struct DsParams {
   float cmul;   // of the gradient side
   float sg;     // its softmax scale
   float capf;   // -s / cmul^2: dX = dS (s + capf Y^2); 0 without a cap
-  float w, wo;  // weights of 2^e of the gradient side and of the other side (mode P2); w of both (mode P1)
+  float w, wo;  // mode P2: weights of 2^e of the gradient side and of the other side; mode P1: weight, and what
+                // the difference of the two e has to be moved by (kTab only)
 };
 
 // dX of 16 columns of a row, packed to bf16 pairs.  yg: base-2 score without
@@ -115,7 +116,8 @@ __device__ __forceinline__ void dx_chunk(const uint64_t (&yg)[8], const uint64_t
       D = f2_fma(W, f2(ex2(a), ex2(b)), f2_mul(WO, f2(ex2(c), ex2(d))));
     } else {
       // p1 = 2^e1; the other side carries -LSE2 + KL
-      D = f2_mul(f2_mul(W, f2(ex2(a), ex2(b))), f2_sub(EG, eo[k]));
+      const uint64_t R = f2_sub(EG, eo[k]);
+      D = f2_mul(f2_mul(W, f2(ex2(a), ex2(b))), kTab != 0 ? f2_add(R, WO) : R);
     }
     float da, db;
     if (MASK) {
@@ -182,10 +184,10 @@ __device__ __forceinline__ void load_scores(uint32_t tg, uint32_t to, uint64_t (
   }
 }
 
-// The part of -lse log2 e that its rounding to fp32 loses, as a factor of 2^e.
-__device__ __forceinline__ float lse_factor(float lse, float neg) {
-  return fmaf(fmaf(-lse, kLog2e, -neg) - lse * kLog2eLo, kLn2, 1.f);
-}
+// What the rounding of x log2 e to fp32 (y) loses.
+__device__ __forceinline__ float log2e_lost(float x, float y) { return fmaf(x, kLog2e, -y) + x * kLog2eLo; }
+// 2^x for a small x.
+__device__ __forceinline__ float exp2_small(float x) { return fmaf(x, kLn2, 1.f); }
 
 template <int V>
 struct Int {
@@ -435,9 +437,10 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
     // the row's -LSE of both sides in base 2 (mode P1: KL with the other
     // side's) and its weights; a row that saw no key (ng = kUnseen, finite, so
     // that nothing below is a NaN) contributes exact zeros.
-    // The table's gradient is a sum over many rows' differences of nearly
-    // equal sums, so there (mode P2) what the rounding of -LSE loses, an error
-    // common to a whole row, goes into the weights of the two exponentials
+    // The table's gradient is a sum of differences of nearly equal sums, so
+    // there (TAB) what the rounding of these and of a far tile's bias loses,
+    // errors common to a whole row, goes back in: into the weights of the
+    // exponentials, and in mode P1 into the difference of the two e
     auto params = [&](int i, float& ng, float& no, float& w, float& wo) {
       const int qi = (qt_lo + i) * kTile + row;
       ng = kUnseen;
@@ -452,14 +455,21 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
             ng = -l2 * kLog2e;
             no = -l1 * kLog2e;
             wo = -w;
-            if (BIAS == kTable) {
-              w *= lse_factor(l2, ng);
-              wo *= lse_factor(l1, no);
+            if (TAB) {
+              w *= exp2_small(log2e_lost(-l2, ng));
+              wo *= exp2_small(log2e_lost(-l1, no));
             }
           } else {
+            const float kl = a.kl[idx], d = kl - l2;
             ng = -l1 * kLog2e;
-            no = (a.kl[idx] - l2) * kLog2e;
+            no = d * kLog2e;
             w *= kLn2;
+            if (TAB) {
+              const float back = d + l2, lost = (kl - back) + (back - d - l2);  // of the subtraction
+              const float g = log2e_lost(-l1, ng);
+              w *= exp2_small(g);
+              wo = g - (log2e_lost(d, no) + lost * kLog2e);
+            }
           }
         }
       }
@@ -487,9 +497,11 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
         tbg = tile_bias(hb[1], rmin, rmax);
         rbo = row_bias(hb[0], tbo, r0, cno);
         rbg = row_bias(hb[1], tbg, r0, cng);
-        if (TAB && kP2) {  // as the roundings of -LSE, see params
-          p.w *= fmaf(flat_lost(hb[1], tbg, rbg, rmax), kLn2, 1.f);
-          p.wo *= fmaf(flat_lost(hb[0], tbo, rbo, rmax), kLn2, 1.f);
+        if (TAB) {
+          const float lg = flat_lost(hb[1], tbg, rbg, rmax), lo = flat_lost(hb[0], tbo, rbo, rmax);
+          p.w *= exp2_small(lg);
+          if (kP2) p.wo *= exp2_small(lo);
+          else p.wo += lg - lo;
         }
       }
       const uint32_t tg = (kP2 ? t_s2 : t_s1) + lane_off + wg * 64, to = (kP2 ? t_s1 : t_s2) + lane_off + wg * 64;
