@@ -56,7 +56,8 @@ class _View(ctypes.Structure):
 
 
 class _Side(ctypes.Structure):
-    _fields_ = [("q", _View), ("k", _View), ("d", _I), ("HK", _I), ("scale", _F), ("softcap", _F), ("slopes", _P),
+    _fields_ = [("q", _View), ("k", _View), ("d", _I), ("HK", _I), ("scale", ctypes.c_double),
+                ("softcap", _F), ("slopes", _P),
                 ("table", _P), ("num_buckets", _I), ("max_distance", _I), ("bidirectional", _I)]
 
 

@@ -295,7 +295,7 @@ typedef struct streamkl_side { /* one attention distribution */
   streamkl_view k;             /* [B][HK][NK][d]; query head h reads key head h / (H / HK) */
   int d;                       /* a multiple of 16 from 16 to 128 */
   int HK;                      /* divides H */
-  float scale;                 /* 0 < scale <= 1e4 */
+  double scale;                /* 0 < scale <= 1e4 */
   float softcap;               /* 0, or 1e-3 .. 1e6 */
   const float* slopes;         /* device [H], or null; each times the largest distance below 1e30 */
   const float* table;          /* device [H][num_buckets] or null (not with slopes); an entry of the type's

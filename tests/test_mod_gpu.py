@@ -46,7 +46,7 @@ def problem(seed=0, B=1, H=2, HK1=None, HK2=None, NQ=150, NK=150, d1=64, d2=64, 
         sc = 1.0 / math.sqrt(d) if sc is None else sc
         kw[t] = dict(scale=sc, softcap=cap, slopes=None if sl is None else sl.cuda(),
                      table=None if tab is None else tab.cuda(), max_distance=maxd, bidirectional=bias == "both ways")
-        p.update({"scale" + t: np.float64(np.float32(sc)), "cap" + t: cap, "slopes" + t: f64(sl), "table" + t: f64(tab),
+        p.update({"scale" + t: np.float64(sc), "cap" + t: cap, "slopes" + t: f64(sl), "table" + t: f64(tab),
                   "maxd" + t: maxd, "both" + t: bias == "both ways"})
     ids = None
     if docs is not None:
