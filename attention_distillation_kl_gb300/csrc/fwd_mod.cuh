@@ -605,7 +605,7 @@ int launch_fwd_mod_k(const ModMaps& m, const ModFwdArgs& a, cudaStream_t st) {
 // not cost the loop over full tiles registers or instructions (with 16 + 2
 // warps a thread has 96).  At 8K x 32 heads, d = 128, causal, one kernel that
 // branched took 635 us without modifications and 962 with both sides capped;
-// these take 474 and 798 (the plain forward 460).
+// these take 464 and 788 (the plain forward 460).
 template <int D1, int D2, bool CAP1, bool CAP2>
 int launch_fwd_mod_c(const ModMaps& m, const ModFwdArgs& a, cudaStream_t st) {
   const bool masked = a.vis.ids_q != nullptr || a.vis.prefix != nullptr;
