@@ -12,9 +12,9 @@
 // TMEM map): one CTA per query head and 128-key tile walks the query tiles
 // that can see it, dK accumulates in TMEM, dQ leaves as fp32 reduce-adds into
 // a workspace that launch_mod_convert rounds to bf16 once at the end.
-// What differs: the dS warps' arithmetic; K and Q rows whose id matches
-// nothing are zeroed in shared memory before a product reads them (they may
-// hold anything); with ids the walk is cut to the query tiles that share one;
+// What differs: the dS warps' arithmetic; K rows whose id matches nothing and
+// Q rows that saw no key are zeroed in shared memory before a product reads
+// them (they may hold anything); with ids the walk is cut to the query tiles that share one;
 // dK goes out as bf16 where one CTA owns it.
 //
 // The table's gradient (kTab): along a warp's 32 x 32 block of dS the
@@ -487,8 +487,11 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
       if (i + 1 < n) params(i + 1, ng, no, w, wo);  // used next tile: the loads overlap this one
       const int rmin = k0 - (q0 + kTile - 1 + off), rmax = rmin + 2 * kTile - 2;
       const bool same = !ids || tiles_same(tk, a.vis.tiles_q[size_t(b) * nqt + qt_lo + i]);
+      // a warp with a row that saw no key masks it: 0 times what such a row
+      // holds need not be 0
       const bool need_mask = (k0 + kTile > a.NK) || (q0 + kTile > a.NQ) || !same ||
-                             (a.vis.causal && rmax > 0 && k0 + kTile > prefix);
+                             (a.vis.causal && rmax > 0 && k0 + kTile > prefix) ||
+                             __any_sync(0xffffffffu, cng == kUnseen);
       const int r0 = k0 + wg * 64 - (qi + off);
       TileBias tbo{kZero, 0.f, 0.f}, tbg = tbo;
       RowBias rbo{0.f, 0.f, cno, cno, nullptr}, rbg{0.f, 0.f, cng, cng, nullptr};
@@ -604,9 +607,9 @@ __global__ void __launch_bounds__(BwdLayout<D1, D2, MODE>::kThreads, 1)
           }
         }
         if (TAB && tbg.how != kLook) (rmax <= -a.reach ? left : right) += total;
-        // queries that match nothing: their Q_g may hold anything (its S
-        // product is done, its dK product waits for this tile's dX)
-        if (!same && wg == 0 && id < 0) zero_row<TG>(sb + L::oQg + (i % L::kQgBufs) * L::kQg, row);
+        // queries that saw no key or match nothing: their Q_g may hold anything
+        // (its S product is done, its dK product waits for this tile's dX)
+        if (wg == 0 && (cng == kUnseen || (!same && id < 0))) zero_row<TG>(sb + L::oQg + (i % L::kQgBufs) * L::kQg, row);
       }
       fence_proxy_async_smem();
       __syncwarp();
