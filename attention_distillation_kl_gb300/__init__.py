@@ -8,6 +8,7 @@ GB300 (sm_103a), calls raise.
 Functions mirror the C ABI in ``include/streamkl.h`` and keep its names.
 """
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -485,25 +486,43 @@ def _mod_call(p1, p2, causal, prefix, doc_q, doc_k):
                                                         for t in (prefix, doc_q, doc_k)))
 
 
+_here = contextlib.nullcontext()
+
+
+def _making(stream):
+    """Where a call's own tensors are made: on the stream that it runs on.  Memory of the
+    current stream may still be in use there, by work that `stream` does not wait for."""
+    return _here if stream is None else torch.cuda.stream(stream)
+
+
+def _handed_over(stream, device, *pairs):
+    """Tensors made by this call for the caller (old one None), who goes on on the current stream."""
+    if stream is not None:
+        here = torch.cuda.current_stream(device)
+        for old, new in pairs:
+            if old is None and new is not None:
+                new.record_stream(here)
+
+
 def _mod_workspace(workspace, need, device, stream):
     """(address, bytes, tensor to keep) of the workspace; torch's own when the caller gives none."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        with _making(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _mod_rows(given, names, shape, device, stream):
-    """Per-row outputs, those given checked; the others made here, used on `stream` too."""
+    """Per-row outputs, those given checked; the others made here."""
     if given[0] is given[1] is given[2] is None and stream is None:
         return [torch.empty(shape, dtype=torch.float32, device=device) for _ in names]
-    out = [_out(t, shape, device, name) for t, name in zip(given, names)]
-    _new_on(stream, *zip(given, out))
+    with _making(stream):
+        out = [_out(t, shape, device, name) for t, name in zip(given, names)]
+    _handed_over(stream, device, *zip(given, out))
     return out
 
 
@@ -515,6 +534,11 @@ def _mod_stream(stream, device):
     if stream is None and _raw_stream is not None:
         return _raw_stream(device.index)
     return _stream(stream)
+
+
+def _check_stream(stream, device):
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream must be one of {device}")
 
 
 def _on_device(fn):
@@ -537,14 +561,6 @@ def _grad_out(t, shape, device, name):
     return t
 
 
-def _new_on(stream, *pairs):
-    """Tensors made by this call (old one None) are used on `stream` too."""
-    if stream is not None:
-        for old, new in pairs:
-            if old is None and new is not None:
-                new.record_stream(stream)
-
-
 @_on_device
 def streamkl_fwd_mod_workspace_bytes(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, num_splits=0):
     """Workspace bytes streamkl_fwd_mod needs for these arguments."""
@@ -562,6 +578,7 @@ def streamkl_fwd_mod(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, 
     library's choice."""
     B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
     dev, num_splits, c = p1.device, int(num_splits), lib()
+    _check_stream(stream, dev)
     need = c.streamkl_fwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, num_splits)
     ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
     kl, lse1, lse2 = _mod_rows((kl, lse1, lse2), ("kl", "lse1", "lse2"), (B, H, NQ), dev, stream)
@@ -590,6 +607,7 @@ def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=
     B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
     g = p2 if mode == STREAMKL_GRAD_P2 else p1
     dev, c = g.device, lib()
+    _check_stream(stream, dev)
     for name, t in (("kl", kl), ("lse1", lse1), ("lse2", lse2), ("dkl", dkl)):
         if t is None:
             raise ValueError(f"{name} is missing")
@@ -601,11 +619,12 @@ def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=
     need = c.streamkl_bwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, int(mode), det, int(want_table))
     ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
     given = (dq, dk, dtable)
-    dq = _grad_out(dq, g.q.shape, dev, "dq")
-    dk = _grad_out(dk, g.k.shape, dev, "dk")
-    if want_table:
-        dtable = _out(dtable, (H, g.num_buckets), dev, "dtable")
-    _new_on(stream, *zip(given, (dq, dk, dtable)))
+    with _making(stream):
+        dq = _grad_out(dq, g.q.shape, dev, "dq")
+        dk = _grad_out(dk, g.k.shape, dev, "dk")
+        if want_table:
+            dtable = _out(dtable, (H, g.num_buckets), dev, "dtable")
+    _handed_over(stream, dev, *zip(given, (dq, dk, dtable)))
     _check(c.streamkl_bwd_mod(p1._c, p2._c, vis, B, H, NQ, NK, kl.data_ptr(), lse1.data_ptr(), lse2.data_ptr(),
                               dkl.data_ptr(), int(mode), det, _view(dq), _view(dk),
                               dtable.data_ptr() if want_table else None, ws, ws_bytes, _mod_stream(stream, dev)),
