@@ -344,7 +344,7 @@ int streamkl_fwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
   if ((tile_width(p1->d) == 64 ? skl::launch_fwd_mod_64(m, t2, a, cs) : skl::launch_fwd_mod_128(m, t2, a, cs)) != 0)
     return STREAMKL_CUDA_ERROR;
   if (splits == 1) return STREAMKL_OK;
-  return as_status(skl::launch_mod_reduce(f.partial, B * H * NQ, splits, kl, lse1, lse2, cs));
+  return as_status(skl::launch_mod_reduce(a, cs));
 }
 
 size_t streamkl_bwd_mod_workspace_bytes(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,

@@ -17,8 +17,8 @@
 // visible chunk, and a chunk whose sums reach 2^64 moves it.  References are
 // whole numbers, so moving one is exact: by d1, d2,
 //   l_t <- l_t 2^-d_t,  acc <- 2^-d1 (acc - (d1 - d2) l1).
-// Scores so low that they can only be a mask written as a bias give no
-// usable reference (kLow): the chunks after them are taken relative to 0.
+// Scores so low that most are a mask written as a bias give no usable
+// reference (kLow): the chunks after them are taken relative to 0.
 //
 // Key tiles run from the last to the first: a causal row then takes its
 // references where a distance bias is largest, and farther tiles only fall
@@ -68,8 +68,6 @@ struct ModFwdLayout {
 
 // The biases a kernel knows: none, slopes only, tables too.
 enum { kNone = 0, kLinear = 1, kAny = 2 };
-
-constexpr float kLow = -1.0e6f;
 
 // The reference that the next chunk's scores are taken against.
 __device__ __forceinline__ float chunk_ref(float m) { return m < kLow ? 0.f : m; }
@@ -230,11 +228,13 @@ __device__ __forceinline__ void merge_stats(ModStats& st, ModStats o) {
   add_chunk(st, o.l1, o.l2, o.acc);
 }
 
-// The row's results.  A row that saw no key, or whose every score is so low
-// on one side that only a mask can have meant it: KL 0, LSE -inf.  (A row of
-// NaNs has no maximum either: its sums say so.)
-__device__ __forceinline__ void write_row(const ModStats& st, float* kl, float* lse1, float* lse2) {
-  const bool low = st.m1 < kLow || st.m2 < kLow;
+// The row's results.  A row that saw no key, or whose largest score on one
+// side is a table's mask (masked1, masked2: HeadBias::masked; however low raw
+// scores or slopes take it, a row without such an entry is computed): KL 0,
+// LSE -inf.  (A row of NaNs has no maximum either: its sums say so.)
+__device__ __forceinline__ void write_row(const ModStats& st, float masked1, float masked2, float* kl, float* lse1,
+                                          float* lse2) {
+  const bool low = st.m1 < masked1 || st.m2 < masked2;
   const bool seen = st.l1 != 0.f && (!low || st.l1 != st.l1 || st.l2 != st.l2);
   *lse1 = seen ? fmaf(st.m1, kLn2, logf(st.l1)) : -INFINITY;
   *lse2 = seen ? fmaf(st.m2, kLn2, logf(st.l2)) : -INFINITY;
@@ -572,7 +572,9 @@ __global__ void __launch_bounds__(ModFwdLayout<D1, D2>::kThreads, 1)
         p[3 * rows] = st.l2;
         p[4 * rows] = st.acc;
       } else {
-        write_row(st, a.kl + idx, a.lse1 + idx, a.lse2 + idx);
+        constexpr bool kTables = KIND == kAny;
+        write_row(st, kTables ? hb[0].masked : -INFINITY, kTables ? hb[1].masked : -INFINITY, a.kl + idx, a.lse1 + idx,
+                  a.lse2 + idx);
       }
     }
   }

@@ -10,9 +10,9 @@ namespace {
 // Merges the key splits: a warp per row, a lane for every 32nd split, then
 // the lanes' states in pairs.  (A thread per row waited for each split's
 // values in turn: 21 us for 512 rows of 19 splits.)
-__global__ void __launch_bounds__(256) mod_reduce_kernel(const float* __restrict__ part, int rows, int num_splits,
-                                                         float* __restrict__ kl, float* __restrict__ lse1,
-                                                         float* __restrict__ lse2) {
+__global__ void __launch_bounds__(256) mod_reduce_kernel(const __grid_constant__ ModFwdArgs a) {
+  const float* __restrict__ part = a.partial;
+  const int rows = a.B * a.H * a.NQ;
   const int lane = threadIdx.x & 31;
   const long long i = (blockIdx.x * 256ll + threadIdx.x) >> 5;
   if (i >= rows) return;
@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(256) mod_reduce_kernel(const float* __restrict
     else merge_stats(st, o);
   };
   ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = lane; s < num_splits; s += 32) {
+  for (int s = lane; s < a.num_splits; s += 32) {
     const float* p = part + size_t(s) * 5 * R + i;
     add(st, ModStats{p[0], p[R], p[2 * R], p[3 * R], p[4 * R]});
   }
@@ -34,7 +34,11 @@ __global__ void __launch_bounds__(256) mod_reduce_kernel(const float* __restrict
                      __shfl_down_sync(0xffffffffu, st.acc, o)};
     if (lane < o) add(st, x);
   }
-  if (lane == 0) write_row(st, kl + i, lse1 + i, lse2 + i);
+  const int h = int(i / a.NQ) % a.H;
+  auto masked = [&](const ModSide& s) {
+    return s.kind == kBiasTable ? s.near[size_t(h) * near_row(s.reach) + near_len(s.reach) + 2] : -INFINITY;
+  };
+  if (lane == 0) write_row(st, masked(a.s1), masked(a.s2), a.kl + i, a.lse1 + i, a.lse2 + i);
 }
 
 }  // namespace
@@ -43,9 +47,9 @@ int launch_fwd_mod_64(const ModMaps& m, int d2, const ModFwdArgs& a, cudaStream_
   return d2 == 64 ? launch_fwd_mod_t<64, 64>(m, a, st) : launch_fwd_mod_t<64, 128>(m, a, st);
 }
 
-int launch_mod_reduce(const float* part, int rows, int num_splits, float* kl, float* lse1, float* lse2,
-                      cudaStream_t st) {
-  mod_reduce_kernel<<<unsigned((rows + 7ll) / 8), 256, 0, st>>>(part, rows, num_splits, kl, lse1, lse2);
+int launch_mod_reduce(const ModFwdArgs& a, cudaStream_t st) {
+  const long long rows = (long long)a.B * a.H * a.NQ;
+  mod_reduce_kernel<<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -48,11 +48,22 @@ __global__ void __launch_bounds__(kAuxThreads) mod_prep_kernel(const __grid_cons
       const int k = bucket_of(p - t.max_distance - kNearPad, t);
       if (t.bmap != nullptr && h == 0) t.bmap[p] = k;
       // a table's lowest values act as a mask: kept finite in base 2
-      const float w = t.table[size_t(h) * t.num_buckets + k], v = w * kLog2e;
+      const float* entries = t.table + size_t(h) * t.num_buckets;
+      const float w = entries[k], v = w * kLog2e;
       float* row = t.near + size_t(h) * near_row(t.max_distance);
       row[p] = v < kNegBig ? kNegBig : (v > -kNegBig ? -kNegBig : v);
       if (p == 0 || p == len - 1)
         row[p == 0 ? len : len + 1] = fabsf(w) < 1.0e6f ? fmaf(w, kLog2e, -v) + w * kLog2eLo : 0.f;
+      if (p < 32) {  // (a row is longer than a warp)
+        float m = -INFINITY;
+        for (int e = p; e < t.num_buckets; e += 32) {
+          const float x = entries[e] * kLog2e;
+          if (x < kLow) m = fmaxf(m, fmaxf(x, kNegBig));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (p == 0) row[len + 2] = 0.5f * m;
+      }
       return;
     }
     blk -= pb.table[s];

@@ -27,8 +27,12 @@ enum { kBiasNone = 0, kBiasSlopes = 1, kBiasTable = 2 };
 
 __host__ __device__ inline int near_len(int reach) { return 2 * (reach + kNearPad) + 1; }
 // A head's row in memory: those, then what the rounding of the first and the
-// last of them to fp32 lost.
-__host__ __device__ inline int near_row(int reach) { return near_len(reach) + 2; }
+// last of them to fp32 lost, then the score below which a row of this head
+// sees only masks (half of the largest entry that is one; without one -inf).
+__host__ __device__ inline int near_row(int reach) { return near_len(reach) + 3; }
+
+// Base 2: table entries below this (-6.9e5) are masks.
+constexpr float kLow = -1.0e6f;
 
 struct ModSide {
   float scale;          // s
@@ -142,8 +146,7 @@ int launch_mod_prep(const ModPrepArgs& a, cudaStream_t st);
 // d1, d2: tile widths, 64 or 128
 int launch_fwd_mod_64(const ModMaps& m, int d2, const ModFwdArgs& a, cudaStream_t st);
 int launch_fwd_mod_128(const ModMaps& m, int d2, const ModFwdArgs& a, cudaStream_t st);
-int launch_mod_reduce(const float* part, int rows, int num_splits, float* kl, float* lse1, float* lse2,
-                      cudaStream_t st);
+int launch_mod_reduce(const ModFwdArgs& a, cudaStream_t st);
 int launch_bwd_mod_p2(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cudaStream_t st);
 int launch_bwd_mod_p1(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cudaStream_t st);
 int launch_mod_finish(const ModFinishArgs& a, cudaStream_t st);
@@ -253,11 +256,12 @@ struct alignas(16) HeadBias {  // of one head, base 2
   float slope;
   float left, right;        // the table's value far to the left and to the right
   float left_lo, right_lo;  // and what its rounding lost
+  float masked;             // a row whose largest score is below this sees only masks
   const float* near;  // its lookup row (shared memory where there is room)
 };
 
 __device__ __forceinline__ HeadBias head_bias(const ModSide& s, int h) {
-  HeadBias b{s.kind, s.reach, 0.f, 0.f, 0.f, 0.f, 0.f, nullptr};
+  HeadBias b{s.kind, s.reach, 0.f, 0.f, 0.f, 0.f, 0.f, -INFINITY, nullptr};
   if (s.kind == kBiasSlopes) b.slope = s.slopes[h] * kLog2e;
   if (s.kind == kBiasTable) {
     const int len = near_len(s.reach);
@@ -266,6 +270,7 @@ __device__ __forceinline__ HeadBias head_bias(const ModSide& s, int h) {
     b.right = b.near[len - 1];
     b.left_lo = b.near[len];
     b.right_lo = b.near[len + 1];
+    b.masked = b.near[len + 2];
   }
   return b;
 }

@@ -298,8 +298,8 @@ typedef struct streamkl_side { /* one attention distribution */
   double scale;                /* 0 < scale <= 1e4 */
   float softcap;               /* 0, or 1e-3 .. 1e6 */
   const float* slopes;         /* device [H], or null; each times the largest distance below 1e30 */
-  const float* table;          /* device [H][num_buckets] or null (not with slopes); an entry of the type's
-                                  lowest value masks its keys (anything beyond +-6.9e29 counts as that) */
+  const float* table;          /* device [H][num_buckets] or null (not with slopes); an entry below -6.9e5
+                                  masks its keys (anything beyond +-6.9e29 counts as +-6.9e29) */
   int num_buckets;             /* with a table: 2 .. 64 (bidirectional: even, at least 4) */
   int max_distance;            /* with a table: above e, at most 4096 */
   int bidirectional;           /* 0 or 1 */
@@ -314,9 +314,12 @@ typedef struct streamkl_visible {
 
 /*
  * Forward: kl, lse1, lse2 (fp32 [B, H, NQ], contiguous).  A row that sees no
- * key gets KL 0 and LSE -inf, and so does one whose every score on either
- * side is below -6.9e5, which only a bias meant as a mask brings about.  What
- * masked positions hold does not matter, NaN and infinities included.  num_splits as in streamkl_fwd_splitk, or 0
+ * key gets KL 0 and LSE -inf, and so does one that on either side sees only
+ * keys which that side's table masks (recognised by its largest score: below
+ * half of the largest masking entry of its head).  A score that is low without
+ * such an entry, by q.k or by slopes, is a score like any other.  What the keys
+ * that causal, prefix or ids hide hold does not matter, NaN and infinities
+ * included.  num_splits as in streamkl_fwd_splitk, or 0
  * for the library's choice (the same for the same sizes; ids are not
  * counted).  workspace: device memory, 16-byte aligned, of at least
  * streamkl_fwd_mod_workspace_bytes(...) bytes with the same arguments, owned
