@@ -14,11 +14,12 @@
 // way to it).  -m_t is added with the bias, in the operation that finishes
 // the score.  Any reference serves as long as no term overflows and the
 // largest does not underflow: a row takes the rounded maximum of its first
-// visible chunk, and a chunk whose sums reach 2^64 moves it.  References are
+// visible chunk, and a chunk whose sums reach 2^64 moves it; a chunk far from
+// it is taken again, relative to its own maximum.  References are
 // whole numbers, so moving one is exact: by d1, d2,
 //   l_t <- l_t 2^-d_t,  acc <- 2^-d1 (acc - (d1 - d2) l1).
-// Scores so low that most are a mask written as a bias give no usable
-// reference (kLow): the chunks after them are taken relative to 0.
+// Scores beyond 10^6 (mostly a mask written as a bias) give no usable
+// reference: the chunks after them are taken relative to 0.
 //
 // Key tiles run from the last to the first: a causal row then takes its
 // references where a distance bias is largest, and farther tiles only fall
@@ -69,8 +70,11 @@ struct ModFwdLayout {
 // The biases a kernel knows: none, slopes only, tables too.
 enum { kNone = 0, kLinear = 1, kAny = 2 };
 
+// Whether scores can be taken against m: beyond that (a mask's score, as a
+// rule) 0 serves better, which loses nothing of scores that are nearer to it.
+__device__ __forceinline__ bool usable(float m) { return fabsf(m) <= -kLow; }
 // The reference that the next chunk's scores are taken against.
-__device__ __forceinline__ float chunk_ref(float m) { return m < kLow ? 0.f : m; }
+__device__ __forceinline__ float chunk_ref(float m) { return usable(m) ? m : 0.f; }
 
 struct ModStats {
   float m1, m2, l1, l2, acc;  // l1 == 0: no key seen yet
@@ -144,17 +148,15 @@ __device__ __forceinline__ void mask_scores(uint64_t (&e1)[N], uint64_t (&e2)[N]
   }
 }
 
-// A chunk with masked columns (those not in bits), the first of a row, or
-// one above its references (r1, r2: what its scores are relative to): the
-// references move to its visible maxima where the row has seen nothing or
-// these are above.  What a masked column holds does not matter.
-template <bool MASK, int N>
-__device__ __forceinline__ void fold_chunk(ModStats& st, uint64_t (&e1)[N], uint64_t (&e2)[N], float r1, float r2,
-                                           uint32_t bits) {
-  if (MASK) {
-    if (bits == 0u) return;
-    mask_scores(e1, e2, bits);
-  }
+// Whether the row has no weight on any key yet.  (While a chunk is taken again
+// one side's sum alone may have become 0.)
+__device__ __forceinline__ bool nothing(const ModStats& st) { return st.l1 == 0.f && st.l2 == 0.f; }
+
+// The references after a chunk: its visible maxima (r1, r2: what its scores
+// are relative to) where the row has seen nothing or these are above its own.
+template <int N>
+__device__ __forceinline__ void chunk_max(const ModStats& st, const uint64_t (&e1)[N], const uint64_t (&e2)[N], float r1,
+                                          float r2, float& m1, float& m2) {
   float t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
@@ -164,15 +166,26 @@ __device__ __forceinline__ void fold_chunk(ModStats& st, uint64_t (&e1)[N], uint
     t1 = max3(t1, a, b);
     t2 = max3(t2, c, d);
   }
-  float m1 = rintf(t1) + r1, m2 = rintf(t2) + r2;
-  if (st.l1 == 0.f) {
-    st.m1 = m1;
-    st.m2 = m2;
-  } else {
+  m1 = rintf(t1) + r1;
+  m2 = rintf(t2) + r2;
+  if (!nothing(st)) {
     m1 = fmaxf(m1, st.m1);
     m2 = fmaxf(m2, st.m2);
-    move_refs(st, m1, m2);
   }
+}
+
+// Moves the references to m1, m2 (of chunk_max), or sets those of a row that has seen nothing.
+__device__ __forceinline__ void take_refs(ModStats& st, float m1, float m2) {
+  if (!nothing(st)) return move_refs(st, m1, m2);
+  st.m1 = m1;
+  st.m2 = m2;
+}
+
+// Adds a chunk, its masked columns at kGone, with the references at m1, m2.
+template <int N>
+__device__ __forceinline__ void fold_chunk(ModStats& st, uint64_t (&e1)[N], uint64_t (&e2)[N], float r1, float r2,
+                                           float m1, float m2) {
+  take_refs(st, m1, m2);
   const uint64_t D1 = f2(r1 - m1, r1 - m1), D2 = f2(r2 - m2, r2 - m2);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
@@ -184,21 +197,30 @@ __device__ __forceinline__ void fold_chunk(ModStats& st, uint64_t (&e1)[N], uint
   add_chunk(st, sum2(s.l1a, s.l1b), sum2(s.l2a, s.l2b), sum2(s.aa, s.ab));
 }
 
-// The whole of it for the row's kCols columns at ts, 16 at a time (they leave
-// the most registers free).  MASK = false: every column is visible.  Called
-// by whole warps.
+// A tile with masked columns, the first of a row, or one above its references:
+// the row's kCols columns at ts, 16 at a time (they leave the most registers
+// free).  MASK = false: every column is visible; what a masked column holds
+// does not matter.  Called by whole warps.
+//
+// Scores are rounded at the size of their distance to the reference.  Where a
+// chunk lies far from it (the keys before were masked by a large finite bias,
+// say: a whole chunk of entries of -65504 put errors of 0.004 into the scores
+// of the next one, and up to 0.02 into KL), it is taken again, against its own
+// maximum.
 template <int kCols, bool CAP1, bool CAP2, int KIND, bool MASK>
 __device__ __forceinline__ void fold_tile(ModStats& st, uint32_t ts, const ModFwdArgs& a, const SideRegs& p1,
                                           const SideRegs& p2, const HeadBias* hb, int rmin, int r0, uint32_t bits) {
   constexpr bool kBiased = KIND != kNone;
+  constexpr float kFar = 64.f;
   TileBias tb1{kZero, 0.f, 0.f}, tb2 = tb1;
   if (kBiased) {
     tb1 = tile_bias(hb[0], rmin, rmin + 2 * kTile - 2);
     tb2 = tile_bias(hb[1], rmin, rmin + 2 * kTile - 2);
   }
+  bool again = false;
 #pragma unroll 1
-  for (int c = 0; c < kCols; c += 16, bits >>= 16) {
-    const uint32_t part = MASK ? bits & 0xffffu : 0xffffu;
+  for (int c = 0; c < kCols;) {
+    const uint32_t part = MASK ? (bits >> c) & 0xffffu : 0xffffu;
     const float ref1 = chunk_ref(st.m1), ref2 = chunk_ref(st.m2);
     RowBias rb1{0.f, 0.f, -ref1, -ref1, nullptr}, rb2{0.f, 0.f, -ref2, -ref2, nullptr};
     if (kBiased) {
@@ -216,7 +238,18 @@ __device__ __forceinline__ void fold_tile(ModStats& st, uint32_t ts, const ModFw
       scores_any<CAP1, kBiased>(x1, e1, a.s1, tb1.how, rb1);
       scores_any<CAP2, kBiased>(x2, e2, a.s2, tb2.how, rb2);
     }
-    fold_chunk<MASK>(st, e1, e2, ref1, ref2, part);
+    if (MASK) mask_scores(e1, e2, part);
+    float m1, m2;
+    chunk_max(st, e1, e2, ref1, ref2, m1, m2);
+    const bool far = part != 0u && ((usable(m1) && fabsf(m1 - ref1) > kFar) || (usable(m2) && fabsf(m2 - ref2) > kFar));
+    if (!again && __any_sync(0xffffffffu, far)) {
+      if (far) take_refs(st, m1, m2);
+      again = true;
+      continue;
+    }
+    if (!MASK || part != 0u) fold_chunk(st, e1, e2, ref1, ref2, m1, m2);
+    again = false;
+    c += 16;
   }
 }
 
@@ -264,7 +297,7 @@ __device__ __forceinline__ bool add_tile(ModStats& st, uint32_t ts, const SideRe
     sums_all(e1, e2, s);
   }
   const float l1 = sum2(s.l1a, s.l1b), l2 = sum2(s.l2a, s.l2b);
-  bool ok = st.l1 != 0.f && st.m1 >= kLow && st.m2 >= kLow;
+  bool ok = st.l1 != 0.f && usable(st.m1) && usable(st.m2);
   ok = ok && l1 < 18446744073709551616.f && l2 < 18446744073709551616.f;  // 2^64
   if (CAP1) ok = ok && z1 <= zmax1;
   if (CAP2) ok = ok && z2 <= zmax2;

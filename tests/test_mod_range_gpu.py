@@ -10,7 +10,7 @@ import torch
 
 import attention_distillation_kl_gb300 as skl
 import mod_reference as ref
-from test_mod_gpu import f64, problem, sides, within
+from test_mod_gpu import check_backward, check_forward, f64, problem, sides, within
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,54 @@ def test_a_tables_mask_is_one_on_one_side_alone(lowest, splits):
     for t, w in zip(rows, (0.0, -math.inf, -math.inf)):
         assert torch.all(t[0, 1, gone] == w)
         assert torch.isfinite(t[0, 1, ~gone]).all() and torch.isfinite(t[0, 0]).all()
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("low", [-1e3, -1e4, -65504.0, -3e5])
+@pytest.mark.parametrize("kind", ["far both ways", "near one way", "far both ways, capped", "near one way, ids"])
+def test_finite_masks_cost_the_other_keys_nothing(kind, low, splits):
+    """A row whose first keys in the kernel's order are masked by a large finite entry: the later keys' scores keep
+    their own accuracy."""
+    both = "both" in kind
+    case = dict(NQ=500, NK=500, H=1, causal=not both, bias1="both ways" if both else "one way",
+                bias2="both ways" if both else "one way")
+    if "capped" in kind:
+        case.update(cap1=30.0, cap2=50.0)
+    if "ids" in kind:
+        case.update(docs="packed")
+    dev, kw, where, p = problem(seed=43, **case)
+    for t in "12":
+        tab = kw[t]["table"]
+        if both:
+            tab[:, 15] = tab[:, 31] = low
+        else:
+            tab[:, :8] = low
+        p["table" + t] = f64(tab)
+    p1, p2 = sides(dev, kw)
+    rows = check_forward(p1, p2, where, p, num_splits=splits)
+    for mode in "12":
+        check_backward(p1, p2, where, p, rows, mode)
+
+
+def test_steep_slopes_to_the_right():
+    """The kernel's first keys are the farthest: 1500 positions x slope 60 below the nearest."""
+    dev, kw, where, p = problem(seed=44, NQ=100, NK=1500, H=1, bias1="slopes", bias2="slopes", causal=False)
+    for t in "12":
+        kw[t]["slopes"][:] = 60.0
+        p["slopes" + t] = f64(kw[t]["slopes"])
+    p1, p2 = sides(dev, kw)
+    rows = check_forward(p1, p2, where, p)
+    for mode in "12":
+        check_backward(p1, p2, where, p, rows, mode)
+
+
+@pytest.mark.parametrize("side", ["1", "2"])
+def test_finite_masks_on_one_side(side):
+    """The other side's weight on the masked keys stays: its sum, of another reference, must not be taken for empty."""
+    for low in (-2e3, -65504.0):
+        dev, kw, where, p = problem(seed=49, NQ=500, NK=500, H=1, bias1="one way", bias2="one way")
+        kw[side]["table"][:, :8] = low
+        p["table" + side] = f64(kw[side]["table"])
+        p1, p2 = sides(dev, kw)
+        rows = check_forward(p1, p2, where, p)
+        check_backward(p1, p2, where, p, rows, "2")
