@@ -2,6 +2,7 @@
 // tensor maps, launches.  Every check that can fail does so before anything
 // is enqueued.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -166,14 +167,20 @@ skl::ModSide side_args(const streamkl_side& s, const float* near) {
   constexpr double kLog2e = 1.4426950408889634, kCut = 1.0e-8;
   const double scale = s.scale * (1.0 + kCut * (s.d / 16));
   m.scale = float(s.scale);
-  m.cmul = float((s.softcap != 0.f ? double(s.softcap) : scale) * kLog2e);
-  m.carg = s.softcap != 0.f ? float(scale / double(s.softcap)) : 0.f;
+  // A cap so far above the scores that u falls below fp32's normal range
+  // changes nothing: tanh(u x) = u x.
+  const double u = s.softcap != 0.f ? scale / double(s.softcap) : 0.0;
+  const bool capped = u >= double(FLT_MIN);
+  m.cmul = float((capped ? double(s.softcap) : scale) * kLog2e);
+  m.carg = capped ? float(u) : 0.f;
   m.poly[0] = m.cmul;
-  m.zmax = INFINITY;
-  if (s.softcap != 0.f) {
+  // (beside a capped side an uncapped one is a polynomial of degree 0, of an
+  // x^2 that has to be finite)
+  m.zmax = 1e36f;
+  if (capped) {
     // cmul tanh(carg x) = x poly(x^2): poly_k = cmul P_k carg^(2k + 1), where
     // those stay inside fp32's normal range
-    const double u = scale / double(s.softcap), c = double(s.softcap) * kLog2e;
+    const double c = double(s.softcap) * kLog2e;
     double p = c * u;
     bool fits = true;
     for (int k = 0; k < 5; ++k, p *= u * u) {

@@ -39,7 +39,7 @@ struct ModSide {
   float cmul;           // multiplies tanh (capped: cap log2 e) or x (s log2 e)
   float carg;           // s / cap; 0 without a cap
   float poly[5];        // Y log2 e = x poly(x^2) where x^2 <= zmax (no cap: cmul, 0, 0, 0, 0)
-  float zmax;           // infinity without a cap; below 0: nowhere
+  float zmax;           // 1e36 without a cap; below 0: nowhere
   int kind;             // kBiasNone, kBiasSlopes, kBiasTable
   int reach;            // table: buckets do not change beyond |r| = reach
   const float* slopes;  // [H]

@@ -158,3 +158,26 @@ def test_finite_masks_on_one_side(side):
         p1, p2 = sides(dev, kw)
         rows = check_forward(p1, p2, where, p)
         check_backward(p1, p2, where, p, rows, "2")
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-38, 1e-42, 1e-300])
+def test_a_cap_far_above_tiny_scores(scale):
+    """Capped scores that are all but zero: every visible key weighs the same."""
+    dev, kw, where, p = problem(seed=45, NQ=150, NK=200, cap1=1e6, cap2=1e6, scale1=scale, scale2=scale)
+    p1, p2 = sides(dev, kw)
+    rows = check_forward(p1, p2, where, p)
+    check_backward(p1, p2, where, p, rows, "2")
+
+
+@pytest.mark.parametrize("capped", ["1", "2"])
+def test_large_products_beside_a_capped_side(capped):
+    """q.k near 1e21 on the side without a cap, whose scale brings the scores back to a few units."""
+    other = "2" if capped == "1" else "1"
+    dev, kw, where, p = problem(seed=46, NQ=150, NK=200, **{"cap" + capped: 30.0, "scale" + other: 1e-21})
+    for x in "qk":
+        dev[x + other].mul_(2.0 ** 34)  # exact in bf16
+        p[x + other] = f64(dev[x + other])
+    p1, p2 = sides(dev, kw)
+    rows = check_forward(p1, p2, where, p)
+    for mode in "12":
+        check_backward(p1, p2, where, p, rows, mode)
