@@ -578,7 +578,8 @@ def streamkl_fwd_mod(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, 
     library's choice."""
     B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
     dev, num_splits, c = p1.device, int(num_splits), lib()
-    _check_stream(stream, dev)
+    if stream is not None:
+        _check_stream(stream, dev)
     need = c.streamkl_fwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, num_splits)
     ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
     kl, lse1, lse2 = _mod_rows((kl, lse1, lse2), ("kl", "lse1", "lse2"), (B, H, NQ), dev, stream)
@@ -607,7 +608,8 @@ def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=
     B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
     g = p2 if mode == STREAMKL_GRAD_P2 else p1
     dev, c = g.device, lib()
-    _check_stream(stream, dev)
+    if stream is not None:
+        _check_stream(stream, dev)
     for name, t in (("kl", kl), ("lse1", lse1), ("lse2", lse2), ("dkl", dkl)):
         if t is None:
             raise ValueError(f"{name} is missing")

@@ -203,10 +203,10 @@ __device__ __forceinline__ void fold_chunk(ModStats& st, uint64_t (&e1)[N], uint
 // does not matter.  Called by whole warps.
 //
 // Scores are rounded at the size of their distance to the reference.  Where a
-// chunk lies far from it (the keys before were masked by a large finite bias,
-// say: a whole chunk of entries of -65504 put errors of 0.004 into the scores
-// of the next one, and up to 0.02 into KL), it is taken again, against its own
-// maximum.
+// chunk's own are much smaller than that (the keys before were masked by a
+// large finite bias, say: a whole chunk of entries of -65504 put errors of
+// 0.004 into the scores of the next one, and up to 0.02 into KL), it is taken
+// again, against its own maximum.
 template <int kCols, bool CAP1, bool CAP2, int KIND, bool MASK>
 __device__ __forceinline__ void fold_tile(ModStats& st, uint32_t ts, const ModFwdArgs& a, const SideRegs& p1,
                                           const SideRegs& p2, const HeadBias* hb, int rmin, int r0, uint32_t bits) {
@@ -221,6 +221,10 @@ __device__ __forceinline__ void fold_tile(ModStats& st, uint32_t ts, const ModFw
 #pragma unroll 1
   for (int c = 0; c < kCols;) {
     const uint32_t part = MASK ? (bits >> c) & 0xffffu : 0xffffu;
+    if (MASK && __all_sync(0xffffffffu, part == 0u)) {
+      c += 16;
+      continue;
+    }
     const float ref1 = chunk_ref(st.m1), ref2 = chunk_ref(st.m2);
     RowBias rb1{0.f, 0.f, -ref1, -ref1, nullptr}, rb2{0.f, 0.f, -ref2, -ref2, nullptr};
     if (kBiased) {
@@ -241,7 +245,8 @@ __device__ __forceinline__ void fold_tile(ModStats& st, uint32_t ts, const ModFw
     if (MASK) mask_scores(e1, e2, part);
     float m1, m2;
     chunk_max(st, e1, e2, ref1, ref2, m1, m2);
-    const bool far = part != 0u && ((usable(m1) && fabsf(m1 - ref1) > kFar) || (usable(m2) && fabsf(m2 - ref2) > kFar));
+    auto above = [&](float m, float ref) { return usable(m) && m - ref > fmaxf(kFar, fabsf(m)); };
+    const bool far = part != 0u && (above(m1, ref1) || above(m2, ref2));
     if (!again && __any_sync(0xffffffffu, far)) {
       if (far) take_refs(st, m1, m2);
       again = true;

@@ -45,24 +45,26 @@ __global__ void __launch_bounds__(kAuxThreads) mod_prep_kernel(const __grid_cons
       const int len = near_len(t.max_distance), chunks = (len + kAuxThreads - 1) / kAuxThreads;
       const int h = blk / chunks, p = (blk - h * chunks) * kAuxThreads + threadIdx.x;
       if (p >= len) return;
+      const float* entries = t.table + size_t(h) * t.num_buckets;
+      float mask = -INFINITY;  // the largest masking entry, by a row's first warp
+      if (p < 32)
+#pragma unroll
+        for (int e = 0; e < kMaxBuckets; e += 32) {
+          const float x = p + e < t.num_buckets ? entries[p + e] * kLog2e : 0.f;
+          if (x < kLow) mask = fmaxf(mask, fmaxf(x, kNegBig));
+        }
       const int k = bucket_of(p - t.max_distance - kNearPad, t);
       if (t.bmap != nullptr && h == 0) t.bmap[p] = k;
       // a table's lowest values act as a mask: kept finite in base 2
-      const float* entries = t.table + size_t(h) * t.num_buckets;
       const float w = entries[k], v = w * kLog2e;
       float* row = t.near + size_t(h) * near_row(t.max_distance);
       row[p] = v < kNegBig ? kNegBig : (v > -kNegBig ? -kNegBig : v);
       if (p == 0 || p == len - 1)
         row[p == 0 ? len : len + 1] = fabsf(w) < 1.0e6f ? fmaf(w, kLog2e, -v) + w * kLog2eLo : 0.f;
       if (p < 32) {  // (a row is longer than a warp)
-        float m = -INFINITY;
-        for (int e = p; e < t.num_buckets; e += 32) {
-          const float x = entries[e] * kLog2e;
-          if (x < kLow) m = fmaxf(m, fmaxf(x, kNegBig));
-        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (p == 0) row[len + 2] = 0.5f * m;
+        for (int o = 16; o > 0; o >>= 1) mask = fmaxf(mask, __shfl_xor_sync(0xffffffffu, mask, o));
+        if (p == 0) row[len + 2] = 0.5f * mask;
       }
       return;
     }
