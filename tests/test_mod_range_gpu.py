@@ -181,3 +181,22 @@ def test_large_products_beside_a_capped_side(capped):
     rows = check_forward(p1, p2, where, p)
     for mode in "12":
         check_backward(p1, p2, where, p, rows, mode)
+
+
+@pytest.mark.parametrize("d", range(16, 129, 16))
+def test_the_scale_is_the_callers(d):
+    """Rows that see one key each, whose products q.k are exact: LSE is scale q.k.  Beside the scale's own rounding
+    (of scale log2 e to 32 bits, the same for all), what a row adds is the rounding of its score and of its LSE, evenly
+    spread within 2^-24 each: over 1024 rows their mean is below 2^-24 / 16 (ten standard deviations)."""
+    n, heads = 128, 8
+    q = torch.ones(1, heads, n, d) * (1 + torch.arange(heads)[None, :, None, None] / 8)
+    k = torch.ones(1, heads, n, d) * (64 + torch.arange(n)[None, None, :, None] / 2)
+    ids = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    q, k, scale = q.bfloat16().cuda(), k.bfloat16().cuda(), 1 / math.sqrt(d)
+    side = skl.AttnSide(q, k, scale)
+    kl, l1, l2 = skl.streamkl_fwd_mod(side, side, doc_q=ids, doc_k=ids)
+    want = scale * (f64(q) * f64(k)).sum(3)
+    rounded = float(np.float32(scale * math.log2(math.e))) / (scale * math.log2(math.e)) - 1
+    for got in (l1, l2):
+        assert abs((f64(got) / want - 1).mean() - rounded) < ref.F32 / 16 + 3e-9  # (ln 2 in 32 bits: 2.7e-9)
+    assert torch.all(kl.abs() < 1e-6)
