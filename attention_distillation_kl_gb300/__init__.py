@@ -188,6 +188,43 @@ def _out(t, shape, device, name):
     return t
 
 
+_here = contextlib.nullcontext()
+
+
+def _making(stream):
+    """Where a call's own tensors are made: on the stream that it runs on.  Memory of the
+    current stream may still be in use there, by work that `stream` does not wait for."""
+    return _here if stream is None else torch.cuda.stream(stream)
+
+
+def _handed_over(stream, device, *pairs):
+    """Tensors made by this call for the caller (old one None), who goes on on the current stream."""
+    if stream is not None:
+        here = torch.cuda.current_stream(device)
+        for old, new in pairs:
+            if old is None and new is not None:
+                new.record_stream(here)
+
+
+def _on_its_stream(fn):
+    """fn (its last parameter is `stream`) as a whole on the stream it is handed, where one is."""
+    at = fn.__code__.co_argcount - 1
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        here = torch.cuda.current_stream()
+        with _making(stream):
+            out = fn(*args, **kw)
+        for t in out:
+            t.record_stream(here)
+        return out
+    return call
+
+
+@_on_its_stream
 def streamkl_fwd(q1, k1, q2, k2, scale, causal, kl=None, lse1=None, lse2=None, stream=None):
     """Per-row KL(P1 || P2), LSE1, LSE2 (fp32 [B, H, NQ]); see include/streamkl.h."""
     B, H, NQ, NK, d1, d2 = _dims(q1, k1, q2, k2)
@@ -209,6 +246,7 @@ def streamkl_suggest_splits(B, H, NQ, NK, causal):
     return int(lib().streamkl_suggest_splits(B, H, NQ, NK, int(bool(causal))))
 
 
+@_on_its_stream
 def streamkl_fwd_splitk(q1, k1, q2, k2, scale, causal, num_splits, workspace=None,
                         kl=None, lse1=None, lse2=None, stream=None):
     """Key-split forward plus merge; ``workspace`` is a caller-owned byte buffer."""
@@ -232,6 +270,7 @@ def streamkl_fwd_splitk(q1, k1, q2, k2, scale, causal, num_splits, workspace=Non
 STREAMKL_STATIC_WORKSPACE_BYTES = 32 << 20
 
 
+@_on_its_stream
 def streamkl_fwd_splitk_noalloc(q1, k1, q2, k2, scale, causal, num_splits, kl=None, lse1=None,
                                 lse2=None, stream=None):
     """Key-split forward that allocates no device memory inside the library.
@@ -255,6 +294,7 @@ def streamkl_fwd_splitk_noalloc(q1, k1, q2, k2, scale, causal, num_splits, kl=No
     return kl, lse1, lse2
 
 
+@_on_its_stream
 def streamkl_bwd(q1, k1, q2, k2, scale, causal, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2,
                  deterministic=False, dq=None, dk=None, stream=None):
     """(dQ, dK) fp32 for the side ``mode`` selects; see include/streamkl.h."""
@@ -273,6 +313,7 @@ def streamkl_bwd(q1, k1, q2, k2, scale, causal, kl, lse1, lse2, dkl, mode=STREAM
     return dq, dk
 
 
+@_on_its_stream
 def streamkl_fwd_scaled(q1, k1, q2, k2, scale1, scale2, causal, kl=None, lse1=None, lse2=None, stream=None):
     """streamkl_fwd with S1 = scale1 Q1 K1^T and S2 = scale2 Q2 K2^T."""
     B, H, NQ, NK, d1, d2 = _dims(q1, k1, q2, k2)
@@ -286,6 +327,7 @@ def streamkl_fwd_scaled(q1, k1, q2, k2, scale1, scale2, causal, kl=None, lse1=No
     return kl, lse1, lse2
 
 
+@_on_its_stream
 def streamkl_fwd_splitk_scaled(q1, k1, q2, k2, scale1, scale2, causal, num_splits, workspace=None,
                                kl=None, lse1=None, lse2=None, stream=None):
     """streamkl_fwd_splitk with a softmax scale per side."""
@@ -305,6 +347,7 @@ def streamkl_fwd_splitk_scaled(q1, k1, q2, k2, scale1, scale2, causal, num_split
     return kl, lse1, lse2
 
 
+@_on_its_stream
 def streamkl_bwd_scaled(q1, k1, q2, k2, scale1, scale2, causal, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2,
                         deterministic=False, dq=None, dk=None, stream=None):
     """streamkl_bwd with a softmax scale per side (kl/lse from streamkl_fwd_scaled)."""
@@ -323,6 +366,7 @@ def streamkl_bwd_scaled(q1, k1, q2, k2, scale1, scale2, causal, kl, lse1, lse2, 
     return dq, dk
 
 
+@_on_its_stream
 def streamkl_fwd_gqa(q1, k1, q2, k2, scale1, scale2, causal, kl=None, lse1=None, lse2=None, stream=None):
     """streamkl_fwd_scaled with grouped key heads: k1 [B, HK1, NK, d1] and
     k2 [B, HK2, NK, d2], query head h reading key head h // (H // HK)."""
@@ -337,6 +381,7 @@ def streamkl_fwd_gqa(q1, k1, q2, k2, scale1, scale2, causal, kl=None, lse1=None,
     return kl, lse1, lse2
 
 
+@_on_its_stream
 def streamkl_fwd_splitk_gqa(q1, k1, q2, k2, scale1, scale2, causal, num_splits, workspace=None,
                             kl=None, lse1=None, lse2=None, stream=None):
     """streamkl_fwd_splitk_scaled with grouped key heads."""
@@ -356,6 +401,7 @@ def streamkl_fwd_splitk_gqa(q1, k1, q2, k2, scale1, scale2, causal, num_splits, 
     return kl, lse1, lse2
 
 
+@_on_its_stream
 def streamkl_bwd_gqa(q1, k1, q2, k2, scale1, scale2, causal, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2,
                      deterministic=False, dq=None, dk=None, stream=None):
     """streamkl_bwd_scaled with grouped key heads: dq [B, H, NQ, dg] per query
@@ -381,6 +427,7 @@ def streamkl_bwd_workspace_bytes(B, H, HK1, HK2, NK, d1, d2, mode=STREAMKL_GRAD_
     return int(lib().streamkl_bwd_workspace_bytes(B, H, HK1, HK2, NK, d1, d2, int(mode), int(bool(deterministic))))
 
 
+@_on_its_stream
 def streamkl_bwd_gqa_ws(q1, k1, q2, k2, scale1, scale2, causal, kl, lse1, lse2, dkl, workspace,
                         mode=STREAMKL_GRAD_P2, deterministic=True, dq=None, dk=None, stream=None):
     """streamkl_bwd_gqa with the deterministic mode's scratch in `workspace`
@@ -403,6 +450,7 @@ def streamkl_bwd_gqa_ws(q1, k1, q2, k2, scale1, scale2, causal, kl, lse1, lse2, 
     return dq, dk
 
 
+@_on_its_stream
 def streamkl_bwd_both(q1, k1, q2, k2, scale1, scale2, causal, kl, lse1, lse2, dkl, deterministic=False,
                       dq1=None, dk1=None, dq2=None, dk2=None, stream=None):
     """(dQ1, dK1, dQ2, dK2) fp32: the gradients of sum(dkl * KL) on both sides."""
@@ -484,24 +532,6 @@ def _mod_call(p1, p2, causal, prefix, doc_q, doc_k):
             raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {p1.device}")
     return B, H, NQ, NK, _Visible(1 if causal else 0, *(None if t is None else t.data_ptr()
                                                         for t in (prefix, doc_q, doc_k)))
-
-
-_here = contextlib.nullcontext()
-
-
-def _making(stream):
-    """Where a call's own tensors are made: on the stream that it runs on.  Memory of the
-    current stream may still be in use there, by work that `stream` does not wait for."""
-    return _here if stream is None else torch.cuda.stream(stream)
-
-
-def _handed_over(stream, device, *pairs):
-    """Tensors made by this call for the caller (old one None), who goes on on the current stream."""
-    if stream is not None:
-        here = torch.cuda.current_stream(device)
-        for old, new in pairs:
-            if old is None and new is not None:
-                new.record_stream(here)
 
 
 def _mod_workspace(workspace, need, device, stream):

@@ -69,3 +69,58 @@ def test_work_pending_on_the_current_stream_does_not_reach_the_results():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
+
+
+PLAIN = ["streamkl_fwd", "streamkl_fwd_splitk", "streamkl_fwd_splitk_noalloc", "streamkl_bwd", "streamkl_fwd_scaled",
+         "streamkl_fwd_splitk_scaled", "streamkl_bwd_scaled", "streamkl_fwd_gqa", "streamkl_fwd_splitk_gqa",
+         "streamkl_bwd_gqa", "streamkl_bwd_gqa_ws", "streamkl_bwd_both"]
+
+
+def test_the_plain_calls_run_on_their_stream_as_a_whole(monkeypatch):
+    import inspect
+    where, marked = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        where[0] = stream
+        yield
+        where[0] = None
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "here")
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: marked.append(s))
+
+    @skl._on_its_stream
+    def call(a, b=2, stream=None):
+        return [torch.full((1,), float(where[0] is not None))]
+
+    for out, n in ((call(1, 2, "other"), 1), (call(1, stream="other"), 1), (call(1), 0), (call(1, 2, None), 0)):
+        assert float(out[0]) == n
+    assert marked == ["here"] * 2
+    for name in PLAIN:
+        assert list(inspect.signature(getattr(skl, name)).parameters)[-1] == "stream"
+        assert hasattr(getattr(skl, name), "__wrapped__"), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("splits", [0, 4])
+def test_work_pending_on_the_current_stream_does_not_reach_the_plain_results(splits):
+    g = torch.Generator().manual_seed(3)
+    x = [torch.randn((1, 4, 512, 64), generator=g).to(torch.bfloat16).cuda() for _ in range(4)]
+    dkl = torch.ones((1, 4, 512), device="cuda")
+
+    def calls(**kw):
+        rows = skl.streamkl_fwd_splitk(*x, 0.125, True, splits, **kw) if splits else skl.streamkl_fwd(*x, 0.125, True, **kw)
+        return list(rows) + list(skl.streamkl_bwd(*x, 0.125, True, *rows, dkl, deterministic=True, **kw))
+
+    want = [t.clone() for t in calls()]
+    sizes = [t.numel() * 4 for t in want] + [skl.streamkl_fwd_splitk_workspace_bytes(1, 4, 512, max(splits, 1))]
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        for n in sizes:
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x5a)
+        got = calls(stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
