@@ -633,8 +633,10 @@ def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=
                      doc_k=None, deterministic=False, table_grad=True, dq=None, dk=None, dtable=None, workspace=None,
                      stream=None):
     """(dq, dk, dtable) for the side `mode` selects: bf16 gradients of its q
-    and k, and fp32 of its table (None when it has none or table_grad is
-    False).  kl, lse1, lse2 come from streamkl_fwd_mod over the same arguments."""
+    and k (each score's gradient is rounded to bf16 before its products, their
+    sums once more), and fp32 of its table (None when it has none or table_grad
+    is False).  kl, lse1, lse2 come from streamkl_fwd_mod over the same
+    arguments."""
     B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
     g = p2 if mode == STREAMKL_GRAD_P2 else p1
     dev, c = g.device, lib()

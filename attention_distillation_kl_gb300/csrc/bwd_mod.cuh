@@ -11,7 +11,7 @@
 // The pipeline is the fused backward's (bwd.cu; the same warps, barriers and
 // TMEM map): one CTA per query head and 128-key tile walks the query tiles
 // that can see it, dK accumulates in TMEM, dQ leaves as fp32 reduce-adds into
-// a workspace that launch_mod_convert rounds to bf16 once at the end.
+// a workspace that launch_mod_finish rounds to bf16 once at the end.
 // What differs: the dS warps' arithmetic; K rows whose id matches nothing and
 // Q rows that saw no key are zeroed in shared memory before a product reads
 // them (they may hold anything); with ids the walk is cut to the query tiles that share one;

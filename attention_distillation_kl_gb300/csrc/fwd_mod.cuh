@@ -643,9 +643,10 @@ int launch_fwd_mod_k(const ModMaps& m, const ModFwdArgs& a, cudaStream_t st) {
 
 // One kernel for each set of modifications: what a side does not have must
 // not cost the loop over full tiles registers or instructions (with 16 + 2
-// warps a thread has 96).  At 8K x 32 heads, d = 128, causal, one kernel that
-// branched took 635 us without modifications and 962 with both sides capped;
-// these take 464 and 788 (the plain forward 460).
+// warps a thread has 96).  At 8K x 32 heads, d = 128, causal, the last kernel
+// that branched (64 columns a warp) took 593 us without modifications and 906
+// with both sides capped, a kernel for each set 497 and 831; these take 468
+// and 778 (the plain forward 460).
 template <int D1, int D2, bool CAP1, bool CAP2>
 int launch_fwd_mod_c(const ModMaps& m, const ModFwdArgs& a, cudaStream_t st) {
   const bool masked = a.vis.ids_q != nullptr || a.vis.prefix != nullptr;

@@ -18,6 +18,8 @@
  *
  * Conventions shared by every entry point
  * ---------------------------------------
+ * (streamkl_fwd_mod and streamkl_bwd_mod have their own layout, scale, head
+ * dims and rule for causal with NQ > NK; they are given there.)
  * Layout: q1 [B, H, NQ, d1], k1 [B, H, NK, d1], q2 [B, H, NQ, d2],
  *   k2 [B, H, NK, d2], bf16, row-major and contiguous (BHSD).  Per-row
  *   vectors (kl, lse1, lse2, dkl) are fp32 [B, H, NQ], contiguous.
@@ -284,6 +286,10 @@ int streamkl_bwd_both(const void* q1, const void* k1, const void* q2, const void
  *   bidirectional = 1, n = num_buckets / 2, d = |r|, and n is added where
  *   r > 0.  With e = n / 2 (rounded down): d for d < e, else
  *   min(n - 1, e + floor((n - e) ln(d / e) / ln(max_distance / e))).
+ *
+ * Size of scores: they are computed in fp32, and a row's P is rebuilt in the
+ * backward from its fp32 LSE, so beyond +-1e6 (masks apart) a row's weights
+ * are no longer known; scores and q.k have to stay below 1e18.
  */
 typedef struct streamkl_view { /* bf16 [B][heads][N][d]; strides in elements, the last dimension dense */
   void* data;                  /* 16-byte aligned */
@@ -338,14 +344,16 @@ int streamkl_fwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
 /*
  * Backward: the gradient of sum_i dkl_i KL_i for the side `mode` selects,
  * from a forward over the same arguments.  dq [B][H][NQ][d] and
- * dk [B][HK][NK][d] of that side are bf16 (the type of q and k), summed in
- * fp32 and rounded once; they are fully overwritten.  dtable (fp32
+ * dk [B][HK][NK][d] of that side are bf16 (the type of q and k); they are
+ * fully overwritten.  Two roundings to bf16 are in them: of the gradient of
+ * each score before its products with k and q (as in the other backward
+ * calls), and of the fp32 sums of those products.  dtable (fp32
  * [H][num_buckets], contiguous, or null): the gradient of that side's table,
  * in fp32 and added in a fixed order; INVALID_ARG when the side has none.
  * No output may overlap an input or another output.
- * Rows that see no key, and positions whose id is negative, get zeros and
- * contribute none, whatever q, k and dkl hold there.  Other masked positions
- * must hold finite values.  deterministic = 1: dq and dk bitwise
+ * Rows that see no key (LSE -inf) get zeros and contribute none, whatever q
+ * and dkl hold there, and so do keys whose id is negative, whatever k holds.
+ * Other keys must hold finite values.  deterministic = 1: dq and dk bitwise
  * reproducible (streamkl_bwd_gqa says how); dtable always is.  workspace as
  * above, with streamkl_bwd_mod_workspace_bytes (table_grad: whether dtable
  * is given).  With no query rows dk and dtable become zeros.
