@@ -501,7 +501,8 @@ class AttnSide:
             raise ValueError("q and k must be on the same device")
         if slopes is not None or table is not None:
             for name, t in (("slopes", slopes), ("table", table)):
-                if t is not None and (t.dtype != torch.float32 or t.device != device or not t.is_contiguous()):
+                if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or
+                                      t.device != device or not t.is_contiguous()):
                     raise TypeError(f"{name} must be a contiguous fp32 tensor on {device}")
             if slopes is not None and tuple(slopes.shape) != (H,):
                 raise ValueError(f"slopes must have one value for each of the {H} heads")
@@ -528,7 +529,8 @@ def _mod_call(p1, p2, causal, prefix, doc_q, doc_k):
     for name, t, shape in (("prefix", prefix, (B,)), ("doc_q", doc_q, (B, NQ)), ("doc_k", doc_k, (B, NK))):
         if t is None:
             continue
-        if t.dtype != torch.int32 or t.device != p1.device or not t.is_contiguous() or tuple(t.shape) != shape:
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != p1.device or \
+                not t.is_contiguous() or tuple(t.shape) != shape:
             raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {p1.device}")
     return B, H, NQ, NK, _Visible(1 if causal else 0, *(None if t is None else t.data_ptr()
                                                         for t in (prefix, doc_q, doc_k)))
@@ -541,7 +543,7 @@ def _mod_workspace(workspace, need, device, stream):
             return None, 0, None
         with _making(stream):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
