@@ -216,7 +216,10 @@ def _on_its_stream(fn):
         if stream is None:
             return fn(*args, **kw)
         here = torch.cuda.current_stream()
-        with _making(stream):
+        on = stream
+        if hasattr(stream, "cuda_stream") and not isinstance(stream, torch.Stream):  # another library's
+            on = torch.cuda.ExternalStream(stream.cuda_stream)
+        with _making(on):
             out = fn(*args, **kw)
         for t in out:
             t.record_stream(here)

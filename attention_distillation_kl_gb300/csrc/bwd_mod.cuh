@@ -14,8 +14,8 @@
 // a workspace that launch_mod_finish rounds to bf16 once at the end.
 // What differs: the dS warps' arithmetic; K rows whose id matches nothing and
 // Q rows that saw no key are zeroed in shared memory before a product reads
-// them (they may hold anything); with ids the walk is cut to the query tiles that share one;
-// dK goes out as bf16 where one CTA owns it.
+// them (they may hold anything); with ids the walk is cut to the query tiles
+// that share one; dK goes out as bf16 where one CTA owns it.
 //
 // The table's gradient (kTab): along a warp's 32 x 32 block of dS the
 // relative position is constant on diagonals, so 32 steps of "shift by one

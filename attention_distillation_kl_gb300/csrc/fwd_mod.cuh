@@ -14,9 +14,9 @@
 // way to it).  -m_t is added with the bias, in the operation that finishes
 // the score.  Any reference serves as long as no term overflows and the
 // largest does not underflow: a row takes the rounded maximum of its first
-// visible chunk, and a chunk whose sums reach 2^64 moves it; a chunk far from
-// it is taken again, relative to its own maximum.  References are
-// whole numbers, so moving one is exact: by d1, d2,
+// visible chunk, and a chunk whose sums reach 2^64 moves it; a chunk of scores
+// much smaller than their distance to it is taken again, relative to its own
+// maximum.  References are whole numbers, so moving one is exact: by d1, d2,
 //   l_t <- l_t 2^-d_t,  acc <- 2^-d1 (acc - (d1 - d2) l1).
 // Scores beyond 10^6 (mostly a mask written as a bias) give no usable
 // reference: the chunks after them are taken relative to 0.
