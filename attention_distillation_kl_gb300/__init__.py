@@ -23,7 +23,7 @@ __all__ = [
     "streamkl_fwd_gqa", "streamkl_fwd_splitk_gqa", "streamkl_bwd_gqa", "streamkl_bwd_both",
     "streamkl_bwd_workspace_bytes", "streamkl_bwd_gqa_ws",
     "AttnSide", "streamkl_fwd_mod", "streamkl_fwd_mod_workspace_bytes", "streamkl_bwd_mod",
-    "streamkl_bwd_mod_workspace_bytes",
+    "streamkl_bwd_mod_workspace_bytes", "Rotary", "streamkl_rotate", "streamkl_pool_blocks",
     "status_string", "STREAMKL_STATIC_WORKSPACE_BYTES",
     "streamkl_get_device_status", "streamkl_probe_ex2", "streamkl_selftest_wait_timeout",
     "streamkl_selftest_turn_timeout",
@@ -62,11 +62,17 @@ class _Side(ctypes.Structure):
                 ("table", _P), ("num_buckets", _I), ("max_distance", _I), ("bidirectional", _I)]
 
 
+class _Rotary(ctypes.Structure):
+    _fields_ = [("positions", _P), ("stride_axis", _LL), ("stride_b", _LL), ("inv_freq", _P), ("axes", _I),
+                ("section", _I * 4), ("interleaved", _I)]
+
+
 class _Visible(ctypes.Structure):
     _fields_ = [("causal", _I), ("prefix", _P), ("doc_q", _P), ("doc_k", _P)]
 
 
 _SP, _VP, _VISP = ctypes.POINTER(_Side), ctypes.POINTER(_View), ctypes.POINTER(_Visible)
+_RP = ctypes.POINTER(_Rotary)
 
 _SIGS = {
     "streamkl_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _P]),
@@ -97,6 +103,8 @@ _SIGS = {
     "streamkl_fwd_mod": (_I, [_SP, _SP, _VISP, _I, _I, _I, _I, _I, _P, _SZ, _P, _P, _P, _P]),
     "streamkl_bwd_mod_workspace_bytes": (_SZ, [_SP, _SP, _VISP, _I, _I, _I, _I, _I, _I, _I]),
     "streamkl_bwd_mod": (_I, [_SP, _SP, _VISP, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _VP, _VP, _P, _P, _SZ, _P]),
+    "streamkl_rotate": (_I, [_VP, _VP, _RP, _I, _I, _I, _I, _I, _P]),
+    "streamkl_pool_blocks": (_I, [_VP, _P, _I, _I, _I, _I, _I, _VP, _P]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
     "streamkl_get_device_status": (_I, []),
     "streamkl_probe_ex2": (_I, [_P, _I, _I, _P]),
@@ -669,6 +677,112 @@ def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=
                               dtable.data_ptr() if want_table else None, ws, ws_bytes, _mod_stream(stream, dev)),
            "streamkl_bwd_mod")
     return dq, dk, dtable if want_table else None
+
+
+def _strided(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bf16 tensor")
+    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+        raise ValueError(f"{name} must be a [B, heads, N, d] tensor whose last dimension is dense")
+    return t
+
+
+def _like_new(shape, device, stream, given, name, dtype=torch.bfloat16):
+    """An output of the call: the caller's, checked, or one made on the call's stream."""
+    if given is not None:
+        if not isinstance(given, torch.Tensor) or given.dtype != dtype or tuple(given.shape) != tuple(shape) or \
+                given.device != device or (given.shape[-1] > 1 and given.stride(-1) != 1):
+            raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device} with a dense "
+                             "last dimension")
+        return given
+    with _making(stream):
+        new = torch.empty(shape, dtype=dtype, device=device)
+    _handed_over(stream, device, (None, new))
+    return new
+
+
+def _at_device(fn):
+    """Runs fn with its first tensor's device current (the library launches there)."""
+    @functools.wraps(fn)
+    def wrapped(x, *a, **k):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device.index == torch.cuda.current_device():
+            return fn(x, *a, **k)
+        with torch.cuda.device(x.device):
+            return fn(x, *a, **k)
+    return wrapped
+
+
+class Rotary:
+    """Rotary positions with several axes (see the header): inv_freq [R] (fp32,
+    contiguous), positions [axes, B, N], or [axes, N] for every batch entry
+    alike (int32, the last dimension dense), sections: the pairs of each axis
+    (None: one axis has all R), interleaved: pairs (2p, 2p + 1) instead of
+    (p, p + R).
+
+    Holds references to its tensors, no copies; may be used for any number of
+    calls while they keep their memory.
+    """
+
+    def __init__(self, inv_freq, positions, sections=None, interleaved=False):
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float32 or not inv_freq.is_cuda or \
+                inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise TypeError("inv_freq must be a contiguous CUDA fp32 tensor of one dimension")
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or \
+                positions.device != inv_freq.device:
+            raise TypeError(f"positions must be an int32 tensor on {inv_freq.device}")
+        if positions.dim() not in (2, 3) or (positions.shape[-1] > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be [axes, B, N] or [axes, N], the last dimension dense")
+        R, axes = inv_freq.shape[0], positions.shape[0]
+        sections = [R] if sections is None else [int(n) for n in sections]
+        if not 1 <= axes <= 4 or len(sections) != axes or sum(sections) != R or min(sections) < 1:
+            raise ValueError(f"sections must give each of the {axes} axes (1 to 4) its share of the {R} pairs")
+        self.inv_freq, self.positions, self.device = inv_freq, positions, inv_freq.device
+        self.batch, self.tokens = (positions.shape[1] if positions.dim() == 3 else None), positions.shape[-1]
+        self._c = _Rotary(positions.data_ptr(), positions.stride(0),
+                          positions.stride(1) if positions.dim() == 3 and self.batch > 1 else 0,
+                          inv_freq.data_ptr(), axes, (_I * 4)(*sections), int(bool(interleaved)))
+
+
+@_at_device
+def streamkl_rotate(x, rotary, inverse=False, out=None, stream=None):
+    """x [B, heads, N, d] (bf16, strides as AttnSide's) turned by the positions
+    of `rotary`, or turned back (inverse=True: also the gradient).  out may be
+    x itself."""
+    _strided(x, "x")
+    B, H, N, d = x.shape
+    if not isinstance(rotary, Rotary):
+        raise TypeError("rotary must be a Rotary")
+    if rotary.device != x.device or rotary.tokens != N or rotary.batch not in (None, B):
+        raise ValueError(f"rotary must hold positions of {N} tokens, and of {B} batch entries or of all alike, on {x.device}")
+    if stream is not None:
+        _check_stream(stream, x.device)
+    if out is not None and out is not x and isinstance(out, torch.Tensor) and out.numel() and \
+            out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+        raise ValueError("out must be x itself or not overlap it")
+    y = _like_new(x.shape, x.device, stream, out, "out")
+    _check(lib().streamkl_rotate(_view(x), _view(y), rotary._c, B, H, N, d, int(bool(inverse)),
+                                 _mod_stream(stream, x.device)), "streamkl_rotate")
+    return y
+
+
+@_at_device
+def streamkl_pool_blocks(k, block, doc_k=None, out=None, stream=None):
+    """One key for each block of `block` keys (32, 64 or 128): the mean of those
+    whose id in doc_k [B, NK] (int32) is not negative, all without ids; bf16
+    [B, HK, ceil(NK / block), d]."""
+    _strided(k, "k")
+    B, HK, NK, d = k.shape
+    if doc_k is not None and (not isinstance(doc_k, torch.Tensor) or doc_k.dtype != torch.int32 or
+                              doc_k.device != k.device or not doc_k.is_contiguous() or tuple(doc_k.shape) != (B, NK)):
+        raise ValueError(f"doc_k must be a contiguous int32 tensor of shape {(B, NK)} on {k.device}")
+    if block not in (32, 64, 128):
+        raise ValueError("block must be 32, 64 or 128")
+    if stream is not None:
+        _check_stream(stream, k.device)
+    y = _like_new((B, HK, -(-NK // block), d), k.device, stream, out, "out")
+    _check(lib().streamkl_pool_blocks(_view(k), None if doc_k is None else doc_k.data_ptr(), B, HK, NK, d, block,
+                                      _view(y), _mod_stream(stream, k.device)), "streamkl_pool_blocks")
+    return y
 
 
 def streamkl_get_device_status():

@@ -366,6 +366,45 @@ int streamkl_bwd_mod(const streamkl_side* p1, const streamkl_side* p2, const str
                      int deterministic, const streamkl_view* dq, const streamkl_view* dk, float* dtable,
                      void* workspace, size_t workspace_bytes, streamkl_stream_t stream);
 
+/*
+ * Rotary positions with several axes (models whose tokens have a place in
+ * time, height and width).  Pair p of a row turns by the angle
+ *   position of the pair's axis * inv_freq[p],
+ * (u, v) -> (u cos - v sin, u sin + v cos); the first section[0] pairs belong
+ * to axis 0, the next section[1] to axis 1, and so on, R pairs in all.  Pair p
+ * is the values (p, p + R), or with interleaved = 1 (2p, 2p + 1); the values
+ * from 2R on stay as they are.  inverse = 1 turns back, which gives the
+ * gradient of x from that of y.  Angles are exact to 1e-7 radians up to
+ * positions of 10^6 and beyond; y is rounded to bf16 once.
+ */
+typedef struct streamkl_rotary {
+  const int* positions;             /* device; token n of batch entry b on axis a: positions[a * stride_axis + b * stride_b + n] */
+  long long stride_axis, stride_b;  /* in ints, not negative (stride_b = 0: the same for the whole batch) */
+  const float* inv_freq;            /* device [R], finite: radians per position */
+  int axes;                         /* 1 .. 4 */
+  int section[4];                   /* pairs of each axis, at least 1; R, their sum, at most d / 2 */
+  int interleaved;                  /* 0 or 1 */
+} streamkl_rotary;
+
+/* y = x turned, both [B][heads][N][d] (d a multiple of 16 up to 256).  y may be x itself, with the same strides;
+ * otherwise they must not overlap. */
+int streamkl_rotate(const streamkl_view* x, const streamkl_view* y, const streamkl_rotary* r, int B, int heads, int N,
+                    int d, int inverse, streamkl_stream_t stream);
+
+/*
+ * Attention KL over selected blocks of keys: the distributions of models that
+ * attend, for each query, only to a few blocks of keys that a cheap score has
+ * chosen.  Key j is in block j / block (block: 32, 64 or 128 keys; the last
+ * one may be shorter).
+ *
+ * streamkl_pool_blocks: one key for each block, the mean of its keys whose id
+ * (doc_k [B][NK], or null: all) is not negative; zeros for a block without
+ * one.  kb is bf16 [B][HK][blocks][d].  What keys with negative ids hold does
+ * not matter.
+ */
+int streamkl_pool_blocks(const streamkl_view* k, const int* doc_k, int B, int HK, int NK, int d, int block,
+                         const streamkl_view* kb, streamkl_stream_t stream);
+
 /* Static, NUL-terminated description of a status value. */
 const char* streamkl_status_string(int status);
 
