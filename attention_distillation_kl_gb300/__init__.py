@@ -24,6 +24,7 @@ __all__ = [
     "streamkl_bwd_workspace_bytes", "streamkl_bwd_gqa_ws",
     "AttnSide", "streamkl_fwd_mod", "streamkl_fwd_mod_workspace_bytes", "streamkl_bwd_mod",
     "streamkl_bwd_mod_workspace_bytes", "Rotary", "streamkl_rotate", "streamkl_pool_blocks",
+    "streamkl_fwd_sel", "streamkl_fwd_sel_workspace_bytes",
     "status_string", "STREAMKL_STATIC_WORKSPACE_BYTES",
     "streamkl_get_device_status", "streamkl_probe_ex2", "streamkl_selftest_wait_timeout",
     "streamkl_selftest_turn_timeout",
@@ -71,8 +72,12 @@ class _Visible(ctypes.Structure):
     _fields_ = [("causal", _I), ("prefix", _P), ("doc_q", _P), ("doc_k", _P)]
 
 
+class _Blocks(ctypes.Structure):
+    _fields_ = [("selected", _P), ("heads", _I), ("count", _I), ("block", _I)]
+
+
 _SP, _VP, _VISP = ctypes.POINTER(_Side), ctypes.POINTER(_View), ctypes.POINTER(_Visible)
-_RP = ctypes.POINTER(_Rotary)
+_RP, _BP = ctypes.POINTER(_Rotary), ctypes.POINTER(_Blocks)
 
 _SIGS = {
     "streamkl_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _P]),
@@ -105,6 +110,8 @@ _SIGS = {
     "streamkl_bwd_mod": (_I, [_SP, _SP, _VISP, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _VP, _VP, _P, _P, _SZ, _P]),
     "streamkl_rotate": (_I, [_VP, _VP, _RP, _I, _I, _I, _I, _I, _P]),
     "streamkl_pool_blocks": (_I, [_VP, _P, _I, _I, _I, _I, _I, _VP, _P]),
+    "streamkl_fwd_sel_workspace_bytes": (_SZ, [_SP, _SP, _VISP, _BP, _I, _I, _I, _I]),
+    "streamkl_fwd_sel": (_I, [_SP, _SP, _VISP, _BP, _I, _I, _I, _I, _P, _SZ, _P, _P, _P, _P]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
     "streamkl_get_device_status": (_I, []),
     "streamkl_probe_ex2": (_I, [_P, _I, _I, _P]),
@@ -783,6 +790,43 @@ def streamkl_pool_blocks(k, block, doc_k=None, out=None, stream=None):
     _check(lib().streamkl_pool_blocks(_view(k), None if doc_k is None else doc_k.data_ptr(), B, HK, NK, d, block,
                                       _view(y), _mod_stream(stream, k.device)), "streamkl_pool_blocks")
     return y
+
+
+def _sel_call(blocks, block, p1):
+    """streamkl_blocks of a selection, its shape and device checked."""
+    B, H, NQ = p1.rows
+    if not isinstance(blocks, torch.Tensor) or blocks.dtype != torch.int32 or blocks.device != p1.device or \
+            blocks.dim() != 4 or not blocks.is_contiguous():
+        raise ValueError(f"blocks must be a contiguous int32 tensor [B, heads, NQ, count] on {p1.device}")
+    if blocks.shape[0] != B or blocks.shape[2] != NQ:
+        raise ValueError(f"blocks must hold a list for each of the {B} x {NQ} queries")
+    return _Blocks(blocks.data_ptr(), blocks.shape[1], blocks.shape[3], int(block))
+
+
+@_on_device
+def streamkl_fwd_sel_workspace_bytes(p1, p2, blocks, block, causal=False, prefix=None, doc_q=None, doc_k=None):
+    """Workspace bytes streamkl_fwd_sel needs for these arguments."""
+    B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
+    return int(lib().streamkl_fwd_sel_workspace_bytes(p1._c, p2._c, vis, _sel_call(blocks, block, p1), B, H, NQ, NK))
+
+
+@_on_device
+def streamkl_fwd_sel(p1, p2, blocks, block, causal=False, prefix=None, doc_q=None, doc_k=None, workspace=None, kl=None,
+                     lse1=None, lse2=None, stream=None):
+    """Per-row KL(P1 || P2), LSE1, LSE2 of two plain AttnSides as
+    streamkl_fwd_mod, over the keys of the blocks that each query selected:
+    blocks int32 [B, heads, NQ, count], entries of keys j // block, any order,
+    negative ones empty; each of its heads serves H // heads query heads."""
+    B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
+    sel, dev, c = _sel_call(blocks, block, p1), p1.device, lib()
+    if stream is not None:
+        _check_stream(stream, dev)
+    need = c.streamkl_fwd_sel_workspace_bytes(p1._c, p2._c, vis, sel, B, H, NQ, NK)
+    ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
+    kl, lse1, lse2 = _mod_rows((kl, lse1, lse2), ("kl", "lse1", "lse2"), (B, H, NQ), dev, stream)
+    _check(c.streamkl_fwd_sel(p1._c, p2._c, vis, sel, B, H, NQ, NK, ws, ws_bytes, kl.data_ptr(), lse1.data_ptr(),
+                              lse2.data_ptr(), _mod_stream(stream, dev)), "streamkl_fwd_sel")
+    return kl, lse1, lse2
 
 
 def streamkl_get_device_status():

@@ -12,12 +12,13 @@
 #include "host.cuh"
 #include "kernels.cuh"
 #include "mod_common.cuh"
+#include "mod_host.cuh"
 #include "streamkl.h"
 #include "views.cuh"
 
-namespace {
+namespace skl {
 
-using namespace skl;
+namespace {
 
 int check_side(const streamkl_side* s, int B, int H, int NQ, int NK, bool data) {
   if (s == nullptr) return STREAMKL_INVALID_ARG;
@@ -30,14 +31,28 @@ int check_side(const streamkl_side* s, int B, int H, int NQ, int NK, bool data) 
   if (s->table != nullptr) {
     if (s->bidirectional != 0 && s->bidirectional != 1) return STREAMKL_INVALID_ARG;
     const int n = s->bidirectional ? s->num_buckets / 2 : s->num_buckets;
-    if (s->num_buckets < 2 || s->num_buckets > skl::kMaxBuckets || n < 2) return STREAMKL_INVALID_ARG;
+    if (s->num_buckets < 2 || s->num_buckets > kMaxBuckets || n < 2) return STREAMKL_INVALID_ARG;
     if (s->bidirectional && s->num_buckets % 2 != 0) return STREAMKL_INVALID_ARG;
-    if (s->max_distance <= n / 2 || s->max_distance > skl::kMaxDistance) return STREAMKL_INVALID_ARG;
+    if (s->max_distance <= n / 2 || s->max_distance > kMaxDistance) return STREAMKL_INVALID_ARG;
   }
   if (s->d < 16 || s->d > 128 || s->d % 16 != 0) return STREAMKL_UNSUPPORTED;
   if (data && (!view_ok(s->q, B, H, NQ) || !view_ok(s->k, B, s->HK, NK))) return STREAMKL_INVALID_ARG;
   return STREAMKL_OK;
 }
+
+// A direction's first distance of each bucket: one distance each up to half
+// of them, then steps of the logarithm up to max_distance.  In 64 bits; a
+// border that is a whole number (the logarithm's steps meet one whenever the
+// ratio is a power) must not round up past itself.
+void bucket_borders(ModPrepArgs::Table& t) {
+  const int n = t.both ? t.num_buckets / 2 : t.num_buckets, e = n / 2;
+  t.per_side = n;
+  for (int i = 0; i < n; ++i)
+    t.first[i] = i <= e ? i
+                        : int(std::ceil(e * std::pow(double(t.max_distance) / e, double(i - e) / (n - e)) * (1.0 - 1e-12)));
+}
+
+}  // namespace
 
 // Sizes, masks and both sides.  *empty: no query row (or head) to compute.
 int check_call(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis, int B, int H, int NQ,
@@ -60,26 +75,8 @@ int check_call(const streamkl_side* p1, const streamkl_side* p2, const streamkl_
   return STREAMKL_OK;
 }
 
-bool make_maps(skl::ModMaps* m, const streamkl_side& p1, const streamkl_side& p2, int B, int H, int NQ, int NK,
-               int q_rows = kTile) {
-  return map_bf16(&m->q1, p1.q, B, H, NQ, p1.d, q_rows) && map_bf16(&m->k1, p1.k, B, p1.HK, NK, p1.d) &&
-         map_bf16(&m->q2, p2.q, B, H, NQ, p2.d, q_rows) && map_bf16(&m->k2, p2.k, B, p2.HK, NK, p2.d);
-}
-
-// A direction's first distance of each bucket: one distance each up to half
-// of them, then steps of the logarithm up to max_distance.  In 64 bits; a
-// border that is a whole number (the logarithm's steps meet one whenever the
-// ratio is a power) must not round up past itself.
-void bucket_borders(skl::ModPrepArgs::Table& t) {
-  const int n = t.both ? t.num_buckets / 2 : t.num_buckets, e = n / 2;
-  t.per_side = n;
-  for (int i = 0; i < n; ++i)
-    t.first[i] = i <= e ? i
-                        : int(std::ceil(e * std::pow(double(t.max_distance) / e, double(i - e) / (n - e)) * (1.0 - 1e-12)));
-}
-
 // The part of the workspace that both calls use: ids and lookup rows.
-void take_prep(Carver& c, skl::ModPrepArgs& a, const streamkl_side* const p[2], const streamkl_visible& vis, int B, int H, int NQ,
+void take_prep(Carver& c, ModPrepArgs& a, const streamkl_side* const p[2], const streamkl_visible& vis, int B, int H, int NQ,
                int NK, int table_grad_side) {
   a.B = B;
   a.H = H;
@@ -100,9 +97,25 @@ void take_prep(Carver& c, skl::ModPrepArgs& a, const streamkl_side* const p[2], 
     a.t[i].max_distance = p[i]->max_distance;
     a.t[i].both = p[i]->bidirectional;
     if (c.base != nullptr) bucket_borders(a.t[i]);
-    a.t[i].near = c.take<float>(size_t(H) * skl::near_row(p[i]->max_distance));
-    if (i == table_grad_side) a.t[i].bmap = c.take<int>(skl::near_len(p[i]->max_distance));
+    a.t[i].near = c.take<float>(size_t(H) * near_row(p[i]->max_distance));
+    if (i == table_grad_side) a.t[i].bmap = c.take<int>(near_len(p[i]->max_distance));
   }
+}
+
+ModVis vis_args(const streamkl_visible& v, const ModPrepArgs& p) {
+  return ModVis{v.causal, v.prefix, p.ids_q, p.ids_k, p.tiles_q, p.tiles_k};
+}
+
+}  // namespace skl
+
+namespace {
+
+using namespace skl;
+
+bool make_maps(skl::ModMaps* m, const streamkl_side& p1, const streamkl_side& p2, int B, int H, int NQ, int NK,
+               int q_rows = kTile) {
+  return map_bf16(&m->q1, p1.q, B, H, NQ, p1.d, q_rows) && map_bf16(&m->k1, p1.k, B, p1.HK, NK, p1.d) &&
+         map_bf16(&m->q2, p2.q, B, H, NQ, p2.d, q_rows) && map_bf16(&m->k2, p2.k, B, p2.HK, NK, p2.d);
 }
 
 skl::ModSide side_args(const streamkl_side& s, const float* near) {
@@ -140,10 +153,6 @@ skl::ModSide side_args(const streamkl_side& s, const float* near) {
   m.slopes = s.slopes;
   m.near = near;
   return m;
-}
-
-skl::ModVis vis_args(const streamkl_visible& v, const skl::ModPrepArgs& p) {
-  return skl::ModVis{v.causal, v.prefix, p.ids_q, p.ids_k, p.tiles_q, p.tiles_k};
 }
 
 struct FwdPlan {

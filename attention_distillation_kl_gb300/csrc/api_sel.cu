@@ -1,0 +1,197 @@
+// C entry points over selected blocks: argument validation, workspace layout,
+// tensor maps, launches.  Every check that can fail does so before anything
+// is enqueued.
+#include <algorithm>
+#include <numeric>
+
+#include "mod_host.cuh"
+#include "sel_common.cuh"
+
+namespace {
+
+using namespace skl;
+
+int num_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+int check_blocks(const streamkl_blocks* s, int B, int H, int NQ, int NK, bool data) {
+  if (s == nullptr) return STREAMKL_INVALID_ARG;
+  if (s->block != 32 && s->block != 64 && s->block != 128) return STREAMKL_INVALID_ARG;
+  if (s->count < 1 || s->count > kMaxSlots) return STREAMKL_INVALID_ARG;
+  if (s->heads < 1 || s->heads > std::max(H, 1) || H % s->heads != 0) return STREAMKL_INVALID_ARG;
+  if ((NK + s->block - 1) / s->block > kMaxSelBlocks) return STREAMKL_UNSUPPORTED;
+  if (data && (s->selected == nullptr || !aligned4(s->selected))) return STREAMKL_INVALID_ARG;
+  if (NQ >= 1 << (32 - kSlotBits) || (long long)B * s->heads * NQ * s->count > (1ll << 31) - 1) return STREAMKL_INVALID_ARG;
+  return STREAMKL_OK;
+}
+
+int check_sel(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis, const streamkl_blocks* sel,
+              int B, int H, int NQ, int NK, bool data, bool* empty) {
+  int s = check_call(p1, p2, vis, B, H, NQ, NK, data, empty);
+  if (s != STREAMKL_OK) return s;
+  for (const streamkl_side* p : {p1, p2})
+    if (p->softcap != 0.f || p->slopes != nullptr || p->table != nullptr) return STREAMKL_UNSUPPORTED;
+  return check_blocks(sel, B, H, NQ, NK, data && !*empty);
+}
+
+// A [B][heads][n][d] view as rows of a 2-D map, boxes of 64 x 1 for gathers.
+// Every row starts at a multiple of the strides' common divisor.
+bool row_map(CUtensorMap* m, SelRows* r, const streamkl_view& v, int B, int heads, int n, int d) {
+  const long long sb = B > 1 ? v.stride_b : 0, sh = heads > 1 ? v.stride_h : 0, sn = n > 1 ? v.stride_n : 0;
+  long long g = std::gcd(std::gcd(sb, sh), sn);
+  if (g == 0) g = (d + 7) / 8 * 8;
+  const long long rows = ((B - 1) * sb + (heads - 1) * sh + (n - 1) * sn) / g + 1;
+  if (rows >= (1ll << 31) - 1 || g >= (1ll << 38)) return false;
+  *r = SelRows{int(sb / g), int(sh / g), int(sn / g), int(rows)};
+  if (m == nullptr) return true;
+  auto fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {cuuint64_t(d), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(g) * 2};
+  cuuint32_t box[2] = {64u, 1u};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(v.data), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Geometry {
+  SelPlan p{};
+  int u1 = 1, u2 = 1;
+};
+
+// Heads that share keys on both sides and a selection form a unit, whose rows
+// share tiles.  (A unit has at most 128 of them.)
+Geometry geometry(const streamkl_side& p1, const streamkl_side& p2, const streamkl_visible& vis, const streamkl_blocks& sel,
+                  int B, int H, int NQ, int NK) {
+  Geometry g;
+  SelPlan& p = g.p;
+  p.B = B;
+  p.H = H;
+  p.NQ = NQ;
+  p.NK = NK;
+  p.HS = sel.heads;
+  p.T = sel.count;
+  p.bs = sel.block;
+  p.blocks = (NK + sel.block - 1) / sel.block;
+  const int units = std::lcm(std::lcm(p1.HK, p2.HK), sel.heads), heads = H / units;
+  p.G = std::min(heads, kTile);
+  while (heads % p.G != 0) --p.G;
+  p.HU = H / p.G;
+  p.queries_per_tile = kTile / p.G;
+  g.u1 = p.HU / p1.HK;
+  g.u2 = p.HU / p2.HK;
+  p.causal = vis.causal;
+  p.prefix = vis.prefix;
+  p.doc_q = vis.doc_q;
+  p.selected = sel.selected;
+  p.words = (p.T + 31) / 32;
+  // chunks of a few steps of a warp at least, and at most 128
+  int span = 1;
+  while (span < p.T && span < 32) span *= 2;
+  p.chunk = std::max(4 * (32 / span), (NQ + 127) / 128);
+  p.chunks = (NQ + p.chunk - 1) / p.chunk;
+  return g;
+}
+
+void take_plan(Carver& c, SelPlan& p) {
+  const size_t heads = size_t(p.B) * p.HS, listed = size_t(p.NQ) * p.T;
+  p.counts = c.take<unsigned>(heads * p.chunks * p.blocks);
+  p.entries = c.take<unsigned>(heads * listed);
+  p.slots = c.take<unsigned>(heads * p.NQ * p.words);
+  const size_t per_item = size_t(p.queries_per_tile) * p.tiles_per_item;
+  p.max_items = int(heads * (listed / per_item + std::min(listed, size_t(p.blocks))));
+  p.items = c.take<SelItem>(p.max_items);
+  p.item_count = c.take<int>(1);
+}
+
+// Tiles of an item: K is read once for all of them, but the last items of a
+// CTA should be a small part of what it does.
+int item_tiles(const SelPlan& p, int sms, int most) {
+  const double tiles = double(p.B) * p.HU * p.NQ * p.T / p.queries_per_tile;
+  return int(std::max(1.0, std::min(double(most), tiles / (16.0 * std::max(sms, 1)))));
+}
+
+struct FwdPlan {
+  ModPrepArgs prep{};
+  Geometry g;
+  float4* rec = nullptr;
+  float* acc = nullptr;
+  size_t bytes = 0;
+};
+
+FwdPlan fwd_plan(const streamkl_side& p1, const streamkl_side& p2, const streamkl_visible& vis, const streamkl_blocks& sel,
+                 int B, int H, int NQ, int NK, int sms, void* ws) {
+  FwdPlan f;
+  Carver c{static_cast<uint8_t*>(ws)};
+  const streamkl_side* const p[2] = {&p1, &p2};
+  take_prep(c, f.prep, p, vis, B, H, NQ, NK, -1);
+  f.g = geometry(p1, p2, vis, sel, B, H, NQ, NK);
+  f.g.p.tiles_per_item = item_tiles(f.g.p, sms, 16);
+  take_plan(c, f.g.p);
+  const size_t pairs = size_t(B) * H * NQ * sel.count;
+  f.rec = c.take<float4>(pairs);
+  f.acc = c.take<float>(pairs);
+  f.bytes = c.used;
+  return f;
+}
+
+bool key_maps(SelMaps* m, const streamkl_side& p1, const streamkl_side& p2, int B, int NK, int bs) {
+  return map_bf16(&m->k1, p1.k, B, p1.HK, NK, p1.d, bs) && map_bf16(&m->k2, p2.k, B, p2.HK, NK, p2.d, bs);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t streamkl_fwd_sel_workspace_bytes(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,
+                                        const streamkl_blocks* sel, int B, int H, int NQ, int NK) {
+  bool empty = false;
+  if (check_sel(p1, p2, vis, sel, B, H, NQ, NK, false, &empty) != STREAMKL_OK || empty) return 0;
+  return fwd_plan(*p1, *p2, *vis, *sel, B, H, NQ, NK, num_sms(), nullptr).bytes;
+}
+
+int streamkl_fwd_sel(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,
+                     const streamkl_blocks* sel, int B, int H, int NQ, int NK, void* workspace, size_t workspace_bytes,
+                     float* kl, float* lse1, float* lse2, streamkl_stream_t stream) {
+  bool empty = false;
+  int s = check_sel(p1, p2, vis, sel, B, H, NQ, NK, true, &empty);
+  if (s != STREAMKL_OK || empty) return s;
+  if (!kl || !lse1 || !lse2 || !aligned16(kl) || !aligned16(lse1) || !aligned16(lse2)) return STREAMKL_INVALID_ARG;
+  SelRows r1, r2;
+  if (!row_map(nullptr, &r1, p1->q, B, H, NQ, p1->d) || !row_map(nullptr, &r2, p2->q, B, H, NQ, p2->d))
+    return STREAMKL_INVALID_ARG;
+  const int sms = num_sms();
+  const FwdPlan f = fwd_plan(*p1, *p2, *vis, *sel, B, H, NQ, NK, sms, workspace);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < f.bytes) return STREAMKL_INVALID_ARG;
+  if ((s = check_device()) != STREAMKL_OK) return s;
+  SelMaps m{};
+  SelFwdArgs a{};
+  if (!row_map(&m.q1, &a.r1, p1->q, B, H, NQ, p1->d) || !row_map(&m.q2, &a.r2, p2->q, B, H, NQ, p2->d) ||
+      !key_maps(&m, *p1, *p2, B, NK, sel->block))
+    return STREAMKL_CUDA_ERROR;
+  a.status = status_word();
+  if (!a.status) return STREAMKL_CUDA_ERROR;
+  a.p = f.g.p;
+  a.u1 = f.g.u1;
+  a.u2 = f.g.u2;
+  a.scale1 = float(p1->scale);
+  a.scale2 = float(p2->scale);
+  a.vis = vis_args(*vis, f.prep);
+  a.rec = f.rec;
+  a.acc = f.acc;
+  a.kl = kl;
+  a.lse1 = lse1;
+  a.lse2 = lse2;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_mod_prep(f.prep, cs) != 0 || launch_sel_plan(a.p, cs) != 0) return STREAMKL_CUDA_ERROR;
+  if (launch_sel_fwd(m, tile_width(p1->d), tile_width(p2->d), a, sms, cs) != 0) return STREAMKL_CUDA_ERROR;
+  return as_status(launch_sel_merge(a, cs));
+}
+
+}  // extern "C"

@@ -1,0 +1,114 @@
+// Attention over selected blocks of keys: what the plan, the forward and the
+// backward share.
+//
+// Every query has up to T blocks of its own, so a tile of consecutive queries
+// shares no keys.  The work is turned round: for each block of keys, the
+// queries that selected it, 128 rows (queries x the heads that share keys) at
+// a time, their rows gathered by TMA.  K is then read once for a list of rows
+// and every product is a full 128-row tile.  The attention KL's share of a
+// (row, block) is five numbers, so what is written between the passes stays
+// small; an output of d values a row would not allow this.
+//
+// The plan (sel_plan.cu) makes these lists, in query order, and cuts them into
+// items of at most tiles_per_item tiles.  Nothing in it depends on the order
+// in which blocks of a launch run but the items' places in their table.
+#pragma once
+
+#include "kernels.cuh"
+#include "mod_common.cuh"
+#include "ptx.cuh"
+
+namespace skl {
+
+constexpr int kMaxSlots = 128;    // blocks of one query
+constexpr int kMaxSelBlocks = 4096;
+constexpr int kSlotBits = 7;
+
+// A piece of one block's list: `count` queries from entries[first].
+struct SelItem {
+  int sel;    // b * HS + selection head
+  int block;
+  int first;  // of all entries
+  int count;
+};
+
+struct SelPlan {
+  int B, H, NQ, NK, HS, T;
+  int bs, blocks;        // keys of a block, blocks of a batch entry
+  int G;                 // query heads of a tile, which share keys and selection
+  int HU;                // units of G heads in a batch entry; HU / HS use the same lists
+  int queries_per_tile;  // 128 / G
+  int tiles_per_item;
+  int causal;
+  const int* prefix;     // [B] or null
+  const int* doc_q;      // [B][NQ] or null
+  const int* selected;   // [B][HS][NQ][T]
+  int chunk, chunks;     // queries whose entries one warp counts, and their number
+  unsigned* counts;      // [B HS][chunks][blocks]: entries of a chunk; then where they start
+  unsigned* entries;     // [B HS][NQ T]: query << kSlotBits | slot
+  unsigned* slots;       // [B HS][NQ][words]: the slots that count
+  int words;             // (T + 31) / 32
+  SelItem* items;
+  int* item_count;       // device
+  int max_items;
+};
+
+// Where an item's tile lies, for every role alike.
+struct SelWork {
+  int b, head0, block, first, count, unit;
+};
+__device__ __forceinline__ SelWork sel_work(const SelPlan& p, int w) {
+  const int per = p.HU / p.HS;
+  const int it = w / per, sub = w - it * per;
+  const int4 v = __ldg(reinterpret_cast<const int4*>(p.items) + it);
+  SelWork k;
+  const int unit = v.x * per + sub;  // b * HU + unit of the batch entry
+  k.b = unit / p.HU;
+  k.head0 = (unit - k.b * p.HU) * p.G;
+  k.block = v.y;
+  k.first = v.z;
+  k.count = v.w;
+  k.unit = unit;
+  return k;
+}
+
+// A [B][heads][N][d] view as rows of a 2-D tensor map: row = b rb + h rh + n rn.
+struct SelRows {
+  int rb, rh, rn;
+  int none;  // a row past the last: reads as zeros
+};
+
+// Four rows of 64 elements, at columns x, into shared memory.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int4 r) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+      : "memory");
+}
+
+struct SelMaps {
+  CUtensorMap q1, q2;  // rows (SelRows), boxes of 64 x 1, 128-byte swizzle
+  CUtensorMap k1, k2;  // 4-D (d, N, heads, B), boxes of 64 x block
+};
+
+struct SelFwdArgs {
+  SelPlan p;
+  SelRows r1, r2;
+  int u1, u2;             // units per key head of each side
+  float scale1, scale2;
+  ModVis vis;
+  float4* rec;            // [B H NQ][T]: m1, m2, l1, l2 of a row's keys in one block
+  float* acc;             // [B H NQ][T]
+  float* kl;
+  float* lse1;
+  float* lse2;
+  int* status;
+  int q_stages, k_bufs;
+};
+
+int launch_sel_plan(const SelPlan& p, cudaStream_t st);
+int launch_sel_fwd(const SelMaps& m, int d1, int d2, const SelFwdArgs& a, int sms, cudaStream_t st);
+int launch_sel_merge(const SelFwdArgs& a, cudaStream_t st);
+
+}  // namespace skl

@@ -1,0 +1,353 @@
+// Forward over selected blocks (sel_common.cuh): the sums of every (row, block)
+// pair, then their merge into KL, LSE1 and LSE2.
+//
+// Persistent CTAs walk the items: K1, K2 of the item's block once, then tiles
+// of 128 gathered rows through a ring of stages.  18 warps:
+//   warp 16     gathers Q1, Q2 rows by TMA, four a lane, and loads K
+//   warp 17     S1 = Q1 K1^T, S2 = Q2 K2^T into one of 4 TMEM buffers (2 for blocks of 128)
+//   warps 0-15  statistics: warpgroup g takes every buffer g; thread = row
+// A row's keys in one block are few, so its references are its own largest
+// scores there (one more read of TMEM), and nothing is rescaled:
+//   e_t = S_t log2 e - m_t,  l_t = sum 2^e_t,  acc = sum 2^e1 (e1 - e2).
+// The merge adds the parts of a row's slots in their order (as merge_stats of
+// the dense forward does for splits), so results do not depend on which CTA
+// took which item.
+#include "fwd_mod.cuh"
+#include "sel_common.cuh"
+
+namespace skl {
+
+namespace {
+
+struct SelFwdLayout {
+  static constexpr int kWGs = 4;
+  static constexpr int kStatWarps = 4 * kWGs;
+  static constexpr int kProdWarp = kStatWarps, kMmaWarp = kStatWarps + 1;
+  static constexpr int kThreads = 32 * (kStatWarps + 2);
+  static constexpr int kMaxStages = 4, kMaxKBufs = 2;
+  // k_full[2], k_empty[2], q_full[4], q_empty[4], s_full[4], s_empty[4], done
+  static constexpr int kNumBars = 2 * kMaxKBufs + 2 * kMaxStages + 8 + 1;
+  static constexpr uint32_t kTail = kNumBars * 8 + 16;
+  static constexpr uint32_t kMost = 232448;
+  static uint32_t bytes(int q_stages, int k_bufs, int d1, int d2, int bs) {
+    return 1024u + uint32_t(d1 + d2) * 2u * uint32_t(q_stages * kTile + k_bufs * bs) + kTail;
+  }
+};
+
+// Products of a K-major operand of `rows` rows, step kk of 16 along d.
+__device__ __forceinline__ uint32_t step_off(int kk, int rows) { return (kk >> 2) * (rows * 128) + (kk & 3) * 32; }
+
+// One row's sums over its block: n visible of the bs columns at ts, ts + bs.
+template <bool MASK>
+__device__ __forceinline__ void block_sums(uint32_t ts, int bs, float c1, float c2, int i, int k0, const SelFwdArgs& a,
+                                           int prefix, int id, const int* kids, ModStats& st) {
+  const int off = a.p.NK - a.p.NQ;
+  float t1 = -INFINITY, t2 = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < bs; c += 16) {
+    uint32_t x1[16], x2[16];
+    tmem_ld2x16(ts + c, ts + bs + c, x1, x2);
+    uint32_t on = 0xffffffffu;
+    if (MASK) on = visible_bits<16>(i, k0 + c, off, a.p.NK, a.p.causal, prefix, id, kids == nullptr ? nullptr : kids + c);
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      float u = __uint_as_float(x1[k]), v = __uint_as_float(x1[k + 1]);
+      float w = __uint_as_float(x2[k]), z = __uint_as_float(x2[k + 1]);
+      if (MASK) {
+        if (!((on >> k) & 1u)) u = w = -INFINITY;
+        if (!((on >> (k + 1)) & 1u)) v = z = -INFINITY;
+      }
+      t1 = max3(t1, u, v);
+      t2 = max3(t2, w, z);
+    }
+  }
+  const float m1 = rintf(t1 * c1), m2 = rintf(t2 * c2);
+  const uint64_t C1 = f2(c1, c1), C2 = f2(c2, c2), M1 = f2(-m1, -m1), M2 = f2(-m2, -m2);
+  ChunkSums s{};
+#pragma unroll 1
+  for (int c = 0; c < bs; c += 16) {
+    uint32_t x1[16], x2[16];
+    uint64_t e1[8], e2[8];
+    tmem_ld2x16(ts + c, ts + bs + c, x1, x2);
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      e1[k / 2] = f2_fma(f2(__uint_as_float(x1[k]), __uint_as_float(x1[k + 1])), C1, M1);
+      e2[k / 2] = f2_fma(f2(__uint_as_float(x2[k]), __uint_as_float(x2[k + 1])), C2, M2);
+    }
+    if (MASK)
+      mask_scores(e1, e2, visible_bits<16>(i, k0 + c, off, a.p.NK, a.p.causal, prefix, id, kids == nullptr ? nullptr : kids + c));
+    sums_all(e1, e2, s);
+  }
+  st = ModStats{m1, m2, sum2(s.l1a, s.l1b), sum2(s.l2a, s.l2b), sum2(s.aa, s.ab)};
+}
+
+template <int D1, int D2>
+__global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
+    sel_fwd_kernel(const __grid_constant__ CUtensorMap tq1, const __grid_constant__ CUtensorMap tk1,
+                   const __grid_constant__ CUtensorMap tq2, const __grid_constant__ CUtensorMap tk2,
+                   const __grid_constant__ SelFwdArgs a) {
+  using L = SelFwdLayout;
+  constexpr uint32_t kQ1 = kTile * D1 * 2, kQ = kTile * (D1 + D2) * 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bs = a.p.bs;
+  const uint32_t kK1 = uint32_t(bs) * D1 * 2, kK = uint32_t(bs) * (D1 + D2) * 2;
+  const uint32_t oQ = a.k_bufs * kK, oBar = oQ + a.q_stages * kQ;
+  auto bar_kfull = [&](int i) { return sb + oBar + 8u * i; };
+  auto bar_kempty = [&](int i) { return sb + oBar + 8u * (L::kMaxKBufs + i); };
+  auto bar_qfull = [&](int i) { return sb + oBar + 8u * (2 * L::kMaxKBufs + i); };
+  auto bar_qempty = [&](int i) { return sb + oBar + 8u * (2 * L::kMaxKBufs + L::kMaxStages + i); };
+  auto bar_sfull = [&](int i) { return sb + oBar + 8u * (2 * L::kMaxKBufs + 2 * L::kMaxStages + i); };
+  auto bar_sempty = [&](int i) { return sb + oBar + 8u * (2 * L::kMaxKBufs + 2 * L::kMaxStages + 4 + i); };
+  const uint32_t bar_done = sb + oBar + 8u * (L::kNumBars - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + oBar + L::kNumBars * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + oBar + L::kNumBars * 8 + 4);
+  const Ctl ctl{abort_flag, a.status};
+  const int bufs = bs == 128 ? 2 : 4;  // of S1, S2 in TMEM, bs columns each
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      const int s_empty = 2 * L::kMaxKBufs + 2 * L::kMaxStages + 4;
+      mbar_init(sb + oBar + 8u * i, i >= s_empty && i < s_empty + 4 ? 4 : 1);  // a warpgroup frees a buffer
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == L::kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int per_tile = a.p.queries_per_tile, G = a.p.G;
+  const int works = min(*a.p.item_count, a.p.max_items) * (a.p.HU / a.p.HS);
+
+  if (warp == L::kProdWarp) {
+    // ---------------------------------------------------------------- TMA producer (32 lanes, 4 rows each)
+    int n = 0, items = 0;
+    bool ok = true;
+    int ql[4], hl[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      ql[x] = (4 * lane + x) / G;
+      hl[x] = (4 * lane + x) - ql[x] * G;
+    }
+    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
+      const SelWork k = sel_work(a.p, w);
+      const int kb = items % a.k_bufs;
+      ok = mbar_wait_warp(bar_kempty(kb), ((items / a.k_bufs) & 1) ^ 1, ctl);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar_kfull(kb), kK);
+        const int hu = k.head0 / G;
+#pragma unroll
+        for (int c = 0; c < D1 / 64; ++c)
+          tma_load_4d(sb + kb * kK + c * (bs * 128), &tk1, bar_kfull(kb), c * 64, k.block * bs, hu / a.u1, k.b);
+#pragma unroll
+        for (int c = 0; c < D2 / 64; ++c)
+          tma_load_4d(sb + kb * kK + kK1 + c * (bs * 128), &tk2, bar_kfull(kb), c * 64, k.block * bs, hu / a.u2, k.b);
+      }
+      for (int e0 = 0; e0 < k.count; e0 += per_tile, ++n) {
+        int4 r1, r2;
+        int* p1 = &r1.x;
+        int* p2 = &r2.x;
+        bool any = false;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int e = e0 + ql[x];
+          const bool on = ql[x] < per_tile && e < k.count;
+          any |= on;
+          const int i = on ? int(__ldg(a.p.entries + k.first + e) >> kSlotBits) : 0, h = k.head0 + hl[x];
+          p1[x] = on ? k.b * a.r1.rb + h * a.r1.rh + i * a.r1.rn : a.r1.none;
+          p2[x] = on ? k.b * a.r2.rb + h * a.r2.rh + i * a.r2.rn : a.r2.none;
+        }
+        const int s = n % a.q_stages;
+        ok = mbar_wait_warp(bar_qempty(s), ((n / a.q_stages) & 1) ^ 1, ctl);
+        if (!ok) break;
+        // (four rows past the last are not read: what the stage holds there gives scores that nobody takes)
+        const int lanes = __popc(__ballot_sync(0xffffffffu, any));
+        if (lane == 0) mbar_arrive_expect_tx(bar_qfull(s), lanes * 4u * (D1 + D2) * 2u);
+        __syncwarp();
+        if (any) {
+          const uint32_t dst = sb + oQ + s * kQ + lane * 512;
+#pragma unroll
+          for (int c = 0; c < D1 / 64; ++c) tma_gather4(dst + c * (kTile * 128), &tq1, bar_qfull(s), c * 64, r1);
+#pragma unroll
+          for (int c = 0; c < D2 / 64; ++c) tma_gather4(dst + kQ1 + c * (kTile * 128), &tq2, bar_qfull(s), c * 64, r2);
+        }
+      }
+    }
+    if (*abort_flag && lane == 0) {  // let the copies already started land before the CTA exits
+      const uint64_t lim = 200000000ull;
+      for (int j = items > a.k_bufs ? items - a.k_bufs : 0; j < items; ++j)
+        mbar_drain(bar_kfull(j % a.k_bufs), (j / a.k_bufs) & 1, lim);
+      for (int j = n > a.q_stages ? n - a.q_stages : 0; j < n; ++j)
+        mbar_drain(bar_qfull(j % a.q_stages), (j / a.q_stages) & 1, lim);
+    }
+  } else if (warp == L::kMmaWarp) {
+    // ---------------------------------------------------------------- MMA issuer
+    const uint32_t leader = elect_one();
+    const uint32_t idesc = idesc_bf16(128, bs, 0, 0);
+    int n = 0, items = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
+      const int count = sel_work(a.p, w).count;
+      const int kb = items % a.k_bufs;
+      ok = mbar_wait_warp(bar_kfull(kb), (items / a.k_bufs) & 1, ctl);
+      const uint64_t k1d = sdesc_sw128(sb + kb * kK, 16, 1024), k2d = sdesc_sw128(sb + kb * kK + kK1, 16, 1024);
+      for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
+        const int s = n % a.q_stages, i = n % bufs;
+        ok = mbar_wait_warp(bar_qfull(s), (n / a.q_stages) & 1, ctl) &&
+             mbar_wait_warp(bar_sempty(i), ((n / bufs) & 1) ^ 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d1 = tmem + uint32_t(i * 2 * bs), d2 = d1 + uint32_t(bs);
+        const uint64_t q1d = sdesc_sw128(sb + oQ + s * kQ, 16, 1024), q2d = sdesc_sw128(sb + oQ + s * kQ + kQ1, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D1 / 16; ++kk)
+          mma_bf16_ss(leader, d1, sdesc_add(q1d, step_off(kk, kTile)), sdesc_add(k1d, step_off(kk, bs)), idesc, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < D2 / 16; ++kk)
+          mma_bf16_ss(leader, d2, sdesc_add(q2d, step_off(kk, kTile)), sdesc_add(k2d, step_off(kk, bs)), idesc, kk > 0);
+        mma_commit(leader, bar_qempty(s));
+        mma_commit(leader, bar_sfull(i));
+      }
+      if (ok) mma_commit(leader, bar_kempty(kb));
+    }
+    mma_commit(leader, bar_done);  // every MMA has finished before TMEM is released
+    mbar_drain(bar_done, 0, 1000000000ull);
+  } else if ((warp >> 2) < bufs) {
+    // ---------------------------------------------------------------- statistics
+    const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int ql = row / G, hl = row - ql * G;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const float c1 = a.scale1 * kLog2e, c2 = a.scale2 * kLog2e;
+    const int nqt = (a.p.NQ + kTile - 1) / kTile, nkt = (a.p.NK + kTile - 1) / kTile;
+    const int off = a.p.NK - a.p.NQ;
+    int n = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < works; w += gridDim.x) {
+      const SelWork k = sel_work(a.p, w);
+      const int k0 = k.block * bs;
+      const int prefix = a.p.prefix != nullptr ? min(max(a.p.prefix[k.b], 0), a.p.NK) : 0;
+      for (int e0 = 0; ok && e0 < k.count; e0 += per_tile, ++n) {
+        if (n % bufs != wg) continue;
+        const int e = e0 + ql;
+        const bool on = ql < per_tile && e < k.count;
+        const unsigned ent = on ? __ldg(a.p.entries + k.first + e) : 0u;
+        const int i = int(ent >> kSlotBits), t = int(ent & ((1u << kSlotBits) - 1u));
+        int id = 0;
+        const int* kids = nullptr;
+        if (a.vis.ids_q != nullptr) {
+          id = a.vis.ids_q[size_t(k.b) * nqt * kTile + i];
+          kids = a.vis.ids_k + size_t(k.b) * nkt * kTile + k0;
+        }
+        const int last = a.p.causal ? min(max(i + off + 1, prefix), a.p.NK) : a.p.NK;
+        const bool whole = __all_sync(0xffffffffu, !on || last >= k0 + bs) && kids == nullptr;
+        const bool idle = __all_sync(0xffffffffu, !on);
+        ok = mbar_wait_warp(bar_sfull(wg), (n / bufs) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
+        if (!idle) {
+          const uint32_t ts = tmem + lane_off + uint32_t(wg * 2 * bs);
+          if (whole) block_sums<false>(ts, bs, c1, c2, i, k0, a, prefix, id, kids, st);
+          else block_sums<true>(ts, bs, c1, c2, i, k0, a, prefix, id, kids, st);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sempty(wg));
+        const size_t at = (size_t(k.b * a.p.H + k.head0 + hl) * a.p.NQ + i) * a.p.T + t;
+        if (on && SKL_CHECK(a.status, i < a.p.NQ && t < a.p.T && k.head0 + hl < a.p.H && k.b < a.p.B)) {
+          // a row that ids hide the whole block from has sums of 2^(-3e38 - ...) = 0, relative to nothing
+          const bool none = st.m1 == -INFINITY && st.l1 == 0.f;
+          a.rec[at] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(st.m1, st.m2, st.l1, st.l2);
+          a.acc[at] = none ? 0.f : st.acc;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == L::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr int kMergeThreads = 256, kMergeLanes = 4;
+
+// Four lanes a row, each with every fourth slot, joined pairwise.
+__global__ void __launch_bounds__(kMergeThreads) sel_merge_kernel(const __grid_constant__ SelFwdArgs a) {
+  const long long rows = (long long)a.p.B * a.p.H * a.p.NQ;
+  const long long r = ((long long)blockIdx.x * kMergeThreads + threadIdx.x) / kMergeLanes;
+  const int part = threadIdx.x % kMergeLanes;
+  const long long row = r < rows ? r : rows - 1;  // (whole warps take part)
+  const int bh = int(row / a.p.NQ), i = int(row - (long long)bh * a.p.NQ), b = bh / a.p.H, h = bh - b * a.p.H;
+  const int sel = b * a.p.HS + h / (a.p.H / a.p.HS);
+  const unsigned* slots = a.p.slots + (size_t(sel) * a.p.NQ + i) * a.p.words;
+  ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int t = part; t < a.p.T; t += kMergeLanes) {
+    if (!((slots[t >> 5] >> (t & 31)) & 1u)) continue;
+    const float4 v = __ldcs(a.rec + row * a.p.T + t);
+    const ModStats o{v.x, v.y, v.z, v.w, __ldcs(a.acc + row * a.p.T + t)};
+    if (o.l1 == 0.f) continue;
+    if (st.l1 == 0.f) st = o;
+    else merge_stats(st, o);
+  }
+#pragma unroll
+  for (int d = 1; d < kMergeLanes; d *= 2) {
+    ModStats o;
+    o.m1 = __shfl_xor_sync(0xffffffffu, st.m1, d);
+    o.m2 = __shfl_xor_sync(0xffffffffu, st.m2, d);
+    o.l1 = __shfl_xor_sync(0xffffffffu, st.l1, d);
+    o.l2 = __shfl_xor_sync(0xffffffffu, st.l2, d);
+    o.acc = __shfl_xor_sync(0xffffffffu, st.acc, d);
+    if (part & d) {  // the same sums in both lanes of a pair
+      const ModStats x = st;
+      st = o;
+      o = x;
+    }
+    if (o.l1 == 0.f) continue;
+    if (st.l1 == 0.f) st = o;
+    else merge_stats(st, o);
+  }
+  if (part == 0 && r < rows) write_row(st, -INFINITY, -INFINITY, a.kl + row, a.lse1 + row, a.lse2 + row);
+}
+
+template <int D1, int D2>
+int launch_sel_fwd_t(const SelMaps& m, const SelFwdArgs& args, int sms, cudaStream_t st) {
+  using L = SelFwdLayout;
+  SelFwdArgs a = args;
+  // two buffers of K (the next item's loads) where they leave two stages of Q, then as many stages as fit
+  a.k_bufs = L::bytes(2, 2, D1, D2, a.p.bs) <= L::kMost ? 2 : 1;
+  a.q_stages = 2;
+  while (a.q_stages < L::kMaxStages && L::bytes(a.q_stages + 1, a.k_bufs, D1, D2, a.p.bs) <= L::kMost) ++a.q_stages;
+  auto kern = sel_fwd_kernel<D1, D2>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kMost);
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)a.p.max_items * (a.p.HU / a.p.HS);
+  const int grid = int(most < sms ? most : sms);
+  kern<<<grid, L::kThreads, L::bytes(a.q_stages, a.k_bufs, D1, D2, a.p.bs), st>>>(m.q1, m.k1, m.q2, m.k2, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int launch_sel_fwd(const SelMaps& m, int d1, int d2, const SelFwdArgs& a, int sms, cudaStream_t st) {
+  if (d1 == 64) return d2 == 64 ? launch_sel_fwd_t<64, 64>(m, a, sms, st) : launch_sel_fwd_t<64, 128>(m, a, sms, st);
+  return d2 == 64 ? launch_sel_fwd_t<128, 64>(m, a, sms, st) : launch_sel_fwd_t<128, 128>(m, a, sms, st);
+}
+
+int launch_sel_merge(const SelFwdArgs& a, cudaStream_t st) {
+  const long long threads = (long long)a.p.B * a.p.H * a.p.NQ * kMergeLanes;
+  sel_merge_kernel<<<unsigned((threads + kMergeThreads - 1) / kMergeThreads), kMergeThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace skl

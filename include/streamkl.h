@@ -405,6 +405,33 @@ int streamkl_rotate(const streamkl_view* x, const streamkl_view* y, const stream
 int streamkl_pool_blocks(const streamkl_view* k, const int* doc_k, int B, int HK, int NK, int d, int block,
                          const streamkl_view* kb, streamkl_stream_t stream);
 
+/*
+ * The blocks that each query attends to: selected[b][hs][i][0 .. count), in any
+ * order; the query heads h with h / (H / heads) = hs share them.  An entry
+ * outside 0 .. blocks - 1 selects nothing (-1 pads a short list), and a block
+ * named twice counts once.
+ */
+typedef struct streamkl_blocks {
+  const int* selected; /* device [B][heads][NQ][count] */
+  int heads;           /* divides H */
+  int count;           /* 1 .. 128 */
+  int block;           /* keys of a block: 32, 64 or 128; at most 4096 blocks */
+} streamkl_blocks;
+
+/*
+ * Forward over selected blocks: kl, lse1, lse2 as streamkl_fwd_mod, over the
+ * keys that are visible (streamkl_visible) and in a selected block; a row that
+ * sees none gets KL 0 and LSE -inf.  Sides may not be modified (softcap,
+ * slopes and table: UNSUPPORTED).  Results are bitwise repeatable.  workspace:
+ * device memory as for streamkl_fwd_mod, of at least
+ * streamkl_fwd_sel_workspace_bytes bytes: about 20 for each row and slot.
+ */
+size_t streamkl_fwd_sel_workspace_bytes(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,
+                                        const streamkl_blocks* sel, int B, int H, int NQ, int NK);
+int streamkl_fwd_sel(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,
+                     const streamkl_blocks* sel, int B, int H, int NQ, int NK, void* workspace, size_t workspace_bytes,
+                     float* kl, float* lse1, float* lse2, streamkl_stream_t stream);
+
 /* Static, NUL-terminated description of a status value. */
 const char* streamkl_status_string(int status);
 

@@ -1,0 +1,80 @@
+"""The calls over selected blocks, without a GPU: refusals (every call here
+fails validation before any CUDA call), empty problems, structures."""
+
+import os
+import re
+
+import pytest
+
+import attention_distillation_kl_gb300 as skl
+from test_mod_cpu import A, L, seen, side, view  # noqa: F401
+
+
+def blocks(selected=A, heads=1, count=4, block=32):
+    return skl._Blocks(selected, heads, count, block)
+
+
+def fwd(L, s1=None, s2=None, vis=None, sel=None, B=1, H=2, NQ=128, NK=128, ws=A, ws_bytes=1 << 40, out=(A, A, A)):
+    return L.streamkl_fwd_sel(s1 or side(), s2 or side(), vis or seen(), sel or blocks(), B, H, NQ, NK, ws, ws_bytes,
+                              *out, None)
+
+
+BAD = [
+    (dict(sel=blocks(selected=0)), skl.STREAMKL_INVALID_ARG), (dict(sel=blocks(selected=A + 2)), skl.STREAMKL_INVALID_ARG),
+    (dict(sel=blocks(heads=0)), skl.STREAMKL_INVALID_ARG), (dict(sel=blocks(heads=3)), skl.STREAMKL_INVALID_ARG),
+    (dict(sel=blocks(heads=4)), skl.STREAMKL_INVALID_ARG), (dict(sel=blocks(count=0)), skl.STREAMKL_INVALID_ARG),
+    (dict(sel=blocks(count=129)), skl.STREAMKL_INVALID_ARG), (dict(sel=blocks(block=16)), skl.STREAMKL_INVALID_ARG),
+    (dict(sel=blocks(block=96)), skl.STREAMKL_INVALID_ARG), (dict(sel=blocks(block=256)), skl.STREAMKL_INVALID_ARG),
+    (dict(NK=32 * 4096 + 1), skl.STREAMKL_UNSUPPORTED),
+    (dict(s1=side(softcap=30.0)), skl.STREAMKL_UNSUPPORTED), (dict(s2=side(slopes=A)), skl.STREAMKL_UNSUPPORTED),
+    (dict(s2=side(table=A, num_buckets=32, max_distance=128)), skl.STREAMKL_UNSUPPORTED),
+    (dict(s1=side(scale=0.0)), skl.STREAMKL_INVALID_ARG), (dict(s1=side(d=72)), skl.STREAMKL_UNSUPPORTED),
+    (dict(s1=side(q=view(A + 8))), skl.STREAMKL_INVALID_ARG), (dict(s2=side(k=view(0))), skl.STREAMKL_INVALID_ARG),
+    (dict(vis=seen(causal=2)), skl.STREAMKL_INVALID_ARG), (dict(vis=seen(prefix=A)), skl.STREAMKL_INVALID_ARG),
+    (dict(vis=seen(doc_q=A)), skl.STREAMKL_INVALID_ARG),
+    (dict(ws=0), skl.STREAMKL_INVALID_ARG), (dict(ws=A + 8), skl.STREAMKL_INVALID_ARG), (dict(ws_bytes=16), skl.STREAMKL_INVALID_ARG),
+    (dict(B=-1), skl.STREAMKL_INVALID_ARG), (dict(NK=0), skl.STREAMKL_INVALID_ARG), (dict(B=70000), skl.STREAMKL_INVALID_ARG),
+    (dict(NQ=1 << 25, H=1, s1=side(HK=1), s2=side(HK=1)), skl.STREAMKL_INVALID_ARG),
+    # rows of 8 elements apart, over more memory than 2^31 of them
+    (dict(s1=side(q=skl._View(A, 0, 1 << 36, 8))), skl.STREAMKL_INVALID_ARG),
+]
+
+
+@pytest.mark.parametrize("kw,status", BAD)
+def test_bad_calls_are_refused(L, kw, status):  # noqa: F811
+    assert fwd(L, **kw) == status
+
+
+def test_forward_outputs_are_checked(L):  # noqa: F811
+    for out in ((0, A, A), (A, A + 4, A), (A, A, 0)):
+        assert fwd(L, out=out) == skl.STREAMKL_INVALID_ARG
+
+
+def test_empty_problems_do_nothing(L):  # noqa: F811
+    none = side(q=view(0), k=view(0))
+    for kw in (dict(NQ=0), dict(B=0)):
+        assert fwd(L, none, none, sel=blocks(selected=0), ws=0, out=(0, 0, 0), **kw) == skl.STREAMKL_OK
+
+
+def test_workspace_bytes(L):  # noqa: F811
+    f = L.streamkl_fwd_sel_workspace_bytes
+    small = f(side(), side(), seen(), blocks(), 1, 2, 128, 128)
+    assert small >= 20 * 2 * 128 * 4
+    assert f(side(), side(), seen(), blocks(count=0), 1, 2, 128, 128) == 0
+    assert f(side(), side(), seen(), blocks(), 1, 2, 0, 128) == 0
+    assert f(side(), side(), seen(0, None, A, A), blocks(), 1, 2, 128, 128) == small + 2 * 128 * 4 + 2 * 16
+
+
+def test_structures_match_the_header():
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                             "streamkl.h")).read()
+    for name, struct in (("blocks", skl._Blocks), ("rotary", skl._Rotary)):
+        body = re.search(r"typedef struct streamkl_%s \{(.*?)\} streamkl_%s;" % (name, name), text, re.S).group(1)
+        body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+        fields = []
+        for decl in body.split(";"):
+            for part in decl.split(","):
+                m = re.search(r"(\w+)\s*(?:\[\d+\])?\s*$", part.strip())
+                if m:
+                    fields.append(m.group(1))
+        assert fields == [f for f, _ in struct._fields_], name

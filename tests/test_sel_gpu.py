@@ -1,0 +1,226 @@
+"""The attention KL over selected blocks on the GPU against the float64
+definitions, element by element within the bounds of mod_reference.py: head
+layouts, lengths from one token on, lists with empty, repeated and foreign
+entries, masks that leave rows empty, strides, streams, graphs."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attention_distillation_kl_gb300 as skl
+import sel_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def f64(t):
+    return None if t is None else t.detach().float().cpu().double().numpy()
+
+
+def problem(seed=0, B=1, H=2, HK1=None, HK2=None, HS=1, NQ=150, NK=150, d1=64, d2=64, bs=32, T=3, sd=1.5, causal=True,
+            prefix=None, docs=None, bshd=False, lists="mixed"):
+    """(sides' tensors, blocks, where, float64 problem).  lists: "mixed" (random
+    blocks, some empty, repeated, unseen or not there), "all" (every block),
+    "none"."""
+    g = torch.Generator().manual_seed(seed)
+    HK1, HK2 = HK1 or H, HK2 or H
+
+    def x(h, n, d):
+        t = (sd * torch.randn((B, h, n, d), generator=g)).to(torch.bfloat16)
+        return t.transpose(1, 2).contiguous().cuda().transpose(1, 2) if bshd else t.cuda()
+
+    dev = dict(q1=x(H, NQ, d1), k1=x(HK1, NK, d1), q2=x(H, NQ, d2), k2=x(HK2, NK, d2))
+    nb = -(-NK // bs)
+    if lists == "all":
+        idx = torch.arange(nb, dtype=torch.int32).expand(B, HS, NQ, nb).contiguous()
+    elif lists == "none":
+        idx = torch.full((B, HS, NQ, T), -1, dtype=torch.int32)
+    else:
+        idx = torch.randint(-1, nb + 1, (B, HS, NQ, T), generator=g, dtype=torch.int32)
+        if T > 1:
+            idx[..., 1] = torch.where(torch.rand(idx[..., 1].shape, generator=g) < 0.2, idx[..., 0], idx[..., 1])
+        idx[:, :, ::17] = -1
+        idx[:, :, 5::23, -1] = 2 ** 31 - 1
+        idx[:, :, 6::23, 0] = -2 ** 31
+    ids = None
+    if docs is not None:
+        if docs == "packed":
+            q = torch.sort(torch.randint(0, 4, (B, NQ), generator=g), dim=1)[0]
+            k = q if NQ == NK else torch.sort(torch.randint(0, 4, (B, NK), generator=g), dim=1)[0]
+            q, k = q.clone(), k.clone()
+            q[:, NQ - NQ // 9:] = -1
+            k[:, NK - NK // 9:] = -1
+        else:
+            q = torch.randint(-2, 6, (B, NQ), generator=g)
+            k = torch.randint(-2, 6, (B, NK), generator=g)
+        ids = q.int(), k.int()
+    p = {k: f64(v) for k, v in dev.items()}
+    for t, d in (("1", d1), ("2", d2)):
+        p.update({"scale" + t: 1 / math.sqrt(d), "cap" + t: 0.0, "slopes" + t: None, "table" + t: None})
+    p.update(blocks=idx.numpy(), bs=bs, causal=causal, prefix=None if prefix is None else np.array(prefix),
+             doc_q=None if ids is None else ids[0].numpy(), doc_k=None if ids is None else ids[1].numpy())
+    where = dict(causal=causal, prefix=None if prefix is None else torch.tensor(prefix, dtype=torch.int32).cuda(),
+                 doc_q=None if ids is None else ids[0].cuda(), doc_k=None if ids is None else ids[1].cuda())
+    return dev, idx.cuda(), where, p
+
+
+def sides(dev):
+    return tuple(skl.AttnSide(dev["q" + t], dev["k" + t], 1 / math.sqrt(dev["q" + t].shape[3])) for t in "12")
+
+
+def within(got, want, bound, what):
+    got = f64(got) if isinstance(got, torch.Tensor) else got
+    assert got.shape == want.shape, what
+    same = np.isinf(want) & (got == want)
+    err = np.abs(np.where(same, 0.0, got) - np.where(same, 0.0, want))
+    assert np.all(np.isfinite(err)), f"{what}: not finite where the definition is"
+    over = err - bound - 1e-30
+    at = np.unravel_index(np.argmax(over), over.shape)
+    assert over[at] <= 0, f"{what} at {at}: {got[at]} for {want[at]}, error {err[at]:.3g}, bound {bound[at]:.3g}"
+
+
+def check_forward(dev, idx, where, p, **kw):
+    got = skl.streamkl_fwd_sel(*sides(dev), idx, p["bs"], **where, **kw)
+    torch.cuda.synchronize()
+    assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
+    want = ref.forward(p)
+    for g, w, b, what in zip(got, want[:3], want[3:], ("KL", "LSE1", "LSE2")):
+        within(g, w, b, what)
+    return got
+
+
+CASES = {
+    "one token": dict(H=1, NQ=1, NK=1, T=1),
+    "one row": dict(H=4, HK1=1, HK2=1, NQ=1, NK=300, T=4),
+    "heads apart": dict(B=2, H=3, HS=3, NQ=200, NK=200),
+    "one list for all heads": dict(B=2, H=6, HK1=2, HK2=3, HS=1, NQ=100, NK=140, T=5),
+    "groups of three": dict(H=6, HK1=2, HK2=2, HS=2, NQ=130, NK=333, T=6, bs=64),
+    "grouped": dict(H=8, HK1=2, HK2=2, HS=2, NQ=300, NK=300, T=4, bs=64, d1=128, d2=128),
+    "student with its own heads": dict(H=8, HK1=2, HK2=8, HS=2, NQ=260, NK=260, T=2, bs=128, d1=128, d2=64),
+    "lists finer than keys": dict(H=8, HK1=1, HK2=2, HS=8, NQ=90, NK=257, T=4, d1=64, d2=128),
+    "more heads than a tile": dict(H=192, HK1=1, HK2=1, HS=1, NQ=9, NK=70, T=3, d1=16, d2=32),
+    "odd head dims": dict(H=2, NQ=77, NK=190, d1=80, d2=112, bs=128, T=2),
+    "narrow": dict(H=2, NQ=77, NK=190, d1=16, d2=48, T=7),
+    "last block short": dict(H=2, NQ=64, NK=129, bs=128, T=2),
+    "not causal": dict(H=4, HK1=2, HK2=2, NQ=190, NK=500, causal=False, bs=64, T=5, bshd=True),
+    "more queries than keys": dict(H=2, NQ=300, NK=100, T=3),
+    "prefix": dict(B=3, H=2, NQ=150, NK=260, prefix=[0, 77, 260], T=5),
+    "packed": dict(B=2, H=4, HK1=2, HK2=2, HS=2, NQ=300, NK=300, docs="packed", T=6, bshd=True),
+    "shuffled ids": dict(B=2, H=2, NQ=200, NK=170, docs="shuffled", T=4, bs=64),
+    "ids and prefix": dict(B=2, H=2, NQ=200, NK=200, docs="packed", prefix=[60, 130], T=4),
+    "33 slots": dict(H=2, NQ=70, NK=900, T=33),
+    "128 slots": dict(H=2, HS=2, NQ=40, NK=700, T=128, causal=False),
+    "every block": dict(H=2, NQ=300, NK=300, lists="all"),
+    "no block": dict(H=2, NQ=100, NK=100, lists="none"),
+    "many blocks": dict(H=1, NQ=200, NK=20000, T=9, d1=64, d2=64),
+    "many rows": dict(H=16, HK1=2, HK2=2, HS=2, NQ=1500, NK=1500, T=5, bs=64, d1=128, d2=128, bshd=True),
+    "peaked": dict(H=2, NQ=200, NK=400, T=6, sd=6.0),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_forward(name):
+    check_forward(*problem(**CASES[name]))
+
+
+def test_every_block_is_the_dense_forward():
+    dev, idx, where, p = problem(H=4, HK1=2, HK2=2, NQ=333, NK=333, bs=64, lists="all", d1=128, d2=128)
+    got = check_forward(dev, idx, where, p)
+    dense = skl.streamkl_fwd_mod(*sides(dev), **where)
+    for g, d in zip(got, dense):
+        assert (g - d).abs().max() <= 1e-4
+
+
+def test_hidden_keys_hold_anything():
+    dev, idx, where, p = problem(B=1, H=2, NQ=200, NK=200, docs="packed", T=2, lists="mixed")
+    want = skl.streamkl_fwd_sel(*sides(dev), idx, p["bs"], **where)
+    idx[idx == 3] = -1
+    p["blocks"] = idx.cpu().numpy()
+    want = check_forward(dev, idx, where, p)
+    pad = where["doc_k"][0] < 0
+    for t in "12":
+        dev["k" + t][:, :, pad] = float("nan")
+        dev["k" + t][:, :, 96:128] = float("inf")     # block 3, which nobody selects
+    got = skl.streamkl_fwd_sel(*sides(dev), idx, p["bs"], **where)
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+    # keys after a causal query
+    dev, idx, where, p = problem(H=1, NQ=64, NK=64, T=1, lists="all")
+    want = skl.streamkl_fwd_sel(*sides(dev), idx, 32, **where)
+    dev["k1"][:, :, 40:] = float("nan")
+    got = skl.streamkl_fwd_sel(*sides(dev), idx, 32, **where)
+    for g, w in zip(got, want):
+        assert torch.equal(g[..., :40], w[..., :40])
+
+
+def test_nan_queries_stay_with_their_rows():
+    dev, idx, where, p = problem(H=4, HK1=2, HK2=2, NQ=100, NK=100)
+    want = skl.streamkl_fwd_sel(*sides(dev), idx, p["bs"], **where)
+    dev["q1"][0, 1, 50] = float("nan")
+    got = skl.streamkl_fwd_sel(*sides(dev), idx, p["bs"], **where)
+    for g, w in zip(got, want):
+        same = g == w
+        same[0, 1, 50] = True
+        assert same.all()
+    assert torch.isnan(got[0][0, 1, 50])
+
+
+def test_strides():
+    """Heads and tokens inside larger tensors, and strides whose common divisor is below the head dim."""
+    dev, idx, where, p = problem(B=2, H=4, HK1=2, HK2=2, NQ=70, NK=90, d1=64, d2=80)
+    want = skl.streamkl_fwd_sel(*sides(dev), idx, p["bs"], **where)
+    for pad_n, pad_h, pad_b in ((0, 0, 0), (8, 0, 0), (0, 40, 0), (16, 8, 24)):
+        other = {}
+        for name, t in dev.items():
+            B, H, N, d = t.shape
+            sn = d + pad_n
+            sh, sb = N * sn + pad_h, 0
+            sb = H * sh + pad_b
+            buf = torch.full((B * sb,), float("nan"), dtype=torch.bfloat16, device="cuda")
+            v = buf.as_strided((B, H, N, d), (sb, sh, sn, 1))
+            v.copy_(t)
+            other[name] = v
+        got = skl.streamkl_fwd_sel(*sides(other), idx, p["bs"], **where)
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
+def test_repeatable_and_order_free():
+    dev, idx, where, p = problem(H=8, HK1=2, HK2=2, HS=2, NQ=700, NK=700, T=6, bs=32)
+    want = skl.streamkl_fwd_sel(*sides(dev), idx, 32, **where)
+    for _ in range(3):
+        for g, w in zip(skl.streamkl_fwd_sel(*sides(dev), idx, 32, **where), want):
+            assert torch.equal(g, w)
+    turned = idx.flip(3).contiguous()
+    p["blocks"] = turned.cpu().numpy()
+    check_forward(dev, turned, where, p)
+
+
+def test_outputs_workspace_streams_and_graphs():
+    dev, idx, where, p = problem(H=4, HK1=2, HK2=2, NQ=200, NK=200, T=4)
+    p1, p2 = sides(dev)
+    want = skl.streamkl_fwd_sel(p1, p2, idx, 32, **where)
+    need = skl.streamkl_fwd_sel_workspace_bytes(p1, p2, idx, 32, **where)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    out = [torch.full_like(w, float("nan")) for w in want]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    got = skl.streamkl_fwd_sel(p1, p2, idx, 32, **where, workspace=ws, kl=out[0], lse1=out[1], lse2=out[2], stream=st)
+    torch.cuda.current_stream().wait_stream(st)
+    assert all(g is o for g, o in zip(got, out))
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+    with pytest.raises(skl.StreamKLError):
+        skl.streamkl_fwd_sel(p1, p2, idx, 32, **where, workspace=ws[: need - 16])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = skl.streamkl_fwd_sel(p1, p2, idx, 32, **where)
+    dev["q2"].copy_(torch.randn_like(dev["q2"], dtype=torch.float32))
+    idx.copy_(idx.roll(1, 2))
+    graph.replay()
+    torch.cuda.synchronize()
+    for g, w in zip(again, skl.streamkl_fwd_sel(p1, p2, idx, 32, **where)):
+        assert torch.equal(g, w)
