@@ -39,25 +39,9 @@ int check_sel(const streamkl_side* p1, const streamkl_side* p2, const streamkl_v
   return check_blocks(sel, B, H, NQ, NK, data && !*empty);
 }
 
-// A [B][heads][n][d] view as rows of a 2-D map, boxes of 64 x 1 for gathers.
-// Every row starts at a multiple of the strides' common divisor.
-bool row_map(CUtensorMap* m, SelRows* r, const streamkl_view& v, int B, int heads, int n, int d) {
-  const long long sb = B > 1 ? v.stride_b : 0, sh = heads > 1 ? v.stride_h : 0, sn = n > 1 ? v.stride_n : 0;
-  long long g = std::gcd(std::gcd(sb, sh), sn);
-  if (g == 0) g = (d + 7) / 8 * 8;
-  const long long rows = ((B - 1) * sb + (heads - 1) * sh + (n - 1) * sn) / g + 1;
-  if (rows >= (1ll << 31) - 1 || g >= (1ll << 38)) return false;
-  *r = SelRows{int(sb / g), int(sh / g), int(sn / g), int(rows)};
-  if (m == nullptr) return true;
-  auto fn = tensor_map_encoder();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {cuuint64_t(d), cuuint64_t(rows)};
-  cuuint64_t strides[1] = {cuuint64_t(g) * 2};
-  cuuint32_t box[2] = {64u, 1u};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(v.data), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+SelRows rows_of(const streamkl_view& v, int B, int heads, int n, int d) {
+  return SelRows{static_cast<const uint8_t*>(v.data), B > 1 ? 2 * v.stride_b : 0, heads > 1 ? 2 * v.stride_h : 0,
+                 n > 1 ? 2 * v.stride_n : 0, d / 8};
 }
 
 struct Geometry {
@@ -163,18 +147,15 @@ int streamkl_fwd_sel(const streamkl_side* p1, const streamkl_side* p2, const str
   int s = check_sel(p1, p2, vis, sel, B, H, NQ, NK, true, &empty);
   if (s != STREAMKL_OK || empty) return s;
   if (!kl || !lse1 || !lse2 || !aligned16(kl) || !aligned16(lse1) || !aligned16(lse2)) return STREAMKL_INVALID_ARG;
-  SelRows r1, r2;
-  if (!row_map(nullptr, &r1, p1->q, B, H, NQ, p1->d) || !row_map(nullptr, &r2, p2->q, B, H, NQ, p2->d))
-    return STREAMKL_INVALID_ARG;
   const int sms = num_sms();
   const FwdPlan f = fwd_plan(*p1, *p2, *vis, *sel, B, H, NQ, NK, sms, workspace);
   if (!workspace || !aligned16(workspace) || workspace_bytes < f.bytes) return STREAMKL_INVALID_ARG;
   if ((s = check_device()) != STREAMKL_OK) return s;
   SelMaps m{};
   SelFwdArgs a{};
-  if (!row_map(&m.q1, &a.r1, p1->q, B, H, NQ, p1->d) || !row_map(&m.q2, &a.r2, p2->q, B, H, NQ, p2->d) ||
-      !key_maps(&m, *p1, *p2, B, NK, sel->block))
-    return STREAMKL_CUDA_ERROR;
+  if (!key_maps(&m, *p1, *p2, B, NK, sel->block)) return STREAMKL_CUDA_ERROR;
+  a.r1 = rows_of(p1->q, B, H, NQ, p1->d);
+  a.r2 = rows_of(p2->q, B, H, NQ, p2->d);
   a.status = status_word();
   if (!a.status) return STREAMKL_CUDA_ERROR;
   a.p = f.g.p;

@@ -4,7 +4,7 @@
 // Every query has up to T blocks of its own, so a tile of consecutive queries
 // shares no keys.  The work is turned round: for each block of keys, the
 // queries that selected it, 128 rows (queries x the heads that share keys) at
-// a time, their rows gathered by TMA.  K is then read once for a list of rows
+// a time, their rows gathered.  K is then read once for a list of rows
 // and every product is a full 128-row tile.  The attention KL's share of a
 // (row, block) is five numbers, so what is written between the passes stays
 // small; an output of d values a row would not allow this.
@@ -72,24 +72,45 @@ __device__ __forceinline__ SelWork sel_work(const SelPlan& p, int w) {
   return k;
 }
 
-// A [B][heads][N][d] view as rows of a 2-D tensor map: row = b rb + h rh + n rn.
+// A [B][heads][N][d] bf16 view (strides in bytes).
 struct SelRows {
-  int rb, rh, rn;
-  int none;  // a row past the last: reads as zeros
+  const uint8_t* base;
+  long long sb, sh, sn;
+  int chunks;  // 16-byte pieces of a row: d / 8
+  __device__ __forceinline__ const uint8_t* at(int b, int h, int i) const { return base + b * sb + h * sh + i * sn; }
 };
 
-// Four rows of 64 elements, at columns x, into shared memory.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int4 r) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
-      : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Copies 16 rows (lane l mod 16 holds the address of row l; null: not copied)
+// into rows [first, first + 16) of a [128][D] operand tile, 16 bytes a lane,
+// swizzled as TMA would.  Called by a whole warp; lanes from `half` on hold
+// the addresses that count.
+template <int D>
+__device__ __forceinline__ void gather_rows(uint32_t tile, int first, unsigned long long mine, int half, int chunks) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at a time
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
+  const uint32_t dst = tile + (c >> 3) * (kTile * 128) + first * 128;
+  const bool in = c < chunks;
+  const uint32_t off = c * 16;
+#pragma unroll
+  for (int r0 = 0; r0 < 16; r0 += kAtOnce) {
+    const int r = r0 + sub;
+    const unsigned long long p = __shfl_sync(0xffffffffu, mine, half + r);
+    if (p != 0 && in)
+      cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), reinterpret_cast<const uint8_t*>(p + off));
+  }
 }
 
 struct SelMaps {
-  CUtensorMap q1, q2;  // rows (SelRows), boxes of 64 x 1, 128-byte swizzle
-  CUtensorMap k1, k2;  // 4-D (d, N, heads, B), boxes of 64 x block
+  CUtensorMap k1, k2;  // 4-D (d, N, heads, B), boxes of 64 x block, 128-byte swizzle
 };
 
 struct SelFwdArgs {
@@ -104,7 +125,7 @@ struct SelFwdArgs {
   float* lse1;
   float* lse2;
   int* status;
-  int q_stages, k_bufs;
+  int slots, k_bufs;
 };
 
 int launch_sel_plan(const SelPlan& p, cudaStream_t st);

@@ -2,16 +2,21 @@
 // pair, then their merge into KL, LSE1 and LSE2.
 //
 // Persistent CTAs walk the items: K1, K2 of the item's block once, then tiles
-// of 128 gathered rows through a ring of stages.  18 warps:
-//   warp 16     gathers Q1, Q2 rows by TMA, four a lane, and loads K
-//   warp 17     S1 = Q1 K1^T, S2 = Q2 K2^T into one of 4 TMEM buffers (2 for blocks of 128)
-//   warps 0-15  statistics: warpgroup g takes every buffer g; thread = row
+// of 128 gathered rows, a side's tile at a time, through a ring of slots.  24 warps:
+//   warps 0-11  statistics: a warpgroup takes every third tile; thread = row
+//   warps 12-19 gather 16 rows each, 16 bytes a lane (cp.async).  TMA takes
+//               some 50 clocks for a copy of few rows, whatever its form: at
+//               rows of 256 bytes out of L2 its gather of four reached 2.5
+//               TB/s, cp.async of 2, 4 and 8 warps 6, 11.6 and 14.3.
+//   warp 20     S1 = Q1 K1^T, S2 = Q2 K2^T into one of 4 TMEM buffers (2 for blocks of 128)
+//   warp 21     K by TMA
 // A row's keys in one block are few, so its references are its own largest
 // scores there (one more read of TMEM), and nothing is rescaled:
 //   e_t = S_t log2 e - m_t,  l_t = sum 2^e_t,  acc = sum 2^e1 (e1 - e2).
 // The merge adds the parts of a row's slots in their order (as merge_stats of
 // the dense forward does for splits), so results do not depend on which CTA
 // took which item.
+#include "bwd_common.cuh"
 #include "fwd_mod.cuh"
 #include "sel_common.cuh"
 
@@ -20,17 +25,21 @@ namespace skl {
 namespace {
 
 struct SelFwdLayout {
-  static constexpr int kWGs = 4;
-  static constexpr int kStatWarps = 4 * kWGs;
-  static constexpr int kProdWarp = kStatWarps, kMmaWarp = kStatWarps + 1;
-  static constexpr int kThreads = 32 * (kStatWarps + 2);
-  static constexpr int kMaxStages = 4, kMaxKBufs = 2;
-  // k_full[2], k_empty[2], q_full[4], q_empty[4], s_full[4], s_empty[4], done
-  static constexpr int kNumBars = 2 * kMaxKBufs + 2 * kMaxStages + 8 + 1;
+  static constexpr int kWGs = 3;  // of statistics
+  static constexpr int kGatherWarp = 4 * kWGs, kGatherWarps = 8;
+  static constexpr int kMmaWarp = kGatherWarp + kGatherWarps, kLoadWarp = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps + 4);
+  static constexpr int kMaxSlots = 8;
+  // Copies of a slot are waited for when two more have been issued.
+  static constexpr int kLag = 2;
+  // k_full[2], k_empty[2], q_full[8], q_empty[8], s_full[4], s_empty[4], done
+  static constexpr int kKFull = 0, kKEmpty = 2, kQFull = 4, kQEmpty = 12, kSFull = 20, kSEmpty = 24, kDone = 28;
+  static constexpr int kNumBars = 29;
   static constexpr uint32_t kTail = kNumBars * 8 + 16;
   static constexpr uint32_t kMost = 232448;
-  static uint32_t bytes(int q_stages, int k_bufs, int d1, int d2, int bs) {
-    return 1024u + uint32_t(d1 + d2) * 2u * uint32_t(q_stages * kTile + k_bufs * bs) + kTail;
+  static constexpr uint32_t slot_bytes(int d1, int d2) { return uint32_t(d1 > d2 ? d1 : d2) * 2u * kTile; }
+  static uint32_t bytes(int slots, int k_bufs, int d1, int d2, int bs) {
+    return 1024u + slots * slot_bytes(d1, d2) + uint32_t(d1 + d2) * 2u * uint32_t(k_bufs * bs) + kTail;
   }
 };
 
@@ -83,25 +92,18 @@ __device__ __forceinline__ void block_sums(uint32_t ts, int bs, float c1, float 
 
 template <int D1, int D2>
 __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
-    sel_fwd_kernel(const __grid_constant__ CUtensorMap tq1, const __grid_constant__ CUtensorMap tk1,
-                   const __grid_constant__ CUtensorMap tq2, const __grid_constant__ CUtensorMap tk2,
+    sel_fwd_kernel(const __grid_constant__ CUtensorMap tk1, const __grid_constant__ CUtensorMap tk2,
                    const __grid_constant__ SelFwdArgs a) {
   using L = SelFwdLayout;
-  constexpr uint32_t kQ1 = kTile * D1 * 2, kQ = kTile * (D1 + D2) * 2;
+  constexpr uint32_t kSlot = L::slot_bytes(D1, D2);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bs = a.p.bs;
   const uint32_t kK1 = uint32_t(bs) * D1 * 2, kK = uint32_t(bs) * (D1 + D2) * 2;
-  const uint32_t oQ = a.k_bufs * kK, oBar = oQ + a.q_stages * kQ;
-  auto bar_kfull = [&](int i) { return sb + oBar + 8u * i; };
-  auto bar_kempty = [&](int i) { return sb + oBar + 8u * (L::kMaxKBufs + i); };
-  auto bar_qfull = [&](int i) { return sb + oBar + 8u * (2 * L::kMaxKBufs + i); };
-  auto bar_qempty = [&](int i) { return sb + oBar + 8u * (2 * L::kMaxKBufs + L::kMaxStages + i); };
-  auto bar_sfull = [&](int i) { return sb + oBar + 8u * (2 * L::kMaxKBufs + 2 * L::kMaxStages + i); };
-  auto bar_sempty = [&](int i) { return sb + oBar + 8u * (2 * L::kMaxKBufs + 2 * L::kMaxStages + 4 + i); };
-  const uint32_t bar_done = sb + oBar + 8u * (L::kNumBars - 1);
+  const uint32_t oQ = a.k_bufs * kK, oBar = oQ + a.slots * kSlot;
+  auto bar = [&](int id) { return sb + oBar + 8u * id; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + oBar + L::kNumBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + oBar + L::kNumBars * 8 + 4);
   const Ctl ctl{abort_flag, a.status};
@@ -109,8 +111,10 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
-      const int s_empty = 2 * L::kMaxKBufs + 2 * L::kMaxStages + 4;
-      mbar_init(sb + oBar + 8u * i, i >= s_empty && i < s_empty + 4 ? 4 : 1);  // a warpgroup frees a buffer
+      int count = 1;
+      if (i >= L::kQFull && i < L::kQEmpty) count = L::kGatherWarps;
+      if (i >= L::kSEmpty && i < L::kDone) count = 4;  // the warps of a warpgroup
+      mbar_init(bar(i), count);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -119,6 +123,10 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  // columns past the head dim (K's are zeros, and no product may meet a NaN there)
+  if (a.r1.chunks < D1 / 8 || a.r2.chunks < D2 / 8)
+    for (uint32_t o = threadIdx.x * 16; o < a.slots * kSlot; o += L::kThreads * 16) st_shared_v4(sb + oQ + o, 0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -126,101 +134,109 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
   const int per_tile = a.p.queries_per_tile, G = a.p.G;
   const int works = min(*a.p.item_count, a.p.max_items) * (a.p.HU / a.p.HS);
 
-  if (warp == L::kProdWarp) {
-    // ---------------------------------------------------------------- TMA producer (32 lanes, 4 rows each)
-    int n = 0, items = 0;
+  if (warp >= L::kGatherWarp && warp < L::kMmaWarp) {
+    // ---------------------------------------------------------------- gather: rows [first, first + 16)
+    const int first = (warp - L::kGatherWarp) * 16;
+    // lanes 0-15 hold the addresses of side 1's rows, lanes 16-31 those of side 2's
+    const int r = first + (lane & 15), ql = r / G, hl = r - ql * G;
+    const SelRows rows = lane < 16 ? a.r1 : a.r2;
+    // a slot's copies have landed: the tensor core may read them
+    auto landed = [&](int m) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kQFull + m % a.slots));
+    };
+    int m = 0;  // slots filled
     bool ok = true;
-    int ql[4], hl[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      ql[x] = (4 * lane + x) / G;
-      hl[x] = (4 * lane + x) - ql[x] * G;
-    }
-    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
+    for (int w = blockIdx.x; ok && w < works; w += gridDim.x) {
       const SelWork k = sel_work(a.p, w);
-      const int kb = items % a.k_bufs;
-      ok = mbar_wait_warp(bar_kempty(kb), ((items / a.k_bufs) & 1) ^ 1, ctl);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar_kfull(kb), kK);
-        const int hu = k.head0 / G;
+      for (int e0 = 0; ok && e0 < k.count; e0 += per_tile) {
+        // (rows past the last are not read: what the slot holds there gives scores that nobody takes)
+        const int e = e0 + ql;
+        const bool on = ql < per_tile && e < k.count;
+        const int i = on ? int(__ldg(a.p.entries + k.first + e) >> kSlotBits) : 0;
+        const unsigned long long at = on ? reinterpret_cast<unsigned long long>(rows.at(k.b, k.head0 + hl, i)) : 0ull;
+#pragma unroll
+        for (int side = 0; side < 2; ++side, ++m) {
+          const int s = m % a.slots;
+          ok = mbar_wait_warp(bar(L::kQEmpty + s), ((m / a.slots) & 1) ^ 1, ctl);
+          if (!ok) break;
+          if (side == 0) gather_rows<D1>(sb + oQ + s * kSlot, first, at, 0, a.r1.chunks);
+          else gather_rows<D2>(sb + oQ + s * kSlot, first, at, 16, a.r2.chunks);
+          cp_async_commit();
+          if (m >= L::kLag) {
+            cp_async_wait<L::kLag>();
+            landed(m - L::kLag);
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+    if (ok)
+      for (int x = m > L::kLag ? m - L::kLag : 0; x < m; ++x) landed(x);
+  } else if (warp >= L::kMmaWarp) {
+    if (warp == L::kLoadWarp && lane == 0) {
+      // -------------------------------------------------------------- K
+      int items = 0;
+      for (int w = blockIdx.x; w < works; w += gridDim.x, ++items) {
+        const SelWork k = sel_work(a.p, w);
+        const int kb = items % a.k_bufs, hu = k.head0 / G;
+        if (!mbar_wait_polled(bar(L::kKEmpty + kb), ((items / a.k_bufs) & 1) ^ 1, ctl)) break;
+        const uint32_t full = bar(L::kKFull + kb);
+        mbar_arrive_expect_tx(full, kK);
 #pragma unroll
         for (int c = 0; c < D1 / 64; ++c)
-          tma_load_4d(sb + kb * kK + c * (bs * 128), &tk1, bar_kfull(kb), c * 64, k.block * bs, hu / a.u1, k.b);
+          tma_load_4d(sb + kb * kK + c * (bs * 128), &tk1, full, c * 64, k.block * bs, hu / a.u1, k.b);
 #pragma unroll
         for (int c = 0; c < D2 / 64; ++c)
-          tma_load_4d(sb + kb * kK + kK1 + c * (bs * 128), &tk2, bar_kfull(kb), c * 64, k.block * bs, hu / a.u2, k.b);
+          tma_load_4d(sb + kb * kK + kK1 + c * (bs * 128), &tk2, full, c * 64, k.block * bs, hu / a.u2, k.b);
       }
-      for (int e0 = 0; e0 < k.count; e0 += per_tile, ++n) {
-        int4 r1, r2;
-        int* p1 = &r1.x;
-        int* p2 = &r2.x;
-        bool any = false;
+      if (*abort_flag)  // let the copies already started land before the CTA exits
+        for (int j = items > a.k_bufs ? items - a.k_bufs : 0; j < items; ++j)
+          mbar_drain(bar(L::kKFull + j % a.k_bufs), (j / a.k_bufs) & 1, 200000000ull);
+    } else if (warp == L::kMmaWarp) {
+      // -------------------------------------------------------------- MMA issuer
+      const uint32_t leader = elect_one();
+      const uint32_t idesc = idesc_bf16(128, bs, 0, 0);
+      int n = 0, m = 0, items = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
+        const int count = sel_work(a.p, w).count;
+        const int kb = items % a.k_bufs;
+        ok = mbar_wait_warp(bar(L::kKFull + kb), (items / a.k_bufs) & 1, ctl);
+        const uint64_t k1d = sdesc_sw128(sb + kb * kK, 16, 1024), k2d = sdesc_sw128(sb + kb * kK + kK1, 16, 1024);
+        for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
+          const int i = n % bufs;
+          const uint32_t d1 = tmem + uint32_t(i * 2 * bs), d2 = d1 + uint32_t(bs);
+          int s = m % a.slots;
+          ok = mbar_wait_warp(bar(L::kSEmpty + i), ((n / bufs) & 1) ^ 1, ctl) &&
+               mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t q1d = sdesc_sw128(sb + oQ + s * kSlot, 16, 1024);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int e = e0 + ql[x];
-          const bool on = ql[x] < per_tile && e < k.count;
-          any |= on;
-          const int i = on ? int(__ldg(a.p.entries + k.first + e) >> kSlotBits) : 0, h = k.head0 + hl[x];
-          p1[x] = on ? k.b * a.r1.rb + h * a.r1.rh + i * a.r1.rn : a.r1.none;
-          p2[x] = on ? k.b * a.r2.rb + h * a.r2.rh + i * a.r2.rn : a.r2.none;
+          for (int kk = 0; kk < D1 / 16; ++kk)
+            mma_bf16_ss(leader, d1, sdesc_add(q1d, step_off(kk, kTile)), sdesc_add(k1d, step_off(kk, bs)), idesc, kk > 0);
+          mma_commit(leader, bar(L::kQEmpty + s));
+          ++m;
+          s = m % a.slots;
+          ok = mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t q2d = sdesc_sw128(sb + oQ + s * kSlot, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D2 / 16; ++kk)
+            mma_bf16_ss(leader, d2, sdesc_add(q2d, step_off(kk, kTile)), sdesc_add(k2d, step_off(kk, bs)), idesc, kk > 0);
+          mma_commit(leader, bar(L::kQEmpty + s));
+          ++m;
+          mma_commit(leader, bar(L::kSFull + i));
         }
-        const int s = n % a.q_stages;
-        ok = mbar_wait_warp(bar_qempty(s), ((n / a.q_stages) & 1) ^ 1, ctl);
-        if (!ok) break;
-        // (four rows past the last are not read: what the stage holds there gives scores that nobody takes)
-        const int lanes = __popc(__ballot_sync(0xffffffffu, any));
-        if (lane == 0) mbar_arrive_expect_tx(bar_qfull(s), lanes * 4u * (D1 + D2) * 2u);
-        __syncwarp();
-        if (any) {
-          const uint32_t dst = sb + oQ + s * kQ + lane * 512;
-#pragma unroll
-          for (int c = 0; c < D1 / 64; ++c) tma_gather4(dst + c * (kTile * 128), &tq1, bar_qfull(s), c * 64, r1);
-#pragma unroll
-          for (int c = 0; c < D2 / 64; ++c) tma_gather4(dst + kQ1 + c * (kTile * 128), &tq2, bar_qfull(s), c * 64, r2);
-        }
+        if (ok) mma_commit(leader, bar(L::kKEmpty + kb));
       }
+      mma_commit(leader, bar(L::kDone));  // every MMA has finished before TMEM is released
+      mbar_drain(bar(L::kDone), 0, 1000000000ull);
     }
-    if (*abort_flag && lane == 0) {  // let the copies already started land before the CTA exits
-      const uint64_t lim = 200000000ull;
-      for (int j = items > a.k_bufs ? items - a.k_bufs : 0; j < items; ++j)
-        mbar_drain(bar_kfull(j % a.k_bufs), (j / a.k_bufs) & 1, lim);
-      for (int j = n > a.q_stages ? n - a.q_stages : 0; j < n; ++j)
-        mbar_drain(bar_qfull(j % a.q_stages), (j / a.q_stages) & 1, lim);
-    }
-  } else if (warp == L::kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issuer
-    const uint32_t leader = elect_one();
-    const uint32_t idesc = idesc_bf16(128, bs, 0, 0);
-    int n = 0, items = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
-      const int count = sel_work(a.p, w).count;
-      const int kb = items % a.k_bufs;
-      ok = mbar_wait_warp(bar_kfull(kb), (items / a.k_bufs) & 1, ctl);
-      const uint64_t k1d = sdesc_sw128(sb + kb * kK, 16, 1024), k2d = sdesc_sw128(sb + kb * kK + kK1, 16, 1024);
-      for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
-        const int s = n % a.q_stages, i = n % bufs;
-        ok = mbar_wait_warp(bar_qfull(s), (n / a.q_stages) & 1, ctl) &&
-             mbar_wait_warp(bar_sempty(i), ((n / bufs) & 1) ^ 1, ctl);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d1 = tmem + uint32_t(i * 2 * bs), d2 = d1 + uint32_t(bs);
-        const uint64_t q1d = sdesc_sw128(sb + oQ + s * kQ, 16, 1024), q2d = sdesc_sw128(sb + oQ + s * kQ + kQ1, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D1 / 16; ++kk)
-          mma_bf16_ss(leader, d1, sdesc_add(q1d, step_off(kk, kTile)), sdesc_add(k1d, step_off(kk, bs)), idesc, kk > 0);
-#pragma unroll
-        for (int kk = 0; kk < D2 / 16; ++kk)
-          mma_bf16_ss(leader, d2, sdesc_add(q2d, step_off(kk, kTile)), sdesc_add(k2d, step_off(kk, bs)), idesc, kk > 0);
-        mma_commit(leader, bar_qempty(s));
-        mma_commit(leader, bar_sfull(i));
-      }
-      if (ok) mma_commit(leader, bar_kempty(kb));
-    }
-    mma_commit(leader, bar_done);  // every MMA has finished before TMEM is released
-    mbar_drain(bar_done, 0, 1000000000ull);
-  } else if ((warp >> 2) < bufs) {
+  } else {
     // ---------------------------------------------------------------- statistics
     const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
     const int ql = row / G, hl = row - ql * G;
@@ -235,7 +251,8 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
       const int k0 = k.block * bs;
       const int prefix = a.p.prefix != nullptr ? min(max(a.p.prefix[k.b], 0), a.p.NK) : 0;
       for (int e0 = 0; ok && e0 < k.count; e0 += per_tile, ++n) {
-        if (n % bufs != wg) continue;
+        if (n % L::kWGs != wg) continue;
+        const int buf = n % bufs;
         const int e = e0 + ql;
         const bool on = ql < per_tile && e < k.count;
         const unsigned ent = on ? __ldg(a.p.entries + k.first + e) : 0u;
@@ -249,18 +266,18 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
         const int last = a.p.causal ? min(max(i + off + 1, prefix), a.p.NK) : a.p.NK;
         const bool whole = __all_sync(0xffffffffu, !on || last >= k0 + bs) && kids == nullptr;
         const bool idle = __all_sync(0xffffffffu, !on);
-        ok = mbar_wait_warp(bar_sfull(wg), (n / bufs) & 1, ctl);
+        ok = mbar_wait_warp(bar(L::kSFull + buf), (n / bufs) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
         ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
         if (!idle) {
-          const uint32_t ts = tmem + lane_off + uint32_t(wg * 2 * bs);
+          const uint32_t ts = tmem + lane_off + uint32_t(buf * 2 * bs);
           if (whole) block_sums<false>(ts, bs, c1, c2, i, k0, a, prefix, id, kids, st);
           else block_sums<true>(ts, bs, c1, c2, i, k0, a, prefix, id, kids, st);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sempty(wg));
+        if (lane == 0) mbar_arrive(bar(L::kSEmpty + buf));
         const size_t at = (size_t(k.b * a.p.H + k.head0 + hl) * a.p.NQ + i) * a.p.T + t;
         if (on && SKL_CHECK(a.status, i < a.p.NQ && t < a.p.T && k.head0 + hl < a.p.H && k.b < a.p.B)) {
           // a row that ids hide the whole block from has sums of 2^(-3e38 - ...) = 0, relative to nothing
@@ -324,16 +341,16 @@ template <int D1, int D2>
 int launch_sel_fwd_t(const SelMaps& m, const SelFwdArgs& args, int sms, cudaStream_t st) {
   using L = SelFwdLayout;
   SelFwdArgs a = args;
-  // two buffers of K (the next item's loads) where they leave two stages of Q, then as many stages as fit
-  a.k_bufs = L::bytes(2, 2, D1, D2, a.p.bs) <= L::kMost ? 2 : 1;
-  a.q_stages = 2;
-  while (a.q_stages < L::kMaxStages && L::bytes(a.q_stages + 1, a.k_bufs, D1, D2, a.p.bs) <= L::kMost) ++a.q_stages;
+  // two buffers of K (the next item's loads) where they leave five slots, then as many slots as fit
+  a.k_bufs = L::bytes(5, 2, D1, D2, a.p.bs) <= L::kMost ? 2 : 1;
+  a.slots = 5;
+  while (a.slots < L::kMaxSlots && L::bytes(a.slots + 1, a.k_bufs, D1, D2, a.p.bs) <= L::kMost) ++a.slots;
   auto kern = sel_fwd_kernel<D1, D2>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kMost);
   if (e != cudaSuccess) return e;
   const long long most = (long long)a.p.max_items * (a.p.HU / a.p.HS);
   const int grid = int(most < sms ? most : sms);
-  kern<<<grid, L::kThreads, L::bytes(a.q_stages, a.k_bufs, D1, D2, a.p.bs), st>>>(m.q1, m.k1, m.q2, m.k2, a);
+  kern<<<grid, L::kThreads, L::bytes(a.slots, a.k_bufs, D1, D2, a.p.bs), st>>>(m.k1, m.k2, a);
   return cudaGetLastError();
 }
 

@@ -35,36 +35,58 @@ __device__ __forceinline__ void walk(const SelPlan& p, int sel, int q0, int q1, 
   while (span < p.T && span < 32) span *= 2;
   const int per = 32 / span, q = lane / span, t0 = lane - q * span;
   const unsigned own = span == 32 ? 0xffffffffu : ((1u << span) - 1u) << (q * span);
-  for (int i0 = q0; i0 < q1; i0 += per) {
-    const int i = i0 + q;
-    const bool row = i < q1 && (ids == nullptr || ids[i] >= 0);
+  // what follows for 32 slots: j, or -1 where a slot does not count
+  auto step = [&](int i, int j, bool on, int w, int t) {
+    const unsigned same = __match_any_sync(0xffffffffu, on ? j : -2 - lane);
+    const unsigned lower = same & ((1u << lane) - 1u);
+    on = on && (lower & own) == 0u;
+    const unsigned all = __ballot_sync(0xffffffffu, on);
+    if (!kFill && t0 == 0 && i < q1) slots[size_t(i) * p.words + w] = (all & own) >> (q * span);
+    const unsigned mine = same & all;  // (of a lane that counts)
+    const unsigned at = on ? counters[j] : 0u;
+    __syncwarp();
+    if (on) {
+      if ((mine & ((1u << lane) - 1u)) == 0u) counters[j] = at + __popc(mine);
+      if (kFill) entries[at + __popc(lower & all)] = (unsigned(i) << kSlotBits) | unsigned(t);
+    }
+    __syncwarp();
+  };
+  auto counts = [&](int i, int j) {
+    return j >= 0 && j < p.blocks && (!p.causal || j * p.bs <= i + off || j * p.bs < prefix);
+  };
+  if (p.words == 1) {
+    constexpr int kAhead = 8;  // loads in flight
+    for (int i0 = q0; i0 < q1; i0 += kAhead * per) {
+      int j[kAhead];
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int i = i0 + s * per + q;
+        const bool row = i < q1 && t0 < p.T && (ids == nullptr || ids[i] >= 0);
+        j[s] = row ? sel_rows[size_t(i) * p.T + t0] : -1;
+      }
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int i = i0 + s * per + q;
+        if (i0 + s * per < q1) step(i, j[s], counts(i, j[s]), 0, t0);
+      }
+    }
+    return;
+  }
+  for (int i = q0; i < q1; ++i) {
+    const bool row = ids == nullptr || ids[i] >= 0;
     int before[kMaxSlots / 32];
 #pragma unroll
     for (int w = 0; w < kMaxSlots / 32; ++w) {
       if (w >= p.words) break;
       const int t = 32 * w + t0;
-      int j = row && t < p.T ? sel_rows[size_t(i) * p.T + t] : -1;
-      bool on = j >= 0 && j < p.blocks;
-      if (on && p.causal) on = j * p.bs <= i + off || j * p.bs < prefix;
-      // (slots of a query with more than 32: against the words before)
+      const int j = row && t < p.T ? sel_rows[size_t(i) * p.T + t] : -1;
+      bool on = counts(i, j);
       before[w] = on ? j : -1;
 #pragma unroll
-      for (int v = 0; v < w; ++v)
+      for (int v = 0; v < w; ++v)  // named in the words before?
         for (int s = 0; s < 32; ++s)
           if (__shfl_sync(0xffffffffu, before[v], s) == j) on = false;
-      const unsigned same = __match_any_sync(0xffffffffu, on ? j : -2 - lane);
-      const unsigned lower = same & ((1u << lane) - 1u);
-      on = on && (lower & own) == 0u;
-      const unsigned all = __ballot_sync(0xffffffffu, on);
-      if (!kFill && t0 == 0 && i < q1) slots[size_t(i) * p.words + w] = (all & own) >> (q * span);
-      const unsigned mine = same & all;  // (of a lane that counts)
-      const unsigned at = on ? counters[j] : 0u;
-      __syncwarp();
-      if (on) {
-        if ((mine & ((1u << lane) - 1u)) == 0u) counters[j] = at + __popc(mine);
-        if (kFill) entries[at + __popc(lower & all)] = (unsigned(i) << kSlotBits) | unsigned(t);
-      }
-      __syncwarp();
+      step(i, j, on, w, t);
     }
   }
 }
