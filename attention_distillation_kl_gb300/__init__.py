@@ -24,7 +24,7 @@ __all__ = [
     "streamkl_bwd_workspace_bytes", "streamkl_bwd_gqa_ws",
     "AttnSide", "streamkl_fwd_mod", "streamkl_fwd_mod_workspace_bytes", "streamkl_bwd_mod",
     "streamkl_bwd_mod_workspace_bytes", "Rotary", "streamkl_rotate", "streamkl_pool_blocks",
-    "streamkl_fwd_sel", "streamkl_fwd_sel_workspace_bytes",
+    "streamkl_fwd_sel", "streamkl_fwd_sel_workspace_bytes", "streamkl_bwd_sel", "streamkl_bwd_sel_workspace_bytes",
     "status_string", "STREAMKL_STATIC_WORKSPACE_BYTES",
     "streamkl_get_device_status", "streamkl_probe_ex2", "streamkl_selftest_wait_timeout",
     "streamkl_selftest_turn_timeout",
@@ -112,6 +112,8 @@ _SIGS = {
     "streamkl_pool_blocks": (_I, [_VP, _P, _I, _I, _I, _I, _I, _VP, _P]),
     "streamkl_fwd_sel_workspace_bytes": (_SZ, [_SP, _SP, _VISP, _BP, _I, _I, _I, _I]),
     "streamkl_fwd_sel": (_I, [_SP, _SP, _VISP, _BP, _I, _I, _I, _I, _P, _SZ, _P, _P, _P, _P]),
+    "streamkl_bwd_sel_workspace_bytes": (_SZ, [_SP, _SP, _VISP, _BP, _I, _I, _I, _I, _I]),
+    "streamkl_bwd_sel": (_I, [_SP, _SP, _VISP, _BP, _I, _I, _I, _I, _P, _P, _P, _P, _I, _VP, _VP, _P, _SZ, _P]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
     "streamkl_get_device_status": (_I, []),
     "streamkl_probe_ex2": (_I, [_P, _I, _I, _P]),
@@ -827,6 +829,42 @@ def streamkl_fwd_sel(p1, p2, blocks, block, causal=False, prefix=None, doc_q=Non
     _check(c.streamkl_fwd_sel(p1._c, p2._c, vis, sel, B, H, NQ, NK, ws, ws_bytes, kl.data_ptr(), lse1.data_ptr(),
                               lse2.data_ptr(), _mod_stream(stream, dev)), "streamkl_fwd_sel")
     return kl, lse1, lse2
+
+
+@_on_device
+def streamkl_bwd_sel_workspace_bytes(p1, p2, blocks, block, mode=STREAMKL_GRAD_P2, causal=False, prefix=None, doc_q=None,
+                                     doc_k=None):
+    """Workspace bytes streamkl_bwd_sel needs for these arguments."""
+    B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
+    return int(lib().streamkl_bwd_sel_workspace_bytes(p1._c, p2._c, vis, _sel_call(blocks, block, p1), B, H, NQ, NK,
+                                                      int(mode)))
+
+
+@_on_device
+def streamkl_bwd_sel(p1, p2, blocks, block, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=False, prefix=None,
+                     doc_q=None, doc_k=None, dq=None, dk=None, workspace=None, stream=None):
+    """(dq, dk) bf16 for the side `mode` selects, from streamkl_fwd_sel over the
+    same arguments; bitwise repeatable."""
+    B, H, NQ, NK, vis = _mod_call(p1, p2, causal, prefix, doc_q, doc_k)
+    g = p2 if mode == STREAMKL_GRAD_P2 else p1
+    sel, dev, c = _sel_call(blocks, block, p1), g.device, lib()
+    if stream is not None:
+        _check_stream(stream, dev)
+    for name, t in (("kl", kl), ("lse1", lse1), ("lse2", lse2), ("dkl", dkl)):
+        if t is None:
+            raise ValueError(f"{name} is missing")
+        _out(t, (B, H, NQ), dev, name)
+    need = c.streamkl_bwd_sel_workspace_bytes(p1._c, p2._c, vis, sel, B, H, NQ, NK, int(mode))
+    ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
+    given = (dq, dk)
+    with _making(stream):
+        dq = _grad_out(dq, g.q.shape, dev, "dq")
+        dk = _grad_out(dk, g.k.shape, dev, "dk")
+    _handed_over(stream, dev, *zip(given, (dq, dk)))
+    _check(c.streamkl_bwd_sel(p1._c, p2._c, vis, sel, B, H, NQ, NK, kl.data_ptr(), lse1.data_ptr(), lse2.data_ptr(),
+                              dkl.data_ptr(), int(mode), _view(dq), _view(dk), ws, ws_bytes, _mod_stream(stream, dev)),
+           "streamkl_bwd_sel")
+    return dq, dk
 
 
 def streamkl_get_device_status():

@@ -125,6 +125,38 @@ FwdPlan fwd_plan(const streamkl_side& p1, const streamkl_side& p2, const streamk
   return f;
 }
 
+struct BwdPlan {
+  ModPrepArgs prep{};
+  Geometry g;
+  float* dq32 = nullptr;
+  unsigned* kmax = nullptr;
+  float* dk_part = nullptr;
+  int pitch = 0;
+  size_t bytes = 0;
+};
+
+BwdPlan bwd_plan(const streamkl_side& p1, const streamkl_side& p2, const streamkl_visible& vis, const streamkl_blocks& sel,
+                 int B, int H, int NQ, int NK, int mode, int sms, void* ws) {
+  BwdPlan f;
+  Carver c{static_cast<uint8_t*>(ws)};
+  const streamkl_side* const p[2] = {&p1, &p2};
+  const streamkl_side& g = mode == STREAMKL_GRAD_P2 ? p2 : p1;
+  f.pitch = (g.d + 31) / 32 * 32;
+  // what starts at zero comes first, in one piece
+  f.dq32 = c.take<float>(size_t(B) * H * NQ * f.pitch);
+  f.kmax = c.take<unsigned>(size_t(B) * g.HK);
+  f.prep.zero = static_cast<uint4*>(ws);
+  f.prep.zero_words = c.used / 16;
+  take_prep(c, f.prep, p, vis, B, H, NQ, NK, -1);
+  f.g = geometry(p1, p2, vis, sel, B, H, NQ, NK);
+  f.g.p.tiles_per_item = item_tiles(f.g.p, sms, 32);
+  take_plan(c, f.g.p);
+  f.g.p.ranges = c.take<int2>(size_t(B) * sel.heads * f.g.p.blocks);
+  f.dk_part = c.take<float>(size_t(f.g.p.max_items) * (f.g.p.HU / f.g.p.HS) * sel.block * g.d);
+  f.bytes = c.used;
+  return f;
+}
+
 bool key_maps(SelMaps* m, const streamkl_side& p1, const streamkl_side& p2, int B, int NK, int bs) {
   return map_bf16(&m->k1, p1.k, B, p1.HK, NK, p1.d, bs) && map_bf16(&m->k2, p2.k, B, p2.HK, NK, p2.d, bs);
 }
@@ -173,6 +205,78 @@ int streamkl_fwd_sel(const streamkl_side* p1, const streamkl_side* p2, const str
   if (launch_mod_prep(f.prep, cs) != 0 || launch_sel_plan(a.p, cs) != 0) return STREAMKL_CUDA_ERROR;
   if (launch_sel_fwd(m, tile_width(p1->d), tile_width(p2->d), a, sms, cs) != 0) return STREAMKL_CUDA_ERROR;
   return as_status(launch_sel_merge(a, cs));
+}
+
+size_t streamkl_bwd_sel_workspace_bytes(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,
+                                        const streamkl_blocks* sel, int B, int H, int NQ, int NK, int mode) {
+  bool empty = false;
+  if (check_sel(p1, p2, vis, sel, B, H, NQ, NK, false, &empty) != STREAMKL_OK || empty) return 0;
+  if (mode != STREAMKL_GRAD_P2 && mode != STREAMKL_GRAD_P1) return 0;
+  return bwd_plan(*p1, *p2, *vis, *sel, B, H, NQ, NK, mode, num_sms(), nullptr).bytes;
+}
+
+int streamkl_bwd_sel(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,
+                     const streamkl_blocks* sel, int B, int H, int NQ, int NK, const float* kl, const float* lse1,
+                     const float* lse2, const float* dkl, int mode, const streamkl_view* dq, const streamkl_view* dk,
+                     void* workspace, size_t workspace_bytes, streamkl_stream_t stream) {
+  bool empty = false;
+  int s = check_sel(p1, p2, vis, sel, B, H, NQ, NK, true, &empty);
+  if (s != STREAMKL_OK) return s;
+  if (mode != STREAMKL_GRAD_P2 && mode != STREAMKL_GRAD_P1) return STREAMKL_INVALID_ARG;
+  const streamkl_side& g = mode == STREAMKL_GRAD_P2 ? *p2 : *p1;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (empty) {  // no query rows: nothing reaches K
+    if (B == 0 || H == 0 || NK == 0) return STREAMKL_OK;
+    if (dk == nullptr || !view_ok(*dk, B, g.HK, NK)) return STREAMKL_INVALID_ARG;
+    ModFinishArgs fin{};
+    fin.rows[0] = {nullptr, B * g.HK, g.HK, NK, g.d, 0, static_cast<__nv_bfloat16*>(dk->data), B > 1 ? dk->stride_b : 0,
+                   g.HK > 1 ? dk->stride_h : 0, NK > 1 ? dk->stride_n : 0};
+    return as_status(launch_mod_finish(fin, cs));
+  }
+  if (!kl || !lse1 || !lse2 || !dkl || !aligned16(kl) || !aligned16(lse1) || !aligned16(lse2) || !aligned16(dkl))
+    return STREAMKL_INVALID_ARG;
+  if (dq == nullptr || dk == nullptr || !view_ok(*dq, B, H, NQ) || !view_ok(*dk, B, g.HK, NK)) return STREAMKL_INVALID_ARG;
+  const int sms = num_sms();
+  const BwdPlan f = bwd_plan(*p1, *p2, *vis, *sel, B, H, NQ, NK, mode, sms, workspace);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < f.bytes) return STREAMKL_INVALID_ARG;
+  if ((s = check_device()) != STREAMKL_OK) return s;
+  SelMaps m{};
+  if (!key_maps(&m, *p1, *p2, B, NK, sel->block)) return STREAMKL_CUDA_ERROR;
+  SelBwdArgs a{};
+  a.status = status_word();
+  if (!a.status) return STREAMKL_CUDA_ERROR;
+  a.p = f.g.p;
+  a.r1 = rows_of(p1->q, B, H, NQ, p1->d);
+  a.r2 = rows_of(p2->q, B, H, NQ, p2->d);
+  a.u1 = f.g.u1;
+  a.u2 = f.g.u2;
+  a.scale1 = float(p1->scale);
+  a.scale2 = float(p2->scale);
+  a.vis = vis_args(*vis, f.prep);
+  a.kl = kl;
+  a.lse1 = lse1;
+  a.lse2 = lse2;
+  a.dkl = dkl;
+  a.dg = g.d;
+  a.pitch = f.pitch;
+  a.dq32 = f.dq32;
+  a.dk_part = f.dk_part;
+  a.kmax = f.kmax;
+  a.dk = dk->data;
+  a.dk_sb = B > 1 ? dk->stride_b : 0;
+  a.dk_sh = g.HK > 1 ? dk->stride_h : 0;
+  a.dk_sn = NK > 1 ? dk->stride_n : 0;
+  a.HK = g.HK;
+  if (launch_mod_prep(f.prep, cs) != 0 || launch_sel_plan(a.p, cs) != 0) return STREAMKL_CUDA_ERROR;
+  if (launch_kmax_strided(g.k.data, B, g.HK, NK, g.d, B > 1 ? g.k.stride_b : 0, g.HK > 1 ? g.k.stride_h : 0,
+                          NK > 1 ? g.k.stride_n : 0, f.prep.ids_k, f.kmax, cs) != 0)
+    return STREAMKL_CUDA_ERROR;
+  if (launch_sel_bwd(m, tile_width(p1->d), tile_width(p2->d), mode, a, sms, cs) != 0 || launch_sel_dk(a, cs) != 0)
+    return STREAMKL_CUDA_ERROR;
+  ModFinishArgs fin{};
+  fin.rows[0] = {f.dq32, B * H, H, NQ, g.d, f.pitch, static_cast<__nv_bfloat16*>(dq->data), B > 1 ? dq->stride_b : 0,
+                 H > 1 ? dq->stride_h : 0, NQ > 1 ? dq->stride_n : 0};
+  return as_status(launch_mod_finish(fin, cs));
 }
 
 }  // extern "C"

@@ -1,0 +1,503 @@
+// Backward over selected blocks (sel_common.cuh): both distributions rebuilt
+// per (tile of gathered rows, block) from the forward's LSEs,
+//   mode P2:  dS = s2 dKL (P2 - P1),   mode P1:  dS = s1 dKL P1 (ln(P1 / P2) - KL),
+//   dQ = dS K,  dK = dS^T Q.
+//
+// Persistent CTAs walk the items.  dK of an item's block accumulates in TMEM
+// and leaves as one fp32 tile an item, which sel_dk_kernel adds in item order.
+// A row of dQ gets a contribution from each of its blocks, out of different
+// CTAs: fp32 reduce-adds of whole rows, each value rounded to its row's grid
+// first (dq_fixed_exp), so that the sums are exact in any order and the result
+// is bitwise repeatable.  19 warps:
+//   warps 0-7   dS (thread = row; a warpgroup takes half of the columns)
+//   warps 8-11  dQ: TMEM -> registers -> a row a thread in shared memory ->
+//               bulk reduce-add; after an item, dK
+//   warps 12-15 gather 32 rows each of both sides, and the rows' parameters
+//   warp 16     S1, S2      warp 17     dK, dQ      warp 18     K by TMA
+// TMEM: S1 [0, 128), S2 [128, 256), dK [256, 384), dQ [384, 512).
+//
+// Bound by the reduce-adds: a row and block bring 4 dg bytes to L2, which takes
+// some 6 TB/s of them (measured alone: rows of 512 bytes over 16 to 64 MB,
+// 5.4 TB/s in pieces of 256 bytes, 2.8 of 128; vector reductions out of
+// registers, coalesced, 6.0), where the rows read take 14.
+#include "sel_common.cuh"
+
+namespace skl {
+
+namespace {
+
+template <int D1, int D2>
+struct SelBwdLayout {
+  static constexpr int kDsWarps = 8, kEpiWarp = 8, kGatherWarp = 12, kGatherWarps = 4;
+  static constexpr int kSWarp = 16, kGradWarp = 17, kLoadWarp = 18;
+  static constexpr int kThreads = 32 * 19;
+  static constexpr int kMaxRing = 8;   // slots of gathered tiles
+  static constexpr int kRows = 6;      // tiles whose rows' parameters are kept
+  enum {
+    kKFull = 0, kKEmpty = 2, kReady = 4, kQFull = 6, kQEmpty = kQFull + kMaxRing, kSFull = kQEmpty + kMaxRing, kSFree,
+    kDsFull, kDsEmpty, kDqFull, kDqEmpty, kDkFull, kDkEmpty, kDone, kNumBars
+  };
+  static constexpr uint32_t kSlot = kTile * 2u * (D1 > D2 ? D1 : D2);
+  static constexpr uint32_t kParams = kRows * kTile * 20u;
+  // operands, dS (64-key blocks of 128 rows), staged rows of dQ (padded by 16 bytes), parameters, barriers
+  static uint32_t bytes(int slots, int k_bufs, int piece, int bs) {
+    return 1024u + slots * kSlot + uint32_t(k_bufs * bs) * (D1 + D2) * 2u + ds_bytes(bs) + stage_bytes(piece) + kParams +
+           kNumBars * 8 + 16;
+  }
+  __host__ __device__ static uint32_t ds_bytes(int bs) { return bs == 128 ? 32768u : 16384u; }
+  __host__ __device__ static uint32_t stage_bytes(int piece) { return kTile * (piece * 4u + 16u); }
+  static constexpr uint32_t kMost = 232448;
+};
+
+// Row bytes of shared memory into dQ: reduce-add of `bytes`, tracked by the thread's bulk groups.
+__device__ __forceinline__ void bulk_reduce_add(float* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
+
+template <int D1, int D2, int MODE>
+__global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
+    sel_bwd_kernel(const __grid_constant__ CUtensorMap tk1, const __grid_constant__ CUtensorMap tk2,
+                   const __grid_constant__ SelBwdArgs a) {
+  using L = SelBwdLayout<D1, D2>;
+  constexpr bool kP2 = MODE == STREAMKL_GRAD_P2;
+  constexpr int DG = kP2 ? D2 : D1, DO = kP2 ? D1 : D2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bs = a.p.bs;
+  const uint32_t kK1 = uint32_t(bs) * D1 * 2, kK = uint32_t(bs) * (D1 + D2) * 2;
+  const uint32_t oDS = a.k_bufs * kK, oQ = oDS + L::ds_bytes(bs), oStage = oQ + a.slots * L::kSlot;
+  const uint32_t oParam = oStage + L::stage_bytes(a.piece), oBar = oParam + L::kParams;
+  auto bar = [&](int id) { return sb + oBar + 8u * id; };
+  float4* params = reinterpret_cast<float4*>(smem + oParam);                          // na, nb, ws, grid
+  int* row_of = reinterpret_cast<int*>(smem + oParam + L::kRows * kTile * 16);        // row of dq32, or -1
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + oBar + L::kNumBars * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + oBar + L::kNumBars * 8 + 4);
+  const Ctl ctl{abort_flag, a.status};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      int count = 1;
+      if (i >= L::kQFull && i < L::kQEmpty) count = L::kGatherWarps;
+      if (i == L::kReady || i == L::kReady + 1 || i == L::kSFree || i == L::kDsFull) count = L::kDsWarps;
+      if (i == L::kDqEmpty || i == L::kDkEmpty) count = 4;
+      if (i == L::kDone) count = 2;
+      mbar_init(bar(i), count);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == L::kGradWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  // columns past the head dim (K's are zeros, and no product may meet a NaN there)
+  if (a.r1.chunks < D1 / 8 || a.r2.chunks < D2 / 8)
+    for (uint32_t o = threadIdx.x * 16; o < a.slots * L::kSlot; o += L::kThreads * 16) st_shared_v4(sb + oQ + o, 0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t t_s1 = tmem, t_s2 = tmem + 128, t_dk = tmem + 256, t_dq = tmem + 384;
+  const int per_tile = a.p.queries_per_tile, G = a.p.G;
+  const int works = min(*a.p.item_count, a.p.max_items) * (a.p.HU / a.p.HS);
+  const bool ids = a.vis.ids_q != nullptr;
+
+  if (warp >= L::kGatherWarp && warp < L::kGatherWarp + L::kGatherWarps) {
+    // ---------------------------------------------------------------- gather: rows [first, first + 32)
+    const int first = (warp - L::kGatherWarp) * 32;
+    const int r = first + lane, ql = r / G, hl = r - ql * G;
+    const SelRows& ro = kP2 ? a.r1 : a.r2;
+    const SelRows& rg = kP2 ? a.r2 : a.r1;
+    const float sg = kP2 ? a.scale2 : a.scale1;
+    const int ug = kP2 ? a.u2 : a.u1;
+    auto landed = [&](int m) {  // a slot's copies have landed: the tensor core may read them
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kQFull + m % a.slots));
+    };
+    int m = 0, n = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < works; w += gridDim.x) {
+      const SelWork k = sel_work(a.p, w);
+      const float kmax = __uint_as_float(a.kmax[k.b * a.HK + (k.head0 / G) / ug] << 16);
+      for (int e0 = 0; ok && e0 < k.count; e0 += per_tile, ++n) {
+        const int e = e0 + ql;
+        bool on = ql < per_tile && e < k.count;
+        const int i = on ? int(__ldg(a.p.entries + k.first + e) >> kSlotBits) : 0, h = k.head0 + hl;
+        const size_t row = size_t(k.b * a.p.H + h) * a.p.NQ + i;
+        // na, nb, ws as in ds_chunk_row.  Rows that saw nothing (they may hold
+        // anything) and rows past the last are zeros, and contribute zeros.
+        float4 par{-INFINITY, kP2 ? -INFINITY : 0.f, 0.f, 0.f};
+        if (on && SKL_CHECK(a.status, i < a.p.NQ && h < a.p.H && k.b < a.p.B)) {
+          const float l1 = a.lse1[row], l2 = a.lse2[row], kl = a.kl[row], dkl = a.dkl[row];
+          on = l1 != -INFINITY;
+          if (on) {
+            par.x = -l1 * kLog2e;
+            par.y = kP2 ? -l2 * kLog2e : -(l1 - l2 + kl);
+            par.z = sg * dkl;
+            par.w = 1.5f * exp2_int(23 - dq_fixed_exp(MODE, sg, dkl, kl, kmax));
+          }
+        }
+        const unsigned long long po = on ? reinterpret_cast<unsigned long long>(ro.at(k.b, h, i)) : 0ull;
+        const unsigned long long pg = on ? reinterpret_cast<unsigned long long>(rg.at(k.b, h, i)) : 0ull;
+#pragma unroll
+        for (int side = 0; side < 2; ++side, ++m) {
+          const int s = m % a.slots;
+          ok = mbar_wait_warp(bar(L::kQEmpty + s), ((m / a.slots) & 1) ^ 1, ctl);
+          if (!ok) break;
+          if (side == 0) {
+            // (the tile whose parameters these replace has been through dQ: kRows tiles cannot be under way)
+            params[(n % L::kRows) * kTile + r] = par;
+            row_of[(n % L::kRows) * kTile + r] = on ? int(row) : -1;
+            gather_rows<DO, 32, true>(sb + oQ + s * L::kSlot, first, po, 0, ro.chunks);
+          } else {
+            gather_rows<DG, 32, true>(sb + oQ + s * L::kSlot, first, pg, 0, rg.chunks);
+          }
+          cp_async_commit();
+          if (m >= 1) {
+            cp_async_wait<1>();
+            landed(m - 1);
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+    if (ok && m > 0) landed(m - 1);
+  } else if (warp == L::kLoadWarp) {
+    // ---------------------------------------------------------------- K
+    if (lane == 0) {
+      int items = 0;
+      for (int w = blockIdx.x; w < works; w += gridDim.x, ++items) {
+        const SelWork k = sel_work(a.p, w);
+        const int kb = items % a.k_bufs, hu = k.head0 / G;
+        if (!mbar_wait_polled(bar(L::kKEmpty + kb), ((items / a.k_bufs) & 1) ^ 1, ctl)) break;
+        const uint32_t full = bar(L::kKFull + kb);
+        mbar_arrive_expect_tx(full, kK);
+#pragma unroll
+        for (int c = 0; c < D1 / 64; ++c)
+          tma_load_4d(sb + kb * kK + c * (bs * 128), &tk1, full, c * 64, k.block * bs, hu / a.u1, k.b);
+#pragma unroll
+        for (int c = 0; c < D2 / 64; ++c)
+          tma_load_4d(sb + kb * kK + kK1 + c * (bs * 128), &tk2, full, c * 64, k.block * bs, hu / a.u2, k.b);
+      }
+      if (*abort_flag)  // let the copies already started land before the CTA exits
+        for (int j = items > a.k_bufs ? items - a.k_bufs : 0; j < items; ++j)
+          mbar_drain(bar(L::kKFull + j % a.k_bufs), (j / a.k_bufs) & 1, 200000000ull);
+    }
+  } else if (warp == L::kSWarp) {
+    // ---------------------------------------------------------------- S issuer
+    const uint32_t leader = elect_one();
+    const uint32_t idesc = idesc_bf16(128, bs, 0, 0);
+    auto product = [&](auto width, uint32_t d, uint32_t q, uint32_t ks) {
+      constexpr int D = decltype(width)::value;
+      const uint64_t qd = sdesc_sw128(q, 16, 1024), kd = sdesc_sw128(ks, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_bf16_ss(leader, d, sdesc_add(qd, step_off(kk, kTile)), sdesc_add(kd, step_off(kk, bs)), idesc, kk > 0);
+    };
+    int m = 0, n = 0, items = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
+      const int count = sel_work(a.p, w).count;
+      const int kb = items % a.k_bufs;
+      const uint32_t k1s = sb + kb * kK, k2s = k1s + kK1;
+      ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (items / a.k_bufs) & 1, ctl);
+      for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
+        int s = m % a.slots;
+        ok = mbar_wait_warp(bar(L::kSFree), (n & 1) ^ 1, ctl) && mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        // the other side first: its slot is released as early as possible
+        product(std::integral_constant<int, DO>{}, kP2 ? t_s1 : t_s2, sb + oQ + s * L::kSlot, kP2 ? k1s : k2s);
+        mma_commit(leader, bar(L::kQEmpty + s));
+        ++m;
+        s = m % a.slots;
+        ok = mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        product(std::integral_constant<int, DG>{}, kP2 ? t_s2 : t_s1, sb + oQ + s * L::kSlot, kP2 ? k2s : k1s);
+        ++m;  // (released by dK)
+        mma_commit(leader, bar(L::kSFull));
+      }
+    }
+    mma_commit(leader, bar(L::kDone));
+  } else if (warp == L::kGradWarp) {
+    // ---------------------------------------------------------------- dK and dQ issuer
+    const uint32_t leader = elect_one();
+    constexpr uint32_t id_dk = idesc_bf16(128, DG, 1, 1);  // A = dS^T M-major, B = Q_g N-major
+    constexpr uint32_t id_dq = idesc_bf16(128, DG, 0, 1);  // A = dS K-major,   B = K_g N-major
+    // (dS^T has 128 rows whatever the block: those past it multiply what lies
+    // behind dS, into rows of dK that nobody reads)
+    const uint64_t dsm = sdesc_sw128(sb + oDS, kTile * 128, 1024), dsk = sdesc_sw128(sb + oDS, 16, 1024);
+    int n = 0, items = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
+      const int count = sel_work(a.p, w).count;
+      const int kb = items % a.k_bufs;
+      const uint64_t kgn = sdesc_sw128(sb + kb * kK + (kP2 ? kK1 : 0u), uint32_t(bs) * 128, 1024);
+      ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (items / a.k_bufs) & 1, ctl) &&
+           mbar_wait_warp(bar(L::kDkEmpty), (items & 1) ^ 1, ctl);
+      bool first = true;
+      for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
+        const int s = (2 * n + 1) % a.slots;
+        ok = mbar_wait_warp(bar(L::kDsFull), n & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t qgn = sdesc_sw128(sb + oQ + s * L::kSlot, kTile * 128, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_bf16_ss(leader, t_dk, sdesc_add(dsm, kk * 2048), sdesc_add(qgn, kk * 2048), id_dk, !first || kk > 0);
+        first = false;
+        mma_commit(leader, bar(L::kQEmpty + s));
+        ok = mbar_wait_warp(bar(L::kDqEmpty), (n & 1) ^ 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        for (int kk = 0; kk < bs / 16; ++kk)
+          mma_bf16_ss(leader, t_dq, sdesc_add(dsk, step_off(kk, kTile)), sdesc_add(kgn, kk * 2048), id_dq, kk > 0);
+        mma_commit(leader, bar(L::kDsEmpty));
+        mma_commit(leader, bar(L::kDqFull));
+      }
+      if (ok) {
+        mma_commit(leader, bar(L::kDkFull));
+        mma_commit(leader, bar(L::kKEmpty + kb));
+      }
+    }
+    mma_commit(leader, bar(L::kDone));
+    mbar_drain(bar(L::kDone), 0, 1000000000ull);  // every MMA has finished before TMEM is released
+  } else if (warp < L::kDsWarps) {
+    // ---------------------------------------------------------------- dS (thread = row)
+    const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int hl = row % G;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const float c1 = a.scale1 * kLog2e, c2 = a.scale2 * kLog2e, nr = -a.scale2 / a.scale1;
+    const uint64_t C1 = f2(c1, c1), C2 = f2(c2, c2), S1 = f2(a.scale1, a.scale1), NR = f2(nr, nr);
+    const int half = (bs + 32) / 64 * 32;                        // columns of warpgroup 0
+    const int col0 = wg == 0 ? 0 : half, col1 = wg == 0 ? half : bs;
+    const int nqt = (a.p.NQ + kTile - 1) / kTile, nkt = (a.p.NK + kTile - 1) / kTile, off = a.p.NK - a.p.NQ;
+    int n = 0, items = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
+      const SelWork k = sel_work(a.p, w);
+      const int k0 = k.block * bs;
+      const int prefix = a.p.prefix != nullptr ? min(max(a.p.prefix[k.b], 0), a.p.NK) : 0;
+      const int* kids = ids ? a.vis.ids_k + size_t(k.b) * nkt * kTile + k0 : nullptr;
+      if (ids) {
+        // keys that match nothing may hold anything: zeros before a product reads them
+        const int kb = items % a.k_bufs;
+        ok = mbar_wait_warp(bar(L::kKFull + kb), (items / a.k_bufs) & 1, ctl);
+        if (!ok) break;
+        if (row < bs && kids[row] < 0) {
+          const uint32_t base = sb + kb * kK + (wg == 0 ? 0u : kK1) + row * 128;
+          for (int c = 0; c < (wg == 0 ? D1 : D2) / 64; ++c)
+#pragma unroll
+            for (int o = 0; o < 128; o += 16) st_shared_v4(base + c * (bs * 128) + o, 0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kReady + kb));
+      }
+      const int row0 = (k.b * a.p.H + k.head0 + hl) * a.p.NQ;  // of query 0
+      for (int e0 = 0; ok && e0 < k.count; e0 += per_tile, ++n) {
+        ok = mbar_wait_warp(bar(L::kSFull), n & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        const float4 par = params[(n % L::kRows) * kTile + row];
+        const int of = row_of[(n % L::kRows) * kTile + row];
+        const int i = of < 0 ? 0 : of - row0;
+        const uint64_t NA = f2(par.x, par.x), NB = f2(par.y, par.y), WW = f2(par.z, par.z);
+        const int last = a.p.causal ? min(max(i + off + 1, prefix), a.p.NK) : a.p.NK;
+        const bool whole = kids == nullptr && __all_sync(0xffffffffu, of < 0 || last >= k0 + bs);
+        const int id = kids != nullptr ? a.vis.ids_q[size_t(k.b) * nqt * kTile + i] : 0;
+        bool waited = false;
+#pragma unroll 1
+        for (int c = col0; c < col1; c += 32) {
+          uint32_t x1[32], x2[32], out[16];
+          tmem_ld2x32(t_s1 + lane_off + c, t_s2 + lane_off + c, x1, x2);
+          if (c + 32 >= col1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kSFree));
+          }
+          ds_chunk_row<MODE, false>(x1, x2, C1, C2, S1, NR, NA, NB, WW, 0, out);
+          if (!whole) {
+            const uint32_t on = visible_bits<32>(i, k0 + c, off, a.p.NK, a.p.causal, prefix, id, kids == nullptr ? nullptr : kids + c);
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              out[x] &= ((on >> (2 * x)) & 1u ? 0xffffu : 0u) | ((on >> (2 * x + 1)) & 1u ? 0xffff0000u : 0u);
+          }
+          if (!waited) {  // the previous tile's products must be done reading dS
+            ok = mbar_wait_warp(bar(L::kDsEmpty), (n & 1) ^ 1, ctl);
+            if (!ok) break;
+            waited = true;
+          }
+          store_cols32_sw128(sb + oDS, row, c, out);
+        }
+        if (!ok) break;
+        if (col0 == col1) {  // blocks of 32: nothing for this warpgroup, which may not run ahead of the other
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kSFree));
+          ok = mbar_wait_warp(bar(L::kDsEmpty), (n & 1) ^ 1, ctl);
+          if (!ok) break;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kDsFull));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- dQ, and dK after an item
+    const int w4 = warp - L::kEpiWarp, row = w4 * 32 + lane;
+    const uint32_t lane_off = uint32_t(w4 * 32) << 16;
+    const int piece = a.piece;
+    const uint32_t stage = sb + oStage + row * (piece * 4u + 16u);  // this thread's
+    int n = 0, items = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
+      const int count = sel_work(a.p, w).count;
+      for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
+        ok = mbar_wait_warp(bar(L::kDqFull), n & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        const float me = params[(n % L::kRows) * kTile + row].w;
+        const int of = row_of[(n % L::kRows) * kTile + row];
+        const uint64_t ME = f2(me, me);
+        float* dst = a.dq32 + size_t(of < 0 ? 0 : of) * a.pitch;
+#pragma unroll 1
+        for (int c = 0; c < DG; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(t_dq + lane_off + c, v);
+          if (c + 32 == DG) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kDqEmpty));
+          }
+          const int in = c % piece;
+          if (in == 0) bulk_wait_read_le<0>();  // what was staged here has been read
+          // on the row's grid of 2^-e: (x + 1.5 2^(23 - e)) - 1.5 2^(23 - e)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float q0, q1, q2, q3;
+            f2_split(f2_sub(f2_add(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), ME), ME), q0, q1);
+            f2_split(f2_sub(f2_add(f2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), ME), ME), q2, q3);
+            st_shared_v4(stage + (in + j) * 4, __float_as_uint(q0), __float_as_uint(q1), __float_as_uint(q2),
+                         __float_as_uint(q3));
+          }
+          const int from = c - in, to = min(c + 32, a.dg);  // the piece's columns so far
+          if (of >= 0 && (in + 32 == piece || c + 32 >= a.dg) && from < a.dg && c < a.dg) {
+            fence_proxy_async_smem();
+            bulk_reduce_add(dst + from, stage, uint32_t(to - from) * 4u);
+            bulk_commit();
+          }
+        }
+      }
+      if (!ok) break;
+      // dK of the item, [bs][dg]
+      ok = mbar_wait_warp(bar(L::kDkFull), items & 1, ctl);
+      if (!ok) break;
+      tc_fence_after();
+      if (w4 * 32 < bs) {
+        float* dst = a.dk_part + (size_t(w) * bs + row) * a.dg;
+#pragma unroll 1
+        for (int c = 0; c < DG; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(t_dk + lane_off + c, v);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            if (c + j < a.dg)
+              __stcs(reinterpret_cast<float4*>(dst + c + j),
+                     make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
+                                 __uint_as_float(v[j + 3])));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kDkEmpty));
+    }
+    bulk_wait_all();  // every reduce has landed before the CTA exits
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == L::kGradWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr int kDkThreads = 256;
+
+// dK of one key head and block: the items' tiles added in order (units of the
+// key head, then a unit's items), rounded to bf16 once.  Four values a thread.
+__global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constant__ SelBwdArgs a) {
+  const int j = blockIdx.x, hk = blockIdx.y % a.HK, b = blockIdx.y / a.HK;
+  const int units = a.p.HU / a.HK, per = a.p.HU / a.p.HS;
+  const int bs = a.p.bs, quads = a.dg / 4, rows = min(bs, a.p.NK - j * bs);
+  for (int x = threadIdx.x; x < rows * quads; x += kDkThreads) {
+    const int key = x / quads, c = (x - key * quads) * 4;
+    float4 sum{0.f, 0.f, 0.f, 0.f};
+    for (int u = hk * units; u < (hk + 1) * units; ++u) {
+      const int sel = b * a.p.HS + u / per, sub = u % per;
+      const int2 r = a.p.ranges[size_t(sel) * a.p.blocks + j];
+      for (int it = r.x; it < r.x + r.y; ++it) {
+        const size_t w = size_t(it) * per + sub;
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(a.dk_part + (w * bs + key) * a.dg + c));
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+      }
+    }
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dk) + b * a.dk_sb + hk * a.dk_sh + (j * bs + key) * a.dk_sn + c;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+  }
+}
+
+template <int D1, int D2, int MODE>
+int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, int sms, cudaStream_t st) {
+  using L = SelBwdLayout<D1, D2>;
+  SelBwdArgs a = args;
+  const int bs = a.p.bs;
+  // Larger pieces of dQ rows first (the reduce-adds bound the kernel), then
+  // two more slots than one tile takes, then a second K, then more slots.
+  auto fits = [&](int slots, int bufs, int piece) { return L::bytes(slots, bufs, piece, bs) <= L::kMost; };
+  constexpr int DG = MODE == STREAMKL_GRAD_P2 ? D2 : D1;
+  a.k_bufs = 1;
+  a.piece = DG == 128 && fits(4, 1, 128) ? 128 : (fits(4, 1, 64) ? 64 : 32);
+  a.slots = fits(4, 1, a.piece) ? 4 : 3;
+  if (fits(a.slots, 2, a.piece)) a.k_bufs = 2;
+  while (a.slots < 6 && fits(a.slots + 1, a.k_bufs, a.piece)) ++a.slots;
+  if (!fits(a.slots, a.k_bufs, a.piece)) return cudaErrorInvalidValue;
+  auto kern = sel_bwd_kernel<D1, D2, MODE>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kMost);
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)a.p.max_items * (a.p.HU / a.p.HS);
+  const int grid = int(most < sms ? most : sms);
+  kern<<<grid, L::kThreads, L::bytes(a.slots, a.k_bufs, a.piece, bs), st>>>(m.k1, m.k2, a);
+  return cudaGetLastError();
+}
+
+template <int D1, int D2>
+int launch_sel_bwd_m(const SelMaps& m, int mode, const SelBwdArgs& a, int sms, cudaStream_t st) {
+  return mode == STREAMKL_GRAD_P2 ? launch_sel_bwd_t<D1, D2, STREAMKL_GRAD_P2>(m, a, sms, st)
+                                  : launch_sel_bwd_t<D1, D2, STREAMKL_GRAD_P1>(m, a, sms, st);
+}
+
+}  // namespace
+
+int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs& a, int sms, cudaStream_t st) {
+  if (d1 == 64)
+    return d2 == 64 ? launch_sel_bwd_m<64, 64>(m, mode, a, sms, st) : launch_sel_bwd_m<64, 128>(m, mode, a, sms, st);
+  return d2 == 64 ? launch_sel_bwd_m<128, 64>(m, mode, a, sms, st) : launch_sel_bwd_m<128, 128>(m, mode, a, sms, st);
+}
+
+int launch_sel_dk(const SelBwdArgs& a, cudaStream_t st) {
+  sel_dk_kernel<<<dim3(unsigned(a.p.blocks), unsigned(a.p.B * a.HK)), kDkThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace skl

@@ -14,6 +14,7 @@
 // in which blocks of a launch run but the items' places in their table.
 #pragma once
 
+#include "bwd_common.cuh"
 #include "kernels.cuh"
 #include "mod_common.cuh"
 #include "ptx.cuh"
@@ -50,6 +51,7 @@ struct SelPlan {
   int words;             // (T + 31) / 32
   SelItem* items;
   int* item_count;       // device
+  int2* ranges;          // [B HS][blocks]: a block's first item and their number, or null
   int max_items;
 };
 
@@ -89,23 +91,27 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Copies 16 rows (lane l mod 16 holds the address of row l; null: not copied)
-// into rows [first, first + 16) of a [128][D] operand tile, 16 bytes a lane,
-// swizzled as TMA would.  Called by a whole warp; lanes from `half` on hold
-// the addresses that count.
-template <int D>
-__device__ __forceinline__ void gather_rows(uint32_t tile, int first, unsigned long long mine, int half, int chunks) {
+// Step kk of 16 along d of a K-major operand of `rows` rows.
+__device__ __forceinline__ uint32_t step_off(int kk, int rows) { return (kk >> 2) * (rows * 128) + (kk & 3) * 32; }
+
+// Copies ROWS rows, at most 32 (lane `from` + r holds the address of row r;
+// null: not copied, or with ZERO zeros), into rows [first, first + ROWS) of a
+// [128][D] operand tile, 16 bytes a lane, swizzled as TMA would.  Called by a
+// whole warp.
+template <int D, int ROWS, bool ZERO>
+__device__ __forceinline__ void gather_rows(uint32_t tile, int first, unsigned long long mine, int from, int chunks) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at a time
   const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
   const uint32_t dst = tile + (c >> 3) * (kTile * 128) + first * 128;
   const bool in = c < chunks;
   const uint32_t off = c * 16;
 #pragma unroll
-  for (int r0 = 0; r0 < 16; r0 += kAtOnce) {
+  for (int r0 = 0; r0 < ROWS; r0 += kAtOnce) {
     const int r = r0 + sub;
-    const unsigned long long p = __shfl_sync(0xffffffffu, mine, half + r);
-    if (p != 0 && in)
-      cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), reinterpret_cast<const uint8_t*>(p + off));
+    const unsigned long long p = __shfl_sync(0xffffffffu, mine, from + r);
+    const uint32_t to = dst + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    if (p != 0 && in) cp_async16(to, reinterpret_cast<const uint8_t*>(p + off));
+    else if (ZERO && in) st_shared_v4(to, 0u, 0u, 0u, 0u);
   }
 }
 
@@ -128,6 +134,29 @@ struct SelFwdArgs {
   int slots, k_bufs;
 };
 
+struct SelBwdArgs {
+  SelPlan p;
+  SelRows r1, r2;
+  int u1, u2;
+  float scale1, scale2;
+  ModVis vis;
+  const float* kl;
+  const float* lse1;
+  const float* lse2;
+  const float* dkl;
+  int dg, pitch;          // head dim of the gradient side; row length of dq32
+  float* dq32;            // [B H NQ][pitch], zeroed: dQ contributions, on their rows' grids
+  float* dk_part;         // [works][bs][dg]: dK of an item
+  const unsigned* kmax;   // per key head of the gradient side (launch_kmax_strided)
+  void* dk;               // bf16 [B][HK][NK][dg]
+  long long dk_sb, dk_sh, dk_sn;
+  int HK;                 // of the gradient side
+  int* status;
+  int slots, k_bufs, piece;
+};
+
+int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs& a, int sms, cudaStream_t st);
+int launch_sel_dk(const SelBwdArgs& a, cudaStream_t st);
 int launch_sel_plan(const SelPlan& p, cudaStream_t st);
 int launch_sel_fwd(const SelMaps& m, int d1, int d2, const SelFwdArgs& a, int sms, cudaStream_t st);
 int launch_sel_merge(const SelFwdArgs& a, cudaStream_t st);

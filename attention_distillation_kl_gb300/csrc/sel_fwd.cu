@@ -16,7 +16,6 @@
 // The merge adds the parts of a row's slots in their order (as merge_stats of
 // the dense forward does for splits), so results do not depend on which CTA
 // took which item.
-#include "bwd_common.cuh"
 #include "fwd_mod.cuh"
 #include "sel_common.cuh"
 
@@ -42,9 +41,6 @@ struct SelFwdLayout {
     return 1024u + slots * slot_bytes(d1, d2) + uint32_t(d1 + d2) * 2u * uint32_t(k_bufs * bs) + kTail;
   }
 };
-
-// Products of a K-major operand of `rows` rows, step kk of 16 along d.
-__device__ __forceinline__ uint32_t step_off(int kk, int rows) { return (kk >> 2) * (rows * 128) + (kk & 3) * 32; }
 
 // One row's sums over its block: n visible of the bs columns at ts, ts + bs.
 template <bool MASK>
@@ -161,8 +157,8 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
           const int s = m % a.slots;
           ok = mbar_wait_warp(bar(L::kQEmpty + s), ((m / a.slots) & 1) ^ 1, ctl);
           if (!ok) break;
-          if (side == 0) gather_rows<D1>(sb + oQ + s * kSlot, first, at, 0, a.r1.chunks);
-          else gather_rows<D2>(sb + oQ + s * kSlot, first, at, 16, a.r2.chunks);
+          if (side == 0) gather_rows<D1, 16, false>(sb + oQ + s * kSlot, first, at, 0, a.r1.chunks);
+          else gather_rows<D2, 16, false>(sb + oQ + s * kSlot, first, at, 16, a.r2.chunks);
           cp_async_commit();
           if (m >= L::kLag) {
             cp_async_wait<L::kLag>();

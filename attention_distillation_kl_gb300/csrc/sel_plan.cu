@@ -176,6 +176,8 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(const __grid_con
       counts[size_t(c) * p.blocks + j] = at;
       at += k;
     }
+    if (p.ranges != nullptr)
+      p.ranges[size_t(sel) * p.blocks + j] = make_int2(region + int(item[r]), int((n[r] + per_item - 1) / per_item));
     const unsigned base = unsigned(sel) * unsigned(p.NQ) * p.T + entry[r];
     for (unsigned k = 0; k * per_item < n[r]; ++k) {
       const int place = region + int(item[r] + k);

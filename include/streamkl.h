@@ -432,6 +432,23 @@ int streamkl_fwd_sel(const streamkl_side* p1, const streamkl_side* p2, const str
                      const streamkl_blocks* sel, int B, int H, int NQ, int NK, void* workspace, size_t workspace_bytes,
                      float* kl, float* lse1, float* lse2, streamkl_stream_t stream);
 
+/*
+ * Backward over selected blocks, from a forward over the same arguments: dq, dk
+ * as streamkl_bwd_mod (bf16, fully overwritten, the same two roundings; no
+ * output may overlap an input or another output).  Keys that nobody selected
+ * get zeros.  Rows with LSE -inf get zeros and contribute none, whatever q and
+ * dkl hold there, and so do keys whose id is negative, whatever k holds; other
+ * keys must hold finite values.  The results are bitwise repeatable: dK is
+ * added in a fixed order, and what a block adds to row i of dq is rounded to
+ * the grid that streamkl_bwd's deterministic mode describes.
+ */
+size_t streamkl_bwd_sel_workspace_bytes(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,
+                                        const streamkl_blocks* sel, int B, int H, int NQ, int NK, int mode);
+int streamkl_bwd_sel(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,
+                     const streamkl_blocks* sel, int B, int H, int NQ, int NK, const float* kl, const float* lse1,
+                     const float* lse2, const float* dkl, int mode, const streamkl_view* dq, const streamkl_view* dk,
+                     void* workspace, size_t workspace_bytes, streamkl_stream_t stream);
+
 /* Static, NUL-terminated description of a status value. */
 const char* streamkl_status_string(int status);
 

@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import attention_distillation_kl_gb300 as skl
+import mod_reference as dense
 import sel_reference as ref
 
 pytestmark = pytest.mark.gpu
@@ -91,6 +92,23 @@ def check_forward(dev, idx, where, p, **kw):
     return got
 
 
+def check_backward(dev, idx, where, p, rows, mode, seed=1, **kw):
+    g = torch.Generator().manual_seed(seed)
+    dkl = (torch.rand(rows[0].shape, generator=g) * 2 - 0.5).cuda()
+    got = skl.streamkl_bwd_sel(*sides(dev), idx, p["bs"], *rows, dkl,
+                               skl.STREAMKL_GRAD_P1 if mode == "1" else skl.STREAMKL_GRAD_P2, **where, **kw)
+    torch.cuda.synchronize()
+    assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
+    want = list(ref.backward(p, *(f64(t) for t in rows), f64(dkl), mode))
+    # every block's contribution to dq is rounded to the row's grid: as grid_error for tiles of 128, with a slot each
+    slots = p["blocks"].shape[3]
+    tiles = -(-p["k1"].shape[2] // 128)
+    want[2] = want[2] + (1 + dense.BF16) * dense.grid_error(p, f64(rows[0]), f64(dkl), mode) * slots / tiles
+    for g_, w, b, what in zip(got, want[:2], want[2:], ("dq", "dk")):
+        within(g_, w, b, f"mode P{mode} {what}")
+    return got, dkl
+
+
 CASES = {
     "one token": dict(H=1, NQ=1, NK=1, T=1),
     "one row": dict(H=4, HK1=1, HK2=1, NQ=1, NK=300, T=4),
@@ -123,6 +141,16 @@ CASES = {
 @pytest.mark.parametrize("name", CASES)
 def test_forward(name):
     check_forward(*problem(**CASES[name]))
+
+
+@pytest.mark.parametrize("mode", ["1", "2"])
+@pytest.mark.parametrize("name", CASES)
+def test_backward(name, mode):
+    dev, idx, where, p = problem(**CASES[name])
+    rows = skl.streamkl_fwd_sel(*sides(dev), idx, p["bs"], **where)
+    got, dkl = check_backward(dev, idx, where, p, rows, mode)
+    again, _ = check_backward(dev, idx, where, p, rows, mode)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
 def test_every_block_is_the_dense_forward():
