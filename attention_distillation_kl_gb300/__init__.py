@@ -24,6 +24,7 @@ __all__ = [
     "streamkl_bwd_workspace_bytes", "streamkl_bwd_gqa_ws",
     "AttnSide", "streamkl_fwd_mod", "streamkl_fwd_mod_workspace_bytes", "streamkl_bwd_mod",
     "streamkl_bwd_mod_workspace_bytes", "Rotary", "streamkl_rotate", "streamkl_pool_blocks",
+    "streamkl_select_blocks", "streamkl_select_blocks_workspace_bytes",
     "streamkl_fwd_sel", "streamkl_fwd_sel_workspace_bytes", "streamkl_bwd_sel", "streamkl_bwd_sel_workspace_bytes",
     "status_string", "STREAMKL_STATIC_WORKSPACE_BYTES",
     "streamkl_get_device_status", "streamkl_probe_ex2", "streamkl_selftest_wait_timeout",
@@ -114,6 +115,8 @@ _SIGS = {
     "streamkl_fwd_sel": (_I, [_SP, _SP, _VISP, _BP, _I, _I, _I, _I, _P, _SZ, _P, _P, _P, _P]),
     "streamkl_bwd_sel_workspace_bytes": (_SZ, [_SP, _SP, _VISP, _BP, _I, _I, _I, _I, _I]),
     "streamkl_bwd_sel": (_I, [_SP, _SP, _VISP, _BP, _I, _I, _I, _I, _P, _P, _P, _P, _I, _VP, _VP, _P, _SZ, _P]),
+    "streamkl_select_blocks_workspace_bytes": (_SZ, [_VISP, *[_I] * 10]),
+    "streamkl_select_blocks": (_I, [_VP, _VP, _VISP, *[_I] * 10, _P, _P, _SZ, _P]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
     "streamkl_get_device_status": (_I, []),
     "streamkl_probe_ex2": (_I, [_P, _I, _I, _P]),
@@ -792,6 +795,51 @@ def streamkl_pool_blocks(k, block, doc_k=None, out=None, stream=None):
     _check(lib().streamkl_pool_blocks(_view(k), None if doc_k is None else doc_k.data_ptr(), B, HK, NK, d, block,
                                       _view(y), _mod_stream(stream, k.device)), "streamkl_pool_blocks")
     return y
+
+
+def _visible(B, NQ, NK, device, causal, prefix, doc_q, doc_k):
+    """streamkl_visible of a call, its shapes and devices checked."""
+    for name, t, shape in (("prefix", prefix, (B,)), ("doc_q", doc_q, (B, NQ)), ("doc_k", doc_k, (B, NK))):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or
+                              not t.is_contiguous() or tuple(t.shape) != shape):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+    return _Visible(1 if causal else 0, *(None if t is None else t.data_ptr() for t in (prefix, doc_q, doc_k)))
+
+
+def streamkl_select_blocks_workspace_bytes(B, H, heads, NQ, NK, d, block, count, causal=False, ids=False, sink=1, local=1):
+    """Workspace bytes streamkl_select_blocks needs (ids: whether doc_q, doc_k are given)."""
+    vis = _Visible(1 if causal else 0, None, 16 if ids else None, 16 if ids else None)  # (which are null is all it asks)
+    return int(lib().streamkl_select_blocks_workspace_bytes(vis, B, H, heads, NQ, NK, d, block, count, sink, local))
+
+
+@_at_device
+def streamkl_select_blocks(q, kb, count, block, NK, causal=False, prefix=None, doc_q=None, doc_k=None, sink=1, local=1,
+                           out=None, workspace=None, stream=None):
+    """The `count` blocks of `block` keys that score best for each query, int32
+    [B, heads, NQ, count], ascending, -1 behind them: kb [B, heads,
+    ceil(NK / block), d] holds a key for each block (streamkl_pool_blocks),
+    and a block's score is the sum of q_h . kb over the H // heads query heads
+    that share a head of kb.  Candidates hold a key that causal, prefix, doc_q
+    and doc_k leave visible; the first `sink` and last `local` of them are
+    always taken.  Ties go to the lowest block."""
+    _strided(q, "q")
+    _strided(kb, "kb")
+    B, H, NQ, d = q.shape
+    heads, dev, c = kb.shape[1], q.device, lib()
+    count, block, NK = int(count), int(block), int(NK)
+    if kb.device != dev or kb.shape[0] != B or kb.shape[3] != d or block < 1 or kb.shape[2] != -(-NK // block):
+        raise ValueError(f"kb must be [{B}, heads, {-(-NK // max(block, 1))}, {d}] on {dev}")
+    vis = _visible(B, NQ, NK, dev, causal, prefix, doc_q, doc_k)
+    if stream is not None:
+        _check_stream(stream, dev)
+    need = c.streamkl_select_blocks_workspace_bytes(vis, B, H, heads, NQ, NK, d, block, count, int(sink), int(local))
+    ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
+    sel = _like_new((B, heads, NQ, max(count, 1)), dev, stream, out, "out", torch.int32)
+    if not sel.is_contiguous():
+        raise ValueError("out must be contiguous")
+    _check(c.streamkl_select_blocks(_view(q), _view(kb), vis, B, H, heads, NQ, NK, d, block, count, int(sink), int(local),
+                                    sel.data_ptr(), ws, ws_bytes, _mod_stream(stream, dev)), "streamkl_select_blocks")
+    return sel
 
 
 def _sel_call(blocks, block, p1):

@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libstreamkl.so")
 DEBUG_LIB = os.path.join(PKG, "libstreamkl_debug.so")
 SOURCES = ["api.cu", "fwd.cu", "fwd_wide.cu", "bwd.cu", "dq_fixed.cu", "bwd_wide_p0.cu", "bwd_wide_p1.cu", "bwd_both.cu",
            "static_ws.cu", "api_mod.cu", "mod_aux.cu", "fwd_mod_64.cu", "fwd_mod_128.cu", "bwd_mod_p2.cu", "bwd_mod_p1.cu",
-           "rotary.cu", "pool.cu", "api_sel.cu", "sel_plan.cu", "sel_fwd.cu", "sel_bwd.cu"]
+           "rotary.cu", "pool.cu", "api_sel.cu", "sel_plan.cu", "sel_fwd.cu", "sel_bwd.cu", "select.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,610 @@
+// The blocks that score best for each query (see streamkl_select_blocks):
+//   score(i, hs, j) = sum over the query heads h of hs of q_h(i) . kb_hs(j).
+//
+// Three steps: norms of the blocks' keys and their id ranges; scores of 128
+// queries x 256 blocks by the tensor core, the heads' products added up in
+// TMEM; then a warp a query finds the count-th best score by bisection and
+// writes the blocks in ascending order.  Queries are taken in strips whose
+// scores stay in L2.
+//
+// The list has to be that of the exact scores, ties to the lowest block, while
+// the tensor core's are fp32 sums.  Their error is at most
+//   eps = (heads d + 64) 2^-23 |q| max |kb|   (|q|: over all heads of hs),
+// the bound for heads d additions in any order, each off by a unit at most.  Where a block
+// lies within 2 eps of the border, those that do are scored again, with
+// products that are exact in fp32 and a sum kept in two floats (an error of
+// 2^-45 of the terms), and the border is drawn by these.
+#include <algorithm>
+#include <cfloat>
+
+#include "bwd_common.cuh"
+#include "mod_host.cuh"
+#include "sel_common.cuh"
+
+namespace skl {
+
+namespace {
+
+struct SelectArgs {
+  int B, H, HS, NQ, NK, d, bs, blocks, T, sink, local;
+  int heads;           // query heads of a selection head
+  int pitch;           // of a score row
+  int tiles_q;         // query tiles of a selection head
+  int tile0, tiles;    // the strip: query tiles of all selection heads
+  int causal;
+  const int* prefix;
+  const int* doc_q;
+  const int* doc_k;
+  SelRows q, kb;
+  float* scores;       // [tiles * 128][pitch]
+  float* norms;        // [tiles * 128]: |q|
+  unsigned* kb_norm;   // [B HS], zeroed: max |kb|, as bits
+  int2* ranges;        // [B][blocks]: smallest and largest id of a block, with ids
+  int* selected;
+  int* status;
+};
+
+constexpr int kPrepThreads = 256;
+
+// At least the root of a sum of squares that was rounded (and of squares that
+// vanished); 0 for nothing but zeros.
+__device__ __forceinline__ float norm_above(float sum, bool some) { return some ? sqrtf(sum) * 1.0001f + 1.0e-17f : 0.f; }
+
+// A warp a block: |kb| of every head, and with ids the range of its keys' ids.
+__global__ void __launch_bounds__(kPrepThreads) select_prep_kernel(const __grid_constant__ SelectArgs a) {
+  const int unit = (blockIdx.x * kPrepThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  if (unit >= a.B * a.blocks) return;
+  const int b = unit / a.blocks, j = unit - b * a.blocks;
+  for (int h = 0; h < a.HS; ++h) {
+    float s = 0.f;
+    uint32_t any = 0;
+    if (lane < a.kb.chunks) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.kb.at(b, h, j)) + lane);
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = __uint_as_float(v[e] << 16), y = __uint_as_float(v[e] & 0xffff0000u);
+        s = fmaf(x, x, fmaf(y, y, s));
+        any |= v[e] & 0x7fff7fffu;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const bool some = __any_sync(0xffffffffu, any != 0u);
+    // (a NaN compares above every number, as bits do)
+    if (lane == 0) atomicMax(a.kb_norm + b * a.HS + h, __float_as_uint(norm_above(s, some)) & 0x7fffffffu);
+  }
+  if (a.doc_k == nullptr) return;
+  int lo = INT_MAX, hi = -1;
+  for (int e = lane; e < a.bs; e += 32) {
+    const int k = j * a.bs + e;
+    const int id = k < a.NK ? a.doc_k[(long long)b * a.NK + k] : -1;
+    if (id >= 0) lo = min(lo, id), hi = max(hi, id);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  if (lane == 0) a.ranges[unit] = make_int2(lo, hi);
+}
+
+// Scores of one tile: 128 queries x kN blocks.  Warps 0-3: |q| of a row a
+// thread while the products run, then the accumulator to memory; warp 4 TMA;
+// warp 5 MMA.  The K loop runs over heads and 64 values of d at a time.  Two
+// CTAs share an SM.
+constexpr int kN = 256;
+constexpr int kScoreThreads = 192, kScoreSlots = 2;
+constexpr uint32_t kQBytes = kTile * 128;  // 64 values of 128 queries
+
+__device__ __forceinline__ void st_global_v8(float* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kScoreThreads, 2)
+    select_score_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tkb,
+                        const __grid_constant__ SelectArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = (a.d + 63) / 64;  // of a row
+  const uint32_t oQ = uint32_t(parts) * kN * 128, oBar = oQ + kScoreSlots * kQBytes;
+  auto bar = [&](int i) { return sb + oBar + 8u * i; };  // kb, full[2], empty[2], done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + oBar + 48);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + oBar + 52);
+  const Ctl ctl{abort_flag, a.status};
+  const int tile = a.tile0 + blockIdx.x;
+  const int sel = tile / a.tiles_q, q0 = (tile - sel * a.tiles_q) * kTile;
+  const int b = sel / a.HS, hs = sel - b * a.HS;
+  const int j0 = blockIdx.y * kN;
+  if (a.causal) {  // no query of the tile may see a block from j0 on
+    const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
+    const bool hidden = (long long)j0 * a.bs > min(q0 + kTile, a.NQ) - 1 + a.NK - a.NQ && (long long)j0 * a.bs >= prefix;
+    if (hidden && blockIdx.y != 0) return;  // (the first ones find |q|)
+  }
+  const int steps = a.heads * parts;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(0), 1);
+    for (int i = 0; i < kScoreSlots; ++i) {
+      mbar_init(bar(1 + i), 1);
+      mbar_init(bar(3 + i), 5);  // the products and four warps have read the slot
+    }
+    mbar_init(bar(5), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_slot), kN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar(0), uint32_t(parts) * kN * 128);
+      for (int c = 0; c < parts; ++c) tma_load_4d(sb + c * (kN * 128), &tkb, bar(0), c * 64, j0, hs, b);
+      int s = 0;
+      for (; s < steps; ++s) {
+        const int i = s % kScoreSlots, h = s / parts, c = s - h * parts;
+        if (!mbar_wait_polled(bar(3 + i), ((s / kScoreSlots) & 1) ^ 1, ctl)) break;
+        mbar_arrive_expect_tx(bar(1 + i), kQBytes);
+        tma_load_4d(sb + oQ + i * kQBytes, &tq, bar(1 + i), c * 64, q0, hs * a.heads + h, b);
+      }
+      if (*abort_flag) {  // let the copies already started land before the CTA exits
+        mbar_drain(bar(0), 0, 200000000ull);
+        for (int x = s > kScoreSlots ? s - kScoreSlots : 0; x < s; ++x)
+          mbar_drain(bar(1 + x % kScoreSlots), (x / kScoreSlots) & 1, 200000000ull);
+      }
+    }
+  } else if (warp == 5) {
+    const uint32_t leader = elect_one();
+    constexpr uint32_t idesc = idesc_bf16(128, kN, 0, 0);
+    bool ok = mbar_wait_warp(bar(0), 0, ctl);
+    for (int s = 0; ok && s < steps; ++s) {
+      const int i = s % kScoreSlots, c = s % parts;
+      ok = mbar_wait_warp(bar(1 + i), (s / kScoreSlots) & 1, ctl);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t qd = sdesc_sw128(sb + oQ + i * kQBytes, 16, 1024), kd = sdesc_sw128(sb + c * (kN * 128), 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ss(leader, tmem, sdesc_add(qd, kk * 32), sdesc_add(kd, kk * 32), idesc, s > 0 || kk > 0);
+      mma_commit(leader, bar(3 + i));
+    }
+    mma_commit(leader, bar(5));
+    mbar_drain(bar(5), 0, 1000000000ull);
+  } else {
+    const int row = warp * 32 + lane;
+    float sum = 0.f;
+    uint32_t any = 0;
+    bool ok = true;
+    for (int s = 0; ok && s < steps; ++s) {
+      const int i = s % kScoreSlots;
+      ok = mbar_wait_warp(bar(1 + i), (s / kScoreSlots) & 1, ctl);
+      if (!ok) break;
+      if (blockIdx.y == 0) {
+        const uint8_t* p = smem + oQ + i * kQBytes + row * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 w = *reinterpret_cast<const uint4*>(p + ((c ^ (row & 7)) << 4));
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = __uint_as_float(v[e] << 16), y = __uint_as_float(v[e] & 0xffff0000u);
+            sum = fmaf(x, x, fmaf(y, y, sum));
+            any |= v[e] & 0x7fff7fffu;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(3 + i));
+    }
+    const size_t at = size_t(blockIdx.x) * kTile + row;
+    if (ok && blockIdx.y == 0) a.norms[at] = norm_above(sum, any != 0u);
+    ok = ok && mbar_wait_warp(bar(5), 0, ctl);
+    if (ok) {
+      tc_fence_after();
+      float* dst = a.scores + at * a.pitch + j0;
+      const int n = min(kN, a.pitch - j0);
+#pragma unroll 1
+      for (int c = 0; c < n; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + (uint32_t(warp * 32) << 16) + c, v);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+          if (c + e < n && q0 + row < a.NQ) st_global_v8(dst + c + e, v + e);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kN);
+  }
+}
+
+// ---------------------------------------------------------------- the best of a row
+
+constexpr int kTopThreads = 256;
+
+struct Wide {  // hi + lo
+  float hi, lo;
+};
+__device__ __forceinline__ Wide wide_add(Wide a, float x) {  // hi and x exactly, what they lose into lo
+  const float s = __fadd_rn(a.hi, x), t = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(x, t));
+  return Wide{s, __fadd_rn(a.lo, e)};
+}
+
+// The score of one block, by the whole warp, as the same double in all lanes (finite).
+__device__ __forceinline__ double exact_score(const SelectArgs& a, int b, int hs, int i, int j) {
+  const int lane = threadIdx.x & 31;
+  Wide s{0.f, 0.f};
+  for (int u = lane; u < a.heads * a.q.chunks; u += 32) {
+    const int h = u / a.q.chunks, c = u - h * a.q.chunks;
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.q.at(b, hs * a.heads + h, i)) + c);
+    const uint4 y = __ldg(reinterpret_cast<const uint4*>(a.kb.at(b, hs, j)) + c);
+    const uint32_t p[4] = {x.x, x.y, x.z, x.w}, r[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s = wide_add(s, __fmul_rn(__uint_as_float(p[e] << 16), __uint_as_float(r[e] << 16)));
+      s = wide_add(s, __fmul_rn(__uint_as_float(p[e] & 0xffff0000u), __uint_as_float(r[e] & 0xffff0000u)));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o), lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+    // (the lower lane's first: the same sum in both)
+    Wide t = lane & o ? Wide{hi, lo} : s;
+    const Wide other = lane & o ? s : Wide{hi, lo};
+    t = wide_add(t, other.hi);
+    t.lo = __fadd_rn(t.lo, other.lo);
+    s = t;
+  }
+  const double d = double(s.hi) + double(s.lo);
+  return d == d ? fmin(fmax(d, -DBL_MAX), DBL_MAX) : -DBL_MAX;
+}
+
+// K values a lane (block 32 k + lane): in registers for K > 0; K = 0: any
+// number of blocks, read from memory each time.
+template <int K>
+__global__ void __launch_bounds__(kTopThreads) select_top_kernel(const __grid_constant__ SelectArgs a) {
+  const int unit = (blockIdx.x * kTopThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  const unsigned below = (1u << lane) - 1u;
+  if (unit >= a.tiles * kTile) return;
+  const int tile = a.tile0 + unit / kTile;
+  const int sel = tile / a.tiles_q, i = (tile - sel * a.tiles_q) * kTile + unit % kTile;
+  if (i >= a.NQ) return;
+  const int b = sel / a.HS, hs = sel - b * a.HS;
+  float* row = a.scores + size_t(unit) * a.pitch;
+  int* out = a.selected + (size_t(sel) * a.NQ + i) * a.T;
+  const int id = a.doc_q != nullptr ? a.doc_q[(long long)b * a.NQ + i] : 0;
+  // blocks that may be candidates: the first `most`
+  int most = a.blocks;
+  if (a.causal) {
+    const int prefix = a.prefix != nullptr ? min(max(a.prefix[b], 0), a.NK) : 0;
+    const int keys = min(max(i + a.NK - a.NQ + 1, prefix), a.NK);
+    most = keys <= 0 ? 0 : (keys - 1) / a.bs + 1;
+  }
+  if (id < 0) most = 0;
+  const int rounds = (most + 31) / 32;
+  const int2* ranges = a.doc_q != nullptr ? a.ranges + size_t(b) * a.blocks : nullptr;
+  auto candidate = [&](int j) {
+    if (j >= most) return false;
+    if (ranges == nullptr) return true;
+    const int2 r = __ldg(ranges + j);
+    return r.x <= id && id <= r.y;
+  };
+  int total = most;
+  if (ranges != nullptr) {
+    total = 0;
+    for (int k = 0; k < rounds; ++k) total += __popc(__ballot_sync(0xffffffffu, candidate(32 * k + lane)));
+  }
+  // Scores as they compete: the first `sink` and last `local` candidates at the
+  // top, what is no candidate below everything.
+  constexpr int kRegs = K > 0 ? K : 1;
+  float v[kRegs];
+  float least = FLT_MAX, best = -FLT_MAX;
+  int seen = 0;
+#pragma unroll
+  for (int k = 0; k < (K > 0 ? K : kMaxSelBlocks / 32); ++k) {
+    if (K > 0) v[k % kRegs] = -INFINITY;
+    if (k >= rounds) {
+      if (K == 0) break;
+      continue;
+    }
+    const int j = 32 * k + lane;
+    const bool can = candidate(j);
+    const unsigned who = __ballot_sync(0xffffffffu, can);
+    const int rank = seen + __popc(who & below);
+    seen += __popc(who);
+    float x = -INFINITY;
+    if (can) {
+      if (rank < a.sink || rank >= total - a.local) {
+        x = INFINITY;
+      } else {
+        x = __ldcg(row + j);
+        x = x == x ? fminf(fmaxf(x, -FLT_MAX), FLT_MAX) : -FLT_MAX;
+        least = fminf(least, x);
+        best = fmaxf(best, x);
+      }
+    }
+    if (K > 0) v[k % kRegs] = x;
+    else if (j < a.pitch) row[j] = x;
+  }
+  auto value = [&](int k) { return K > 0 ? v[k % kRegs] : (32 * k + lane < a.pitch ? row[32 * k + lane] : -INFINITY); };
+  auto each = [&](auto f) {
+    if (K > 0) {
+#pragma unroll
+      for (int k = 0; k < kRegs; ++k) f(k, v[k]);
+    } else {
+      for (int k = 0; k < rounds; ++k) f(k, value(k));
+    }
+  };
+  // The T-th best score, and how those next to it are told apart.
+  enum { kEvery, kForced, kAbove, kFirst, kChosen, kDeep };
+  int how = kEvery, need = 0;
+  float cut = 0.f, window = 0.f;
+  unsigned chosen = 0;
+  double deep[K == 0 ? kMaxSelBlocks / 32 : kRegs];
+  auto sum_over = [&](auto f) {
+    int n = 0;
+    each([&](int, float x) { n += f(x) ? 1 : 0; });
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  auto sure = [&](float x) { return x > cut + window || x == INFINITY; };
+  auto near = [&](float x) { return !sure(x) && x >= cut - window && x > -INFINITY; };
+  if (total > a.T) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    }
+    // Bisection: at least T scores are lo or above; fewer are hi or above (or lo is the best).  First by distance, then
+    // by the number of floats between the two, which ends.
+    float lo = least, hi = best;
+    int n_lo = total;
+    const int n_hi = sum_over([&](float x) { return x >= hi; });
+    if (n_hi >= a.T) lo = hi, n_lo = n_hi;
+    for (int step = 0; n_lo != a.T && lo < hi; ++step) {
+      float mid = 0.5f * lo + 0.5f * hi;
+      if (step >= 24 || !(mid > lo && mid < hi)) {
+        auto key = [](float x) {
+          const int f = __float_as_int(x);
+          return f >= 0 ? (long long)f : -(long long)(f & 0x7fffffff);
+        };
+        const long long m = (key(lo) + key(hi)) >> 1;
+        mid = m >= 0 ? __int_as_float(int(m)) : -__int_as_float(int(-m));
+        if (!(mid > lo && mid < hi)) break;  // neighbours
+      }
+      const int n = sum_over([&](float x) { return x >= mid; });
+      if (n >= a.T) lo = mid, n_lo = n;
+      else hi = mid;
+    }
+    float a_min = INFINITY, b_max = -INFINITY;  // the T-th best, the best behind it
+    each([&](int, float x) {
+      if (x >= lo) a_min = fminf(a_min, x);
+      else b_max = fmaxf(b_max, x);
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a_min = fminf(a_min, __shfl_xor_sync(0xffffffffu, a_min, o));
+      b_max = fmaxf(b_max, __shfl_xor_sync(0xffffffffu, b_max, o));
+    }
+    const float eps = float(a.heads * a.d + 64) * 1.1920929e-7f * a.norms[unit] * __uint_as_float(a.kb_norm[b * a.HS + hs]);
+    cut = a_min;
+    if (a_min == INFINITY) {
+      how = kForced;
+    } else if (n_lo == a.T && a_min - b_max > 2.f * eps) {
+      how = kAbove;
+    } else {
+      window = eps == eps ? 2.f * eps : INFINITY;
+      need = a.T - sum_over(sure);
+      const int n = sum_over(near);
+      if (n == need || window == 0.f) {  // all of them; or scores of 0, all equal
+        how = kFirst;
+      } else if (n <= 32) {
+        how = kChosen;
+        double mine = 0.0;
+        int at = 0;
+        each([&](int k, float x) {
+          for (unsigned who = __ballot_sync(0xffffffffu, near(x)); who != 0u; who &= who - 1u, ++at) {
+            const double s = exact_score(a, b, hs, i, 32 * k + __ffs(who) - 1);
+            if (lane == at) mine = s;
+          }
+        });
+        int better = 0;
+        for (int o = 0; o < n; ++o) {
+          const double s = __shfl_sync(0xffffffffu, mine, o);
+          better += s > mine || (s == mine && o < lane) ? 1 : 0;
+        }
+        chosen = __ballot_sync(0xffffffffu, lane < n && better < need);
+      } else {
+        // many (equal keys, say): a lane keeps the scores of its blocks, and the best are taken one by one
+        how = kDeep;
+        each([&](int k, float x) {
+          double mine = -INFINITY;
+          for (unsigned who = __ballot_sync(0xffffffffu, near(x)); who != 0u; who &= who - 1u) {
+            const int l = __ffs(who) - 1;
+            const double s = exact_score(a, b, hs, i, 32 * k + l);
+            if (lane == l) mine = s;
+          }
+          deep[k] = mine;
+        });
+        for (int left = need; left > 0; --left) {
+          double s = -INFINITY;
+          int j = INT_MAX;
+          each([&](int k, float) {
+            if (deep[k] > s && deep[k] != INFINITY) s = deep[k], j = 32 * k + lane;
+          });
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const double t = __shfl_xor_sync(0xffffffffu, s, o);
+            const int u = __shfl_xor_sync(0xffffffffu, j, o);
+            if (t > s || (t == s && u < j)) s = t, j = u;
+          }
+          each([&](int k, float) {
+            if (32 * k + lane == j) deep[k] = INFINITY;  // taken
+          });
+        }
+      }
+    }
+  }
+  // in ascending order
+  int place = 0, ord = 0;
+  each([&](int k, float x) {
+    bool take = x > -INFINITY;
+    if (how == kForced) take = x == INFINITY;
+    if (how == kAbove) take = x >= cut;
+    if (how >= kFirst) {
+      const bool in = near(x);
+      const unsigned who = __ballot_sync(0xffffffffu, in);
+      const int o = ord + __popc(who & below);
+      ord += __popc(who);
+      take = sure(x);
+      if (in) take = how == kFirst ? o < need : (how == kChosen ? ((chosen >> o) & 1u) != 0u : deep[k] == INFINITY);
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, take);
+    const int at = place + __popc(who & below);
+    if (take && at < a.T) out[at] = 32 * k + lane;
+    place += __popc(who);
+  });
+  for (int t = place + lane; t < a.T; t += 32) out[t] = -1;
+}
+
+int launch_select(const CUtensorMap& tq, const CUtensorMap& tkb, SelectArgs a, int strip, cudaStream_t st) {
+  const int all = a.B * a.HS * a.tiles_q;
+  cudaError_t e = cudaMemsetAsync(a.kb_norm, 0, size_t(a.B) * a.HS * 4, st);
+  if (e != cudaSuccess) return e;
+  select_prep_kernel<<<unsigned((a.B * a.blocks + kPrepThreads / 32 - 1) / (kPrepThreads / 32)), kPrepThreads, 0, st>>>(a);
+  const int parts = (a.d + 63) / 64;
+  const int smem = 1024 + parts * kN * 128 + kScoreSlots * int(kQBytes) + 64;
+  e = cudaFuncSetAttribute(select_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           1024 + 2 * kN * 128 + kScoreSlots * int(kQBytes) + 64);
+  if (e != cudaSuccess) return e;
+  for (a.tile0 = 0; a.tile0 < all; a.tile0 += strip) {
+    a.tiles = std::min(strip, all - a.tile0);
+    select_score_kernel<<<dim3(unsigned(a.tiles), unsigned((a.blocks + kN - 1) / kN)), kScoreThreads, smem, st>>>(tq, tkb, a);
+    const unsigned grid = unsigned(a.tiles) * kTile / (kTopThreads / 32);
+    if (a.blocks <= 256) select_top_kernel<8><<<grid, kTopThreads, 0, st>>>(a);
+    else if (a.blocks <= 512) select_top_kernel<16><<<grid, kTopThreads, 0, st>>>(a);
+    else if (a.blocks <= 1024) select_top_kernel<32><<<grid, kTopThreads, 0, st>>>(a);
+    else select_top_kernel<0><<<grid, kTopThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+struct SelectPlan {
+  SelectArgs a{};
+  int strip = 0;  // query tiles
+  size_t bytes = 0;
+};
+
+int check_select(const streamkl_view* q, const streamkl_view* kb, const streamkl_visible* vis, int B, int H, int heads,
+                 int NQ, int NK, int d, int block, int count, int sink, int local, const int* selected, bool data) {
+  if (B < 0 || H < 0 || NQ < 0 || NK < 0 || vis == nullptr) return STREAMKL_INVALID_ARG;
+  if (vis->causal != 0 && vis->causal != 1) return STREAMKL_INVALID_ARG;
+  if (vis->prefix != nullptr && !vis->causal) return STREAMKL_INVALID_ARG;
+  if ((vis->doc_q == nullptr) != (vis->doc_k == nullptr)) return STREAMKL_INVALID_ARG;
+  if (!aligned4(vis->prefix) || !aligned4(vis->doc_q) || !aligned4(vis->doc_k)) return STREAMKL_INVALID_ARG;
+  if (block != 32 && block != 64 && block != 128) return STREAMKL_INVALID_ARG;
+  if (count < 1 || count > kMaxSlots || sink < 0 || local < 0 || sink > count || local > count - sink)
+    return STREAMKL_INVALID_ARG;
+  if (heads < 1 || heads > std::max(H, 1) || H % heads != 0) return STREAMKL_INVALID_ARG;
+  if (d < 16 || d > 128 || d % 16 != 0) return STREAMKL_UNSUPPORTED;
+  const long long blocks = ((long long)NK + block - 1) / block;
+  if (blocks > kMaxSelBlocks) return STREAMKL_UNSUPPORTED;
+  if ((long long)B * H > 65535 || (long long)B * H * std::max(NQ, NK) > (1ll << 31) - 1 - 65535 * kTile)
+    return STREAMKL_INVALID_ARG;
+  if ((long long)B * heads * NQ * count > (1ll << 31) - 1) return STREAMKL_INVALID_ARG;
+  if (!data || B == 0 || H == 0 || NQ == 0) return STREAMKL_OK;
+  if (selected == nullptr || !aligned4(selected)) return STREAMKL_INVALID_ARG;
+  if (NK == 0) return STREAMKL_INVALID_ARG;
+  if (q == nullptr || kb == nullptr || !view_ok(*q, B, H, NQ) || !view_ok(*kb, B, heads, int(blocks))) return STREAMKL_INVALID_ARG;
+  return STREAMKL_OK;
+}
+
+SelectPlan select_plan(const streamkl_visible& vis, int B, int H, int heads, int NQ, int NK, int d, int block, int count,
+                       int sink, int local, void* ws) {
+  SelectPlan f;
+  SelectArgs& a = f.a;
+  a.B = B;
+  a.H = H;
+  a.HS = heads;
+  a.NQ = NQ;
+  a.NK = NK;
+  a.d = d;
+  a.bs = block;
+  a.blocks = (NK + block - 1) / block;
+  a.T = count;
+  a.sink = sink;
+  a.local = local;
+  a.heads = H / heads;
+  a.pitch = (a.blocks + 7) / 8 * 8;
+  a.tiles_q = tiles(NQ);
+  a.causal = vis.causal;
+  a.prefix = vis.prefix;
+  a.doc_q = vis.doc_q;
+  a.doc_k = vis.doc_k;
+  // strips of 64 MB of scores: about half of L2
+  const long long all = (long long)B * heads * a.tiles_q;
+  f.strip = int(std::max(1ll, std::min(all, (64ll << 20) / (4ll * kTile * a.pitch))));
+  Carver c{static_cast<uint8_t*>(ws)};
+  const size_t pad = (32 - (reinterpret_cast<uintptr_t>(ws) & 31u)) & 31u;  // score rows start at 32 bytes
+  c.used = pad;
+  a.scores = c.take<float>(size_t(f.strip) * kTile * a.pitch);
+  a.norms = c.take<float>(size_t(f.strip) * kTile);
+  a.kb_norm = c.take<unsigned>(size_t(B) * heads);
+  if (vis.doc_q != nullptr) a.ranges = c.take<int2>(size_t(B) * a.blocks);
+  f.bytes = c.used - pad + 16;
+  return f;
+}
+
+}  // namespace
+
+}  // namespace skl
+
+extern "C" {
+
+size_t streamkl_select_blocks_workspace_bytes(const streamkl_visible* vis, int B, int H, int heads, int NQ, int NK, int d,
+                                              int block, int count, int sink, int local) {
+  using namespace skl;
+  if (check_select(nullptr, nullptr, vis, B, H, heads, NQ, NK, d, block, count, sink, local, nullptr, false) != STREAMKL_OK)
+    return 0;
+  if (B == 0 || H == 0 || NQ == 0 || NK == 0) return 0;
+  return select_plan(*vis, B, H, heads, NQ, NK, d, block, count, sink, local, nullptr).bytes;
+}
+
+int streamkl_select_blocks(const streamkl_view* q, const streamkl_view* kb, const streamkl_visible* vis, int B, int H,
+                           int heads, int NQ, int NK, int d, int block, int count, int sink, int local, int* selected,
+                           void* workspace, size_t workspace_bytes, streamkl_stream_t stream) {
+  using namespace skl;
+  int s = check_select(q, kb, vis, B, H, heads, NQ, NK, d, block, count, sink, local, selected, true);
+  if (s != STREAMKL_OK) return s;
+  if (B == 0 || H == 0 || NQ == 0) return STREAMKL_OK;
+  SelectPlan f = select_plan(*vis, B, H, heads, NQ, NK, d, block, count, sink, local, workspace);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < f.bytes) return STREAMKL_INVALID_ARG;
+  if ((s = check_device()) != STREAMKL_OK) return s;
+  CUtensorMap tq, tkb;
+  if (!map_bf16(&tq, *q, B, H, NQ, d) || !map_bf16(&tkb, *kb, B, heads, f.a.blocks, d, kN)) return STREAMKL_CUDA_ERROR;
+  auto rows = [&](const streamkl_view& v, int hd, int n) {
+    return SelRows{static_cast<const uint8_t*>(v.data), B > 1 ? 2 * v.stride_b : 0, hd > 1 ? 2 * v.stride_h : 0,
+                   n > 1 ? 2 * v.stride_n : 0, d / 8};
+  };
+  f.a.q = rows(*q, H, NQ);
+  f.a.kb = rows(*kb, heads, f.a.blocks);
+  f.a.selected = selected;
+  f.a.status = status_word();
+  if (!f.a.status) return STREAMKL_CUDA_ERROR;
+  return as_status(launch_select(tq, tkb, f.a, f.strip, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

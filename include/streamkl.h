@@ -419,6 +419,26 @@ typedef struct streamkl_blocks {
 } streamkl_blocks;
 
 /*
+ * The blocks that score best for each query: block j scores
+ *   sum over the query heads h with h / (H / heads) = hs of q_h(i) . kb_hs(j),
+ * and its candidates are the blocks with a key that the query may see: one at
+ * or before it (causal) or in the prefix, and, with ids, a block whose smallest
+ * and largest id (negative ones aside) enclose the query's.  selected
+ * [B][heads][NQ][count] gets the `count` best candidates in ascending order and
+ * -1 behind them; the first `sink` and the last `local` candidates always are
+ * among them (sink + local <= count).  The order is that of the exact scores,
+ * ties go to the lowest block; differences below 1e-30 are not resolved, and
+ * what a query whose q is not finite selects is not specified.  q is bf16
+ * [B][H][NQ][d], kb [B][heads][blocks][d] (streamkl_pool_blocks, or any other).
+ * workspace: as above, with streamkl_select_blocks_workspace_bytes.
+ */
+size_t streamkl_select_blocks_workspace_bytes(const streamkl_visible* vis, int B, int H, int heads, int NQ, int NK, int d,
+                                              int block, int count, int sink, int local);
+int streamkl_select_blocks(const streamkl_view* q, const streamkl_view* kb, const streamkl_visible* vis, int B, int H,
+                           int heads, int NQ, int NK, int d, int block, int count, int sink, int local, int* selected,
+                           void* workspace, size_t workspace_bytes, streamkl_stream_t stream);
+
+/*
  * Forward over selected blocks: kl, lse1, lse2 as streamkl_fwd_mod, over the
  * keys that are visible (streamkl_visible) and in a selected block; a row that
  * sees none gets KL 0 and LSE -inf.  Sides may not be modified (softcap,

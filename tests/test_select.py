@@ -1,0 +1,230 @@
+"""Selected blocks against float64 scores: the same lists, ties to the lowest
+block, forced and masked ones, and the refusals, without a GPU."""
+
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import attention_distillation_kl_gb300 as skl
+
+A = 4096
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(skl.library_path):
+        import __graft_entry__
+        __graft_entry__.build()
+    return skl.lib()
+
+
+def seen(causal=0, prefix=None, doc_q=None, doc_k=None):
+    return skl._Visible(causal, prefix, doc_q, doc_k)
+
+
+def call(L, q=None, kb=None, vis=None, B=1, H=4, heads=2, NQ=100, NK=300, d=64, block=32, count=4, sink=1, local=1, out=A,
+         ws=A, ws_bytes=1 << 40):
+    v = skl._View(A, 1 << 20, 1 << 16, d)
+    return L.streamkl_select_blocks(q or v, kb or v, vis or seen(), B, H, heads, NQ, NK, d, block, count, sink, local, out,
+                                    ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(vis=seen(2)), 1), (dict(vis=seen(0, A)), 1), (dict(vis=seen(0, None, A)), 1), (dict(vis=seen(1, A + 1)), 1),
+    (dict(block=48), 1), (dict(block=0), 1), (dict(count=0), 1), (dict(count=129), 1), (dict(sink=-1), 1),
+    (dict(local=-1), 1), (dict(sink=3, local=2), 1), (dict(sink=5, local=0), 1), (dict(heads=3), 1), (dict(heads=0), 1),
+    (dict(heads=8), 1), (dict(d=8), 2), (dict(d=72), 2), (dict(d=144), 2), (dict(NK=32 * 4096 + 1), 2), (dict(NK=0), 1),
+    (dict(NQ=-1), 1), (dict(out=0), 1), (dict(out=A + 2), 1), (dict(ws=0), 1), (dict(ws=A + 8), 1), (dict(ws_bytes=64), 1),
+    (dict(q=skl._View(0, 64, 64, 64)), 1), (dict(kb=skl._View(A, 64, 64, 4)), 1), (dict(B=20000), 1),
+    (dict(NK=2 ** 31 - 1, H=1, heads=1), 2),
+])
+def test_refusals(L, kw, status):
+    assert call(L, **kw) == status
+
+
+def test_empty_and_workspace(L):
+    assert call(L, NQ=0, out=0, ws=0) == 0 and call(L, B=0, out=0, ws=0) == 0
+    f = skl.streamkl_select_blocks_workspace_bytes
+    assert f(1, 4, 2, 100, 300, 64, 32, 4) >= 2 * 128 * 16 * 4
+    assert f(1, 4, 2, 100, 300, 64, 32, 0) == 0
+    assert f(1, 4, 2, 100, 300, 64, 32, 4, ids=True) > f(1, 4, 2, 100, 300, 64, 32, 4)
+    assert f(1, 32, 8, 1 << 17, 1 << 17, 128, 32, 16) < 80 << 20  # strips
+
+
+def expected(q, kb, T, bs, NK, causal, prefix, ids, sink, local):
+    q, kb = q.double().cpu().numpy(), kb.double().cpu().numpy()
+    B, H, NQ, _ = q.shape
+    hs, nb = kb.shape[1], kb.shape[2]
+    out = np.full((B, hs, NQ, T), -1, np.int32)
+    for b in range(B):
+        for h in range(hs):
+            g = H // hs
+            score = q[b, h * g:(h + 1) * g].sum(0) @ kb[b, h].T
+            for i in range(NQ):
+                first = np.arange(nb) * bs
+                can = np.ones(nb, bool)
+                if causal:
+                    can = first <= i + NK - NQ
+                    if prefix is not None:
+                        can |= first < prefix[b]
+                if ids is not None:
+                    x = ids[0][b, i]
+                    k = np.concatenate([ids[1][b], np.full(nb * bs - NK, -1)]).reshape(nb, bs)
+                    lo = np.where(k >= 0, k, 2 ** 31 - 1).min(1)
+                    can &= (x >= 0) & (lo <= x) & (x <= k.max(1))
+                c = np.nonzero(can)[0]
+                forced = set(c[:sink]) | set(c[len(c) - local:] if local else [])
+                rest = sorted((j for j in c if j not in forced), key=lambda j: (-score[i, j], j))
+                take = sorted(list(forced) + rest[:max(0, T - len(forced))])
+                out[b, h, i, :len(take)] = take
+    return out
+
+
+def run(B=1, H=4, HS=2, NQ=100, NK=300, d=64, bs=32, T=4, causal=True, prefix=None, docs=None, sink=1, local=1, bshd=False,
+        seed=0, make=None):
+    g = torch.Generator().manual_seed(seed)
+    nb = -(-NK // bs)
+    q = torch.randn((B, H, NQ, d), generator=g)
+    kb = torch.randn((B, HS, nb, d), generator=g)
+    if make:
+        q, kb = make(q, kb)
+    q, kb = q.to(torch.bfloat16), kb.to(torch.bfloat16)
+    ids = None
+    if docs == "packed":
+        k = torch.sort(torch.randint(0, 4, (B, NK), generator=g), dim=1)[0]
+        k[:, NK - NK // 9:] = -1
+        ids = k[:, NK - NQ:].int().contiguous(), k.int()
+    elif docs == "shuffled":
+        ids = torch.randint(-2, 9, (B, NQ), generator=g).int(), torch.randint(-5, 9, (B, NK), generator=g).int()
+    lay = (lambda t: t.transpose(1, 2).contiguous().cuda().transpose(1, 2)) if bshd else (lambda t: t.cuda())
+    kw = dict(causal=causal, prefix=None if prefix is None else torch.tensor(prefix, dtype=torch.int32).cuda(),
+              doc_q=None if ids is None else ids[0].cuda(), doc_k=None if ids is None else ids[1].cuda(), sink=sink,
+              local=local)
+    got = skl.streamkl_select_blocks(lay(q), lay(kb), T, bs, NK, **kw)
+    torch.cuda.synchronize()
+    assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
+    want = expected(q, kb, T, bs, NK, causal, prefix, None if ids is None else [x.numpy() for x in ids], sink, local)
+    assert np.array_equal(got.cpu().numpy(), want)
+    return lay(q), lay(kb), kw, got
+
+
+CASES = {
+    "one token": dict(H=1, HS=1, NQ=1, NK=1, T=1, sink=0),
+    "one query": dict(H=8, HS=2, NQ=1, NK=1000, T=8),
+    "grouped": dict(H=8, HS=2, NQ=300, NK=1500, T=6, d=128),
+    "heads apart": dict(B=2, H=3, HS=3, NQ=130, NK=600, T=5, bshd=True),
+    "one list for all": dict(H=6, HS=1, NQ=129, NK=900, T=7, d=80, bs=64),
+    "not causal": dict(H=4, HS=4, NQ=70, NK=2000, T=12, causal=False, bs=64, sink=0, local=0),
+    "no forced": dict(NQ=300, NK=300, T=3, sink=0, local=0),
+    "all forced": dict(NQ=300, NK=300, T=4, sink=2, local=2),
+    "fewer candidates than places": dict(NQ=200, NK=200, T=16),
+    "more queries than keys": dict(NQ=300, NK=100, T=3),
+    "prefix": dict(B=3, NQ=150, NK=400, prefix=[0, 177, 400], T=5),
+    "packed": dict(B=2, NQ=400, NK=400, docs="packed", T=4),
+    "packed, few queries": dict(B=2, NQ=40, NK=700, docs="packed", T=4, sink=2),
+    "shuffled ids": dict(B=2, NQ=100, NK=500, docs="shuffled", T=4, causal=False),
+    "300 blocks": dict(H=2, HS=1, NQ=40, NK=300 * 32, T=32),
+    "600 blocks": dict(H=2, HS=1, NQ=40, NK=600 * 32 - 5, T=16, causal=False),
+    "1500 blocks": dict(H=2, HS=2, NQ=20, NK=1500 * 32, T=24, docs="packed"),
+    "4096 blocks": dict(H=1, HS=1, NQ=5, NK=4096 * 32, T=128, causal=False, d=16),
+    "128 places": dict(H=1, HS=1, NQ=50, NK=200 * 32, T=128, d=32),
+    "large blocks": dict(NQ=500, NK=5000, bs=128, T=9, d=112),
+}
+
+
+@gpu
+@pytest.mark.parametrize("name", CASES)
+def test_lists(name):
+    run(**CASES[name])
+
+
+def whole_numbers(q, kb):
+    """Small whole numbers: many exact ties."""
+    return q.round().clamp(-1, 1), kb.round().clamp(-1, 1)
+
+
+def equal_keys(q, kb):
+    kb[:, :, 3:] = kb[:, :, 3:4]
+    return q, kb
+
+
+def zeros(q, kb):
+    q[:, :, ::2] = 0
+    kb[:, :, 5::3] = 0
+    return q, kb
+
+
+def near(q, kb):
+    """Keys one rounding apart: sums of fp32 do not tell all of them apart."""
+    kb[:] = kb[:, :, :1]
+    bump = torch.zeros_like(kb)
+    at = torch.arange(kb.shape[2]) % kb.shape[3]
+    bump[:, :, torch.arange(kb.shape[2]), at] = 2.0 ** -7
+    return q, kb * (1 + bump)
+
+
+def cancelling(q, kb):
+    """Large products that cancel, and what is left decides."""
+    q[..., 1::2] = -q[..., ::2]
+    kb[..., ::2] = 64.0
+    kb[..., 1::2] = 64.0
+    kb[..., 0] += torch.randn(kb.shape[:3], generator=torch.Generator().manual_seed(1))
+    return q, kb
+
+
+@gpu
+@pytest.mark.parametrize("make", [whole_numbers, equal_keys, zeros, near, cancelling])
+@pytest.mark.parametrize("shape", [dict(NQ=200, NK=2000, T=6), dict(NQ=60, NK=40000, T=16, causal=False, H=2, HS=1)])
+def test_ties_and_close_scores(make, shape):
+    run(make=make, **shape)
+
+
+@gpu
+def test_sizes_of_scores():
+    run(make=lambda q, kb: (q * 1e10, kb * 1e10))
+    run(make=lambda q, kb: (q * 1e-12, kb * 1e-8))
+
+
+@gpu
+def test_not_finite_queries_stay_in_bounds():
+    q, kb, kw, want = run(NQ=64, NK=2000, T=6, causal=False)
+    q[0, 0, 5] = float("nan")
+    q[0, 2, 7, 3] = float("inf")
+    kw["causal"] = False
+    got = skl.streamkl_select_blocks(q, kb, 6, 32, 2000, **kw)
+    assert got.min() >= -1 and got.max() < 63
+    same = torch.ones(64, dtype=torch.bool)
+    same[[5, 7]] = False
+    assert torch.equal(got[:, :, same], want[:, :, same])
+
+
+@gpu
+def test_strips_streams_and_graphs():
+    q, kb, kw, want = run(H=2, HS=1, NQ=300, NK=900, T=5, bshd=True)
+    need = skl.streamkl_select_blocks_workspace_bytes(1, 2, 1, 300, 900, 64, 32, 5, causal=True)
+    ws = torch.full((need + 16,), 255, dtype=torch.uint8, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    out = torch.full_like(want, 7)
+    assert skl.streamkl_select_blocks(q, kb, 5, 32, 900, **kw, out=out, workspace=ws[16:], stream=st) is out
+    torch.cuda.current_stream().wait_stream(st)
+    assert torch.equal(out, want)
+    with pytest.raises(skl.StreamKLError):
+        skl.streamkl_select_blocks(q, kb, 5, 32, 900, **kw, workspace=ws[: need - 16])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = skl.streamkl_select_blocks(q, kb, 5, 32, 900, **kw)
+    q.copy_(torch.randn(q.shape, device="cuda"))
+    graph.replay()
+    assert torch.equal(again, skl.streamkl_select_blocks(q, kb, 5, 32, 900, **kw))
+    # more queries than one strip holds: 64 MB of scores
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = torch.randn((1, 2, 12000, 32), generator=g, device="cuda").to(torch.bfloat16)
+    kb = torch.randn((1, 2, 1875, 32), generator=g, device="cuda").to(torch.bfloat16)
+    whole = skl.streamkl_select_blocks(q, kb, 4, 32, 60000)
+    for i0 in range(0, 12000, 4000):
+        part = skl.streamkl_select_blocks(q[:, :, i0:i0 + 4000], kb, 4, 32, 60000)
+        assert torch.equal(part, whole[:, :, i0:i0 + 4000])
