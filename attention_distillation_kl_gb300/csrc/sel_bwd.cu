@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       int count = 1;
-      if (i >= L::kQFull && i < L::kQEmpty) count = L::kGatherWarps;
+      if (i >= L::kQFull && i < L::kQEmpty) count = 33 * L::kGatherWarps;
       if (i == L::kReady || i == L::kReady + 1 || i == L::kSFree || i == L::kDsFull) count = L::kDsWarps;
       if (i == L::kDqEmpty || i == L::kDkEmpty) count = 4;
       if (i == L::kDone) count = 2;
@@ -114,65 +114,88 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     const SelRows& rg = kP2 ? a.r2 : a.r1;
     const float sg = kP2 ? a.scale2 : a.scale1;
     const int ug = kP2 ? a.u2 : a.u1;
-    auto landed = [&](int m) {  // a slot's copies have landed: the tensor core may read them
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kQFull + m % a.slots));
+    // A row's pointers and numbers are read a tile ahead of its copies, its entry two tiles.
+    struct Row {
+      unsigned long long po, pg;
+      float l1, l2, kl, dkl, kmax;
+      int row;  // -1: none
     };
-    int m = 0, n = 0;
+    auto row_of_entry = [&](const SelWork& k, unsigned ent) {
+      Row x{0ull, 0ull, -INFINITY, 0.f, 0.f, 0.f, 0.f, -1};
+      const int i = int(ent >> kSlotBits), h = k.head0 + hl;
+      if (ent == kNoEntry || !SKL_CHECK(a.status, i < a.p.NQ && h < a.p.H && k.b < a.p.B)) return x;
+      x.row = (k.b * a.p.H + h) * a.p.NQ + i;
+      x.po = reinterpret_cast<unsigned long long>(ro.at(k.b, h, i));
+      x.pg = reinterpret_cast<unsigned long long>(rg.at(k.b, h, i));
+      x.l1 = __ldg(a.lse1 + x.row);
+      x.l2 = __ldg(a.lse2 + x.row);
+      x.kl = __ldg(a.kl + x.row);
+      x.dkl = __ldg(a.dkl + x.row);
+      x.kmax = __uint_as_float(__ldg(a.kmax + k.b * a.HK + (k.head0 / G) / ug) << 16);
+      return x;
+    };
+    SelWalk walk(a.p, works);
+    int e0 = 0, m = 0, n = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < works; w += gridDim.x) {
-      const SelWork k = sel_work(a.p, w);
-      const float kmax = __uint_as_float(a.kmax[k.b * a.HK + (k.head0 / G) / ug] << 16);
-      for (int e0 = 0; ok && e0 < k.count; e0 += per_tile, ++n) {
-        const int e = e0 + ql;
-        bool on = ql < per_tile && e < k.count;
-        const int i = on ? int(__ldg(a.p.entries + k.first + e) >> kSlotBits) : 0, h = k.head0 + hl;
-        const size_t row = size_t(k.b * a.p.H + h) * a.p.NQ + i;
-        // na, nb, ws as in ds_chunk_row.  Rows that saw nothing (they may hold
-        // anything) and rows past the last are zeros, and contribute zeros.
-        float4 par{-INFINITY, kP2 ? -INFINITY : 0.f, 0.f, 0.f};
-        if (on && SKL_CHECK(a.status, i < a.p.NQ && h < a.p.H && k.b < a.p.B)) {
-          const float l1 = a.lse1[row], l2 = a.lse2[row], kl = a.kl[row], dkl = a.dkl[row];
-          on = l1 != -INFINITY;
-          if (on) {
-            par.x = -l1 * kLog2e;
-            par.y = kP2 ? -l2 * kLog2e : -(l1 - l2 + kl);
-            par.z = sg * dkl;
-            par.w = 1.5f * exp2_int(23 - dq_fixed_exp(MODE, sg, dkl, kl, kmax));
-          }
-        }
-        const unsigned long long po = on ? reinterpret_cast<unsigned long long>(ro.at(k.b, h, i)) : 0ull;
-        const unsigned long long pg = on ? reinterpret_cast<unsigned long long>(rg.at(k.b, h, i)) : 0ull;
-#pragma unroll
-        for (int side = 0; side < 2; ++side, ++m) {
-          const int s = m % a.slots;
-          ok = mbar_wait_warp(bar(L::kQEmpty + s), ((m / a.slots) & 1) ^ 1, ctl);
-          if (!ok) break;
-          if (side == 0) {
-            // (the tile whose parameters these replace has been through dQ: kRows tiles cannot be under way)
-            params[(n % L::kRows) * kTile + r] = par;
-            row_of[(n % L::kRows) * kTile + r] = on ? int(row) : -1;
-            gather_rows<DO, 32, true>(sb + oQ + s * L::kSlot, first, po, 0, ro.chunks);
-          } else {
-            gather_rows<DG, 32, true>(sb + oQ + s * L::kSlot, first, pg, 0, rg.chunks);
-          }
-          cp_async_commit();
-          if (m >= 1) {
-            cp_async_wait<1>();
-            landed(m - 1);
-          }
-        }
+    auto step = [&]() {
+      e0 += per_tile;
+      if (e0 >= walk.count) {
+        walk.advance(a.p);
+        e0 = 0;
       }
+    };
+    const bool place = ql < per_tile;
+    bool more = walk.more();  // a tile to copy
+    Row x = row_of_entry(walk.get(a.p), entry_of(a.p, walk, ql, place));
+    step();
+    bool next = walk.more();
+    SelWork k = walk.get(a.p);
+    unsigned ent = entry_of(a.p, walk, e0 + ql, place);
+    while (ok && more) {
+      const Row y = row_of_entry(k, next ? ent : kNoEntry);
+      const bool then = next;
+      step();
+      next = walk.more();
+      k = walk.get(a.p);
+      ent = entry_of(a.p, walk, e0 + ql, place);
+      // na, nb, ws as in ds_chunk_row.  Rows that saw nothing (they may hold
+      // anything) and rows past the last are zeros, and contribute zeros.
+      const bool on = x.row >= 0 && x.l1 != -INFINITY;
+      float4 par{-INFINITY, kP2 ? -INFINITY : 0.f, 0.f, 0.f};
+      if (on) {
+        par.x = -x.l1 * kLog2e;
+        par.y = kP2 ? -x.l2 * kLog2e : -(x.l1 - x.l2 + x.kl);
+        par.z = sg * x.dkl;
+        par.w = 1.5f * exp2_int(23 - dq_fixed_exp(MODE, sg, x.dkl, x.kl, x.kmax));
+      }
+#pragma unroll
+      for (int side = 0; side < 2; ++side, ++m) {
+        const int s = m % a.slots;
+        ok = mbar_wait_warp(bar(L::kQEmpty + s), ((m / a.slots) & 1) ^ 1, ctl);
+        if (!ok) break;
+        if (side == 0) {
+          // (the tile whose parameters these replace has been through dQ: kRows tiles cannot be under way)
+          params[(n % L::kRows) * kTile + r] = par;
+          row_of[(n % L::kRows) * kTile + r] = on ? x.row : -1;
+          gather_rows<DO, 32, true>(sb + oQ + s * L::kSlot, first, on ? x.po : 0ull, 0, ro.chunks);
+        } else {
+          gather_rows<DG, 32, true>(sb + oQ + s * L::kSlot, first, on ? x.pg : 0ull, 0, rg.chunks);
+        }
+        cp_async_arrive(bar(L::kQFull + s));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kQFull + s));  // parameters and zeros, which are plain stores
+      }
+      x = y;
+      more = then;
+      ++n;
     }
-    cp_async_wait<0>();
-    if (ok && m > 0) landed(m - 1);
+    cp_async_wait_all();
   } else if (warp == L::kLoadWarp) {
     // ---------------------------------------------------------------- K
     if (lane == 0) {
       int items = 0;
-      for (int w = blockIdx.x; w < works; w += gridDim.x, ++items) {
-        const SelWork k = sel_work(a.p, w);
+      for (SelWalk walk(a.p, works); walk.more(); walk.advance(a.p), ++items) {
+        const SelWork k = walk.get(a.p);
         const int kb = items % a.k_bufs, hu = k.head0 / G;
         if (!mbar_wait_polled(bar(L::kKEmpty + kb), ((items / a.k_bufs) & 1) ^ 1, ctl)) break;
         const uint32_t full = bar(L::kKFull + kb);
@@ -201,8 +224,8 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     };
     int m = 0, n = 0, items = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
-      const int count = sel_work(a.p, w).count;
+    for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
+      const int count = walk.count;
       const int kb = items % a.k_bufs;
       const uint32_t k1s = sb + kb * kK, k2s = k1s + kK1;
       ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (items / a.k_bufs) & 1, ctl);
@@ -210,6 +233,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         int s = m % a.slots;
         ok = mbar_wait_warp(bar(L::kSFree), (n & 1) ^ 1, ctl) && mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
         if (!ok) break;
+        fence_proxy_async_smem();  // (copies of cp.async)
         tc_fence_after();
         // the other side first: its slot is released as early as possible
         product(std::integral_constant<int, DO>{}, kP2 ? t_s1 : t_s2, sb + oQ + s * L::kSlot, kP2 ? k1s : k2s);
@@ -218,6 +242,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         s = m % a.slots;
         ok = mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
         if (!ok) break;
+        fence_proxy_async_smem();
         tc_fence_after();
         product(std::integral_constant<int, DG>{}, kP2 ? t_s2 : t_s1, sb + oQ + s * L::kSlot, kP2 ? k2s : k1s);
         ++m;  // (released by dK)
@@ -235,8 +260,8 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     const uint64_t dsm = sdesc_sw128(sb + oDS, kTile * 128, 1024), dsk = sdesc_sw128(sb + oDS, 16, 1024);
     int n = 0, items = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
-      const int count = sel_work(a.p, w).count;
+    for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
+      const int count = walk.count;
       const int kb = items % a.k_bufs;
       const uint64_t kgn = sdesc_sw128(sb + kb * kK + (kP2 ? kK1 : 0u), uint32_t(bs) * 128, 1024);
       ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (items / a.k_bufs) & 1, ctl) &&
@@ -280,8 +305,8 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     const int nqt = (a.p.NQ + kTile - 1) / kTile, nkt = (a.p.NK + kTile - 1) / kTile, off = a.p.NK - a.p.NQ;
     int n = 0, items = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
-      const SelWork k = sel_work(a.p, w);
+    for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
+      const SelWork k = walk.get(a.p);
       const int k0 = k.block * bs;
       const int prefix = a.p.prefix != nullptr ? min(max(a.p.prefix[k.b], 0), a.p.NK) : 0;
       const int* kids = ids ? a.vis.ids_k + size_t(k.b) * nkt * kTile + k0 : nullptr;
@@ -301,7 +326,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         if (lane == 0) mbar_arrive(bar(L::kReady + kb));
       }
       const int row0 = (k.b * a.p.H + k.head0 + hl) * a.p.NQ;  // of query 0
-      for (int e0 = 0; ok && e0 < k.count; e0 += per_tile, ++n) {
+      for (int e0 = 0; ok && e0 < walk.count; e0 += per_tile, ++n) {
         ok = mbar_wait_warp(bar(L::kSFull), n & 1, ctl);
         if (!ok) break;
         tc_fence_after();
@@ -357,8 +382,8 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     const uint32_t stage = sb + oStage + row * (piece * 4u + 16u);  // this thread's
     int n = 0, items = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
-      const int count = sel_work(a.p, w).count;
+    for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
+      const int count = walk.count;
       for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
         ok = mbar_wait_warp(bar(L::kDqFull), n & 1, ctl);
         if (!ok) break;
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (w4 * 32 < bs) {
-        float* dst = a.dk_part + (size_t(w) * bs + row) * a.dg;
+        float* dst = a.dk_part + (size_t(walk.w) * bs + row) * a.dg;
 #pragma unroll 1
         for (int c = 0; c < DG; c += 32) {
           uint32_t v[32];

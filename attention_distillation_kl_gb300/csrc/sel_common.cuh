@@ -55,23 +55,50 @@ struct SelPlan {
   int max_items;
 };
 
-// Where an item's tile lies, for every role alike.
+// What an item is about.
 struct SelWork {
-  int b, head0, block, first, count, unit;
+  int b, head0, block, unit;
 };
-__device__ __forceinline__ SelWork sel_work(const SelPlan& p, int w) {
-  const int per = p.HU / p.HS;
-  const int it = w / per, sub = w - it * per;
-  const int4 v = __ldg(reinterpret_cast<const int4*>(p.items) + it);
-  SelWork k;
-  const int unit = v.x * per + sub;  // b * HU + unit of the batch entry
-  k.b = unit / p.HU;
-  k.head0 = (unit - k.b * p.HU) * p.G;
-  k.block = v.y;
-  k.first = v.z;
-  k.count = v.w;
-  k.unit = unit;
-  return k;
+
+// A CTA's items, in order, every role for itself: works blockIdx.x,
+// blockIdx.x + gridDim.x, ...; the one behind the current one is read ahead.
+// (Read where they are used, items and entries put two trips to memory into
+// every tile's chain: 731 us instead of what the copies allow.)
+struct SelWalk {
+  int w, works, first, count;  // entries of the current item
+  int4 raw, next;
+
+  __device__ __forceinline__ SelWalk(const SelPlan& p, int all) : w(blockIdx.x), works(all) {
+    raw = read(p, w);
+    next = read(p, w + gridDim.x);
+    first = raw.z;
+    count = raw.w;
+  }
+  __device__ __forceinline__ int4 read(const SelPlan& p, int at) const {
+    return at < works ? __ldg(reinterpret_cast<const int4*>(p.items) + at / (p.HU / p.HS)) : int4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ bool more() const { return w < works; }
+  __device__ __forceinline__ void advance(const SelPlan& p) {
+    w += gridDim.x;
+    raw = next;
+    next = read(p, w + gridDim.x);
+    first = raw.z;
+    count = raw.w;
+  }
+  __device__ __forceinline__ SelWork get(const SelPlan& p) const {
+    const int per = p.HU / p.HS;
+    SelWork k;
+    k.unit = raw.x * per + w % per;  // b * HU + unit of the batch entry
+    k.b = k.unit / p.HU;
+    k.head0 = (k.unit - k.b * p.HU) * p.G;
+    k.block = raw.y;
+    return k;
+  }
+};
+constexpr unsigned kNoEntry = 0xffffffffu;
+// Entry e of the walk's item, for a row with a place in the tile.
+__device__ __forceinline__ unsigned entry_of(const SelPlan& p, const SelWalk& k, int e, bool place) {
+  return place && e < k.count ? __ldg(p.entries + k.first + e) : kNoEntry;
 }
 
 // A [B][heads][N][d] bf16 view (strides in bytes).
@@ -85,11 +112,14 @@ struct SelRows {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// This thread's arrival on `bar` once its copies so far have landed.  The one
+// that waits for them and hands them to the tensor core puts the proxy fence
+// between the two: a fence of each copying warp held up its next copies (731
+// us instead of @@ for the forward at 16384 queries x 32 heads).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Step kk of 16 along d of a K-major operand of `rows` rows.
 __device__ __forceinline__ uint32_t step_off(int kk, int rows) { return (kk >> 2) * (rows * 128) + (kk & 3) * 32; }

@@ -29,8 +29,6 @@ struct SelFwdLayout {
   static constexpr int kMmaWarp = kGatherWarp + kGatherWarps, kLoadWarp = kMmaWarp + 1;
   static constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps + 4);
   static constexpr int kMaxSlots = 8;
-  // Copies of a slot are waited for when two more have been issued.
-  static constexpr int kLag = 2;
   // k_full[2], k_empty[2], q_full[8], q_empty[8], s_full[4], s_empty[4], done
   static constexpr int kKFull = 0, kKEmpty = 2, kQFull = 4, kQEmpty = 12, kSFull = 20, kSEmpty = 24, kDone = 28;
   static constexpr int kNumBars = 29;
@@ -108,7 +106,7 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       int count = 1;
-      if (i >= L::kQFull && i < L::kQEmpty) count = L::kGatherWarps;
+      if (i >= L::kQFull && i < L::kQEmpty) count = 32 * L::kGatherWarps;
       if (i >= L::kSEmpty && i < L::kDone) count = 4;  // the warps of a warpgroup
       mbar_init(bar(i), count);
     }
@@ -136,46 +134,41 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
     // lanes 0-15 hold the addresses of side 1's rows, lanes 16-31 those of side 2's
     const int r = first + (lane & 15), ql = r / G, hl = r - ql * G;
     const SelRows rows = lane < 16 ? a.r1 : a.r2;
-    // a slot's copies have landed: the tensor core may read them
-    auto landed = [&](int m) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kQFull + m % a.slots));
-    };
     int m = 0;  // slots filled
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < works; w += gridDim.x) {
-      const SelWork k = sel_work(a.p, w);
-      for (int e0 = 0; ok && e0 < k.count; e0 += per_tile) {
-        // (rows past the last are not read: what the slot holds there gives scores that nobody takes)
-        const int e = e0 + ql;
-        const bool on = ql < per_tile && e < k.count;
-        const int i = on ? int(__ldg(a.p.entries + k.first + e) >> kSlotBits) : 0;
-        const unsigned long long at = on ? reinterpret_cast<unsigned long long>(rows.at(k.b, k.head0 + hl, i)) : 0ull;
+    SelWalk walk(a.p, works);
+    int e0 = 0;
+    unsigned ent = entry_of(a.p, walk, ql, ql < per_tile);
+    SelWork k = walk.get(a.p);
+    while (ok && walk.more()) {
+      // (rows past the last are not read: what the slot holds there gives scores that nobody takes)
+      const unsigned long long at = ent != kNoEntry ? reinterpret_cast<unsigned long long>(
+                                                          rows.at(k.b, k.head0 + hl, int(ent >> kSlotBits)))
+                                                    : 0ull;
+      e0 += per_tile;
+      if (e0 >= walk.count) {
+        walk.advance(a.p);
+        e0 = 0;
+        k = walk.get(a.p);
+      }
+      ent = entry_of(a.p, walk, e0 + ql, ql < per_tile);
 #pragma unroll
-        for (int side = 0; side < 2; ++side, ++m) {
-          const int s = m % a.slots;
-          ok = mbar_wait_warp(bar(L::kQEmpty + s), ((m / a.slots) & 1) ^ 1, ctl);
-          if (!ok) break;
-          if (side == 0) gather_rows<D1, 16, false>(sb + oQ + s * kSlot, first, at, 0, a.r1.chunks);
-          else gather_rows<D2, 16, false>(sb + oQ + s * kSlot, first, at, 16, a.r2.chunks);
-          cp_async_commit();
-          if (m >= L::kLag) {
-            cp_async_wait<L::kLag>();
-            landed(m - L::kLag);
-          }
-        }
+      for (int side = 0; side < 2; ++side, ++m) {
+        const int s = m % a.slots;
+        ok = mbar_wait_warp(bar(L::kQEmpty + s), ((m / a.slots) & 1) ^ 1, ctl);
+        if (!ok) break;
+        if (side == 0) gather_rows<D1, 16, false>(sb + oQ + s * kSlot, first, at, 0, a.r1.chunks);
+        else gather_rows<D2, 16, false>(sb + oQ + s * kSlot, first, at, 16, a.r2.chunks);
+        cp_async_arrive(bar(L::kQFull + s));
       }
     }
-    cp_async_wait<0>();
-    if (ok)
-      for (int x = m > L::kLag ? m - L::kLag : 0; x < m; ++x) landed(x);
+    cp_async_wait_all();
   } else if (warp >= L::kMmaWarp) {
     if (warp == L::kLoadWarp && lane == 0) {
       // -------------------------------------------------------------- K
       int items = 0;
-      for (int w = blockIdx.x; w < works; w += gridDim.x, ++items) {
-        const SelWork k = sel_work(a.p, w);
+      for (SelWalk walk(a.p, works); walk.more(); walk.advance(a.p), ++items) {
+        const SelWork k = walk.get(a.p);
         const int kb = items % a.k_bufs, hu = k.head0 / G;
         if (!mbar_wait_polled(bar(L::kKEmpty + kb), ((items / a.k_bufs) & 1) ^ 1, ctl)) break;
         const uint32_t full = bar(L::kKFull + kb);
@@ -196,8 +189,8 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
       const uint32_t idesc = idesc_bf16(128, bs, 0, 0);
       int n = 0, m = 0, items = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < works; w += gridDim.x, ++items) {
-        const int count = sel_work(a.p, w).count;
+      for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
+        const int count = walk.count;
         const int kb = items % a.k_bufs;
         ok = mbar_wait_warp(bar(L::kKFull + kb), (items / a.k_bufs) & 1, ctl);
         const uint64_t k1d = sdesc_sw128(sb + kb * kK, 16, 1024), k2d = sdesc_sw128(sb + kb * kK + kK1, 16, 1024);
@@ -208,6 +201,7 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
           ok = mbar_wait_warp(bar(L::kSEmpty + i), ((n / bufs) & 1) ^ 1, ctl) &&
                mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
           if (!ok) break;
+          fence_proxy_async_smem();  // (copies of cp.async)
           tc_fence_after();
           const uint64_t q1d = sdesc_sw128(sb + oQ + s * kSlot, 16, 1024);
 #pragma unroll
@@ -218,6 +212,7 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
           s = m % a.slots;
           ok = mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
           if (!ok) break;
+          fence_proxy_async_smem();  // (copies of cp.async)
           tc_fence_after();
           const uint64_t q2d = sdesc_sw128(sb + oQ + s * kSlot, 16, 1024);
 #pragma unroll
@@ -240,48 +235,55 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
     const float c1 = a.scale1 * kLog2e, c2 = a.scale2 * kLog2e;
     const int nqt = (a.p.NQ + kTile - 1) / kTile, nkt = (a.p.NK + kTile - 1) / kTile;
     const int off = a.p.NK - a.p.NQ;
-    int n = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; ok && w < works; w += gridDim.x) {
-      const SelWork k = sel_work(a.p, w);
-      const int k0 = k.block * bs;
-      const int prefix = a.p.prefix != nullptr ? min(max(a.p.prefix[k.b], 0), a.p.NK) : 0;
-      for (int e0 = 0; ok && e0 < k.count; e0 += per_tile, ++n) {
-        if (n % L::kWGs != wg) continue;
-        const int buf = n % bufs;
-        const int e = e0 + ql;
-        const bool on = ql < per_tile && e < k.count;
-        const unsigned ent = on ? __ldg(a.p.entries + k.first + e) : 0u;
-        const int i = int(ent >> kSlotBits), t = int(ent & ((1u << kSlotBits) - 1u));
-        int id = 0;
-        const int* kids = nullptr;
-        if (a.vis.ids_q != nullptr) {
-          id = a.vis.ids_q[size_t(k.b) * nqt * kTile + i];
-          kids = a.vis.ids_k + size_t(k.b) * nkt * kTile + k0;
-        }
-        const int last = a.p.causal ? min(max(i + off + 1, prefix), a.p.NK) : a.p.NK;
-        const bool whole = __all_sync(0xffffffffu, !on || last >= k0 + bs) && kids == nullptr;
-        const bool idle = __all_sync(0xffffffffu, !on);
-        ok = mbar_wait_warp(bar(L::kSFull + buf), (n / bufs) & 1, ctl);
-        if (!ok) break;
-        tc_fence_after();
-        ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
-        if (!idle) {
-          const uint32_t ts = tmem + lane_off + uint32_t(buf * 2 * bs);
-          if (whole) block_sums<false>(ts, bs, c1, c2, i, k0, a, prefix, id, kids, st);
-          else block_sums<true>(ts, bs, c1, c2, i, k0, a, prefix, id, kids, st);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kSEmpty + buf));
-        const size_t at = (size_t(k.b * a.p.H + k.head0 + hl) * a.p.NQ + i) * a.p.T + t;
-        if (on && SKL_CHECK(a.status, i < a.p.NQ && t < a.p.T && k.head0 + hl < a.p.H && k.b < a.p.B)) {
-          // a row that ids hide the whole block from has sums of 2^(-3e38 - ...) = 0, relative to nothing
-          const bool none = st.m1 == -INFINITY && st.l1 == 0.f;
-          a.rec[at] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(st.m1, st.m2, st.l1, st.l2);
-          a.acc[at] = none ? 0.f : st.acc;
-        }
+    const bool place = ql < per_tile;
+    SelWalk walk(a.p, works);
+    int e0 = 0, n = wg;
+    // to this warpgroup's next tile
+    auto skip = [&](int tiles) {
+      e0 += tiles * per_tile;
+      while (walk.more() && e0 >= walk.count) {
+        e0 -= (walk.count + per_tile - 1) / per_tile * per_tile;
+        walk.advance(a.p);
       }
+    };
+    skip(wg);
+    unsigned ent = entry_of(a.p, walk, e0 + ql, place);
+    while (walk.more()) {
+      const SelWork k = walk.get(a.p);
+      const int k0 = k.block * bs, buf = n % bufs;
+      const int prefix = a.p.prefix != nullptr ? min(max(a.p.prefix[k.b], 0), a.p.NK) : 0;
+      const bool on = ent != kNoEntry;
+      const int i = on ? int(ent >> kSlotBits) : 0, t = int(ent & ((1u << kSlotBits) - 1u));
+      skip(L::kWGs);
+      ent = entry_of(a.p, walk, e0 + ql, place);
+      int id = 0;
+      const int* kids = nullptr;
+      if (a.vis.ids_q != nullptr) {
+        id = a.vis.ids_q[size_t(k.b) * nqt * kTile + i];
+        kids = a.vis.ids_k + size_t(k.b) * nkt * kTile + k0;
+      }
+      const int last = a.p.causal ? min(max(i + off + 1, prefix), a.p.NK) : a.p.NK;
+      const bool whole = __all_sync(0xffffffffu, !on || last >= k0 + bs) && kids == nullptr;
+      const bool idle = __all_sync(0xffffffffu, !on);
+      if (!mbar_wait_warp(bar(L::kSFull + buf), (n / bufs) & 1, ctl)) break;
+      tc_fence_after();
+      ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
+      if (!idle) {
+        const uint32_t ts = tmem + lane_off + uint32_t(buf * 2 * bs);
+        if (whole) block_sums<false>(ts, bs, c1, c2, i, k0, a, prefix, id, kids, st);
+        else block_sums<true>(ts, bs, c1, c2, i, k0, a, prefix, id, kids, st);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kSEmpty + buf));
+      const size_t at = (size_t(k.b * a.p.H + k.head0 + hl) * a.p.NQ + i) * a.p.T + t;
+      if (on && SKL_CHECK(a.status, i < a.p.NQ && t < a.p.T && k.head0 + hl < a.p.H && k.b < a.p.B)) {
+        // a row that ids hide the whole block from has sums of 2^(-3e38 - ...) = 0, relative to nothing
+        const bool none = st.m1 == -INFINITY && st.l1 == 0.f;
+        a.rec[at] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(st.m1, st.m2, st.l1, st.l2);
+        a.acc[at] = none ? 0.f : st.acc;
+      }
+      n += L::kWGs;
     }
   }
 
