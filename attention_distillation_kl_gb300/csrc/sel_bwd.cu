@@ -177,9 +177,9 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
           // (the tile whose parameters these replace has been through dQ: kRows tiles cannot be under way)
           params[(n % L::kRows) * kTile + r] = par;
           row_of[(n % L::kRows) * kTile + r] = on ? x.row : -1;
-          gather_rows<DO, 32, true>(sb + oQ + s * L::kSlot, first, on ? x.po : 0ull, 0, ro.chunks);
+          gather_rows<DO, true>(sb + oQ + s * L::kSlot, first, on ? x.po : 0ull, ro.chunks);
         } else {
-          gather_rows<DG, 32, true>(sb + oQ + s * L::kSlot, first, on ? x.pg : 0ull, 0, rg.chunks);
+          gather_rows<DG, true>(sb + oQ + s * L::kSlot, first, on ? x.pg : 0ull, rg.chunks);
         }
         cp_async_arrive(bar(L::kQFull + s));
         __syncwarp();

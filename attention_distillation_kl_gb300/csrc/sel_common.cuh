@@ -124,25 +124,42 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // Step kk of 16 along d of a K-major operand of `rows` rows.
 __device__ __forceinline__ uint32_t step_off(int kk, int rows) { return (kk >> 2) * (rows * 128) + (kk & 3) * 32; }
 
-// Copies ROWS rows, at most 32 (lane `from` + r holds the address of row r;
-// null: not copied, or with ZERO zeros), into rows [first, first + ROWS) of a
-// [128][D] operand tile, 16 bytes a lane, swizzled as TMA would.  Called by a
-// whole warp.
-template <int D, int ROWS, bool ZERO>
-__device__ __forceinline__ void gather_rows(uint32_t tile, int first, unsigned long long mine, int from, int chunks) {
-  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at a time
-  const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
-  const uint32_t dst = tile + (c >> 3) * (kTile * 128) + first * 128;
-  const bool in = c < chunks;
-  const uint32_t off = c * 16;
+// Copies 32 rows (lane r holds the address of row r; 0: not copied, or with
+// ZERO zeros) into rows [first, first + 32) of a [128][D] operand tile,
+// swizzled as TMA would: 64 bytes of 8 rows at a time, so that all but four
+// addresses a lane are constants away.  Called by a whole warp.
+template <int D, bool ZERO>
+__device__ __forceinline__ void gather_rows(uint32_t tile, int first, unsigned long long mine, int chunks) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const uint32_t even = tile + (first + r) * 128 + ((c ^ r) << 4), odd = even ^ 64u;
 #pragma unroll
-  for (int r0 = 0; r0 < ROWS; r0 += kAtOnce) {
-    const int r = r0 + sub;
-    const unsigned long long p = __shfl_sync(0xffffffffu, mine, from + r);
-    const uint32_t to = dst + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-    if (p != 0 && in) cp_async16(to, reinterpret_cast<const uint8_t*>(p + off));
-    else if (ZERO && in) st_shared_v4(to, 0u, 0u, 0u, 0u);
+  for (int k = 0; k < 4; ++k) {
+    const unsigned long long row = __shfl_sync(0xffffffffu, mine, r + 8 * k);
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(row) + c * 16;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const uint32_t to = (j & 1 ? odd : even) + k * 1024 + (j >> 1) * (kTile * 128);
+      if (c + 4 * j < chunks) {
+        if (row != 0) cp_async16(to, p + 64 * j);
+        else if (ZERO) st_shared_v4(to, 0u, 0u, 0u, 0u);
+      }
+    }
   }
+}
+
+// D (+)= A B^T for `steps` of 16 along the contraction: operand descriptors by
+// their low words, which alone change (the address is their low 14 bits).
+__device__ __forceinline__ void mma_step(uint32_t leader, uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, q;\n\t}" ::"r"(d),
+      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
 }
 
 struct SelMaps {

@@ -2,14 +2,14 @@
 // pair, then their merge into KL, LSE1 and LSE2.
 //
 // Persistent CTAs walk the items: K1, K2 of the item's block once, then tiles
-// of 128 gathered rows, a side's tile at a time, through a ring of slots.  24 warps:
+// of 128 gathered rows, a side's tile at a time, through a ring of slots.  18 warps:
 //   warps 0-11  statistics: a warpgroup takes every third tile; thread = row
-//   warps 12-19 gather 16 rows each, 16 bytes a lane (cp.async).  TMA takes
+//   warps 12-15 gather 32 rows each, 16 bytes a lane (cp.async).  TMA takes
 //               some 50 clocks for a copy of few rows, whatever its form: at
 //               rows of 256 bytes out of L2 its gather of four reached 2.5
-//               TB/s, cp.async of 2, 4 and 8 warps 6, 11.6 and 14.3.
-//   warp 20     S1 = Q1 K1^T, S2 = Q2 K2^T into one of 4 TMEM buffers (2 for blocks of 128)
-//   warp 21     K by TMA
+//               TB/s, cp.async of 4 and 8 warps 11.6 and 14.3.
+//   warp 16     S1 = Q1 K1^T, S2 = Q2 K2^T into one of 4 TMEM buffers (2 for blocks of 128)
+//   warp 17     K by TMA
 // A row's keys in one block are few, so its references are its own largest
 // scores there (one more read of TMEM), and nothing is rescaled:
 //   e_t = S_t log2 e - m_t,  l_t = sum 2^e_t,  acc = sum 2^e1 (e1 - e2).
@@ -25,9 +25,9 @@ namespace {
 
 struct SelFwdLayout {
   static constexpr int kWGs = 3;  // of statistics
-  static constexpr int kGatherWarp = 4 * kWGs, kGatherWarps = 8;
+  static constexpr int kGatherWarp = 4 * kWGs, kGatherWarps = 4;
   static constexpr int kMmaWarp = kGatherWarp + kGatherWarps, kLoadWarp = kMmaWarp + 1;
-  static constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps + 4);
+  static constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps + 2);
   static constexpr int kMaxSlots = 8;
   // k_full[2], k_empty[2], q_full[8], q_empty[8], s_full[4], s_empty[4], done
   static constexpr int kKFull = 0, kKEmpty = 2, kQFull = 4, kQEmpty = 12, kSFull = 20, kSEmpty = 24, kDone = 28;
@@ -129,37 +129,39 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
   const int works = min(*a.p.item_count, a.p.max_items) * (a.p.HU / a.p.HS);
 
   if (warp >= L::kGatherWarp && warp < L::kMmaWarp) {
-    // ---------------------------------------------------------------- gather: rows [first, first + 16)
-    const int first = (warp - L::kGatherWarp) * 16;
-    // lanes 0-15 hold the addresses of side 1's rows, lanes 16-31 those of side 2's
-    const int r = first + (lane & 15), ql = r / G, hl = r - ql * G;
-    const SelRows rows = lane < 16 ? a.r1 : a.r2;
-    int m = 0;  // slots filled
+    // ---------------------------------------------------------------- gather: rows [first, first + 32)
+    const int first = (warp - L::kGatherWarp) * 32;
+    const int r = first + lane, ql = r / G, hl = r - ql * G;
+    const bool place = ql < per_tile;
+    int s = 0, m = 0;  // the slot, and how often the ring has been round
     bool ok = true;
     SelWalk walk(a.p, works);
     int e0 = 0;
-    unsigned ent = entry_of(a.p, walk, ql, ql < per_tile);
+    unsigned ent = entry_of(a.p, walk, ql, place);
     SelWork k = walk.get(a.p);
+    const uint8_t *b1 = a.r1.at(k.b, k.head0 + hl, 0), *b2 = a.r2.at(k.b, k.head0 + hl, 0);
     while (ok && walk.more()) {
       // (rows past the last are not read: what the slot holds there gives scores that nobody takes)
-      const unsigned long long at = ent != kNoEntry ? reinterpret_cast<unsigned long long>(
-                                                          rows.at(k.b, k.head0 + hl, int(ent >> kSlotBits)))
-                                                    : 0ull;
+      const int i = int(ent >> kSlotBits);
+      const unsigned long long p1 = ent != kNoEntry ? reinterpret_cast<unsigned long long>(b1 + i * a.r1.sn) : 0ull;
+      const unsigned long long p2 = ent != kNoEntry ? reinterpret_cast<unsigned long long>(b2 + i * a.r2.sn) : 0ull;
       e0 += per_tile;
       if (e0 >= walk.count) {
         walk.advance(a.p);
         e0 = 0;
         k = walk.get(a.p);
+        b1 = a.r1.at(k.b, k.head0 + hl, 0);
+        b2 = a.r2.at(k.b, k.head0 + hl, 0);
       }
-      ent = entry_of(a.p, walk, e0 + ql, ql < per_tile);
+      ent = entry_of(a.p, walk, e0 + ql, place);
 #pragma unroll
-      for (int side = 0; side < 2; ++side, ++m) {
-        const int s = m % a.slots;
-        ok = mbar_wait_warp(bar(L::kQEmpty + s), ((m / a.slots) & 1) ^ 1, ctl);
+      for (int side = 0; side < 2; ++side) {
+        ok = mbar_wait_warp(bar(L::kQEmpty + s), (m & 1) ^ 1, ctl);
         if (!ok) break;
-        if (side == 0) gather_rows<D1, 16, false>(sb + oQ + s * kSlot, first, at, 0, a.r1.chunks);
-        else gather_rows<D2, 16, false>(sb + oQ + s * kSlot, first, at, 16, a.r2.chunks);
+        if (side == 0) gather_rows<D1, false>(sb + oQ + s * kSlot, first, p1, a.r1.chunks);
+        else gather_rows<D2, false>(sb + oQ + s * kSlot, first, p2, a.r2.chunks);
         cp_async_arrive(bar(L::kQFull + s));
+        if (++s == a.slots) s = 0, ++m;
       }
     }
     cp_async_wait_all();
@@ -187,40 +189,35 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
       // -------------------------------------------------------------- MMA issuer
       const uint32_t leader = elect_one();
       const uint32_t idesc = idesc_bf16(128, bs, 0, 0);
-      int n = 0, m = 0, items = 0;
+      const uint32_t dhi = uint32_t(sdesc_sw128(0, 16, 1024) >> 32), dlo = uint32_t(sdesc_sw128(0, 16, 1024));
+      int n = 0, s = 0, m = 0, items = 0;
       bool ok = true;
+      // S of one side: the tile in slot s by K at ks
+      auto product = [&](auto width, uint32_t d, uint32_t ks) {
+        constexpr int D = decltype(width)::value;
+        ok = mbar_wait_warp(bar(L::kQFull + s), m & 1, ctl);
+        if (!ok) return;
+        fence_proxy_async_smem();  // (copies of cp.async)
+        tc_fence_after();
+        const uint32_t q = dlo + ((sb + oQ + s * kSlot) >> 4), kd = dlo + (ks >> 4), half = bs * 8;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_step(leader, d, q + (kk >> 2) * (kTile * 8) + (kk & 3) * 2, dhi, kd + (kk >> 2) * half + (kk & 3) * 2, dhi, idesc,
+                   kk > 0);
+        mma_commit(leader, bar(L::kQEmpty + s));
+        if (++s == a.slots) s = 0, ++m;
+      };
       for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
         const int count = walk.count;
         const int kb = items % a.k_bufs;
         ok = mbar_wait_warp(bar(L::kKFull + kb), (items / a.k_bufs) & 1, ctl);
-        const uint64_t k1d = sdesc_sw128(sb + kb * kK, 16, 1024), k2d = sdesc_sw128(sb + kb * kK + kK1, 16, 1024);
         for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
-          const int i = n % bufs;
-          const uint32_t d1 = tmem + uint32_t(i * 2 * bs), d2 = d1 + uint32_t(bs);
-          int s = m % a.slots;
-          ok = mbar_wait_warp(bar(L::kSEmpty + i), ((n / bufs) & 1) ^ 1, ctl) &&
-               mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
-          if (!ok) break;
-          fence_proxy_async_smem();  // (copies of cp.async)
-          tc_fence_after();
-          const uint64_t q1d = sdesc_sw128(sb + oQ + s * kSlot, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < D1 / 16; ++kk)
-            mma_bf16_ss(leader, d1, sdesc_add(q1d, step_off(kk, kTile)), sdesc_add(k1d, step_off(kk, bs)), idesc, kk > 0);
-          mma_commit(leader, bar(L::kQEmpty + s));
-          ++m;
-          s = m % a.slots;
-          ok = mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
-          if (!ok) break;
-          fence_proxy_async_smem();  // (copies of cp.async)
-          tc_fence_after();
-          const uint64_t q2d = sdesc_sw128(sb + oQ + s * kSlot, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < D2 / 16; ++kk)
-            mma_bf16_ss(leader, d2, sdesc_add(q2d, step_off(kk, kTile)), sdesc_add(k2d, step_off(kk, bs)), idesc, kk > 0);
-          mma_commit(leader, bar(L::kQEmpty + s));
-          ++m;
-          mma_commit(leader, bar(L::kSFull + i));
+          const int i = n & (bufs - 1);
+          const uint32_t d1 = tmem + uint32_t(i * 2 * bs);
+          ok = mbar_wait_warp(bar(L::kSEmpty + i), ((n / bufs) & 1) ^ 1, ctl);
+          if (ok) product(std::integral_constant<int, D1>{}, d1, sb + kb * kK);
+          if (ok) product(std::integral_constant<int, D2>{}, d1 + uint32_t(bs), sb + kb * kK + kK1);
+          if (ok) mma_commit(leader, bar(L::kSFull + i));
         }
         if (ok) mma_commit(leader, bar(L::kKEmpty + kb));
       }
@@ -238,23 +235,31 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
     const bool place = ql < per_tile;
     SelWalk walk(a.p, works);
     int e0 = 0, n = wg;
-    // to this warpgroup's next tile
+    // to this warpgroup's next tile; whether that is of another item
     auto skip = [&](int tiles) {
-      e0 += tiles * per_tile;
-      while (walk.more() && e0 >= walk.count) {
+      bool other = false;
+      for (e0 += tiles * per_tile; walk.more() && e0 >= walk.count; other = true) {
         e0 -= (walk.count + per_tile - 1) / per_tile * per_tile;
         walk.advance(a.p);
       }
+      return other;
     };
     skip(wg);
     unsigned ent = entry_of(a.p, walk, e0 + ql, place);
-    while (walk.more()) {
-      const SelWork k = walk.get(a.p);
-      const int k0 = k.block * bs, buf = n % bufs;
-      const int prefix = a.p.prefix != nullptr ? min(max(a.p.prefix[k.b], 0), a.p.NK) : 0;
+    SelWork k;
+    size_t first = 0;  // record of the row's query 0
+    int prefix = 0;
+    for (bool other = true, more = walk.more(); more;) {
+      if (other) {
+        k = walk.get(a.p);
+        first = size_t(k.b * a.p.H + k.head0 + hl) * a.p.NQ * a.p.T;
+        if (a.p.prefix != nullptr) prefix = min(max(a.p.prefix[k.b], 0), a.p.NK);
+      }
+      const int k0 = k.block * bs, buf = n & (bufs - 1);
       const bool on = ent != kNoEntry;
       const int i = on ? int(ent >> kSlotBits) : 0, t = int(ent & ((1u << kSlotBits) - 1u));
-      skip(L::kWGs);
+      other = skip(L::kWGs);
+      more = walk.more();
       ent = entry_of(a.p, walk, e0 + ql, place);
       int id = 0;
       const int* kids = nullptr;
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kSEmpty + buf));
-      const size_t at = (size_t(k.b * a.p.H + k.head0 + hl) * a.p.NQ + i) * a.p.T + t;
+      const size_t at = first + size_t(i) * a.p.T + t;
       if (on && SKL_CHECK(a.status, i < a.p.NQ && t < a.p.T && k.head0 + hl < a.p.H && k.b < a.p.B)) {
         // a row that ids hide the whole block from has sums of 2^(-3e38 - ...) = 0, relative to nothing
         const bool none = st.m1 == -INFINITY && st.l1 == 0.f;
