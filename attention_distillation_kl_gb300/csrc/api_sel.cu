@@ -98,7 +98,7 @@ void take_plan(Carver& c, SelPlan& p) {
 // CTA should be a small part of what it does.
 int item_tiles(const SelPlan& p, int sms, int most) {
   const double tiles = double(p.B) * p.HU * p.NQ * p.T / p.queries_per_tile;
-  return int(std::max(1.0, std::min(double(most), tiles / (16.0 * std::max(sms, 1)))));
+  return int(std::max(1.0, std::min(double(most), tiles / (8.0 * std::max(sms, 1)))));
 }
 
 struct FwdPlan {
@@ -131,6 +131,7 @@ struct BwdPlan {
   float* dq32 = nullptr;
   unsigned* kmax = nullptr;
   float* dk_part = nullptr;
+  float4* rows = nullptr;
   int pitch = 0;
   size_t bytes = 0;
 };
@@ -152,6 +153,7 @@ BwdPlan bwd_plan(const streamkl_side& p1, const streamkl_side& p2, const streamk
   f.g.p.tiles_per_item = item_tiles(f.g.p, sms, 32);
   take_plan(c, f.g.p);
   f.g.p.ranges = c.take<int2>(size_t(B) * sel.heads * f.g.p.blocks);
+  f.rows = c.take<float4>(size_t(B) * H * NQ);
   f.dk_part = c.take<float>(size_t(f.g.p.max_items) * (f.g.p.HU / f.g.p.HS) * sel.block * g.d);
   f.bytes = c.used;
   return f;
@@ -261,6 +263,7 @@ int streamkl_bwd_sel(const streamkl_side* p1, const streamkl_side* p2, const str
   a.pitch = f.pitch;
   a.dq32 = f.dq32;
   a.dk_part = f.dk_part;
+  a.rows = f.rows;
   a.kmax = f.kmax;
   a.dk = dk->data;
   a.dk_sb = B > 1 ? dk->stride_b : 0;

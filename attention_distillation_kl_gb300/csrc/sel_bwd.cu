@@ -6,20 +6,23 @@
 // Persistent CTAs walk the items.  dK of an item's block accumulates in TMEM
 // and leaves as one fp32 tile an item, which sel_dk_kernel adds in item order.
 // A row of dQ gets a contribution from each of its blocks, out of different
-// CTAs: fp32 reduce-adds of whole rows, each value rounded to its row's grid
-// first (dq_fixed_exp), so that the sums are exact in any order and the result
-// is bitwise repeatable.  19 warps:
+// CTAs: fp32 vector reductions, each value rounded to its row's grid first
+// (dq_fixed_exp), so that the sums are exact in any order and the result is
+// bitwise repeatable.  19 warps:
 //   warps 0-7   dS (thread = row; a warpgroup takes half of the columns)
-//   warps 8-11  dQ: TMEM -> registers -> a row a thread in shared memory ->
-//               bulk reduce-add; after an item, dK
+//   warps 8-11  dQ: TMEM -> registers, four lanes to 8 values of a row, so that
+//               every reduction covers whole sectors; after an item, dK
 //   warps 12-15 gather 32 rows each of both sides, and the rows' parameters
+//               (sel_rows_kernel)
 //   warp 16     S1, S2      warp 17     dK, dQ      warp 18     K by TMA
-// TMEM: S1 [0, 128), S2 [128, 256), dK [256, 384), dQ [384, 512).
+// TMEM: S1, S2 of bs columns from 0; then, with blocks up to 64, dK [128, 256)
+// and two buffers of dQ, else dK [256, 384) and one.
 //
-// Bound by the reduce-adds: a row and block bring 4 dg bytes to L2, which takes
-// some 6 TB/s of them (measured alone: rows of 512 bytes over 16 to 64 MB,
-// 5.4 TB/s in pieces of 256 bytes, 2.8 of 128; vector reductions out of
-// registers, coalesced, 6.0), where the rows read take 14.
+// Bound by the reductions: a row and block bring 4 dg bytes to L2, which takes
+// some 6 TB/s of them (measured alone, rows of 512 bytes over 16 to 64 MB: 6.0
+// as vector reductions of whole sectors, 3.1 of half sectors, 5.4 and 2.8 as
+// bulk reductions in pieces of 256 and 128 bytes), where rows that are read
+// come at 14.
 #include "sel_common.cuh"
 
 namespace skl {
@@ -31,28 +34,63 @@ struct SelBwdLayout {
   static constexpr int kDsWarps = 8, kEpiWarp = 8, kGatherWarp = 12, kGatherWarps = 4;
   static constexpr int kSWarp = 16, kGradWarp = 17, kLoadWarp = 18;
   static constexpr int kThreads = 32 * 19;
-  static constexpr int kMaxRing = 8;   // slots of gathered tiles
-  static constexpr int kRows = 6;      // tiles whose rows' parameters are kept
+  static constexpr int kMaxRing = 6;   // slots of gathered tiles
+  // Tiles whose rows' parameters are kept.  Those of tile n are replaced with the copies of tile n + kRows, which wait
+  // for the dK of tile n + kRows - 1 - slots / 2 at least; that of n + 3 has waited for dQ of n + 2, and this one for
+  // the warps of dQ to have read tile n.
+  static constexpr int kRows = 7;
   enum {
     kKFull = 0, kKEmpty = 2, kReady = 4, kQFull = 6, kQEmpty = kQFull + kMaxRing, kSFull = kQEmpty + kMaxRing, kSFree,
-    kDsFull, kDsEmpty, kDqFull, kDqEmpty, kDkFull, kDkEmpty, kDone, kNumBars
+    kDsFull, kDsEmpty, kDqFull, kDqEmpty = kDqFull + 2, kDkFull = kDqEmpty + 2, kDkEmpty, kDone, kNumBars
   };
   static constexpr uint32_t kSlot = kTile * 2u * (D1 > D2 ? D1 : D2);
   static constexpr uint32_t kParams = kRows * kTile * 20u;
-  // operands, dS (64-key blocks of 128 rows), staged rows of dQ (padded by 16 bytes), parameters, barriers
-  static uint32_t bytes(int slots, int k_bufs, int piece, int bs) {
-    return 1024u + slots * kSlot + uint32_t(k_bufs * bs) * (D1 + D2) * 2u + ds_bytes(bs) + stage_bytes(piece) + kParams +
-           kNumBars * 8 + 16;
+  // operands, dS (64-key blocks of 128 rows), parameters, barriers
+  static uint32_t bytes(int slots, int k_bufs, int bs) {
+    return 1024u + slots * kSlot + uint32_t(k_bufs * bs) * (D1 + D2) * 2u + ds_bytes(bs) + kParams + kNumBars * 8 + 16;
   }
   __host__ __device__ static uint32_t ds_bytes(int bs) { return bs == 128 ? 32768u : 16384u; }
-  __host__ __device__ static uint32_t stage_bytes(int piece) { return kTile * (piece * 4u + 16u); }
   static constexpr uint32_t kMost = 232448;
+  static_assert(kRows - 1 - kMaxRing / 2 >= 3, "see kRows");
 };
 
-// Row bytes of shared memory into dQ: reduce-add of `bytes`, tracked by the thread's bulk groups.
-__device__ __forceinline__ void bulk_reduce_add(float* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-               : "memory");
+__device__ __forceinline__ void red_add2(float* p, float x, float y) {
+  asm volatile("red.global.add.v2.f32 [%0], {%1,%2};" ::"l"(p), "f"(x), "f"(y) : "memory");
+}
+
+// 64 columns of 16 rows, and the wait for them: lane l holds, for every 8
+// columns e, v[4 e] and v[4 e + 1]: row l / 4, columns 8 e + 2 (l % 4) and the
+// next; v[4 e + 2], v[4 e + 3]: the same of row l / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t t, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SKL_R8(v, 0), SKL_R8(v, 8), SKL_R8(v, 16), SKL_R8(v, 24)
+      : "r"(t)
+      : "memory");
+}
+
+constexpr int kRowThreads = 256;
+
+// What dS and dQ need of every row: na, nb, ws as in ds_chunk_row, and the
+// addend that rounds to its grid.  A row that saw nothing has na = -inf.
+__global__ void __launch_bounds__(kRowThreads) sel_rows_kernel(const __grid_constant__ SelBwdArgs a, int mode) {
+  const long long row = (long long)blockIdx.x * kRowThreads + threadIdx.x;
+  if (row >= (long long)a.p.B * a.p.H * a.p.NQ) return;
+  const bool p2 = mode == STREAMKL_GRAD_P2;
+  const float l1 = a.lse1[row], l2 = a.lse2[row], kl = a.kl[row], dkl = a.dkl[row], sg = p2 ? a.scale2 : a.scale1;
+  float4 par{-INFINITY, p2 ? -INFINITY : 0.f, 0.f, 0.f};
+  if (l1 != -INFINITY) {
+    const int bh = int(row / a.p.NQ), b = bh / a.p.H, h = bh - b * a.p.H;
+    const float kmax = __uint_as_float(a.kmax[b * a.HK + h / (a.p.H / a.HK)] << 16);
+    par.x = -l1 * kLog2e;
+    par.y = p2 ? -l2 * kLog2e : -(l1 - l2 + kl);
+    par.z = sg * dkl;
+    par.w = 1.5f * exp2_int(23 - dq_fixed_exp(mode, sg, dkl, kl, kmax));
+  }
+  a.rows[row] = par;
 }
 
 template <int D1, int D2, int MODE>
@@ -68,8 +106,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bs = a.p.bs;
   const uint32_t kK1 = uint32_t(bs) * D1 * 2, kK = uint32_t(bs) * (D1 + D2) * 2;
-  const uint32_t oDS = a.k_bufs * kK, oQ = oDS + L::ds_bytes(bs), oStage = oQ + a.slots * L::kSlot;
-  const uint32_t oParam = oStage + L::stage_bytes(a.piece), oBar = oParam + L::kParams;
+  const uint32_t oDS = a.k_bufs * kK, oQ = oDS + L::ds_bytes(bs), oParam = oQ + a.slots * L::kSlot, oBar = oParam + L::kParams;
   auto bar = [&](int id) { return sb + oBar + 8u * id; };
   float4* params = reinterpret_cast<float4*>(smem + oParam);                          // na, nb, ws, grid
   int* row_of = reinterpret_cast<int*>(smem + oParam + L::kRows * kTile * 16);        // row of dq32, or -1
@@ -82,7 +119,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       int count = 1;
       if (i >= L::kQFull && i < L::kQEmpty) count = 33 * L::kGatherWarps;
       if (i == L::kReady || i == L::kReady + 1 || i == L::kSFree || i == L::kDsFull) count = L::kDsWarps;
-      if (i == L::kDqEmpty || i == L::kDkEmpty) count = 4;
+      if (i == L::kDqEmpty || i == L::kDqEmpty + 1 || i == L::kDkEmpty) count = 4;
       if (i == L::kDone) count = 2;
       mbar_init(bar(i), count);
     }
@@ -101,7 +138,8 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t t_s1 = tmem, t_s2 = tmem + 128, t_dk = tmem + 256, t_dq = tmem + 384;
+  const int dq_bufs = bs == 128 ? 1 : 2;
+  const uint32_t t_s1 = tmem, t_s2 = tmem + bs, t_dk = tmem + (bs == 128 ? 256 : 128), t_dq = t_dk + 128;
   const int per_tile = a.p.queries_per_tile, G = a.p.G;
   const int works = min(*a.p.item_count, a.p.max_items) * (a.p.HU / a.p.HS);
   const bool ids = a.vis.ids_q != nullptr;
@@ -112,82 +150,76 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     const int r = first + lane, ql = r / G, hl = r - ql * G;
     const SelRows& ro = kP2 ? a.r1 : a.r2;
     const SelRows& rg = kP2 ? a.r2 : a.r1;
-    const float sg = kP2 ? a.scale2 : a.scale1;
-    const int ug = kP2 ? a.u2 : a.u1;
-    // A row's pointers and numbers are read a tile ahead of its copies, its entry two tiles.
-    struct Row {
-      unsigned long long po, pg;
-      float l1, l2, kl, dkl, kmax;
-      int row;  // -1: none
-    };
-    auto row_of_entry = [&](const SelWork& k, unsigned ent) {
-      Row x{0ull, 0ull, -INFINITY, 0.f, 0.f, 0.f, 0.f, -1};
-      const int i = int(ent >> kSlotBits), h = k.head0 + hl;
-      if (ent == kNoEntry || !SKL_CHECK(a.status, i < a.p.NQ && h < a.p.H && k.b < a.p.B)) return x;
-      x.row = (k.b * a.p.H + h) * a.p.NQ + i;
-      x.po = reinterpret_cast<unsigned long long>(ro.at(k.b, h, i));
-      x.pg = reinterpret_cast<unsigned long long>(rg.at(k.b, h, i));
-      x.l1 = __ldg(a.lse1 + x.row);
-      x.l2 = __ldg(a.lse2 + x.row);
-      x.kl = __ldg(a.kl + x.row);
-      x.dkl = __ldg(a.dkl + x.row);
-      x.kmax = __uint_as_float(__ldg(a.kmax + k.b * a.HK + (k.head0 / G) / ug) << 16);
-      return x;
-    };
+    const bool place = ql < per_tile;
     SelWalk walk(a.p, works);
-    int e0 = 0, m = 0, n = 0;
-    bool ok = true;
-    auto step = [&]() {
+    int e0 = 0;
+    // the lane's row 0 of both sides and its number, in the current item
+    const uint8_t *bo = nullptr, *bg = nullptr;
+    int row0 = 0;
+    auto enter = [&]() {
+      const SelWork k = walk.get(a.p);
+      bo = ro.at(k.b, k.head0 + hl, 0);
+      bg = rg.at(k.b, k.head0 + hl, 0);
+      row0 = (k.b * a.p.H + k.head0 + hl) * a.p.NQ;
+    };
+    // A row's parameters are read a tile ahead of its copies, its entry two tiles.
+    unsigned ent = entry_of(a.p, walk, ql, place);
+    unsigned long long po = 0, pg = 0;  // of the tile to copy
+    float4 par;
+    int row = -1;
+    auto look = [&]() {  // at the row of `ent`
+      po = pg = 0;
+      par = make_float4(-INFINITY, kP2 ? -INFINITY : 0.f, 0.f, 0.f);
+      row = -1;
+      if (ent == kNoEntry) return;
+      const int i = int(ent >> kSlotBits);
+      if (!SKL_CHECK(a.status, i < a.p.NQ)) return;
+      row = row0 + i;
+      par = __ldg(a.rows + row);
+      po = reinterpret_cast<unsigned long long>(bo + i * ro.sn);
+      pg = reinterpret_cast<unsigned long long>(bg + i * rg.sn);
+    };
+    auto step = [&]() {  // to the next tile's entry
       e0 += per_tile;
       if (e0 >= walk.count) {
         walk.advance(a.p);
         e0 = 0;
+        enter();
       }
-    };
-    const bool place = ql < per_tile;
-    bool more = walk.more();  // a tile to copy
-    Row x = row_of_entry(walk.get(a.p), entry_of(a.p, walk, ql, place));
-    step();
-    bool next = walk.more();
-    SelWork k = walk.get(a.p);
-    unsigned ent = entry_of(a.p, walk, e0 + ql, place);
-    while (ok && more) {
-      const Row y = row_of_entry(k, next ? ent : kNoEntry);
-      const bool then = next;
-      step();
-      next = walk.more();
-      k = walk.get(a.p);
       ent = entry_of(a.p, walk, e0 + ql, place);
-      // na, nb, ws as in ds_chunk_row.  Rows that saw nothing (they may hold
-      // anything) and rows past the last are zeros, and contribute zeros.
-      const bool on = x.row >= 0 && x.l1 != -INFINITY;
-      float4 par{-INFINITY, kP2 ? -INFINITY : 0.f, 0.f, 0.f};
-      if (on) {
-        par.x = -x.l1 * kLog2e;
-        par.y = kP2 ? -x.l2 * kLog2e : -(x.l1 - x.l2 + x.kl);
-        par.z = sg * x.dkl;
-        par.w = 1.5f * exp2_int(23 - dq_fixed_exp(MODE, sg, x.dkl, x.kl, x.kmax));
-      }
+    };
+    int s = 0, m = 0, n = 0;  // slot, rounds of the ring, place of the tile's parameters
+    bool ok = true, more = walk.more();
+    enter();
+    look();
+    step();
+    while (ok && more) {
+      more = walk.more();
+      const unsigned long long xo = po, xg = pg;
+      const float4 x = par;
+      const int of = row;
+      look();
+      step();
+      // rows that saw nothing (they may hold anything) and rows past the last
+      // are zeros, and contribute zeros
+      const bool on = of >= 0 && x.x != -INFINITY;
 #pragma unroll
-      for (int side = 0; side < 2; ++side, ++m) {
-        const int s = m % a.slots;
-        ok = mbar_wait_warp(bar(L::kQEmpty + s), ((m / a.slots) & 1) ^ 1, ctl);
+      for (int side = 0; side < 2; ++side) {
+        ok = mbar_wait_warp(bar(L::kQEmpty + s), (m & 1) ^ 1, ctl);
         if (!ok) break;
         if (side == 0) {
-          // (the tile whose parameters these replace has been through dQ: kRows tiles cannot be under way)
-          params[(n % L::kRows) * kTile + r] = par;
-          row_of[(n % L::kRows) * kTile + r] = on ? x.row : -1;
-          gather_rows<DO, true>(sb + oQ + s * L::kSlot, first, on ? x.po : 0ull, ro.chunks);
+          params[n * kTile + r] = x;
+          row_of[n * kTile + r] = on ? of : -1;
+          if (++n == L::kRows) n = 0;
+          gather_rows<DO, true>(sb + oQ + s * L::kSlot, first, on ? xo : 0ull, ro.chunks);
         } else {
-          gather_rows<DG, true>(sb + oQ + s * L::kSlot, first, on ? x.pg : 0ull, rg.chunks);
+          gather_rows<DG, true>(sb + oQ + s * L::kSlot, first, on ? xg : 0ull, rg.chunks);
         }
         cp_async_arrive(bar(L::kQFull + s));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kQFull + s));  // parameters and zeros, which are plain stores
+        if (++s == a.slots) s = 0, ++m;
       }
-      x = y;
-      more = then;
-      ++n;
     }
     cp_async_wait_all();
   } else if (warp == L::kLoadWarp) {
@@ -215,37 +247,37 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     // ---------------------------------------------------------------- S issuer
     const uint32_t leader = elect_one();
     const uint32_t idesc = idesc_bf16(128, bs, 0, 0);
-    auto product = [&](auto width, uint32_t d, uint32_t q, uint32_t ks) {
+    const uint32_t dhi = uint32_t(sdesc_sw128(0, 16, 1024) >> 32), dlo = uint32_t(sdesc_sw128(0, 16, 1024));
+    int n = 0, s = 0, m = 0, items = 0;
+    bool ok = true;
+    auto product = [&](auto width, uint32_t d, uint32_t ks) {  // the tile in slot s by K at ks
       constexpr int D = decltype(width)::value;
-      const uint64_t qd = sdesc_sw128(q, 16, 1024), kd = sdesc_sw128(ks, 16, 1024);
+      ok = mbar_wait_warp(bar(L::kQFull + s), m & 1, ctl);
+      if (!ok) return;
+      fence_proxy_async_smem();  // (copies of cp.async)
+      tc_fence_after();
+      const uint32_t q = dlo + ((sb + oQ + s * L::kSlot) >> 4), kd = dlo + (ks >> 4), half = bs * 8;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(leader, d, sdesc_add(qd, step_off(kk, kTile)), sdesc_add(kd, step_off(kk, bs)), idesc, kk > 0);
+        mma_step(leader, d, q + (kk >> 2) * (kTile * 8) + (kk & 3) * 2, dhi, kd + (kk >> 2) * half + (kk & 3) * 2, dhi, idesc,
+                 kk > 0);
     };
-    int m = 0, n = 0, items = 0;
-    bool ok = true;
     for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
       const int count = walk.count;
       const int kb = items % a.k_bufs;
       const uint32_t k1s = sb + kb * kK, k2s = k1s + kK1;
       ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (items / a.k_bufs) & 1, ctl);
       for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
-        int s = m % a.slots;
-        ok = mbar_wait_warp(bar(L::kSFree), (n & 1) ^ 1, ctl) && mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
+        ok = mbar_wait_warp(bar(L::kSFree), (n & 1) ^ 1, ctl);
         if (!ok) break;
-        fence_proxy_async_smem();  // (copies of cp.async)
-        tc_fence_after();
         // the other side first: its slot is released as early as possible
-        product(std::integral_constant<int, DO>{}, kP2 ? t_s1 : t_s2, sb + oQ + s * L::kSlot, kP2 ? k1s : k2s);
-        mma_commit(leader, bar(L::kQEmpty + s));
-        ++m;
-        s = m % a.slots;
-        ok = mbar_wait_warp(bar(L::kQFull + s), (m / a.slots) & 1, ctl);
+        product(std::integral_constant<int, DO>{}, kP2 ? t_s1 : t_s2, kP2 ? k1s : k2s);
         if (!ok) break;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        product(std::integral_constant<int, DG>{}, kP2 ? t_s2 : t_s1, sb + oQ + s * L::kSlot, kP2 ? k2s : k1s);
-        ++m;  // (released by dK)
+        mma_commit(leader, bar(L::kQEmpty + s));
+        if (++s == a.slots) s = 0, ++m;
+        product(std::integral_constant<int, DG>{}, kP2 ? t_s2 : t_s1, kP2 ? k2s : k1s);
+        if (!ok) break;
+        if (++s == a.slots) s = 0, ++m;  // (released by dK)
         mma_commit(leader, bar(L::kSFull));
       }
     }
@@ -257,34 +289,38 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     constexpr uint32_t id_dq = idesc_bf16(128, DG, 0, 1);  // A = dS K-major,   B = K_g N-major
     // (dS^T has 128 rows whatever the block: those past it multiply what lies
     // behind dS, into rows of dK that nobody reads)
-    const uint64_t dsm = sdesc_sw128(sb + oDS, kTile * 128, 1024), dsk = sdesc_sw128(sb + oDS, 16, 1024);
+    const uint64_t m_major = sdesc_sw128(0, kTile * 128, 1024), k_major = sdesc_sw128(0, 16, 1024),
+                   k_rows = sdesc_sw128(0, uint32_t(bs) * 128, 1024);
+    const uint32_t dhi = uint32_t(k_major >> 32);  // (the same for all three)
+    const uint32_t ds_m = uint32_t(m_major) + ((sb + oDS) >> 4), ds_k = uint32_t(k_major) + ((sb + oDS) >> 4);
     int n = 0, items = 0;
     bool ok = true;
     for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
       const int count = walk.count;
       const int kb = items % a.k_bufs;
-      const uint64_t kgn = sdesc_sw128(sb + kb * kK + (kP2 ? kK1 : 0u), uint32_t(bs) * 128, 1024);
+      const uint32_t kg = uint32_t(k_rows) + ((sb + kb * kK + (kP2 ? kK1 : 0u)) >> 4);
       ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (items / a.k_bufs) & 1, ctl) &&
            mbar_wait_warp(bar(L::kDkEmpty), (items & 1) ^ 1, ctl);
       bool first = true;
       for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
-        const int s = (2 * n + 1) % a.slots;
+        const int s = (2 * n + 1) % a.slots, qb = n & (dq_bufs - 1);
         ok = mbar_wait_warp(bar(L::kDsFull), n & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t qgn = sdesc_sw128(sb + oQ + s * L::kSlot, kTile * 128, 1024);
+        const uint32_t qg = uint32_t(m_major) + ((sb + oQ + s * L::kSlot) >> 4);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_bf16_ss(leader, t_dk, sdesc_add(dsm, kk * 2048), sdesc_add(qgn, kk * 2048), id_dk, !first || kk > 0);
+          mma_step(leader, t_dk, ds_m + kk * 128, dhi, qg + kk * 128, dhi, id_dk, !first || kk > 0);
         first = false;
         mma_commit(leader, bar(L::kQEmpty + s));
-        ok = mbar_wait_warp(bar(L::kDqEmpty), (n & 1) ^ 1, ctl);
+        ok = mbar_wait_warp(bar(L::kDqEmpty + qb), ((n / dq_bufs) & 1) ^ 1, ctl);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t t = t_dq + qb * 128;
         for (int kk = 0; kk < bs / 16; ++kk)
-          mma_bf16_ss(leader, t_dq, sdesc_add(dsk, step_off(kk, kTile)), sdesc_add(kgn, kk * 2048), id_dq, kk > 0);
+          mma_step(leader, t, ds_k + (kk >> 2) * (kTile * 8) + (kk & 3) * 2, dhi, kg + kk * 128, dhi, id_dq, kk > 0);
         mma_commit(leader, bar(L::kDsEmpty));
-        mma_commit(leader, bar(L::kDqFull));
+        mma_commit(leader, bar(L::kDqFull + qb));
       }
       if (ok) {
         mma_commit(leader, bar(L::kDkFull));
@@ -378,45 +414,52 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     // ---------------------------------------------------------------- dQ, and dK after an item
     const int w4 = warp - L::kEpiWarp, row = w4 * 32 + lane;
     const uint32_t lane_off = uint32_t(w4 * 32) << 16;
-    const int piece = a.piece;
-    const uint32_t stage = sb + oStage + row * (piece * 4u + 16u);  // this thread's
-    int n = 0, items = 0;
+    int n = 0, place = 0, items = 0;
     bool ok = true;
     for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
       const int count = walk.count;
       for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
-        ok = mbar_wait_warp(bar(L::kDqFull), n & 1, ctl);
+        const int qb = n & (dq_bufs - 1);
+        ok = mbar_wait_warp(bar(L::kDqFull + qb), (n / dq_bufs) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        const float me = params[(n % L::kRows) * kTile + row].w;
-        const int of = row_of[(n % L::kRows) * kTile + row];
-        const uint64_t ME = f2(me, me);
-        float* dst = a.dq32 + size_t(of < 0 ? 0 : of) * a.pitch;
-#pragma unroll 1
-        for (int c = 0; c < DG; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(t_dq + lane_off + c, v);
-          if (c + 32 == DG) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::kDqEmpty));
-          }
-          const int in = c % piece;
-          if (in == 0) bulk_wait_read_le<0>();  // what was staged here has been read
-          // on the row's grid of 2^-e: (x + 1.5 2^(23 - e)) - 1.5 2^(23 - e)
+        // the lane's four rows: w4 * 32 + lane / 4 + 8 x
+        float me[4];
+        float* dst[4];
+        bool on[4];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float q0, q1, q2, q3;
-            f2_split(f2_sub(f2_add(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), ME), ME), q0, q1);
-            f2_split(f2_sub(f2_add(f2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), ME), ME), q2, q3);
-            st_shared_v4(stage + (in + j) * 4, __float_as_uint(q0), __float_as_uint(q1), __float_as_uint(q2),
-                         __float_as_uint(q3));
-          }
-          const int from = c - in, to = min(c + 32, a.dg);  // the piece's columns so far
-          if (of >= 0 && (in + 32 == piece || c + 32 >= a.dg) && from < a.dg && c < a.dg) {
-            fence_proxy_async_smem();
-            bulk_reduce_add(dst + from, stage, uint32_t(to - from) * 4u);
-            bulk_commit();
+        for (int x = 0; x < 4; ++x) {
+          const int at = place * kTile + w4 * 32 + (lane >> 2) + 8 * x;
+          const int of = row_of[at];
+          me[x] = params[at].w;
+          on[x] = of >= 0;
+          dst[x] = a.dq32 + size_t(on[x] ? of : 0) * a.pitch + 2 * (lane & 3);
+        }
+        if (++place == L::kRows) place = 0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+          for (int c = 0; c < DG; c += 64) {
+            uint32_t v[32];
+            tmem_ld_16x64(t_dq + qb * 128 + lane_off + (uint32_t(16 * half) << 16) + c, v);
+            if (half == 1 && c + 64 == DG) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(L::kDqEmpty + qb));
+            }
+            // on the row's grid of 2^-e: (x + 1.5 2^(23 - e)) - 1.5 2^(23 - e)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint64_t ME = f2(me[2 * half + x], me[2 * half + x]);
+              float* p = dst[2 * half + x] + c;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float q0, q1;
+                f2_split(f2_sub(f2_add(f2(__uint_as_float(v[4 * e + 2 * x]), __uint_as_float(v[4 * e + 2 * x + 1])), ME), ME),
+                         q0, q1);
+                if (on[2 * half + x] && c + 8 * e < a.dg) red_add2(p + 8 * e, q0, q1);
+              }
+            }
           }
         }
       }
@@ -443,7 +486,6 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kDkEmpty));
     }
-    bulk_wait_all();  // every reduce has landed before the CTA exits
   }
 
   tc_fence_before();
@@ -457,29 +499,38 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
 constexpr int kDkThreads = 256;
 
 // dK of one key head and block: the items' tiles added in order (units of the
-// key head, then a unit's items), rounded to bf16 once.  Four values a thread.
+// key head, then a unit's items), rounded to bf16 once.  Four values a thread;
+// the items of a unit are read four at a time.
 __global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constant__ SelBwdArgs a) {
   const int j = blockIdx.x, hk = blockIdx.y % a.HK, b = blockIdx.y / a.HK;
   const int units = a.p.HU / a.HK, per = a.p.HU / a.p.HS;
-  const int bs = a.p.bs, quads = a.dg / 4, rows = min(bs, a.p.NK - j * bs);
-  for (int x = threadIdx.x; x < rows * quads; x += kDkThreads) {
-    const int key = x / quads, c = (x - key * quads) * 4;
-    float4 sum{0.f, 0.f, 0.f, 0.f};
-    for (int u = hk * units; u < (hk + 1) * units; ++u) {
-      const int sel = b * a.p.HS + u / per, sub = u % per;
-      const int2 r = a.p.ranges[size_t(sel) * a.p.blocks + j];
-      for (int it = r.x; it < r.x + r.y; ++it) {
-        const size_t w = size_t(it) * per + sub;
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(a.dk_part + (w * bs + key) * a.dg + c));
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
-      }
+  const int bs = a.p.bs, quads = a.dg / 4;
+  const int x = blockIdx.z * kDkThreads + threadIdx.x;
+  const int key = x / quads, c = (x - key * quads) * 4;
+  if (key >= min(bs, a.p.NK - j * bs)) return;
+  float4 sum{0.f, 0.f, 0.f, 0.f};
+  auto add = [&](const float4& v) {
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  };
+  const size_t item = size_t(bs) * a.dg * per;  // from an item's tile to the next one's, in a unit
+  for (int u = hk * units; u < (hk + 1) * units; ++u) {
+    const int2 r = __ldg(a.p.ranges + size_t(b * a.p.HS + u / per) * a.p.blocks + j);
+    const float* p = a.dk_part + ((size_t(r.x) * per + u % per) * bs + key) * a.dg + c;
+    int it = 0;
+    for (; it + 4 <= r.y; it += 4, p += 4 * item) {
+      float4 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __ldcs(reinterpret_cast<const float4*>(p + e * item));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) add(v[e]);
     }
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dk) + b * a.dk_sb + hk * a.dk_sh + (j * bs + key) * a.dk_sn + c;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+    for (; it < r.y; ++it, p += item) add(__ldcs(reinterpret_cast<const float4*>(p)));
   }
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dk) + b * a.dk_sb + hk * a.dk_sh + (j * bs + key) * a.dk_sn + c;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
 }
 
 template <int D1, int D2, int MODE>
@@ -487,22 +538,20 @@ int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, int sms, cudaStre
   using L = SelBwdLayout<D1, D2>;
   SelBwdArgs a = args;
   const int bs = a.p.bs;
-  // Larger pieces of dQ rows first (the reduce-adds bound the kernel), then
-  // two more slots than one tile takes, then a second K, then more slots.
-  auto fits = [&](int slots, int bufs, int piece) { return L::bytes(slots, bufs, piece, bs) <= L::kMost; };
-  constexpr int DG = MODE == STREAMKL_GRAD_P2 ? D2 : D1;
+  // Two tiles' slots, then a second K, then more slots.
+  auto fits = [&](int slots, int bufs) { return L::bytes(slots, bufs, bs) <= L::kMost; };
   a.k_bufs = 1;
-  a.piece = DG == 128 && fits(4, 1, 128) ? 128 : (fits(4, 1, 64) ? 64 : 32);
-  a.slots = fits(4, 1, a.piece) ? 4 : 3;
-  if (fits(a.slots, 2, a.piece)) a.k_bufs = 2;
-  while (a.slots < 6 && fits(a.slots + 1, a.k_bufs, a.piece)) ++a.slots;
-  if (!fits(a.slots, a.k_bufs, a.piece)) return cudaErrorInvalidValue;
+  a.slots = fits(4, 1) ? 4 : 3;
+  if (fits(a.slots, 2)) a.k_bufs = 2;
+  while (a.slots < L::kMaxRing && fits(a.slots + 1, a.k_bufs)) ++a.slots;
+  if (!fits(a.slots, a.k_bufs)) return cudaErrorInvalidValue;
   auto kern = sel_bwd_kernel<D1, D2, MODE>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kMost);
   if (e != cudaSuccess) return e;
-  const long long most = (long long)a.p.max_items * (a.p.HU / a.p.HS);
+  const long long most = (long long)a.p.max_items * (a.p.HU / a.p.HS), rows = (long long)a.p.B * a.p.H * a.p.NQ;
   const int grid = int(most < sms ? most : sms);
-  kern<<<grid, L::kThreads, L::bytes(a.slots, a.k_bufs, a.piece, bs), st>>>(m.k1, m.k2, a);
+  sel_rows_kernel<<<unsigned((rows + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st>>>(a, MODE);
+  kern<<<grid, L::kThreads, L::bytes(a.slots, a.k_bufs, bs), st>>>(m.k1, m.k2, a);
   return cudaGetLastError();
 }
 
@@ -521,7 +570,8 @@ int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs&
 }
 
 int launch_sel_dk(const SelBwdArgs& a, cudaStream_t st) {
-  sel_dk_kernel<<<dim3(unsigned(a.p.blocks), unsigned(a.p.B * a.HK)), kDkThreads, 0, st>>>(a);
+  const unsigned parts = unsigned((a.p.bs * (a.dg / 4) + kDkThreads - 1) / kDkThreads);
+  sel_dk_kernel<<<dim3(unsigned(a.p.blocks), unsigned(a.p.B * a.HK), parts), kDkThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -199,7 +199,8 @@ struct SelBwdArgs {
   long long dk_sb, dk_sh, dk_sn;
   int HK;                 // of the gradient side
   int* status;
-  int slots, k_bufs, piece;
+  float4* rows;           // [B H NQ], of sel_rows_kernel
+  int slots, k_bufs;
 };
 
 int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs& a, int sms, cudaStream_t st);
