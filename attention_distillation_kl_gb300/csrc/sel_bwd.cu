@@ -211,9 +211,9 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
           params[n * kTile + r] = x;
           row_of[n * kTile + r] = on ? of : -1;
           if (++n == L::kRows) n = 0;
-          gather_rows<DO, true>(sb + oQ + s * L::kSlot, first, on ? xo : 0ull, ro.chunks);
+          gather_rows<DO, true>(sb + oQ + s * L::kSlot, first, on ? xo : 0ull, ro);
         } else {
-          gather_rows<DG, true>(sb + oQ + s * L::kSlot, first, on ? xg : 0ull, rg.chunks);
+          gather_rows<DG, true>(sb + oQ + s * L::kSlot, first, on ? xg : 0ull, rg);
         }
         cp_async_arrive(bar(L::kQFull + s));
         __syncwarp();

@@ -112,6 +112,10 @@ struct SelRows {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// 16 bytes, or zeros with size 0 (nothing is read).
+__device__ __forceinline__ void cp_async16_size(uint32_t dst, const void* src, uint32_t size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
 // This thread's arrival on `bar` once its copies so far have landed.  The one
 // that waits for them and hands them to the tensor core puts the proxy fence
 // between the two: a fence of each copying warp held up its next copies (731
@@ -127,21 +131,23 @@ __device__ __forceinline__ uint32_t step_off(int kk, int rows) { return (kk >> 2
 // Copies 32 rows (lane r holds the address of row r; 0: not copied, or with
 // ZERO zeros) into rows [first, first + 32) of a [128][D] operand tile,
 // swizzled as TMA would: 64 bytes of 8 rows at a time, so that all but four
-// addresses a lane are constants away.  Called by a whole warp.
+// addresses a lane are constants away, and no branch between them.  Called by
+// a whole warp.
 template <int D, bool ZERO>
-__device__ __forceinline__ void gather_rows(uint32_t tile, int first, unsigned long long mine, int chunks) {
+__device__ __forceinline__ void gather_rows(uint32_t tile, int first, unsigned long long mine, const SelRows& rows) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const uint32_t even = tile + (first + r) * 128 + ((c ^ r) << 4), odd = even ^ 64u;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const unsigned long long row = __shfl_sync(0xffffffffu, mine, r + 8 * k);
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(row) + c * 16;
+    const uint8_t* p = (row != 0 ? reinterpret_cast<const uint8_t*>(row) : rows.base) + c * 16;
+    const uint32_t size = row != 0 ? 16u : 0u;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       const uint32_t to = (j & 1 ? odd : even) + k * 1024 + (j >> 1) * (kTile * 128);
-      if (c + 4 * j < chunks) {
-        if (row != 0) cp_async16(to, p + 64 * j);
-        else if (ZERO) st_shared_v4(to, 0u, 0u, 0u, 0u);
+      if (c + 4 * j < rows.chunks) {
+        if (ZERO) cp_async16_size(to, p + 64 * j, size);
+        else if (row != 0) cp_async16(to, p + 64 * j);
       }
     }
   }

@@ -158,8 +158,8 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
       for (int side = 0; side < 2; ++side) {
         ok = mbar_wait_warp(bar(L::kQEmpty + s), (m & 1) ^ 1, ctl);
         if (!ok) break;
-        if (side == 0) gather_rows<D1, false>(sb + oQ + s * kSlot, first, p1, a.r1.chunks);
-        else gather_rows<D2, false>(sb + oQ + s * kSlot, first, p2, a.r2.chunks);
+        if (side == 0) gather_rows<D1, false>(sb + oQ + s * kSlot, first, p1, a.r1);
+        else gather_rows<D2, false>(sb + oQ + s * kSlot, first, p2, a.r2);
         cp_async_arrive(bar(L::kQFull + s));
         if (++s == a.slots) s = 0, ++m;
       }
