@@ -83,22 +83,23 @@ Geometry geometry(const streamkl_side& p1, const streamkl_side& p2, const stream
   return g;
 }
 
-void take_plan(Carver& c, SelPlan& p) {
+// row_bytes: what a query head's rows hold in L2 while their lists run.
+void take_plan(Carver& c, SelPlan& p, double row_bytes, int sms, bool places) {
   const size_t heads = size_t(p.B) * p.HS, listed = size_t(p.NQ) * p.T;
   p.counts = c.take<unsigned>(heads * p.chunks * p.blocks);
   p.entries = c.take<unsigned>(heads * listed);
   p.slots = c.take<unsigned>(heads * p.NQ * p.words);
-  const size_t per_item = size_t(p.queries_per_tile) * p.tiles_per_item;
-  p.max_items = int(heads * (listed / per_item + std::min(listed, size_t(p.blocks))));
-  p.items = c.take<SelItem>(p.max_items);
-  p.item_count = c.take<int>(1);
-}
-
-// Tiles of an item: K is read once for all of them, but the last items of a
-// CTA should be a small part of what it does.
-int item_tiles(const SelPlan& p, int sms, int most) {
-  const double tiles = double(p.B) * p.HU * p.NQ * p.T / p.queries_per_tile;
-  return int(std::max(1.0, std::min(double(most), tiles / (8.0 * std::max(sms, 1)))));
+  p.cap = int(std::min(listed, size_t(p.blocks)));
+  p.lists = c.take<int4>(heads * p.cap);
+  p.sizes = c.take<int2>(heads);
+  if (places) p.place = c.take<int>(heads * p.blocks);
+  // As many selection heads at a time as a third of L2 holds.
+  const double fits = 40.0e6 / (row_bytes * (p.H / p.HS) * p.NQ);
+  p.group = int(std::max(1.0, std::min(double(heads), fits)));
+  p.groups = int((heads + p.group - 1) / p.group);
+  const size_t most = heads * (p.HU / p.HS) * (listed / p.queries_per_tile + p.cap);  // tiles
+  p.ctas = int(std::min(size_t(std::max(sms, 1)), most));
+  p.starts = c.take<int4>(size_t(p.groups) * p.ctas);
 }
 
 struct FwdPlan {
@@ -116,8 +117,7 @@ FwdPlan fwd_plan(const streamkl_side& p1, const streamkl_side& p2, const streamk
   const streamkl_side* const p[2] = {&p1, &p2};
   take_prep(c, f.prep, p, vis, B, H, NQ, NK, -1);
   f.g = geometry(p1, p2, vis, sel, B, H, NQ, NK);
-  f.g.p.tiles_per_item = item_tiles(f.g.p, sms, 16);
-  take_plan(c, f.g.p);
+  take_plan(c, f.g.p, 2.0 * (p1.d + p2.d), sms, false);
   const size_t pairs = size_t(B) * H * NQ * sel.count;
   f.rec = c.take<float4>(pairs);
   f.acc = c.take<float>(pairs);
@@ -150,11 +150,11 @@ BwdPlan bwd_plan(const streamkl_side& p1, const streamkl_side& p2, const streamk
   f.prep.zero_words = c.used / 16;
   take_prep(c, f.prep, p, vis, B, H, NQ, NK, -1);
   f.g = geometry(p1, p2, vis, sel, B, H, NQ, NK);
-  f.g.p.tiles_per_item = item_tiles(f.g.p, sms, 32);
-  take_plan(c, f.g.p);
-  f.g.p.ranges = c.take<int2>(size_t(B) * sel.heads * f.g.p.blocks);
+  take_plan(c, f.g.p, 2.0 * (p1.d + p2.d) + 4.0 * f.pitch, sms, true);
   f.rows = c.take<float4>(size_t(B) * H * NQ);
-  f.dk_part = c.take<float>(size_t(f.g.p.max_items) * (f.g.p.HU / f.g.p.HS) * sel.block * g.d);
+  // (SelWalk::meeting stays below this)
+  const size_t meetings = size_t(B) * sel.heads * f.g.p.cap * (f.g.p.HU / f.g.p.HS) + size_t(f.g.p.groups) * f.g.p.ctas;
+  f.dk_part = c.take<float>(meetings * sel.block * g.d);
   f.bytes = c.used;
   return f;
 }
@@ -205,7 +205,7 @@ int streamkl_fwd_sel(const streamkl_side* p1, const streamkl_side* p2, const str
   a.lse2 = lse2;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (launch_mod_prep(f.prep, cs) != 0 || launch_sel_plan(a.p, cs) != 0) return STREAMKL_CUDA_ERROR;
-  if (launch_sel_fwd(m, tile_width(p1->d), tile_width(p2->d), a, sms, cs) != 0) return STREAMKL_CUDA_ERROR;
+  if (launch_sel_fwd(m, tile_width(p1->d), tile_width(p2->d), a, cs) != 0) return STREAMKL_CUDA_ERROR;
   return as_status(launch_sel_merge(a, cs));
 }
 
@@ -274,7 +274,7 @@ int streamkl_bwd_sel(const streamkl_side* p1, const streamkl_side* p2, const str
   if (launch_kmax_strided(g.k.data, B, g.HK, NK, g.d, B > 1 ? g.k.stride_b : 0, g.HK > 1 ? g.k.stride_h : 0,
                           NK > 1 ? g.k.stride_n : 0, f.prep.ids_k, f.kmax, cs) != 0)
     return STREAMKL_CUDA_ERROR;
-  if (launch_sel_bwd(m, tile_width(p1->d), tile_width(p2->d), mode, a, sms, cs) != 0 || launch_sel_dk(a, cs) != 0)
+  if (launch_sel_bwd(m, tile_width(p1->d), tile_width(p2->d), mode, a, cs) != 0 || launch_sel_dk(a, cs) != 0)
     return STREAMKL_CUDA_ERROR;
   ModFinishArgs fin{};
   fin.rows[0] = {f.dq32, B * H, H, NQ, g.d, f.pitch, static_cast<__nv_bfloat16*>(dq->data), B > 1 ? dq->stride_b : 0,

@@ -3,18 +3,22 @@
 //   mode P2:  dS = s2 dKL (P2 - P1),   mode P1:  dS = s1 dKL P1 (ln(P1 / P2) - KL),
 //   dQ = dS K,  dK = dS^T Q.
 //
-// Persistent CTAs walk the items.  dK of an item's block accumulates in TMEM
-// and leaves as one fp32 tile an item, which sel_dk_kernel adds in item order.
+// Persistent CTAs walk their lists.  dK of a list's block accumulates in TMEM
+// and leaves as one fp32 tile for each CTA that had a share of the list, which
+// sel_dk_kernel adds in order.
 // A row of dQ gets a contribution from each of its blocks, out of different
 // CTAs: fp32 vector reductions, each value rounded to its row's grid first
 // (dq_fixed_exp), so that the sums are exact in any order and the result is
-// bitwise repeatable.  19 warps:
+// bitwise repeatable.  24 warps:
 //   warps 0-7   dS (thread = row; a warpgroup takes half of the columns)
-//   warps 8-11  dQ: TMEM -> registers, four lanes to 8 values of a row, so that
-//               every reduction covers whole sectors; after an item, dK
-//   warps 12-15 gather 32 rows each of both sides, and the rows' parameters
+//   warps 8-15  dQ: TMEM -> registers, four lanes to 8 values of a row, so that
+//               every reduction covers whole sectors (a warpgroup takes every
+//               other tile: half of its time is spent waiting to issue them);
+//               after a list, dK (half of the columns each)
+//   warps 16-19 gather 32 rows each of both sides, and the rows' parameters
 //               (sel_rows_kernel)
-//   warp 16     S1, S2      warp 17     dK, dQ      warp 18     K by TMA
+//   warp 20     S1, S2      warp 21     dK, dQ      warp 22     K by TMA
+//   warp 23     tells the others what to take (SelShare)
 // TMEM: S1, S2 of bs columns from 0; then, with blocks up to 64, dK [128, 256)
 // and two buffers of dQ, else dK [256, 384) and one.
 //
@@ -31,9 +35,9 @@ namespace {
 
 template <int D1, int D2>
 struct SelBwdLayout {
-  static constexpr int kDsWarps = 8, kEpiWarp = 8, kGatherWarp = 12, kGatherWarps = 4;
-  static constexpr int kSWarp = 16, kGradWarp = 17, kLoadWarp = 18;
-  static constexpr int kThreads = 32 * 19;
+  static constexpr int kDsWarps = 8, kEpiWarp = 8, kEpiWGs = 2, kGatherWarp = 16, kGatherWarps = 4;
+  static constexpr int kSWarp = 20, kGradWarp = 21, kLoadWarp = 22, kWalkWarp = 23;
+  static constexpr int kThreads = 32 * (kWalkWarp + 1);
   static constexpr int kMaxRing = 6;   // slots of gathered tiles
   // Tiles whose rows' parameters are kept.  Those of tile n are replaced with the copies of tile n + kRows, which wait
   // for the dK of tile n + kRows - 1 - slots / 2 at least; that of n + 3 has waited for dQ of n + 2, and this one for
@@ -41,13 +45,13 @@ struct SelBwdLayout {
   static constexpr int kRows = 7;
   enum {
     kKFull = 0, kKEmpty = 2, kReady = 4, kQFull = 6, kQEmpty = kQFull + kMaxRing, kSFull = kQEmpty + kMaxRing, kSFree,
-    kDsFull, kDsEmpty, kDqFull, kDqEmpty = kDqFull + 2, kDkFull = kDqEmpty + 2, kDkEmpty, kDone, kNumBars
+    kDsFull, kDsEmpty, kDqFull, kDqEmpty = kDqFull + 2, kDkFull = kDqEmpty + 2, kDkEmpty, kDone, kTold, kNumBars = (kTold + 2 * kShares + 1) / 2 * 2  // (16-byte words behind them)
   };
   static constexpr uint32_t kSlot = kTile * 2u * (D1 > D2 ? D1 : D2);
   static constexpr uint32_t kParams = kRows * kTile * 20u;
   // operands, dS (64-key blocks of 128 rows), parameters, barriers
   static uint32_t bytes(int slots, int k_bufs, int bs) {
-    return 1024u + slots * kSlot + uint32_t(k_bufs * bs) * (D1 + D2) * 2u + ds_bytes(bs) + kParams + kNumBars * 8 + 16;
+    return 1024u + slots * kSlot + uint32_t(k_bufs * bs) * (D1 + D2) * 2u + ds_bytes(bs) + kParams + kNumBars * 8 + kShares * sizeof(SelShare) + 16;
   }
   __host__ __device__ static uint32_t ds_bytes(int bs) { return bs == 128 ? 32768u : 16384u; }
   static constexpr uint32_t kMost = 232448;
@@ -70,6 +74,29 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t t, uint32_t (&v)[32]) {
       : SKL_R8(v, 0), SKL_R8(v, 8), SKL_R8(v, 16), SKL_R8(v, 24)
       : "r"(t)
       : "memory");
+}
+
+// dS of 16 columns of a row, as pairs of bf16 (ds_chunk_row without its mask).
+template <int MODE>
+__device__ __forceinline__ void ds_columns(const uint32_t (&x1)[16], const uint32_t (&x2)[16], uint64_t C1, uint64_t C2,
+                                           uint64_t S1, uint64_t NR, uint64_t NA, uint64_t NB, uint64_t WW, uint32_t (&out)[8]) {
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) {
+    const uint64_t X1 = f2(__uint_as_float(x1[k]), __uint_as_float(x1[k + 1]));
+    const uint64_t X2 = f2(__uint_as_float(x2[k]), __uint_as_float(x2[k + 1]));
+    float a, b;
+    f2_split(f2_fma(X1, C1, NA), a, b);
+    const uint64_t P1 = f2(ex2(a), ex2(b));
+    uint64_t D;
+    if (MODE == STREAMKL_GRAD_P2) {
+      f2_split(f2_fma(X2, C2, NB), a, b);
+      D = f2_mul(WW, f2_sub(f2(ex2(a), ex2(b)), P1));
+    } else {
+      D = f2_mul(f2_mul(WW, P1), f2_fma(f2_fma(X2, NR, X1), S1, NB));
+    }
+    f2_split(D, a, b);
+    out[k / 2] = pack_bf16(a, b);
+  }
 }
 
 constexpr int kRowThreads = 256;
@@ -110,8 +137,10 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
   auto bar = [&](int id) { return sb + oBar + 8u * id; };
   float4* params = reinterpret_cast<float4*>(smem + oParam);                          // na, nb, ws, grid
   int* row_of = reinterpret_cast<int*>(smem + oParam + L::kRows * kTile * 16);        // row of dq32, or -1
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + oBar + L::kNumBars * 8);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + oBar + L::kNumBars * 8 + 4);
+  SelShare* shares = reinterpret_cast<SelShare*>(smem + oBar + L::kNumBars * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shares + kShares);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t told = sb + oBar + 8u * L::kTold;
   const Ctl ctl{abort_flag, a.status};
 
   if (threadIdx.x == 0) {
@@ -119,7 +148,9 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       int count = 1;
       if (i >= L::kQFull && i < L::kQEmpty) count = 33 * L::kGatherWarps;
       if (i == L::kReady || i == L::kReady + 1 || i == L::kSFree || i == L::kDsFull) count = L::kDsWarps;
-      if (i == L::kDqEmpty || i == L::kDqEmpty + 1 || i == L::kDkEmpty) count = 4;
+      if (i == L::kDqEmpty || i == L::kDqEmpty + 1) count = 4;
+      if (i == L::kDkEmpty) count = 4 * L::kEpiWGs;
+      if (i >= L::kTold + kShares) count = L::kWalkWarp;  // the warps before it
       if (i == L::kDone) count = 2;
       mbar_init(bar(i), count);
     }
@@ -141,7 +172,6 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
   const int dq_bufs = bs == 128 ? 1 : 2;
   const uint32_t t_s1 = tmem, t_s2 = tmem + bs, t_dk = tmem + (bs == 128 ? 256 : 128), t_dq = t_dk + 128;
   const int per_tile = a.p.queries_per_tile, G = a.p.G;
-  const int works = min(*a.p.item_count, a.p.max_items) * (a.p.HU / a.p.HS);
   const bool ids = a.vis.ids_q != nullptr;
 
   if (warp >= L::kGatherWarp && warp < L::kGatherWarp + L::kGatherWarps) {
@@ -151,19 +181,21 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     const SelRows& ro = kP2 ? a.r1 : a.r2;
     const SelRows& rg = kP2 ? a.r2 : a.r1;
     const bool place = ql < per_tile;
-    SelWalk walk(a.p, works);
+    SelReader share(shares, told);
     int e0 = 0;
-    // the lane's row 0 of both sides and its number, in the current item
+    // the lane's row 0 of both sides and its number, in the current share
     const uint8_t *bo = nullptr, *bg = nullptr;
     int row0 = 0;
     auto enter = [&]() {
-      const SelWork k = walk.get(a.p);
-      bo = ro.at(k.b, k.head0 + hl, 0);
-      bg = rg.at(k.b, k.head0 + hl, 0);
-      row0 = (k.b * a.p.H + k.head0 + hl) * a.p.NQ;
+      if (!share.next(ctl)) return false;
+      bo = ro.at(share.b, share.head0 + hl, 0);
+      bg = rg.at(share.b, share.head0 + hl, 0);
+      row0 = (share.b * a.p.H + share.head0 + hl) * a.p.NQ;
+      return true;
     };
+    bool ahead = enter();  // `ent` is of a tile
     // A row's parameters are read a tile ahead of its copies, its entry two tiles.
-    unsigned ent = entry_of(a.p, walk, ql, place);
+    unsigned ent = entry_of(a.p, share, ql, place);
     unsigned long long po = 0, pg = 0;  // of the tile to copy
     float4 par;
     int row = -1;
@@ -181,20 +213,18 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     };
     auto step = [&]() {  // to the next tile's entry
       e0 += per_tile;
-      if (e0 >= walk.count) {
-        walk.advance(a.p);
+      if (ahead && e0 >= share.count) {
+        ahead = enter();
         e0 = 0;
-        enter();
       }
-      ent = entry_of(a.p, walk, e0 + ql, place);
+      ent = entry_of(a.p, share, e0 + ql, place);
     };
     int s = 0, m = 0, n = 0;  // slot, rounds of the ring, place of the tile's parameters
-    bool ok = true, more = walk.more();
-    enter();
+    bool ok = true, more = ahead;
     look();
     step();
     while (ok && more) {
-      more = walk.more();
+      more = ahead;
       const unsigned long long xo = po, xg = pg;
       const float4 x = par;
       const int of = row;
@@ -224,31 +254,31 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     cp_async_wait_all();
   } else if (warp == L::kLoadWarp) {
     // ---------------------------------------------------------------- K
-    if (lane == 0) {
-      int items = 0;
-      for (SelWalk walk(a.p, works); walk.more(); walk.advance(a.p), ++items) {
-        const SelWork k = walk.get(a.p);
-        const int kb = items % a.k_bufs, hu = k.head0 / G;
-        if (!mbar_wait_polled(bar(L::kKEmpty + kb), ((items / a.k_bufs) & 1) ^ 1, ctl)) break;
-        const uint32_t full = bar(L::kKFull + kb);
-        mbar_arrive_expect_tx(full, kK);
+    int kept = 0;
+    for (SelReader share(shares, told); share.next(ctl); ++kept) {
+      const int kb = kept % a.k_bufs, hu = share.head0 / G;
+      if (!mbar_wait_warp(bar(L::kKEmpty + kb), ((kept / a.k_bufs) & 1) ^ 1, ctl)) break;
+      if (lane != 0) continue;
+      const uint32_t full = bar(L::kKFull + kb);
+      mbar_arrive_expect_tx(full, kK);
 #pragma unroll
-        for (int c = 0; c < D1 / 64; ++c)
-          tma_load_4d(sb + kb * kK + c * (bs * 128), &tk1, full, c * 64, k.block * bs, hu / a.u1, k.b);
+      for (int c = 0; c < D1 / 64; ++c)
+        tma_load_4d(sb + kb * kK + c * (bs * 128), &tk1, full, c * 64, share.block * bs, hu / a.u1, share.b);
 #pragma unroll
-        for (int c = 0; c < D2 / 64; ++c)
-          tma_load_4d(sb + kb * kK + kK1 + c * (bs * 128), &tk2, full, c * 64, k.block * bs, hu / a.u2, k.b);
-      }
-      if (*abort_flag)  // let the copies already started land before the CTA exits
-        for (int j = items > a.k_bufs ? items - a.k_bufs : 0; j < items; ++j)
-          mbar_drain(bar(L::kKFull + j % a.k_bufs), (j / a.k_bufs) & 1, 200000000ull);
+      for (int c = 0; c < D2 / 64; ++c)
+        tma_load_4d(sb + kb * kK + kK1 + c * (bs * 128), &tk2, full, c * 64, share.block * bs, hu / a.u2, share.b);
     }
+    if (*abort_flag && lane == 0)  // let the copies already started land before the CTA exits
+      for (int j = kept > a.k_bufs ? kept - a.k_bufs : 0; j < kept; ++j)
+        mbar_drain(bar(L::kKFull + j % a.k_bufs), (j / a.k_bufs) & 1, 200000000ull);
+  } else if (warp == L::kWalkWarp) {
+    if (lane == 0) tell_shares(a.p, shares, told, ctl);
   } else if (warp == L::kSWarp) {
     // ---------------------------------------------------------------- S issuer
     const uint32_t leader = elect_one();
     const uint32_t idesc = idesc_bf16(128, bs, 0, 0);
     const uint32_t dhi = uint32_t(sdesc_sw128(0, 16, 1024) >> 32), dlo = uint32_t(sdesc_sw128(0, 16, 1024));
-    int n = 0, s = 0, m = 0, items = 0;
+    int n = 0, s = 0, m = 0, kept = 0;
     bool ok = true;
     auto product = [&](auto width, uint32_t d, uint32_t ks) {  // the tile in slot s by K at ks
       constexpr int D = decltype(width)::value;
@@ -262,12 +292,11 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         mma_step(leader, d, q + (kk >> 2) * (kTile * 8) + (kk & 3) * 2, dhi, kd + (kk >> 2) * half + (kk & 3) * 2, dhi, idesc,
                  kk > 0);
     };
-    for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
-      const int count = walk.count;
-      const int kb = items % a.k_bufs;
+    for (SelReader share(shares, told); ok && share.next(ctl); ++kept) {
+      const int kb = kept % a.k_bufs;
       const uint32_t k1s = sb + kb * kK, k2s = k1s + kK1;
-      ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (items / a.k_bufs) & 1, ctl);
-      for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
+      ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (kept / a.k_bufs) & 1, ctl);
+      for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n) {
         ok = mbar_wait_warp(bar(L::kSFree), (n & 1) ^ 1, ctl);
         if (!ok) break;
         // the other side first: its slot is released as early as possible
@@ -293,16 +322,15 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
                    k_rows = sdesc_sw128(0, uint32_t(bs) * 128, 1024);
     const uint32_t dhi = uint32_t(k_major >> 32);  // (the same for all three)
     const uint32_t ds_m = uint32_t(m_major) + ((sb + oDS) >> 4), ds_k = uint32_t(k_major) + ((sb + oDS) >> 4);
-    int n = 0, items = 0;
+    int n = 0, kept = 0;
     bool ok = true;
-    for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
-      const int count = walk.count;
-      const int kb = items % a.k_bufs;
+    for (SelReader share(shares, told); ok && share.next(ctl); ++kept) {
+      const int kb = kept % a.k_bufs;
       const uint32_t kg = uint32_t(k_rows) + ((sb + kb * kK + (kP2 ? kK1 : 0u)) >> 4);
-      ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (items / a.k_bufs) & 1, ctl) &&
-           mbar_wait_warp(bar(L::kDkEmpty), (items & 1) ^ 1, ctl);
+      ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (kept / a.k_bufs) & 1, ctl) &&
+           mbar_wait_warp(bar(L::kDkEmpty), (kept & 1) ^ 1, ctl);
       bool first = true;
-      for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
+      for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n) {
         const int s = (2 * n + 1) % a.slots, qb = n & (dq_bufs - 1);
         ok = mbar_wait_warp(bar(L::kDsFull), n & 1, ctl);
         if (!ok) break;
@@ -313,14 +341,16 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
           mma_step(leader, t_dk, ds_m + kk * 128, dhi, qg + kk * 128, dhi, id_dk, !first || kk > 0);
         first = false;
         mma_commit(leader, bar(L::kQEmpty + s));
-        ok = mbar_wait_warp(bar(L::kDqEmpty + qb), ((n / dq_bufs) & 1) ^ 1, ctl);
+        // the accumulator's last tile has been read (barriers go by the warpgroups of dQ, which see every phase of theirs)
+        const int before = n - dq_bufs;
+        ok = before < 0 || mbar_wait_warp(bar(L::kDqEmpty + (before & 1)), (before >> 1) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
         const uint32_t t = t_dq + qb * 128;
         for (int kk = 0; kk < bs / 16; ++kk)
           mma_step(leader, t, ds_k + (kk >> 2) * (kTile * 8) + (kk & 3) * 2, dhi, kg + kk * 128, dhi, id_dq, kk > 0);
         mma_commit(leader, bar(L::kDsEmpty));
-        mma_commit(leader, bar(L::kDqFull + qb));
+        mma_commit(leader, bar(L::kDqFull + (n & 1)));
       }
       if (ok) {
         mma_commit(leader, bar(L::kDkFull));
@@ -339,17 +369,16 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     const int half = (bs + 32) / 64 * 32;                        // columns of warpgroup 0
     const int col0 = wg == 0 ? 0 : half, col1 = wg == 0 ? half : bs;
     const int nqt = (a.p.NQ + kTile - 1) / kTile, nkt = (a.p.NK + kTile - 1) / kTile, off = a.p.NK - a.p.NQ;
-    int n = 0, items = 0;
+    int n = 0, kept = 0;
     bool ok = true;
-    for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
-      const SelWork k = walk.get(a.p);
-      const int k0 = k.block * bs;
-      const int prefix = a.p.prefix != nullptr ? min(max(a.p.prefix[k.b], 0), a.p.NK) : 0;
-      const int* kids = ids ? a.vis.ids_k + size_t(k.b) * nkt * kTile + k0 : nullptr;
+    for (SelReader share(shares, told); ok && share.next(ctl); ++kept) {
+      const int k0 = share.block * bs;
+      const int prefix = a.p.prefix != nullptr ? min(max(a.p.prefix[share.b], 0), a.p.NK) : 0;
+      const int* kids = ids ? a.vis.ids_k + size_t(share.b) * nkt * kTile + k0 : nullptr;
       if (ids) {
         // keys that match nothing may hold anything: zeros before a product reads them
-        const int kb = items % a.k_bufs;
-        ok = mbar_wait_warp(bar(L::kKFull + kb), (items / a.k_bufs) & 1, ctl);
+        const int kb = kept % a.k_bufs;
+        ok = mbar_wait_warp(bar(L::kKFull + kb), (kept / a.k_bufs) & 1, ctl);
         if (!ok) break;
         if (row < bs && kids[row] < 0) {
           const uint32_t base = sb + kb * kK + (wg == 0 ? 0u : kK1) + row * 128;
@@ -361,8 +390,8 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kReady + kb));
       }
-      const int row0 = (k.b * a.p.H + k.head0 + hl) * a.p.NQ;  // of query 0
-      for (int e0 = 0; ok && e0 < walk.count; e0 += per_tile, ++n) {
+      const int row0 = (share.b * a.p.H + share.head0 + hl) * a.p.NQ;  // of query 0
+      for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n) {
         ok = mbar_wait_warp(bar(L::kSFull), n & 1, ctl);
         if (!ok) break;
         tc_fence_after();
@@ -372,22 +401,22 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         const uint64_t NA = f2(par.x, par.x), NB = f2(par.y, par.y), WW = f2(par.z, par.z);
         const int last = a.p.causal ? min(max(i + off + 1, prefix), a.p.NK) : a.p.NK;
         const bool whole = kids == nullptr && __all_sync(0xffffffffu, of < 0 || last >= k0 + bs);
-        const int id = kids != nullptr ? a.vis.ids_q[size_t(k.b) * nqt * kTile + i] : 0;
+        const int id = kids != nullptr ? a.vis.ids_q[size_t(share.b) * nqt * kTile + i] : 0;
         bool waited = false;
 #pragma unroll 1
-        for (int c = col0; c < col1; c += 32) {
-          uint32_t x1[32], x2[32], out[16];
-          tmem_ld2x32(t_s1 + lane_off + c, t_s2 + lane_off + c, x1, x2);
-          if (c + 32 >= col1) {
+        for (int c = col0; c < col1; c += 16) {
+          uint32_t x1[16], x2[16], out[8];
+          tmem_ld2x16(t_s1 + lane_off + c, t_s2 + lane_off + c, x1, x2);
+          if (c + 16 >= col1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::kSFree));
           }
-          ds_chunk_row<MODE, false>(x1, x2, C1, C2, S1, NR, NA, NB, WW, 0, out);
+          ds_columns<MODE>(x1, x2, C1, C2, S1, NR, NA, NB, WW, out);
           if (!whole) {
-            const uint32_t on = visible_bits<32>(i, k0 + c, off, a.p.NK, a.p.causal, prefix, id, kids == nullptr ? nullptr : kids + c);
+            const uint32_t on = visible_bits<16>(i, k0 + c, off, a.p.NK, a.p.causal, prefix, id, kids == nullptr ? nullptr : kids + c);
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
+            for (int x = 0; x < 8; ++x)
               out[x] &= ((on >> (2 * x)) & 1u ? 0xffffu : 0u) | ((on >> (2 * x + 1)) & 1u ? 0xffff0000u : 0u);
           }
           if (!waited) {  // the previous tile's products must be done reading dS
@@ -395,7 +424,10 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
             if (!ok) break;
             waited = true;
           }
-          store_cols32_sw128(sb + oDS, row, c, out);
+          // into 64-key blocks of 128-byte rows, swizzled
+          const uint32_t to = sb + oDS + (c >> 6) * (kTile * 128) + row * 128, piece = (c & 63) >> 3;
+          st_shared_v4(to + ((piece ^ (row & 7)) << 4), out[0], out[1], out[2], out[3]);
+          st_shared_v4(to + (((piece + 1) ^ (row & 7)) << 4), out[4], out[5], out[6], out[7]);
         }
         if (!ok) break;
         if (col0 == col1) {  // blocks of 32: nothing for this warpgroup, which may not run ahead of the other
@@ -411,16 +443,16 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       }
     }
   } else {
-    // ---------------------------------------------------------------- dQ, and dK after an item
-    const int w4 = warp - L::kEpiWarp, row = w4 * 32 + lane;
+    // ---------------------------------------------------------------- dQ, and dK after a list
+    const int wg = (warp - L::kEpiWarp) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lane_off = uint32_t(w4 * 32) << 16;
-    int n = 0, place = 0, items = 0;
+    int n = 0, place = 0, kept = 0;
     bool ok = true;
-    for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
-      const int count = walk.count;
-      for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
+    for (SelReader share(shares, told); ok && share.next(ctl); ++kept) {
+      for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n, place = place + 1 == L::kRows ? 0 : place + 1) {
+        if ((n & 1) != wg) continue;
         const int qb = n & (dq_bufs - 1);
-        ok = mbar_wait_warp(bar(L::kDqFull + qb), (n / dq_bufs) & 1, ctl);
+        ok = mbar_wait_warp(bar(L::kDqFull + wg), (n >> 1) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
         // the lane's four rows: w4 * 32 + lane / 4 + 8 x
@@ -435,7 +467,6 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
           on[x] = of >= 0;
           dst[x] = a.dq32 + size_t(on[x] ? of : 0) * a.pitch + 2 * (lane & 3);
         }
-        if (++place == L::kRows) place = 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll 1
@@ -445,7 +476,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
             if (half == 1 && c + 64 == DG) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(bar(L::kDqEmpty + qb));
+              if (lane == 0) mbar_arrive(bar(L::kDqEmpty + wg));
             }
             // on the row's grid of 2^-e: (x + 1.5 2^(23 - e)) - 1.5 2^(23 - e)
 #pragma unroll
@@ -464,14 +495,14 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         }
       }
       if (!ok) break;
-      // dK of the item, [bs][dg]
-      ok = mbar_wait_warp(bar(L::kDkFull), items & 1, ctl);
+      // dK of the list, [bs][dg]
+      ok = mbar_wait_warp(bar(L::kDkFull), kept & 1, ctl);
       if (!ok) break;
       tc_fence_after();
       if (w4 * 32 < bs) {
-        float* dst = a.dk_part + (size_t(walk.w) * bs + row) * a.dg;
+        float* dst = a.dk_part + (size_t(share.meeting) * bs + row) * a.dg;
 #pragma unroll 1
-        for (int c = 0; c < DG; c += 32) {
+        for (int c = wg * (DG / 2); c < (wg + 1) * (DG / 2); c += 32) {
           uint32_t v[32];
           tmem_ld32(t_dk + lane_off + c, v);
 #pragma unroll
@@ -498,43 +529,48 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
 
 constexpr int kDkThreads = 256;
 
-// dK of one key head and block: the items' tiles added in order (units of the
-// key head, then a unit's items), rounded to bf16 once.  Four values a thread;
-// the items of a unit are read four at a time.
+// dK of one key head and block: the shares of its lists (a unit each), of the
+// CTAs that met them, in order, rounded to bf16 once.  Four values a thread.
 __global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constant__ SelBwdArgs a) {
+  const SelPlan& p = a.p;
   const int j = blockIdx.x, hk = blockIdx.y % a.HK, b = blockIdx.y / a.HK;
-  const int units = a.p.HU / a.HK, per = a.p.HU / a.p.HS;
-  const int bs = a.p.bs, quads = a.dg / 4;
+  const int units = p.HU / a.HK, per = p.HU / p.HS;
+  const int bs = p.bs, quads = a.dg / 4;
   const int x = blockIdx.z * kDkThreads + threadIdx.x;
   const int key = x / quads, c = (x - key * quads) * 4;
-  if (key >= min(bs, a.p.NK - j * bs)) return;
+  if (key >= min(bs, p.NK - j * bs)) return;
   float4 sum{0.f, 0.f, 0.f, 0.f};
-  auto add = [&](const float4& v) {
-    sum.x += v.x;
-    sum.y += v.y;
-    sum.z += v.z;
-    sum.w += v.w;
-  };
-  const size_t item = size_t(bs) * a.dg * per;  // from an item's tile to the next one's, in a unit
   for (int u = hk * units; u < (hk + 1) * units; ++u) {
-    const int2 r = __ldg(a.p.ranges + size_t(b * a.p.HS + u / per) * a.p.blocks + j);
-    const float* p = a.dk_part + ((size_t(r.x) * per + u % per) * bs + key) * a.dg + c;
-    int it = 0;
-    for (; it + 4 <= r.y; it += 4, p += 4 * item) {
-      float4 v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __ldcs(reinterpret_cast<const float4*>(p + e * item));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) add(v[e]);
+    const int s = b * p.HS + u / per, sub = u % per, i = __ldg(p.place + size_t(s) * p.blocks + j);
+    if (i < 0) continue;
+    // the list's tiles among its group's, and the CTAs whose parts hold them (see find_start)
+    const int g = s / p.group;
+    long long total = 0, at = 0;
+    for (int k = g * p.group; k < min(p.B * p.HS, (g + 1) * p.group); ++k) {
+      if (k == s) at = total;
+      total += (long long)__ldg(p.sizes + k).y * per;
     }
-    for (; it < r.y; ++it, p += item) add(__ldcs(reinterpret_cast<const float4*>(p)));
+    const int4 l = __ldg(p.lists + size_t(s) * p.cap + i);
+    const int n = (l.z + p.queries_per_tile - 1) / p.queries_per_tile;
+    at += (long long)l.w * per + (long long)sub * n;
+    const int c0 = int(((at + 1) * p.ctas - 1) / total), c1 = int(((at + n) * p.ctas - 1) / total);
+    const float* part = a.dk_part + ((((size_t(s) * p.cap + i) * per + sub + size_t(g) * p.ctas + c0) * bs) + key) * a.dg + c;
+#pragma unroll 4
+    for (int k = c0; k <= c1; ++k, part += size_t(bs) * a.dg) {
+      if (total < p.ctas && k * total / p.ctas == (k + 1) * total / p.ctas) continue;  // a part without a tile
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(part));
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
   }
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dk) + b * a.dk_sb + hk * a.dk_sh + (j * bs + key) * a.dk_sn + c;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
 }
 
 template <int D1, int D2, int MODE>
-int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, int sms, cudaStream_t st) {
+int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, cudaStream_t st) {
   using L = SelBwdLayout<D1, D2>;
   SelBwdArgs a = args;
   const int bs = a.p.bs;
@@ -548,25 +584,24 @@ int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, int sms, cudaStre
   auto kern = sel_bwd_kernel<D1, D2, MODE>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kMost);
   if (e != cudaSuccess) return e;
-  const long long most = (long long)a.p.max_items * (a.p.HU / a.p.HS), rows = (long long)a.p.B * a.p.H * a.p.NQ;
-  const int grid = int(most < sms ? most : sms);
+  const long long rows = (long long)a.p.B * a.p.H * a.p.NQ;
   sel_rows_kernel<<<unsigned((rows + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st>>>(a, MODE);
-  kern<<<grid, L::kThreads, L::bytes(a.slots, a.k_bufs, bs), st>>>(m.k1, m.k2, a);
+  kern<<<a.p.ctas, L::kThreads, L::bytes(a.slots, a.k_bufs, bs), st>>>(m.k1, m.k2, a);
   return cudaGetLastError();
 }
 
 template <int D1, int D2>
-int launch_sel_bwd_m(const SelMaps& m, int mode, const SelBwdArgs& a, int sms, cudaStream_t st) {
-  return mode == STREAMKL_GRAD_P2 ? launch_sel_bwd_t<D1, D2, STREAMKL_GRAD_P2>(m, a, sms, st)
-                                  : launch_sel_bwd_t<D1, D2, STREAMKL_GRAD_P1>(m, a, sms, st);
+int launch_sel_bwd_m(const SelMaps& m, int mode, const SelBwdArgs& a, cudaStream_t st) {
+  return mode == STREAMKL_GRAD_P2 ? launch_sel_bwd_t<D1, D2, STREAMKL_GRAD_P2>(m, a, st)
+                                  : launch_sel_bwd_t<D1, D2, STREAMKL_GRAD_P1>(m, a, st);
 }
 
 }  // namespace
 
-int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs& a, int sms, cudaStream_t st) {
+int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs& a, cudaStream_t st) {
   if (d1 == 64)
-    return d2 == 64 ? launch_sel_bwd_m<64, 64>(m, mode, a, sms, st) : launch_sel_bwd_m<64, 128>(m, mode, a, sms, st);
-  return d2 == 64 ? launch_sel_bwd_m<128, 64>(m, mode, a, sms, st) : launch_sel_bwd_m<128, 128>(m, mode, a, sms, st);
+    return d2 == 64 ? launch_sel_bwd_m<64, 64>(m, mode, a, st) : launch_sel_bwd_m<64, 128>(m, mode, a, st);
+  return d2 == 64 ? launch_sel_bwd_m<128, 64>(m, mode, a, st) : launch_sel_bwd_m<128, 128>(m, mode, a, st);
 }
 
 int launch_sel_dk(const SelBwdArgs& a, cudaStream_t st) {

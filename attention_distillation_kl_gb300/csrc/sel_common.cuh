@@ -9,9 +9,10 @@
 // (row, block) is five numbers, so what is written between the passes stays
 // small; an output of d values a row would not allow this.
 //
-// The plan (sel_plan.cu) makes these lists, in query order, and cuts them into
-// items of at most tiles_per_item tiles.  Nothing in it depends on the order
-// in which blocks of a launch run but the items' places in their table.
+// The plan (sel_plan.cu) makes these lists, in query order.  All lists' tiles in
+// a row are cut into as many equal parts as there are CTAs, whatever block a cut
+// falls into; several selection heads at a time, as many as L2 holds the rows
+// of.  Nothing in the plan depends on the order in which blocks of a launch run.
 #pragma once
 
 #include "bwd_common.cuh"
@@ -25,21 +26,12 @@ constexpr int kMaxSlots = 128;    // blocks of one query
 constexpr int kMaxSelBlocks = 4096;
 constexpr int kSlotBits = 7;
 
-// A piece of one block's list: `count` queries from entries[first].
-struct SelItem {
-  int sel;    // b * HS + selection head
-  int block;
-  int first;  // of all entries
-  int count;
-};
-
 struct SelPlan {
   int B, H, NQ, NK, HS, T;
   int bs, blocks;        // keys of a block, blocks of a batch entry
   int G;                 // query heads of a tile, which share keys and selection
   int HU;                // units of G heads in a batch entry; HU / HS use the same lists
   int queries_per_tile;  // 128 / G
-  int tiles_per_item;
   int causal;
   const int* prefix;     // [B] or null
   const int* doc_q;      // [B][NQ] or null
@@ -49,55 +41,152 @@ struct SelPlan {
   unsigned* entries;     // [B HS][NQ T]: query << kSlotBits | slot
   unsigned* slots;       // [B HS][NQ][words]: the slots that count
   int words;             // (T + 31) / 32
-  SelItem* items;
-  int* item_count;       // device
-  int2* ranges;          // [B HS][blocks]: a block's first item and their number, or null
-  int max_items;
+  // Lists that are not empty, of every selection head in block order:
+  // block, first entry (of all), entries, tiles before it.  `cap` places a head.
+  int4* lists;           // [B HS][cap]
+  int cap;
+  int2* sizes;           // [B HS]: lists, tiles
+  int* place;            // [B HS][blocks]: a block's list, or -1 (null: not needed)
+  int group, groups;     // selection heads at a time, and how many times
+  int ctas;
+  int4* starts;          // [groups][ctas]: (selection head, unit), list, its tile, tiles of the part
 };
 
-// What an item is about.
-struct SelWork {
-  int b, head0, block, unit;
-};
-
-// A CTA's items, in order, every role for itself: works blockIdx.x,
-// blockIdx.x + gridDim.x, ...; the one behind the current one is read ahead.
-// (Read where they are used, items and entries put two trips to memory into
-// every tile's chain: 731 us instead of what the copies allow.)
+// A CTA's shares of lists, in order: `count` entries from `first` on.  What
+// comes next is read ahead.
 struct SelWalk {
-  int w, works, first, count;  // entries of the current item
-  int4 raw, next;
+  int first, count;
+  int g, left;        // group, tiles of the part from the current list on
+  int s, sub, i, n;   // selection head, unit of it, list, the head's lists
+  int tile, tiles;    // the current list's first tile and number of tiles here
+  int4 cur, next, start;
 
-  __device__ __forceinline__ SelWalk(const SelPlan& p, int all) : w(blockIdx.x), works(all) {
-    raw = read(p, w);
-    next = read(p, w + gridDim.x);
-    first = raw.z;
-    count = raw.w;
+  __device__ __forceinline__ explicit SelWalk(const SelPlan& p) : g(-1) {
+    start = part(p, 0);
+    enter(p);
   }
-  __device__ __forceinline__ int4 read(const SelPlan& p, int at) const {
-    return at < works ? __ldg(reinterpret_cast<const int4*>(p.items) + at / (p.HU / p.HS)) : int4{0, 0, 0, 0};
+  __device__ __forceinline__ int4 part(const SelPlan& p, int at) const {
+    return at < p.groups ? __ldg(p.starts + size_t(at) * p.ctas + blockIdx.x) : int4{0, 0, 0, 0};
   }
-  __device__ __forceinline__ bool more() const { return w < works; }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void list(const SelPlan& p, int4 now) {
+    cur = now;
+    next = i + 1 < n ? __ldg(p.lists + size_t(s) * p.cap + i + 1) : int4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void here(const SelPlan& p) {  // the current list's share
+    const int per = p.queries_per_tile;
+    tiles = min((cur.z + per - 1) / per - tile, left);
+    first = cur.y + tile * per;
+    count = min(cur.z - tile * per, tiles * per);
+  }
+  __device__ __forceinline__ void enter(const SelPlan& p) {  // the next group's part
+    left = 0;
+    count = first = tiles = tile = 0;
+    while (left == 0 && ++g < p.groups) {
+      const int4 v = start;
+      start = part(p, g + 1);
+      left = v.w;
+      if (left == 0) continue;
+      const int per = p.HU / p.HS;
+      s = v.x / per;
+      sub = v.x - s * per;
+      i = v.y;
+      tile = v.z;
+      n = __ldg(p.sizes + s).x;
+      list(p, __ldg(p.lists + size_t(s) * p.cap + i));
+      here(p);
+    }
+  }
   __device__ __forceinline__ void advance(const SelPlan& p) {
-    w += gridDim.x;
-    raw = next;
-    next = read(p, w + gridDim.x);
-    first = raw.z;
-    count = raw.w;
+    left -= tiles;
+    if (left <= 0) return enter(p);
+    tile = 0;
+    if (++sub == p.HU / p.HS) {
+      sub = 0;
+      if (++i < n) {
+        list(p, next);
+      } else {
+        i = 0;
+        do n = __ldg(p.sizes + ++s).x;  // (tiles are left, so lists are)
+        while (n == 0);
+        list(p, __ldg(p.lists + size_t(s) * p.cap));
+      }
+    }
+    here(p);
   }
-  __device__ __forceinline__ SelWork get(const SelPlan& p) const {
-    const int per = p.HU / p.HS;
-    SelWork k;
-    k.unit = raw.x * per + w % per;  // b * HU + unit of the batch entry
-    k.b = k.unit / p.HU;
-    k.head0 = (k.unit - k.b * p.HU) * p.G;
-    k.block = raw.y;
-    return k;
+  // A number of its own for every (list, CTA) that meet: along the parts one or
+  // the other goes up.
+  __device__ __forceinline__ long long meeting(const SelPlan& p) const {
+    return ((long long)s * p.cap + i) * (p.HU / p.HS) + sub + (long long)g * p.ctas + blockIdx.x;
+  }
+};
+// What the other warps of a CTA are told about a share; count 0: there are no more.
+struct alignas(16) SelShare {
+  int first, count, b, head0;
+  int block, unit;             // unit of the batch entry: head0 / G
+  unsigned long long meeting;  // SelWalk::meeting
+};
+constexpr int kShares = 8;  // told ahead
+
+// One warp walks and tells; the others read every share once, when they come to
+// it.  (A walk in every warp cost the statistics their registers: 783 us for
+// the forward at 16384 queries x 32 heads, where 479 had been.)  Barriers: full
+// [kShares] (1 arrival), then empty [kShares] (one for each reading warp).
+__device__ __forceinline__ void tell_shares(const SelPlan& p, SelShare* shares, uint32_t bars, Ctl ctl) {
+  SelWalk walk(p);
+  for (int q = 0;; ++q) {
+    const int at = q % kShares;
+    if (!mbar_wait_polled(bars + 8u * (kShares + at), ((q / kShares) & 1) ^ 1, ctl)) return;
+    SelShare x{0, 0, 0, 0, 0, 0, 0ull};
+    const bool more = walk.more();
+    if (more) {
+      const int unit = walk.s * (p.HU / p.HS) + walk.sub;
+      x.first = walk.first;
+      x.count = walk.count;
+      x.b = unit / p.HU;
+      x.unit = unit - x.b * p.HU;
+      x.head0 = x.unit * p.G;
+      x.block = walk.cur.x;
+      x.meeting = walk.meeting(p);
+    }
+    shares[at] = x;
+    mbar_arrive(bars + 8u * at);
+    if (!more) return;
+    walk.advance(p);
+  }
+}
+
+struct SelReader {
+  const SelShare* shares;
+  uint32_t bars;
+  int q;
+  int first, count, b, head0, block;
+  unsigned long long meeting;
+
+  __device__ __forceinline__ SelReader(const SelShare* s, uint32_t barriers) : shares(s), bars(barriers), q(0), count(0) {}
+  // Called by a whole warp; false at the end (and on an abort).
+  __device__ __forceinline__ bool next(Ctl ctl) {
+    const int at = q % kShares;
+    if (!mbar_wait_warp(bars + 8u * at, (q / kShares) & 1, ctl)) {
+      count = 0;
+      return false;
+    }
+    const int4 v = *reinterpret_cast<const int4*>(shares + at);
+    first = v.x;
+    count = v.y;
+    b = v.z;
+    head0 = v.w;
+    block = shares[at].block;
+    meeting = shares[at].meeting;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8u * (kShares + at));
+    ++q;
+    return count > 0;
   }
 };
 constexpr unsigned kNoEntry = 0xffffffffu;
-// Entry e of the walk's item, for a row with a place in the tile.
-__device__ __forceinline__ unsigned entry_of(const SelPlan& p, const SelWalk& k, int e, bool place) {
+// Entry e of the reader's share, for a row with a place in the tile.
+__device__ __forceinline__ unsigned entry_of(const SelPlan& p, const SelReader& k, int e, bool place) {
   return place && e < k.count ? __ldg(p.entries + k.first + e) : kNoEntry;
 }
 
@@ -199,7 +288,7 @@ struct SelBwdArgs {
   const float* dkl;
   int dg, pitch;          // head dim of the gradient side; row length of dq32
   float* dq32;            // [B H NQ][pitch], zeroed: dQ contributions, on their rows' grids
-  float* dk_part;         // [works][bs][dg]: dK of an item
+  float* dk_part;         // [meetings][bs][dg]: a CTA's dK of a list
   const unsigned* kmax;   // per key head of the gradient side (launch_kmax_strided)
   void* dk;               // bf16 [B][HK][NK][dg]
   long long dk_sb, dk_sh, dk_sn;
@@ -209,10 +298,10 @@ struct SelBwdArgs {
   int slots, k_bufs;
 };
 
-int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs& a, int sms, cudaStream_t st);
+int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs& a, cudaStream_t st);
 int launch_sel_dk(const SelBwdArgs& a, cudaStream_t st);
 int launch_sel_plan(const SelPlan& p, cudaStream_t st);
-int launch_sel_fwd(const SelMaps& m, int d1, int d2, const SelFwdArgs& a, int sms, cudaStream_t st);
+int launch_sel_fwd(const SelMaps& m, int d1, int d2, const SelFwdArgs& a, cudaStream_t st);
 int launch_sel_merge(const SelFwdArgs& a, cudaStream_t st);
 
 }  // namespace skl

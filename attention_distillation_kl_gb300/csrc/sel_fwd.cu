@@ -1,8 +1,8 @@
 // Forward over selected blocks (sel_common.cuh): the sums of every (row, block)
 // pair, then their merge into KL, LSE1 and LSE2.
 //
-// Persistent CTAs walk the items: K1, K2 of the item's block once, then tiles
-// of 128 gathered rows, a side's tile at a time, through a ring of slots.  18 warps:
+// Persistent CTAs walk their lists: K1, K2 of the list's block once, then tiles
+// of 128 gathered rows, a side's tile at a time, through a ring of slots.  19 warps:
 //   warps 0-11  statistics: a warpgroup takes every third tile; thread = row
 //   warps 12-15 gather 32 rows each, 16 bytes a lane (cp.async).  TMA takes
 //               some 50 clocks for a copy of few rows, whatever its form: at
@@ -10,12 +10,13 @@
 //               TB/s, cp.async of 4 and 8 warps 11.6 and 14.3.
 //   warp 16     S1 = Q1 K1^T, S2 = Q2 K2^T into one of 4 TMEM buffers (2 for blocks of 128)
 //   warp 17     K by TMA
+//   warp 18     tells the others what to take (SelShare)
 // A row's keys in one block are few, so its references are its own largest
 // scores there (one more read of TMEM), and nothing is rescaled:
 //   e_t = S_t log2 e - m_t,  l_t = sum 2^e_t,  acc = sum 2^e1 (e1 - e2).
 // The merge adds the parts of a row's slots in their order (as merge_stats of
 // the dense forward does for splits), so results do not depend on which CTA
-// took which item.
+// took which list.
 #include "fwd_mod.cuh"
 #include "sel_common.cuh"
 
@@ -26,13 +27,18 @@ namespace {
 struct SelFwdLayout {
   static constexpr int kWGs = 3;  // of statistics
   static constexpr int kGatherWarp = 4 * kWGs, kGatherWarps = 4;
-  static constexpr int kMmaWarp = kGatherWarp + kGatherWarps, kLoadWarp = kMmaWarp + 1;
-  static constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps + 2);
+  static constexpr int kMmaWarp = kGatherWarp + kGatherWarps, kLoadWarp = kMmaWarp + 1, kWalkWarp = kMmaWarp + 2;
+  static constexpr int kThreads = 32 * (kWalkWarp + 1);
   static constexpr int kMaxSlots = 8;
-  // k_full[2], k_empty[2], q_full[8], q_empty[8], s_full[4], s_empty[4], done
-  static constexpr int kKFull = 0, kKEmpty = 2, kQFull = 4, kQEmpty = 12, kSFull = 20, kSEmpty = 24, kDone = 28;
-  static constexpr int kNumBars = 29;
-  static constexpr uint32_t kTail = kNumBars * 8 + 16;
+  // k_full[2], k_empty[2], q_full[8], q_empty[8], s_full[12], s_empty[4], done, shares.  (A warpgroup waits for every
+  // phase of the barriers that it waits for: each belongs to one warpgroup and one buffer of S.)
+  static constexpr int kTurns = 12;
+  static_assert(kTurns % kWGs == 0 && kTurns % 4 == 0, "a turn is of one warpgroup and one buffer");
+  static constexpr int kKFull = 0, kKEmpty = 2, kQFull = 4, kQEmpty = 12, kSFull = 20, kSEmpty = kSFull + kTurns,
+                       kDone = kSEmpty + 4, kTold = kDone + 1;
+  static constexpr int kNumBars = (kTold + 2 * kShares + 1) / 2 * 2;  // (16-byte words behind them)
+  static_assert(kNumBars % 2 == 0, "shares are aligned");
+  static constexpr uint32_t kTail = kNumBars * 8 + kShares * sizeof(SelShare) + 16;
   static constexpr uint32_t kMost = 232448;
   static constexpr uint32_t slot_bytes(int d1, int d2) { return uint32_t(d1 > d2 ? d1 : d2) * 2u * kTile; }
   static uint32_t bytes(int slots, int k_bufs, int d1, int d2, int bs) {
@@ -98,16 +104,19 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
   const uint32_t kK1 = uint32_t(bs) * D1 * 2, kK = uint32_t(bs) * (D1 + D2) * 2;
   const uint32_t oQ = a.k_bufs * kK, oBar = oQ + a.slots * kSlot;
   auto bar = [&](int id) { return sb + oBar + 8u * id; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + oBar + L::kNumBars * 8);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + oBar + L::kNumBars * 8 + 4);
+  SelShare* shares = reinterpret_cast<SelShare*>(smem + oBar + L::kNumBars * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shares + kShares);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const Ctl ctl{abort_flag, a.status};
   const int bufs = bs == 128 ? 2 : 4;  // of S1, S2 in TMEM, bs columns each
+  const uint32_t told = sb + oBar + 8u * L::kTold;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       int count = 1;
       if (i >= L::kQFull && i < L::kQEmpty) count = 32 * L::kGatherWarps;
       if (i >= L::kSEmpty && i < L::kDone) count = 4;  // the warps of a warpgroup
+      if (i >= L::kTold + kShares) count = L::kWalkWarp;  // the warps before it
       mbar_init(bar(i), count);
     }
     *abort_flag = 0;
@@ -126,7 +135,6 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int per_tile = a.p.queries_per_tile, G = a.p.G;
-  const int works = min(*a.p.item_count, a.p.max_items) * (a.p.HU / a.p.HS);
 
   if (warp >= L::kGatherWarp && warp < L::kMmaWarp) {
     // ---------------------------------------------------------------- gather: rows [first, first + 32)
@@ -135,25 +143,28 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
     const bool place = ql < per_tile;
     int s = 0, m = 0;  // the slot, and how often the ring has been round
     bool ok = true;
-    SelWalk walk(a.p, works);
+    SelReader share(shares, told);
+    const uint8_t *b1 = nullptr, *b2 = nullptr;  // the lane's row 0 of both sides
+    auto enter = [&]() {
+      if (!share.next(ctl)) return false;
+      b1 = a.r1.at(share.b, share.head0 + hl, 0);
+      b2 = a.r2.at(share.b, share.head0 + hl, 0);
+      return true;
+    };
+    bool more = enter();
     int e0 = 0;
-    unsigned ent = entry_of(a.p, walk, ql, place);
-    SelWork k = walk.get(a.p);
-    const uint8_t *b1 = a.r1.at(k.b, k.head0 + hl, 0), *b2 = a.r2.at(k.b, k.head0 + hl, 0);
-    while (ok && walk.more()) {
+    unsigned ent = entry_of(a.p, share, ql, place);
+    while (ok && more) {
       // (rows past the last are not read: what the slot holds there gives scores that nobody takes)
       const int i = int(ent >> kSlotBits);
       const unsigned long long p1 = ent != kNoEntry ? reinterpret_cast<unsigned long long>(b1 + i * a.r1.sn) : 0ull;
       const unsigned long long p2 = ent != kNoEntry ? reinterpret_cast<unsigned long long>(b2 + i * a.r2.sn) : 0ull;
       e0 += per_tile;
-      if (e0 >= walk.count) {
-        walk.advance(a.p);
+      if (e0 >= share.count) {
+        more = enter();
         e0 = 0;
-        k = walk.get(a.p);
-        b1 = a.r1.at(k.b, k.head0 + hl, 0);
-        b2 = a.r2.at(k.b, k.head0 + hl, 0);
       }
-      ent = entry_of(a.p, walk, e0 + ql, place);
+      ent = entry_of(a.p, share, e0 + ql, place);
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
         ok = mbar_wait_warp(bar(L::kQEmpty + s), (m & 1) ^ 1, ctl);
@@ -166,31 +177,33 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
     }
     cp_async_wait_all();
   } else if (warp >= L::kMmaWarp) {
-    if (warp == L::kLoadWarp && lane == 0) {
+    if (warp == L::kWalkWarp) {
+      if (lane == 0) tell_shares(a.p, shares, told, ctl);
+    } else if (warp == L::kLoadWarp) {
       // -------------------------------------------------------------- K
-      int items = 0;
-      for (SelWalk walk(a.p, works); walk.more(); walk.advance(a.p), ++items) {
-        const SelWork k = walk.get(a.p);
-        const int kb = items % a.k_bufs, hu = k.head0 / G;
-        if (!mbar_wait_polled(bar(L::kKEmpty + kb), ((items / a.k_bufs) & 1) ^ 1, ctl)) break;
+      int kept = 0;
+      for (SelReader share(shares, told); share.next(ctl); ++kept) {
+        const int kb = kept % a.k_bufs, hu = share.head0 / G;
+        if (!mbar_wait_warp(bar(L::kKEmpty + kb), ((kept / a.k_bufs) & 1) ^ 1, ctl)) break;
+        if (lane != 0) continue;
         const uint32_t full = bar(L::kKFull + kb);
         mbar_arrive_expect_tx(full, kK);
 #pragma unroll
         for (int c = 0; c < D1 / 64; ++c)
-          tma_load_4d(sb + kb * kK + c * (bs * 128), &tk1, full, c * 64, k.block * bs, hu / a.u1, k.b);
+          tma_load_4d(sb + kb * kK + c * (bs * 128), &tk1, full, c * 64, share.block * bs, hu / a.u1, share.b);
 #pragma unroll
         for (int c = 0; c < D2 / 64; ++c)
-          tma_load_4d(sb + kb * kK + kK1 + c * (bs * 128), &tk2, full, c * 64, k.block * bs, hu / a.u2, k.b);
+          tma_load_4d(sb + kb * kK + kK1 + c * (bs * 128), &tk2, full, c * 64, share.block * bs, hu / a.u2, share.b);
       }
-      if (*abort_flag)  // let the copies already started land before the CTA exits
-        for (int j = items > a.k_bufs ? items - a.k_bufs : 0; j < items; ++j)
+      if (*abort_flag && lane == 0)  // let the copies already started land before the CTA exits
+        for (int j = kept > a.k_bufs ? kept - a.k_bufs : 0; j < kept; ++j)
           mbar_drain(bar(L::kKFull + j % a.k_bufs), (j / a.k_bufs) & 1, 200000000ull);
     } else if (warp == L::kMmaWarp) {
       // -------------------------------------------------------------- MMA issuer
       const uint32_t leader = elect_one();
       const uint32_t idesc = idesc_bf16(128, bs, 0, 0);
       const uint32_t dhi = uint32_t(sdesc_sw128(0, 16, 1024) >> 32), dlo = uint32_t(sdesc_sw128(0, 16, 1024));
-      int n = 0, s = 0, m = 0, items = 0;
+      int n = 0, s = 0, m = 0, kept = 0;
       bool ok = true;
       // S of one side: the tile in slot s by K at ks
       auto product = [&](auto width, uint32_t d, uint32_t ks) {
@@ -207,17 +220,16 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
         mma_commit(leader, bar(L::kQEmpty + s));
         if (++s == a.slots) s = 0, ++m;
       };
-      for (SelWalk walk(a.p, works); ok && walk.more(); walk.advance(a.p), ++items) {
-        const int count = walk.count;
-        const int kb = items % a.k_bufs;
-        ok = mbar_wait_warp(bar(L::kKFull + kb), (items / a.k_bufs) & 1, ctl);
-        for (int e0 = 0; ok && e0 < count; e0 += per_tile, ++n) {
+      for (SelReader share(shares, told); ok && share.next(ctl); ++kept) {
+        const int kb = kept % a.k_bufs;
+        ok = mbar_wait_warp(bar(L::kKFull + kb), (kept / a.k_bufs) & 1, ctl);
+        for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n) {
           const int i = n & (bufs - 1);
           const uint32_t d1 = tmem + uint32_t(i * 2 * bs);
           ok = mbar_wait_warp(bar(L::kSEmpty + i), ((n / bufs) & 1) ^ 1, ctl);
           if (ok) product(std::integral_constant<int, D1>{}, d1, sb + kb * kK);
           if (ok) product(std::integral_constant<int, D2>{}, d1 + uint32_t(bs), sb + kb * kK + kK1);
-          if (ok) mma_commit(leader, bar(L::kSFull + i));
+          if (ok) mma_commit(leader, bar(L::kSFull + n % L::kTurns));
         }
         if (ok) mma_commit(leader, bar(L::kKEmpty + kb));
       }
@@ -233,44 +245,44 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
     const int nqt = (a.p.NQ + kTile - 1) / kTile, nkt = (a.p.NK + kTile - 1) / kTile;
     const int off = a.p.NK - a.p.NQ;
     const bool place = ql < per_tile;
-    SelWalk walk(a.p, works);
+    SelReader share(shares, told);
     int e0 = 0, n = wg;
-    // to this warpgroup's next tile; whether that is of another item
+    bool more = share.next(ctl);
+    // to this warpgroup's next tile; whether that is of another share
     auto skip = [&](int tiles) {
       bool other = false;
-      for (e0 += tiles * per_tile; walk.more() && e0 >= walk.count; other = true) {
-        e0 -= (walk.count + per_tile - 1) / per_tile * per_tile;
-        walk.advance(a.p);
+      for (e0 += tiles * per_tile; more && e0 >= share.count; other = true) {
+        e0 -= (share.count + per_tile - 1) / per_tile * per_tile;
+        more = share.next(ctl);
       }
       return other;
     };
     skip(wg);
-    unsigned ent = entry_of(a.p, walk, e0 + ql, place);
-    SelWork k;
+    unsigned ent = entry_of(a.p, share, e0 + ql, place);
     size_t first = 0;  // record of the row's query 0
-    int prefix = 0;
-    for (bool other = true, more = walk.more(); more;) {
+    int prefix = 0, b = 0, k0 = 0;
+    for (bool other = true, here = more; here; here = more) {
       if (other) {
-        k = walk.get(a.p);
-        first = size_t(k.b * a.p.H + k.head0 + hl) * a.p.NQ * a.p.T;
-        if (a.p.prefix != nullptr) prefix = min(max(a.p.prefix[k.b], 0), a.p.NK);
+        b = share.b;
+        k0 = share.block * bs;
+        first = size_t(b * a.p.H + share.head0 + hl) * a.p.NQ * a.p.T;
+        if (a.p.prefix != nullptr) prefix = min(max(a.p.prefix[b], 0), a.p.NK);
       }
-      const int k0 = k.block * bs, buf = n & (bufs - 1);
+      const int buf = n & (bufs - 1);
       const bool on = ent != kNoEntry;
       const int i = on ? int(ent >> kSlotBits) : 0, t = int(ent & ((1u << kSlotBits) - 1u));
       other = skip(L::kWGs);
-      more = walk.more();
-      ent = entry_of(a.p, walk, e0 + ql, place);
+      ent = entry_of(a.p, share, e0 + ql, place);
       int id = 0;
       const int* kids = nullptr;
       if (a.vis.ids_q != nullptr) {
-        id = a.vis.ids_q[size_t(k.b) * nqt * kTile + i];
-        kids = a.vis.ids_k + size_t(k.b) * nkt * kTile + k0;
+        id = a.vis.ids_q[size_t(b) * nqt * kTile + i];
+        kids = a.vis.ids_k + size_t(b) * nkt * kTile + k0;
       }
       const int last = a.p.causal ? min(max(i + off + 1, prefix), a.p.NK) : a.p.NK;
       const bool whole = __all_sync(0xffffffffu, !on || last >= k0 + bs) && kids == nullptr;
       const bool idle = __all_sync(0xffffffffu, !on);
-      if (!mbar_wait_warp(bar(L::kSFull + buf), (n / bufs) & 1, ctl)) break;
+      if (!mbar_wait_warp(bar(L::kSFull + n % L::kTurns), (n / L::kTurns) & 1, ctl)) break;
       tc_fence_after();
       ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
       if (!idle) {
@@ -282,7 +294,7 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kSEmpty + buf));
       const size_t at = first + size_t(i) * a.p.T + t;
-      if (on && SKL_CHECK(a.status, i < a.p.NQ && t < a.p.T && k.head0 + hl < a.p.H && k.b < a.p.B)) {
+      if (on && SKL_CHECK(a.status, i < a.p.NQ && t < a.p.T && b < a.p.B)) {
         // a row that ids hide the whole block from has sums of 2^(-3e38 - ...) = 0, relative to nothing
         const bool none = st.m1 == -INFINITY && st.l1 == 0.f;
         a.rec[at] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(st.m1, st.m2, st.l1, st.l2);
@@ -341,27 +353,25 @@ __global__ void __launch_bounds__(kMergeThreads) sel_merge_kernel(const __grid_c
 }
 
 template <int D1, int D2>
-int launch_sel_fwd_t(const SelMaps& m, const SelFwdArgs& args, int sms, cudaStream_t st) {
+int launch_sel_fwd_t(const SelMaps& m, const SelFwdArgs& args, cudaStream_t st) {
   using L = SelFwdLayout;
   SelFwdArgs a = args;
-  // two buffers of K (the next item's loads) where they leave five slots, then as many slots as fit
+  // two buffers of K (the next list's loads) where they leave five slots, then as many slots as fit
   a.k_bufs = L::bytes(5, 2, D1, D2, a.p.bs) <= L::kMost ? 2 : 1;
   a.slots = 5;
   while (a.slots < L::kMaxSlots && L::bytes(a.slots + 1, a.k_bufs, D1, D2, a.p.bs) <= L::kMost) ++a.slots;
   auto kern = sel_fwd_kernel<D1, D2>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kMost);
   if (e != cudaSuccess) return e;
-  const long long most = (long long)a.p.max_items * (a.p.HU / a.p.HS);
-  const int grid = int(most < sms ? most : sms);
-  kern<<<grid, L::kThreads, L::bytes(a.slots, a.k_bufs, D1, D2, a.p.bs), st>>>(m.k1, m.k2, a);
+  kern<<<a.p.ctas, L::kThreads, L::bytes(a.slots, a.k_bufs, D1, D2, a.p.bs), st>>>(m.k1, m.k2, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int launch_sel_fwd(const SelMaps& m, int d1, int d2, const SelFwdArgs& a, int sms, cudaStream_t st) {
-  if (d1 == 64) return d2 == 64 ? launch_sel_fwd_t<64, 64>(m, a, sms, st) : launch_sel_fwd_t<64, 128>(m, a, sms, st);
-  return d2 == 64 ? launch_sel_fwd_t<128, 64>(m, a, sms, st) : launch_sel_fwd_t<128, 128>(m, a, sms, st);
+int launch_sel_fwd(const SelMaps& m, int d1, int d2, const SelFwdArgs& a, cudaStream_t st) {
+  if (d1 == 64) return d2 == 64 ? launch_sel_fwd_t<64, 64>(m, a, st) : launch_sel_fwd_t<64, 128>(m, a, st);
+  return d2 == 64 ? launch_sel_fwd_t<128, 64>(m, a, st) : launch_sel_fwd_t<128, 128>(m, a, st);
 }
 
 int launch_sel_merge(const SelFwdArgs& a, cudaStream_t st) {

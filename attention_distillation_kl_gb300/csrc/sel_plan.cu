@@ -1,13 +1,13 @@
 // The plan of attention over selected blocks (sel_common.cuh): for each block
-// the queries that selected it, in order, and the items that cut these lists.
+// the queries that selected it, in order, and each CTA's part of these lists.
 //
-// Three kernels.  A warp owns a chunk of queries and the blocks' counters of
-// that chunk, in shared memory; it takes 32 slots at a time, and lanes with the
-// same block find one another by a warp match, so no order of atomics enters:
-// count; then one CTA for each selection head turns counts into places and
-// writes items; then the same walk again writes the entries.  A block that a
-// query names twice counts once, and one that it cannot see, or that does not
-// exist, does not count.
+// A warp owns a chunk of queries and the blocks' counters of that chunk, in
+// shared memory; it takes 32 slots at a time, and lanes with the same block find
+// one another by a warp match, so no order of atomics enters: count; then one
+// CTA for each selection head turns counts into places and lists; then the same
+// walk again writes the entries, while other blocks of that launch find where
+// every CTA's part starts.  A block that a query names twice counts once, and
+// one that it cannot see, or that does not exist, does not count.
 #include <algorithm>
 
 #include "sel_common.cuh"
@@ -91,12 +91,44 @@ __device__ __forceinline__ void walk(const SelPlan& p, int sel, int q0, int q1, 
   }
 }
 
+// Where CTA c's part of a group's tiles starts, and how long it is: tiles
+// [c total / ctas, (c + 1) total / ctas) of the group's.
+__device__ __forceinline__ void find_start(const SelPlan& p, int u) {
+  const int g = u / p.ctas, c = u - g * p.ctas, per = p.HU / p.HS;
+  const int s0 = g * p.group, s1 = min(p.B * p.HS, s0 + p.group);
+  long long total = 0;
+  for (int s = s0; s < s1; ++s) total += (long long)p.sizes[s].y * per;
+  long long at = c * total / p.ctas;
+  const int len = int((c + 1) * total / p.ctas - at);
+  int4 out{0, 0, 0, len};
+  if (len > 0) {
+    int s = s0;
+    for (; at >= (long long)p.sizes[s].y * per; ++s) at -= (long long)p.sizes[s].y * per;
+    const int4* lists = p.lists + size_t(s) * p.cap;
+    int lo = 0, hi = p.sizes[s].x - 1;  // the last list that starts at or before it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if ((long long)lists[mid].w * per <= at) lo = mid;
+      else hi = mid - 1;
+    }
+    const int4 l = lists[lo];
+    const int in = int(at - (long long)l.w * per), n = (l.z + p.queries_per_tile - 1) / p.queries_per_tile;
+    out = make_int4(s * per + in / n, lo, in % n, len);
+  }
+  p.starts[u] = out;
+}
+
 template <bool kFill>
 __global__ void __launch_bounds__(32 * kPlanWarps) sel_walk_kernel(const __grid_constant__ SelPlan p) {
   extern __shared__ unsigned shared_counters[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sel = blockIdx.y, c = blockIdx.x * kPlanWarps + warp;
-  if (!kFill && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.item_count = 0;
+  const int walkers = (p.chunks + kPlanWarps - 1) / kPlanWarps;
+  const int sel = blockIdx.x / walkers, c = (blockIdx.x - sel * walkers) * kPlanWarps + warp;
+  if (sel >= p.B * p.HS) {  // (kFill only)
+    const int u = (blockIdx.x - p.B * p.HS * walkers) * 32 * kPlanWarps + threadIdx.x;
+    if (u < p.groups * p.ctas) find_start(p, u);
+    return;
+  }
   if (c >= p.chunks) return;
   unsigned* counters = shared_counters + warp * p.blocks;
   unsigned* mine = p.counts + (size_t(sel) * p.chunks + c) * p.blocks;
@@ -107,90 +139,69 @@ __global__ void __launch_bounds__(32 * kPlanWarps) sel_walk_kernel(const __grid_
     for (int j = lane; j < p.blocks; j += 32) mine[j] = counters[j];
 }
 
-// Exclusive sums over the CTA's threads of two values; the totals in sum_a, sum_b.
-__device__ __forceinline__ void scan2(unsigned a, unsigned b, unsigned& before_a, unsigned& before_b, unsigned& sum_a,
-                                      unsigned& sum_b) {
-  __shared__ uint2 part[kScanThreads / 32];
+// Exclusive sums over the CTA's threads of three values (and of all in `sum`).
+__device__ __forceinline__ uint3 scan3(uint3 v, uint3& sum) {
+  __shared__ uint3 part[kScanThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned x = a, y = b;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const unsigned u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) x += u, y += v;
-  }
-  if (lane == 31) part[warp] = make_uint2(x, y);
-  __syncthreads();
-  if (warp == 0) {
-    uint2 s = lane < kScanThreads / 32 ? part[lane] : make_uint2(0, 0);
+  auto up = [&](uint3& x) {
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const unsigned u = __shfl_up_sync(0xffffffffu, s.x, o), v = __shfl_up_sync(0xffffffffu, s.y, o);
-      if (lane >= o) s.x += u, s.y += v;
+      const unsigned a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o),
+                     c = __shfl_up_sync(0xffffffffu, x.z, o);
+      if (lane >= o) x.x += a, x.y += b, x.z += c;
     }
-    if (lane < kScanThreads / 32) part[lane] = s;
+  };
+  uint3 x = v;
+  up(x);
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    uint3 s = part[lane];
+    up(s);
+    part[lane] = s;
   }
   __syncthreads();
-  const uint2 up = warp > 0 ? part[warp - 1] : make_uint2(0, 0), all = part[kScanThreads / 32 - 1];
-  before_a = up.x + x - a;
-  before_b = up.y + y - b;
-  sum_a = all.x;
-  sum_b = all.y;
+  static_assert(kScanThreads == 1024, "a warp sums the warps");
+  const uint3 before = warp > 0 ? part[warp - 1] : make_uint3(0, 0, 0);
+  sum = part[kScanThreads / 32 - 1];
   __syncthreads();
+  return make_uint3(before.x + x.x - v.x, before.y + x.y - v.y, before.z + x.z - v.z);
 }
 
 __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(const __grid_constant__ SelPlan p) {
-  __shared__ int region;
   const int sel = blockIdx.x;
   unsigned* counts = p.counts + size_t(sel) * p.chunks * p.blocks;
-  const unsigned per_item = unsigned(p.queries_per_tile) * p.tiles_per_item;
-  // items in all first: they are one stretch of the table
-  unsigned total_items = 0;
-  constexpr int kRounds = kMaxSelBlocks / kScanThreads;
-  unsigned n[kRounds], entry[kRounds], item[kRounds];
-  unsigned entries_before = 0;
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    if (r * kScanThreads >= p.blocks) break;
-    const int j = r * kScanThreads + threadIdx.x;
-    n[r] = 0;
+  const unsigned per = p.queries_per_tile, base = unsigned(sel) * unsigned(p.NQ) * p.T;
+  uint3 before{0, 0, 0};  // entries, lists, tiles
+  for (int j0 = 0; j0 < p.blocks; j0 += kScanThreads) {
+    const int j = j0 + threadIdx.x;
+    unsigned n = 0;
     if (j < p.blocks)
-#pragma unroll 8
-      for (int c = 0; c < p.chunks; ++c) n[r] += counts[size_t(c) * p.blocks + j];
-    unsigned be, bi, se, si;
-    scan2(n[r], (n[r] + per_item - 1) / per_item, be, bi, se, si);
-    entry[r] = entries_before + be;
-    item[r] = total_items + bi;
-    entries_before += se;
-    total_items += si;
-  }
-  if (threadIdx.x == 0) region = atomicAdd(p.item_count, int(total_items));
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int j = r * kScanThreads + threadIdx.x;
-    if (j >= p.blocks) break;
-    unsigned at = entry[r];
-#pragma unroll 8
+#pragma unroll 16
+      for (int c = 0; c < p.chunks; ++c) n += counts[size_t(c) * p.blocks + j];
+    uint3 sum;
+    uint3 at = scan3(make_uint3(n, n != 0u ? 1u : 0u, (n + per - 1) / per), sum);
+    at = make_uint3(at.x + before.x, at.y + before.y, at.z + before.z);
+    before = make_uint3(before.x + sum.x, before.y + sum.y, before.z + sum.z);
+    if (j >= p.blocks) continue;
+    if (n != 0u) p.lists[size_t(sel) * p.cap + at.y] = make_int4(j, int(base + at.x), int(n), int(at.z));
+    if (p.place != nullptr) p.place[size_t(sel) * p.blocks + j] = n != 0u ? int(at.y) : -1;
+    unsigned to = at.x;
+#pragma unroll 16
     for (int c = 0; c < p.chunks; ++c) {
       const unsigned k = counts[size_t(c) * p.blocks + j];
-      counts[size_t(c) * p.blocks + j] = at;
-      at += k;
-    }
-    if (p.ranges != nullptr)
-      p.ranges[size_t(sel) * p.blocks + j] = make_int2(region + int(item[r]), int((n[r] + per_item - 1) / per_item));
-    const unsigned base = unsigned(sel) * unsigned(p.NQ) * p.T + entry[r];
-    for (unsigned k = 0; k * per_item < n[r]; ++k) {
-      const int place = region + int(item[r] + k);
-      if (place < p.max_items)
-        p.items[place] = SelItem{sel, j, int(base + k * per_item), int(min(per_item, n[r] - k * per_item))};
+      counts[size_t(c) * p.blocks + j] = to;
+      to += k;
     }
   }
+  if (threadIdx.x == 0) p.sizes[sel] = make_int2(int(before.y), int(before.z));
 }
 
 }  // namespace
 
 int launch_sel_plan(const SelPlan& p, cudaStream_t st) {
-  const dim3 grid(unsigned((p.chunks + kPlanWarps - 1) / kPlanWarps), unsigned(p.B * p.HS));
+  const unsigned walkers = unsigned((p.chunks + kPlanWarps - 1) / kPlanWarps * p.B * p.HS);
+  const unsigned finders = unsigned((p.groups * p.ctas + 32 * kPlanWarps - 1) / (32 * kPlanWarps));
   const int smem = kPlanWarps * p.blocks * int(sizeof(unsigned));
   for (auto kern : {sel_walk_kernel<false>, sel_walk_kernel<true>}) {
     // (always the most: threads that launch at once would set each other's size)
@@ -198,9 +209,9 @@ int launch_sel_plan(const SelPlan& p, cudaStream_t st) {
                                                kPlanWarps * kMaxSelBlocks * int(sizeof(unsigned)));
     if (e != cudaSuccess) return e;
   }
-  sel_walk_kernel<false><<<grid, 32 * kPlanWarps, smem, st>>>(p);
+  sel_walk_kernel<false><<<walkers, 32 * kPlanWarps, smem, st>>>(p);
   sel_scan_kernel<<<p.B * p.HS, kScanThreads, 0, st>>>(p);
-  sel_walk_kernel<true><<<grid, 32 * kPlanWarps, smem, st>>>(p);
+  sel_walk_kernel<true><<<walkers + finders, 32 * kPlanWarps, smem, st>>>(p);
   return cudaGetLastError();
 }
 
