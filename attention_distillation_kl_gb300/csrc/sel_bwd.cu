@@ -11,22 +11,21 @@
 // (dq_fixed_exp), so that the sums are exact in any order and the result is
 // bitwise repeatable.  24 warps:
 //   warps 0-7   dS (thread = row; a warpgroup takes half of the columns)
-//   warps 8-15  dQ: TMEM -> registers, four lanes to 8 values of a row, so that
-//               every reduction covers whole sectors (a warpgroup takes every
-//               other tile: half of its time is spent waiting to issue them);
-//               after a list, dK (half of the columns each)
+//   warps 8-15  dQ (a warpgroup takes half of the columns): TMEM -> registers ->
+//               shared memory, 16 rows x 32 values at a time, so that 8 lanes
+//               reduce a whole line of 128 bytes; after a list, dK
 //   warps 16-19 gather 32 rows each of both sides, and the rows' parameters
 //               (sel_rows_kernel)
 //   warp 20     S1, S2      warp 21     dK, dQ      warp 22     K by TMA
 //   warp 23     tells the others what to take (SelShare)
-// TMEM: S1, S2 of bs columns from 0; then, with blocks up to 64, dK [128, 256)
-// and two buffers of dQ, else dK [256, 384) and one.
+// TMEM: S1, S2 of bs columns (two buffers with blocks up to 64), dK [256, 384),
+// dQ [384, 512).
 //
 // Bound by the reductions: a row and block bring 4 dg bytes to L2, which takes
-// some 6 TB/s of them (measured alone, rows of 512 bytes over 16 to 64 MB: 6.0
-// as vector reductions of whole sectors, 3.1 of half sectors, 5.4 and 2.8 as
-// bulk reductions in pieces of 256 and 128 bytes), where rows that are read
-// come at 14.
+// some 6.4 TB/s of them (measured alone, rows of 512 bytes over 32 MB: 6.4 with 8
+// or 32 lanes to a line, 3.8 with lanes to sectors of several lines, 3.1 with a
+// row a lane; as bulk reductions 5.4 in pieces of 256 bytes and 2.8 in 128),
+// where rows that are read come at 14.
 #include "sel_common.cuh"
 
 namespace skl {
@@ -38,40 +37,50 @@ struct SelBwdLayout {
   static constexpr int kDsWarps = 8, kEpiWarp = 8, kEpiWGs = 2, kGatherWarp = 16, kGatherWarps = 4;
   static constexpr int kSWarp = 20, kGradWarp = 21, kLoadWarp = 22, kWalkWarp = 23;
   static constexpr int kThreads = 32 * (kWalkWarp + 1);
-  static constexpr int kMaxRing = 6;   // slots of gathered tiles
-  // Tiles whose rows' parameters are kept.  Those of tile n are replaced with the copies of tile n + kRows, which wait
-  // for the dK of tile n + kRows - 1 - slots / 2 at least; that of n + 3 has waited for dQ of n + 2, and this one for
-  // the warps of dQ to have read tile n.
-  static constexpr int kRows = 7;
+  static constexpr int kMaxRing = 6;  // slots of gathered tiles
+  // Tiles whose rows' parameters and numbers are kept.  Those of tile n are replaced with the copies of tile n + kParams
+  // (kNumbers), which wait for the dK of tile n + that - 1 - slots / 2 at least: behind the dS of n, which reads the
+  // parameters, and behind the dQ of n + 1, which waits until the warps of dQ have read the numbers of n.
+  static constexpr int kParams = 4, kNumbers = 8;
+  static_assert(kParams - 1 - kMaxRing / 2 >= 0 && kNumbers - 1 - kMaxRing / 2 >= 2, "see above");
   enum {
-    kKFull = 0, kKEmpty = 2, kReady = 4, kQFull = 6, kQEmpty = kQFull + kMaxRing, kSFull = kQEmpty + kMaxRing, kSFree,
-    kDsFull, kDsEmpty, kDqFull, kDqEmpty = kDqFull + 2, kDkFull = kDqEmpty + 2, kDkEmpty, kDone, kTold, kNumBars = (kTold + 2 * kShares + 1) / 2 * 2  // (16-byte words behind them)
+    kKFull = 0, kKEmpty = 2, kReady = 4, kQFull = 6, kQEmpty = kQFull + kMaxRing, kSFull = kQEmpty + kMaxRing,
+    kSFree = kSFull + 2, kDsFull = kSFree + 2, kDsEmpty, kDqFull, kDqEmpty, kDkFull, kDkEmpty, kDone, kTold,
+    kNumBars = (kTold + 2 * kShares + 1) / 2 * 2  // (16-byte words behind them)
   };
   static constexpr uint32_t kSlot = kTile * 2u * (D1 > D2 ? D1 : D2);
-  static constexpr uint32_t kParams = kRows * kTile * 20u;
-  // operands, dS (64-key blocks of 128 rows), parameters, barriers
+  static constexpr uint32_t kParamBytes = kParams * kTile * 16u, kNumberBytes = kNumbers * kTile * 5u;
+  static constexpr uint32_t kPitch = 144, kStage = 4 * kEpiWGs * 16 * kPitch;  // staged rows of 32 values, padded
+  // operands, dS (64-key blocks of 128 rows), staged rows, parameters, numbers, barriers
   static uint32_t bytes(int slots, int k_bufs, int bs) {
-    return 1024u + slots * kSlot + uint32_t(k_bufs * bs) * (D1 + D2) * 2u + ds_bytes(bs) + kParams + kNumBars * 8 + kShares * sizeof(SelShare) + 16;
+    return 1024u + slots * kSlot + uint32_t(k_bufs * bs) * (D1 + D2) * 2u + ds_bytes(bs) + kStage + kParamBytes +
+           kNumberBytes + kNumBars * 8 + kShares * sizeof(SelShare) + 16;
   }
   __host__ __device__ static uint32_t ds_bytes(int bs) { return bs == 128 ? 32768u : 16384u; }
   static constexpr uint32_t kMost = 232448;
-  static_assert(kRows - 1 - kMaxRing / 2 >= 3, "see kRows");
 };
 
-__device__ __forceinline__ void red_add2(float* p, float x, float y) {
-  asm volatile("red.global.add.v2.f32 [%0], {%1,%2};" ::"l"(p), "f"(x), "f"(y) : "memory");
+__device__ __forceinline__ void red_add4(float* p, float4 v) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1,%2,%3,%4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
-// 64 columns of 16 rows, and the wait for them: lane l holds, for every 8
+// 32 columns of 16 rows, and the wait for them: lane l holds, for every 8
 // columns e, v[4 e] and v[4 e + 1]: row l / 4, columns 8 e + 2 (l % 4) and the
 // next; v[4 e + 2], v[4 e + 3]: the same of row l / 4 + 8.
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t t, uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t t, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : SKL_R8(v, 0), SKL_R8(v, 8), SKL_R8(v, 16), SKL_R8(v, 24)
+      : SKL_R8(v, 0), SKL_R8(v, 8)
       : "r"(t)
       : "memory");
 }
@@ -102,7 +111,7 @@ __device__ __forceinline__ void ds_columns(const uint32_t (&x1)[16], const uint3
 constexpr int kRowThreads = 256;
 
 // What dS and dQ need of every row: na, nb, ws as in ds_chunk_row, and the
-// addend that rounds to its grid.  A row that saw nothing has na = -inf.
+// exponent of its grid.  A row that saw nothing has na = -inf.
 __global__ void __launch_bounds__(kRowThreads) sel_rows_kernel(const __grid_constant__ SelBwdArgs a, int mode) {
   const long long row = (long long)blockIdx.x * kRowThreads + threadIdx.x;
   if (row >= (long long)a.p.B * a.p.H * a.p.NQ) return;
@@ -115,7 +124,7 @@ __global__ void __launch_bounds__(kRowThreads) sel_rows_kernel(const __grid_cons
     par.x = -l1 * kLog2e;
     par.y = p2 ? -l2 * kLog2e : -(l1 - l2 + kl);
     par.z = sg * dkl;
-    par.w = 1.5f * exp2_int(23 - dq_fixed_exp(mode, sg, dkl, kl, kmax));
+    par.w = float(dq_fixed_exp(mode, sg, dkl, kl, kmax));
   }
   a.rows[row] = par;
 }
@@ -133,10 +142,12 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bs = a.p.bs;
   const uint32_t kK1 = uint32_t(bs) * D1 * 2, kK = uint32_t(bs) * (D1 + D2) * 2;
-  const uint32_t oDS = a.k_bufs * kK, oQ = oDS + L::ds_bytes(bs), oParam = oQ + a.slots * L::kSlot, oBar = oParam + L::kParams;
+  const uint32_t oDS = a.k_bufs * kK, oQ = oDS + L::ds_bytes(bs), oStage = oQ + a.slots * L::kSlot;
+  const uint32_t oParam = oStage + L::kStage, oNumber = oParam + L::kParamBytes, oBar = oNumber + L::kNumberBytes;
   auto bar = [&](int id) { return sb + oBar + 8u * id; };
-  float4* params = reinterpret_cast<float4*>(smem + oParam);                          // na, nb, ws, grid
-  int* row_of = reinterpret_cast<int*>(smem + oParam + L::kRows * kTile * 16);        // row of dq32, or -1
+  float4* params = reinterpret_cast<float4*>(smem + oParam);                   // na, nb, ws
+  int* row_of = reinterpret_cast<int*>(smem + oNumber);                        // row of dq32, or -1
+  int8_t* grid_of = reinterpret_cast<int8_t*>(row_of + L::kNumbers * kTile);   // the exponent of its grid
   SelShare* shares = reinterpret_cast<SelShare*>(smem + oBar + L::kNumBars * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shares + kShares);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -147,9 +158,10 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     for (int i = 0; i < L::kNumBars; ++i) {
       int count = 1;
       if (i >= L::kQFull && i < L::kQEmpty) count = 33 * L::kGatherWarps;
-      if (i == L::kReady || i == L::kReady + 1 || i == L::kSFree || i == L::kDsFull) count = L::kDsWarps;
-      if (i == L::kDqEmpty || i == L::kDqEmpty + 1) count = 4;
-      if (i == L::kDkEmpty) count = 4 * L::kEpiWGs;
+      if (i == L::kReady || i == L::kReady + 1 || i == L::kSFree || i == L::kSFree + 1 ||
+          i == L::kDsFull)
+        count = L::kDsWarps;
+      if (i == L::kDqEmpty || i == L::kDkEmpty) count = 4 * L::kEpiWGs;
       if (i >= L::kTold + kShares) count = L::kWalkWarp;  // the warps before it
       if (i == L::kDone) count = 2;
       mbar_init(bar(i), count);
@@ -169,8 +181,8 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int dq_bufs = bs == 128 ? 1 : 2;
-  const uint32_t t_s1 = tmem, t_s2 = tmem + bs, t_dk = tmem + (bs == 128 ? 256 : 128), t_dq = t_dk + 128;
+  const int s_bufs = bs == 128 ? 1 : 2;
+  const uint32_t t_s1 = tmem, t_s2 = tmem + bs, t_dk = tmem + 256, t_dq = tmem + 384;  // (S buffers 128 columns apart)
   const int per_tile = a.p.queries_per_tile, G = a.p.G;
   const bool ids = a.vis.ids_q != nullptr;
 
@@ -219,7 +231,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       }
       ent = entry_of(a.p, share, e0 + ql, place);
     };
-    int s = 0, m = 0, n = 0;  // slot, rounds of the ring, place of the tile's parameters
+    int s = 0, m = 0, n = 0;  // slot, rounds of the ring, tiles
     bool ok = true, more = ahead;
     look();
     step();
@@ -238,9 +250,10 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         ok = mbar_wait_warp(bar(L::kQEmpty + s), (m & 1) ^ 1, ctl);
         if (!ok) break;
         if (side == 0) {
-          params[n * kTile + r] = x;
-          row_of[n * kTile + r] = on ? of : -1;
-          if (++n == L::kRows) n = 0;
+          params[n % L::kParams * kTile + r] = on ? x : make_float4(-INFINITY, kP2 ? -INFINITY : 0.f, 0.f, 0.f);
+          row_of[n % L::kNumbers * kTile + r] = on ? of : -1;
+          grid_of[n % L::kNumbers * kTile + r] = int8_t(int(x.w));
+          ++n;
           gather_rows<DO, true>(sb + oQ + s * L::kSlot, first, on ? xo : 0ull, ro);
         } else {
           gather_rows<DG, true>(sb + oQ + s * L::kSlot, first, on ? xg : 0ull, rg);
@@ -297,17 +310,18 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       const uint32_t k1s = sb + kb * kK, k2s = k1s + kK1;
       ok = mbar_wait_warp(bar((ids ? L::kReady : L::kKFull) + kb), (kept / a.k_bufs) & 1, ctl);
       for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n) {
-        ok = mbar_wait_warp(bar(L::kSFree), (n & 1) ^ 1, ctl);
+        const int sbuf = n & (s_bufs - 1);
+        ok = mbar_wait_warp(bar(L::kSFree + sbuf), ((n / s_bufs) & 1) ^ 1, ctl);
         if (!ok) break;
         // the other side first: its slot is released as early as possible
-        product(std::integral_constant<int, DO>{}, kP2 ? t_s1 : t_s2, kP2 ? k1s : k2s);
+        product(std::integral_constant<int, DO>{}, (kP2 ? t_s1 : t_s2) + 128 * sbuf, kP2 ? k1s : k2s);
         if (!ok) break;
         mma_commit(leader, bar(L::kQEmpty + s));
         if (++s == a.slots) s = 0, ++m;
-        product(std::integral_constant<int, DG>{}, kP2 ? t_s2 : t_s1, kP2 ? k2s : k1s);
+        product(std::integral_constant<int, DG>{}, (kP2 ? t_s2 : t_s1) + 128 * sbuf, kP2 ? k2s : k1s);
         if (!ok) break;
         if (++s == a.slots) s = 0, ++m;  // (released by dK)
-        mma_commit(leader, bar(L::kSFull));
+        mma_commit(leader, bar(L::kSFull + sbuf));
       }
     }
     mma_commit(leader, bar(L::kDone));
@@ -331,7 +345,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
            mbar_wait_warp(bar(L::kDkEmpty), (kept & 1) ^ 1, ctl);
       bool first = true;
       for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n) {
-        const int s = (2 * n + 1) % a.slots, qb = n & (dq_bufs - 1);
+        const int s = (2 * n + 1) % a.slots;
         ok = mbar_wait_warp(bar(L::kDsFull), n & 1, ctl);
         if (!ok) break;
         tc_fence_after();
@@ -341,16 +355,13 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
           mma_step(leader, t_dk, ds_m + kk * 128, dhi, qg + kk * 128, dhi, id_dk, !first || kk > 0);
         first = false;
         mma_commit(leader, bar(L::kQEmpty + s));
-        // the accumulator's last tile has been read (barriers go by the warpgroups of dQ, which see every phase of theirs)
-        const int before = n - dq_bufs;
-        ok = before < 0 || mbar_wait_warp(bar(L::kDqEmpty + (before & 1)), (before >> 1) & 1, ctl);
+        ok = mbar_wait_warp(bar(L::kDqEmpty), (n & 1) ^ 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t t = t_dq + qb * 128;
         for (int kk = 0; kk < bs / 16; ++kk)
-          mma_step(leader, t, ds_k + (kk >> 2) * (kTile * 8) + (kk & 3) * 2, dhi, kg + kk * 128, dhi, id_dq, kk > 0);
+          mma_step(leader, t_dq, ds_k + (kk >> 2) * (kTile * 8) + (kk & 3) * 2, dhi, kg + kk * 128, dhi, id_dq, kk > 0);
         mma_commit(leader, bar(L::kDsEmpty));
-        mma_commit(leader, bar(L::kDqFull + (n & 1)));
+        mma_commit(leader, bar(L::kDqFull));
       }
       if (ok) {
         mma_commit(leader, bar(L::kDkFull));
@@ -392,11 +403,13 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       }
       const int row0 = (share.b * a.p.H + share.head0 + hl) * a.p.NQ;  // of query 0
       for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n) {
-        ok = mbar_wait_warp(bar(L::kSFull), n & 1, ctl);
+        const int sbuf = n & (s_bufs - 1);
+        const uint32_t ts = tmem + lane_off + 128 * sbuf;
+        ok = mbar_wait_warp(bar(L::kSFull + sbuf), (n / s_bufs) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        const float4 par = params[(n % L::kRows) * kTile + row];
-        const int of = row_of[(n % L::kRows) * kTile + row];
+        const float4 par = params[(n % L::kParams) * kTile + row];
+        const int of = row_of[(n % L::kNumbers) * kTile + row];
         const int i = of < 0 ? 0 : of - row0;
         const uint64_t NA = f2(par.x, par.x), NB = f2(par.y, par.y), WW = f2(par.z, par.z);
         const int last = a.p.causal ? min(max(i + off + 1, prefix), a.p.NK) : a.p.NK;
@@ -406,11 +419,11 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
 #pragma unroll 1
         for (int c = col0; c < col1; c += 16) {
           uint32_t x1[16], x2[16], out[8];
-          tmem_ld2x16(t_s1 + lane_off + c, t_s2 + lane_off + c, x1, x2);
+          tmem_ld2x16(ts + c, ts + bs + c, x1, x2);
           if (c + 16 >= col1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::kSFree));
+            if (lane == 0) mbar_arrive(bar(L::kSFree + sbuf));
           }
           ds_columns<MODE>(x1, x2, C1, C2, S1, NR, NA, NB, WW, out);
           if (!whole) {
@@ -433,7 +446,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         if (col0 == col1) {  // blocks of 32: nothing for this warpgroup, which may not run ahead of the other
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::kSFree));
+          if (lane == 0) mbar_arrive(bar(L::kSFree + sbuf));
           ok = mbar_wait_warp(bar(L::kDsEmpty), (n & 1) ^ 1, ctl);
           if (!ok) break;
         }
@@ -446,51 +459,61 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     // ---------------------------------------------------------------- dQ, and dK after a list
     const int wg = (warp - L::kEpiWarp) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lane_off = uint32_t(w4 * 32) << 16;
-    int n = 0, place = 0, kept = 0;
+    const uint32_t stage = sb + oStage + (warp - L::kEpiWarp) * (16 * L::kPitch);
+    // staged by row lane / 4 (and + 8), read by row lane / 8 + 4 x
+    const uint32_t to = stage + (lane >> 2) * L::kPitch + (lane & 3) * 8, from = stage + (lane >> 3) * L::kPitch + (lane & 7) * 16;
+    int n = 0, kept = 0;
     bool ok = true;
     for (SelReader share(shares, told); ok && share.next(ctl); ++kept) {
-      for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n, place = place + 1 == L::kRows ? 0 : place + 1) {
-        if ((n & 1) != wg) continue;
-        const int qb = n & (dq_bufs - 1);
-        ok = mbar_wait_warp(bar(L::kDqFull + wg), (n >> 1) & 1, ctl);
+      for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n) {
+        ok = mbar_wait_warp(bar(L::kDqFull), n & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        // the lane's four rows: w4 * 32 + lane / 4 + 8 x
-        float me[4];
-        float* dst[4];
-        bool on[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int at = place * kTile + w4 * 32 + (lane >> 2) + 8 * x;
-          const int of = row_of[at];
-          me[x] = params[at].w;
-          on[x] = of >= 0;
-          dst[x] = a.dq32 + size_t(on[x] ? of : 0) * a.pitch + 2 * (lane & 3);
-        }
+        const int at = (n % L::kNumbers) * kTile + w4 * 32;
+        const int* rows = row_of + at + (lane >> 3);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-          for (int c = 0; c < DG; c += 64) {
-            uint32_t v[32];
-            tmem_ld_16x64(t_dq + qb * 128 + lane_off + (uint32_t(16 * half) << 16) + c, v);
-            if (half == 1 && c + 64 == DG) {
+          float me[2];
+          float* dst[4];
+          bool on[4];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) me[x] = 1.5f * exp2_int(23 - grid_of[at + 16 * half + (lane >> 2) + 8 * x]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int of = rows[16 * half + 4 * x];
+            on[x] = of >= 0;
+            dst[x] = a.dq32 + size_t(on[x] ? of : 0) * a.pitch + 4 * (lane & 7);
+          }
+#pragma unroll
+          for (int part = 0; part < DG / 64; ++part) {
+            const int c = (wg * (DG / 64) + part) * 32;
+            uint32_t v[16];
+            tmem_ld_16x32(t_dq + lane_off + (uint32_t(16 * half) << 16) + c, v);
+            if (half == 1 && part == DG / 64 - 1) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(bar(L::kDqEmpty + wg));
+              if (lane == 0) mbar_arrive(bar(L::kDqEmpty));
             }
             // on the row's grid of 2^-e: (x + 1.5 2^(23 - e)) - 1.5 2^(23 - e)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint64_t ME = f2(me[2 * half + x], me[2 * half + x]);
-              float* p = dst[2 * half + x] + c;
+              const uint64_t ME = f2(me[x], me[x]);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
+              for (int e = 0; e < 4; ++e) {
                 float q0, q1;
                 f2_split(f2_sub(f2_add(f2(__uint_as_float(v[4 * e + 2 * x]), __uint_as_float(v[4 * e + 2 * x + 1])), ME), ME),
                          q0, q1);
-                if (on[2 * half + x] && c + 8 * e < a.dg) red_add2(p + 8 * e, q0, q1);
+                st_shared_v2(to + 8 * x * L::kPitch + e * 32, q0, q1);
               }
             }
+            __syncwarp();
+            const bool within = c + 4 * (lane & 7) < a.dg;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float4 q = ld_shared_v4(from + 4 * x * L::kPitch);
+              if (on[x] && within) red_add4(dst[x] + c, q);
+            }
+            __syncwarp();
           }
         }
       }
