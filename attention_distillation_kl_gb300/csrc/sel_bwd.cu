@@ -12,8 +12,8 @@
 // bitwise repeatable.  24 warps:
 //   warps 0-7   dS (thread = row; a warpgroup takes half of the columns)
 //   warps 8-15  dQ (a warpgroup takes half of the columns): TMEM -> registers ->
-//               shared memory, 16 rows x 32 values at a time, so that 8 lanes
-//               reduce a whole line of 128 bytes; after a list, dK
+//               shared memory, 8 rows x 32 values at a time, so that 8 lanes
+//               reduce a whole line of 128 bytes; after a list, dK alike
 //   warps 16-19 gather 32 rows each of both sides, and the rows' parameters
 //               (sel_rows_kernel)
 //   warp 20     S1, S2      warp 21     dK, dQ      warp 22     K by TMA
@@ -38,23 +38,24 @@ struct SelBwdLayout {
   static constexpr int kSWarp = 20, kGradWarp = 21, kLoadWarp = 22, kWalkWarp = 23;
   static constexpr int kThreads = 32 * (kWalkWarp + 1);
   static constexpr int kMaxRing = 6;  // slots of gathered tiles
-  // Tiles whose rows' parameters and numbers are kept.  Those of tile n are replaced with the copies of tile n + kParams
-  // (kNumbers), which wait for the dK of tile n + that - 1 - slots / 2 at least: behind the dS of n, which reads the
-  // parameters, and behind the dQ of n + 1, which waits until the warps of dQ have read the numbers of n.
-  static constexpr int kParams = 4, kNumbers = 8;
-  static_assert(kParams - 1 - kMaxRing / 2 >= 0 && kNumbers - 1 - kMaxRing / 2 >= 2, "see above");
+  // Tiles whose rows' parameters and numbers are kept.  Those of tile n are replaced with the copies of tile n + that,
+  // which wait for the dK of tile n + that - 1 - slots / 2 at least: behind the dS of n, which reads the parameters, and
+  // of n + 2, whose dS was stored behind the dQ of n + 1, which waits until the warps of dQ have read the numbers of n.
+  __host__ __device__ static int params(int slots) { return 1 + slots / 2; }
+  __host__ __device__ static int numbers(int slots) { return 3 + slots / 2; }
   enum {
     kKFull = 0, kKEmpty = 2, kReady = 4, kQFull = 6, kQEmpty = kQFull + kMaxRing, kSFull = kQEmpty + kMaxRing,
     kSFree = kSFull + 2, kDsFull = kSFree + 2, kDsEmpty, kDqFull, kDqEmpty, kDkFull, kDkEmpty, kDone, kTold,
     kNumBars = (kTold + 2 * kShares + 1) / 2 * 2  // (16-byte words behind them)
   };
   static constexpr uint32_t kSlot = kTile * 2u * (D1 > D2 ? D1 : D2);
-  static constexpr uint32_t kParamBytes = kParams * kTile * 16u, kNumberBytes = kNumbers * kTile * 5u;
-  static constexpr uint32_t kPitch = 144, kStage = 4 * kEpiWGs * 16 * kPitch;  // staged rows of 32 values, padded
+  __host__ __device__ static uint32_t param_bytes(int slots) { return uint32_t(params(slots)) * kTile * 12u; }
+  __host__ __device__ static uint32_t number_bytes(int slots) { return uint32_t(numbers(slots)) * kTile * 5u; }
+  static constexpr uint32_t kPitch = 144, kStage = 4 * kEpiWGs * 8 * kPitch;  // staged rows of 32 values, padded
   // operands, dS (64-key blocks of 128 rows), staged rows, parameters, numbers, barriers
   static uint32_t bytes(int slots, int k_bufs, int bs) {
-    return 1024u + slots * kSlot + uint32_t(k_bufs * bs) * (D1 + D2) * 2u + ds_bytes(bs) + kStage + kParamBytes +
-           kNumberBytes + kNumBars * 8 + kShares * sizeof(SelShare) + 16;
+    return 1024u + slots * kSlot + uint32_t(k_bufs * bs) * (D1 + D2) * 2u + ds_bytes(bs) + kStage + param_bytes(slots) +
+           number_bytes(slots) + kNumBars * 8 + kShares * sizeof(SelShare) + 16;
   }
   __host__ __device__ static uint32_t ds_bytes(int bs) { return bs == 128 ? 32768u : 16384u; }
   static constexpr uint32_t kMost = 232448;
@@ -143,11 +144,13 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
   const int bs = a.p.bs;
   const uint32_t kK1 = uint32_t(bs) * D1 * 2, kK = uint32_t(bs) * (D1 + D2) * 2;
   const uint32_t oDS = a.k_bufs * kK, oQ = oDS + L::ds_bytes(bs), oStage = oQ + a.slots * L::kSlot;
-  const uint32_t oParam = oStage + L::kStage, oNumber = oParam + L::kParamBytes, oBar = oNumber + L::kNumberBytes;
+  const uint32_t oParam = oStage + L::kStage, oNumber = oParam + L::param_bytes(a.slots),
+                 oBar = oNumber + L::number_bytes(a.slots);
+  const int n_params = L::params(a.slots), n_numbers = L::numbers(a.slots);
   auto bar = [&](int id) { return sb + oBar + 8u * id; };
-  float4* params = reinterpret_cast<float4*>(smem + oParam);                   // na, nb, ws
+  float* params = reinterpret_cast<float*>(smem + oParam);                     // na, nb, ws: [tile][3][128]
   int* row_of = reinterpret_cast<int*>(smem + oNumber);                        // row of dq32, or -1
-  int8_t* grid_of = reinterpret_cast<int8_t*>(row_of + L::kNumbers * kTile);   // the exponent of its grid
+  int8_t* grid_of = reinterpret_cast<int8_t*>(row_of + n_numbers * kTile);   // the exponent of its grid
   SelShare* shares = reinterpret_cast<SelShare*>(smem + oBar + L::kNumBars * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shares + kShares);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       }
       ent = entry_of(a.p, share, e0 + ql, place);
     };
-    int s = 0, m = 0, n = 0;  // slot, rounds of the ring, tiles
+    int s = 0, m = 0, at_p = 0, at_n = 0;  // slot, rounds of the ring, places of parameters and numbers
     bool ok = true, more = ahead;
     look();
     step();
@@ -250,10 +253,14 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         ok = mbar_wait_warp(bar(L::kQEmpty + s), (m & 1) ^ 1, ctl);
         if (!ok) break;
         if (side == 0) {
-          params[n % L::kParams * kTile + r] = on ? x : make_float4(-INFINITY, kP2 ? -INFINITY : 0.f, 0.f, 0.f);
-          row_of[n % L::kNumbers * kTile + r] = on ? of : -1;
-          grid_of[n % L::kNumbers * kTile + r] = int8_t(int(x.w));
-          ++n;
+          float* to = params + at_p * (3 * kTile) + r;
+          to[0] = on ? x.x : -INFINITY;
+          to[kTile] = on ? x.y : (kP2 ? -INFINITY : 0.f);
+          to[2 * kTile] = on ? x.z : 0.f;
+          row_of[at_n * kTile + r] = on ? of : -1;
+          grid_of[at_n * kTile + r] = int8_t(int(x.w));
+          if (++at_p == n_params) at_p = 0;
+          if (++at_n == n_numbers) at_n = 0;
           gather_rows<DO, true>(sb + oQ + s * L::kSlot, first, on ? xo : 0ull, ro);
         } else {
           gather_rows<DG, true>(sb + oQ + s * L::kSlot, first, on ? xg : 0ull, rg);
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     const int half = (bs + 32) / 64 * 32;                        // columns of warpgroup 0
     const int col0 = wg == 0 ? 0 : half, col1 = wg == 0 ? half : bs;
     const int nqt = (a.p.NQ + kTile - 1) / kTile, nkt = (a.p.NK + kTile - 1) / kTile, off = a.p.NK - a.p.NQ;
-    int n = 0, kept = 0;
+    int n = 0, kept = 0, at_p = 0, at_n = 0;
     bool ok = true;
     for (SelReader share(shares, told); ok && share.next(ctl); ++kept) {
       const int k0 = share.block * bs;
@@ -408,10 +415,13 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
         ok = mbar_wait_warp(bar(L::kSFull + sbuf), (n / s_bufs) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        const float4 par = params[(n % L::kParams) * kTile + row];
-        const int of = row_of[(n % L::kNumbers) * kTile + row];
+        const float* par = params + at_p * (3 * kTile) + row;
+        if (++at_p == n_params) at_p = 0;
+        const int of = row_of[at_n * kTile + row];
+        if (++at_n == n_numbers) at_n = 0;
         const int i = of < 0 ? 0 : of - row0;
-        const uint64_t NA = f2(par.x, par.x), NB = f2(par.y, par.y), WW = f2(par.z, par.z);
+        const float na = par[0], nb = par[kTile], ws = par[2 * kTile];
+        const uint64_t NA = f2(na, na), NB = f2(nb, nb), WW = f2(ws, ws);
         const int last = a.p.causal ? min(max(i + off + 1, prefix), a.p.NK) : a.p.NK;
         const bool whole = kids == nullptr && __all_sync(0xffffffffu, of < 0 || last >= k0 + bs);
         const int id = kids != nullptr ? a.vis.ids_q[size_t(share.b) * nqt * kTile + i] : 0;
@@ -457,20 +467,20 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- dQ, and dK after a list
-    const int wg = (warp - L::kEpiWarp) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
+    const int wg = (warp - L::kEpiWarp) >> 2, w4 = warp & 3;
     const uint32_t lane_off = uint32_t(w4 * 32) << 16;
-    const uint32_t stage = sb + oStage + (warp - L::kEpiWarp) * (16 * L::kPitch);
-    // staged by row lane / 4 (and + 8), read by row lane / 8 + 4 x
+    const uint32_t stage = sb + oStage + (warp - L::kEpiWarp) * (8 * L::kPitch);
+    // staged by row lane / 4, read by rows lane / 8 and + 4
     const uint32_t to = stage + (lane >> 2) * L::kPitch + (lane & 3) * 8, from = stage + (lane >> 3) * L::kPitch + (lane & 7) * 16;
-    int n = 0, kept = 0;
+    int n = 0, kept = 0, at_n = 0;
     bool ok = true;
     for (SelReader share(shares, told); ok && share.next(ctl); ++kept) {
       for (int e0 = 0; ok && e0 < share.count; e0 += per_tile, ++n) {
         ok = mbar_wait_warp(bar(L::kDqFull), n & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        const int at = (n % L::kNumbers) * kTile + w4 * 32;
-        const int* rows = row_of + at + (lane >> 3);
+        const int at = at_n * kTile + w4 * 32;
+        if (++at_n == n_numbers) at_n = 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float me[2];
@@ -480,7 +490,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
           for (int x = 0; x < 2; ++x) me[x] = 1.5f * exp2_int(23 - grid_of[at + 16 * half + (lane >> 2) + 8 * x]);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int of = rows[16 * half + 4 * x];
+            const int of = row_of[at + 16 * half + (lane >> 3) + 4 * x];
             on[x] = of >= 0;
             dst[x] = a.dq32 + size_t(on[x] ? of : 0) * a.pitch + 4 * (lane & 7);
           }
@@ -494,26 +504,26 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(L::kDqEmpty));
             }
-            // on the row's grid of 2^-e: (x + 1.5 2^(23 - e)) - 1.5 2^(23 - e)
+            const bool within = c + 4 * (lane & 7) < a.dg;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
+              // on the row's grid of 2^-e: (x + 1.5 2^(23 - e)) - 1.5 2^(23 - e)
               const uint64_t ME = f2(me[x], me[x]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 float q0, q1;
                 f2_split(f2_sub(f2_add(f2(__uint_as_float(v[4 * e + 2 * x]), __uint_as_float(v[4 * e + 2 * x + 1])), ME), ME),
                          q0, q1);
-                st_shared_v2(to + 8 * x * L::kPitch + e * 32, q0, q1);
+                st_shared_v2(to + e * 32, q0, q1);
               }
-            }
-            __syncwarp();
-            const bool within = c + 4 * (lane & 7) < a.dg;
+              __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float4 q = ld_shared_v4(from + 4 * x * L::kPitch);
-              if (on[x] && within) red_add4(dst[x] + c, q);
+              for (int y = 0; y < 2; ++y) {
+                const float4 q = ld_shared_v4(from + 4 * y * L::kPitch);
+                if (on[2 * x + y] && within) red_add4(dst[2 * x + y] + c, q);
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
         }
       }
@@ -523,18 +533,29 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (w4 * 32 < bs) {
-        float* dst = a.dk_part + (size_t(share.meeting) * bs + row) * a.dg;
+        float* dst = a.dk_part + (size_t(share.meeting) * bs + w4 * 32 + (lane >> 3)) * a.dg + 4 * (lane & 7);
 #pragma unroll 1
-        for (int c = wg * (DG / 2); c < (wg + 1) * (DG / 2); c += 32) {
-          uint32_t v[32];
-          tmem_ld32(t_dk + lane_off + c, v);
+        for (int half = 0; half < 2; ++half)
+#pragma unroll 1
+          for (int part = 0; part < DG / 64; ++part) {
+            const int c = (wg * (DG / 64) + part) * 32;
+            uint32_t v[16];
+            tmem_ld_16x32(t_dk + lane_off + (uint32_t(16 * half) << 16) + c, v);
+            const bool within = c + 4 * (lane & 7) < a.dg;
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            if (c + j < a.dg)
-              __stcs(reinterpret_cast<float4*>(dst + c + j),
-                     make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
-                                 __uint_as_float(v[j + 3])));
-        }
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                st_shared_v2(to + e * 32, __uint_as_float(v[4 * e + 2 * x]), __uint_as_float(v[4 * e + 2 * x + 1]));
+              __syncwarp();
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float4 q = ld_shared_v4(from + 4 * y * L::kPitch);
+                if (within) __stcs(reinterpret_cast<float4*>(dst + (16 * half + 8 * x + 4 * y) * a.dg + c), q);
+              }
+              __syncwarp();
+            }
+          }
       }
       tc_fence_before();
       __syncwarp();
@@ -566,16 +587,17 @@ __global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constan
   for (int u = hk * units; u < (hk + 1) * units; ++u) {
     const int s = b * p.HS + u / per, sub = u % per, i = __ldg(p.place + size_t(s) * p.blocks + j);
     if (i < 0) continue;
-    // the list's tiles among its group's, and the CTAs whose parts hold them (see find_start)
+    // the list's place among its group's costs, and the CTAs whose parts hold its tiles (see find_cut)
     const int g = s / p.group;
     long long total = 0, at = 0;
     for (int k = g * p.group; k < min(p.B * p.HS, (g + 1) * p.group); ++k) {
       if (k == s) at = total;
-      total += (long long)__ldg(p.sizes + k).y * per;
+      const int2 size = __ldg(p.sizes + k);
+      total += (long long)(size.x + size.y) * per;
     }
     const int4 l = __ldg(p.lists + size_t(s) * p.cap + i);
     const int n = (l.z + p.queries_per_tile - 1) / p.queries_per_tile;
-    at += (long long)l.w * per + (long long)sub * n;
+    at += (long long)(l.w + i) * per + (long long)sub * (n + 1) + 1;  // of its first tile
     const int c0 = int(((at + 1) * p.ctas - 1) / total), c1 = int(((at + n) * p.ctas - 1) / total);
     const float* part = a.dk_part + ((((size_t(s) * p.cap + i) * per + sub + size_t(g) * p.ctas + c0) * bs) + key) * a.dg + c;
 #pragma unroll 4
@@ -597,10 +619,13 @@ int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, cudaStream_t st) 
   using L = SelBwdLayout<D1, D2>;
   SelBwdArgs a = args;
   const int bs = a.p.bs;
-  // Two tiles' slots, then a second K, then more slots.
+  // Two tiles' slots; then a fifth one first where lists are long (their change costs a load of K), else a second K.
   auto fits = [&](int slots, int bufs) { return L::bytes(slots, bufs, bs) <= L::kMost; };
   a.k_bufs = 1;
   a.slots = fits(4, 1) ? 4 : 3;
+  const double listed = double(a.p.NQ) * a.p.T / a.p.queries_per_tile;  // tiles of a selection head's lists
+  const bool longer = listed >= 16.0 * (a.p.cap + double(a.p.ctas) * a.p.HS / a.p.HU);
+  if (longer && fits(5, 1)) a.slots = 5;
   if (fits(a.slots, 2)) a.k_bufs = 2;
   while (a.slots < L::kMaxRing && fits(a.slots + 1, a.k_bufs)) ++a.slots;
   if (!fits(a.slots, a.k_bufs)) return cudaErrorInvalidValue;

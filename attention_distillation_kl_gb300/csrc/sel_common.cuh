@@ -10,8 +10,8 @@
 // small; an output of d values a row would not allow this.
 //
 // The plan (sel_plan.cu) makes these lists, in query order.  All lists' tiles in
-// a row are cut into as many equal parts as there are CTAs, whatever block a cut
-// falls into; several selection heads at a time, as many as L2 holds the rows
+// a row are cut into as many parts of equal cost as there are CTAs, whatever
+// block a cut falls into; several selection heads at a time, as many as L2 holds the rows
 // of.  Nothing in the plan depends on the order in which blocks of a launch run.
 #pragma once
 

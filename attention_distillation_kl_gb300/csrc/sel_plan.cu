@@ -91,29 +91,47 @@ __device__ __forceinline__ void walk(const SelPlan& p, int sel, int q0, int q1, 
   }
 }
 
-// Where CTA c's part of a group's tiles starts, and how long it is: tiles
-// [c total / ctas, (c + 1) total / ctas) of the group's.
+// Where a group's tiles are cut.  What a list takes counts as a tile more than
+// it has (its K, its start in the pipeline, its dK): CTA c begins at the tile of
+// cost c total / ctas.
+struct SelCut {
+  int s, i, sub, t;  // t: the list's tile
+  long long tile;    // among the group's
+};
+__device__ __forceinline__ SelCut find_cut(const SelPlan& p, int s0, long long at) {
+  const int per = p.HU / p.HS;
+  SelCut k{s0, 0, 0, 0, 0};
+  for (; at >= (long long)(p.sizes[k.s].x + p.sizes[k.s].y) * per; ++k.s) {
+    at -= (long long)(p.sizes[k.s].x + p.sizes[k.s].y) * per;
+    k.tile += (long long)p.sizes[k.s].y * per;
+  }
+  const int4* lists = p.lists + size_t(k.s) * p.cap;
+  int hi = p.sizes[k.s].x - 1;  // the last list that starts at or before it
+  while (k.i < hi) {
+    const int mid = (k.i + hi + 1) / 2;
+    if ((long long)(lists[mid].w + mid) * per <= at) k.i = mid;
+    else hi = mid - 1;
+  }
+  const int4 l = lists[k.i];
+  const int in = int(at - (long long)(l.w + k.i) * per), n = (l.z + p.queries_per_tile - 1) / p.queries_per_tile;
+  k.sub = in / (n + 1);
+  k.t = max(in % (n + 1) - 1, 0);
+  k.tile += (long long)l.w * per + (long long)k.sub * n + k.t;
+  return k;
+}
 __device__ __forceinline__ void find_start(const SelPlan& p, int u) {
   const int g = u / p.ctas, c = u - g * p.ctas, per = p.HU / p.HS;
   const int s0 = g * p.group, s1 = min(p.B * p.HS, s0 + p.group);
-  long long total = 0;
-  for (int s = s0; s < s1; ++s) total += (long long)p.sizes[s].y * per;
-  long long at = c * total / p.ctas;
-  const int len = int((c + 1) * total / p.ctas - at);
-  int4 out{0, 0, 0, len};
-  if (len > 0) {
-    int s = s0;
-    for (; at >= (long long)p.sizes[s].y * per; ++s) at -= (long long)p.sizes[s].y * per;
-    const int4* lists = p.lists + size_t(s) * p.cap;
-    int lo = 0, hi = p.sizes[s].x - 1;  // the last list that starts at or before it
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if ((long long)lists[mid].w * per <= at) lo = mid;
-      else hi = mid - 1;
-    }
-    const int4 l = lists[lo];
-    const int in = int(at - (long long)l.w * per), n = (l.z + p.queries_per_tile - 1) / p.queries_per_tile;
-    out = make_int4(s * per + in / n, lo, in % n, len);
+  long long total = 0, tiles = 0;
+  for (int s = s0; s < s1; ++s) {
+    total += (long long)(p.sizes[s].x + p.sizes[s].y) * per;
+    tiles += (long long)p.sizes[s].y * per;
+  }
+  int4 out{0, 0, 0, 0};
+  if (total > 0) {
+    const SelCut k = find_cut(p, s0, c * total / p.ctas);
+    const long long end = c + 1 == p.ctas ? tiles : find_cut(p, s0, (c + 1) * total / p.ctas).tile;
+    out = make_int4(k.s * per + k.sub, k.i, k.t, int(end - k.tile));
   }
   p.starts[u] = out;
 }
