@@ -47,6 +47,7 @@ SelRows rows_of(const streamkl_view& v, int B, int heads, int n, int d) {
 struct Geometry {
   SelPlan p{};
   int u1 = 1, u2 = 1;
+  bool one_kernel = false;  // makes the plan
 };
 
 // Heads that share keys on both sides and a selection form a unit, whose rows
@@ -75,18 +76,24 @@ Geometry geometry(const streamkl_side& p1, const streamkl_side& p2, const stream
   p.doc_q = vis.doc_q;
   p.selected = sel.selected;
   p.words = (p.T + 31) / 32;
-  // chunks of a few steps of a warp at least, and at most 128
+  // Up to 512 queries x slots a warp, one kernel (a CTA's 32 warps for a selection head); else chunks of a few steps of a
+  // warp at least, and at most 256 (their counts are read twice).  At 16384 queries x 16 slots x 8 selection heads a walk
+  // and the scan took 24 and 12 us with 128 chunks, 17 and 22 with 512.
   int span = 1;
   while (span < p.T && span < 32) span *= 2;
-  p.chunk = std::max(4 * (32 / span), (NQ + 127) / 128);
+  const int step = 32 / span, warps = std::min(32, kPlanShared / (4 * p.blocks));
+  const int few = (NQ + warps - 1) / warps;
+  g.one_kernel = p.words == 1 && (long long)few * span <= 512;
+  p.chunk = g.one_kernel ? few : std::max(4 * step, (NQ + 255) / 256);
   p.chunks = (NQ + p.chunk - 1) / p.chunk;
   return g;
 }
 
 // row_bytes: what a query head's rows hold in L2 while their lists run.
-void take_plan(Carver& c, SelPlan& p, double row_bytes, int sms, bool places) {
+void take_plan(Carver& c, Geometry& g, double row_bytes, int sms, bool places) {
+  SelPlan& p = g.p;
   const size_t heads = size_t(p.B) * p.HS, listed = size_t(p.NQ) * p.T;
-  p.counts = c.take<unsigned>(heads * p.chunks * p.blocks);
+  if (!g.one_kernel) p.counts = c.take<unsigned>(heads * p.chunks * p.blocks);
   p.entries = c.take<unsigned>(heads * listed);
   p.slots = c.take<unsigned>(heads * p.NQ * p.words);
   p.cap = int(std::min(listed, size_t(p.blocks)));
@@ -99,7 +106,6 @@ void take_plan(Carver& c, SelPlan& p, double row_bytes, int sms, bool places) {
   p.groups = int((heads + p.group - 1) / p.group);
   const size_t most = heads * (p.HU / p.HS) * (listed / p.queries_per_tile + p.cap);  // tiles
   p.ctas = int(std::min(size_t(std::max(sms, 1)), most));
-  p.starts = c.take<int4>(size_t(p.groups) * p.ctas);
 }
 
 struct FwdPlan {
@@ -117,7 +123,7 @@ FwdPlan fwd_plan(const streamkl_side& p1, const streamkl_side& p2, const streamk
   const streamkl_side* const p[2] = {&p1, &p2};
   take_prep(c, f.prep, p, vis, B, H, NQ, NK, -1);
   f.g = geometry(p1, p2, vis, sel, B, H, NQ, NK);
-  take_plan(c, f.g.p, 2.0 * (p1.d + p2.d), sms, false);
+  take_plan(c, f.g, 2.0 * (p1.d + p2.d), sms, false);
   const size_t pairs = size_t(B) * H * NQ * sel.count;
   f.rec = c.take<float4>(pairs);
   f.acc = c.take<float>(pairs);
@@ -150,7 +156,7 @@ BwdPlan bwd_plan(const streamkl_side& p1, const streamkl_side& p2, const streamk
   f.prep.zero_words = c.used / 16;
   take_prep(c, f.prep, p, vis, B, H, NQ, NK, -1);
   f.g = geometry(p1, p2, vis, sel, B, H, NQ, NK);
-  take_plan(c, f.g.p, 2.0 * (p1.d + p2.d) + 4.0 * f.pitch, sms, true);
+  take_plan(c, f.g, 2.0 * (p1.d + p2.d) + 4.0 * f.pitch, sms, true);
   f.rows = c.take<float4>(size_t(B) * H * NQ);
   // (SelWalk::meeting stays below this)
   const size_t meetings = size_t(B) * sel.heads * f.g.p.cap * (f.g.p.HU / f.g.p.HS) + size_t(f.g.p.groups) * f.g.p.ctas;

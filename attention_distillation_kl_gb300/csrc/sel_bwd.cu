@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
       for (int j = kept > a.k_bufs ? kept - a.k_bufs : 0; j < kept; ++j)
         mbar_drain(bar(L::kKFull + j % a.k_bufs), (j / a.k_bufs) & 1, 200000000ull);
   } else if (warp == L::kWalkWarp) {
-    if (lane == 0) tell_shares(a.p, shares, told, ctl);
+    tell_shares(a.p, shares, told, ctl);
   } else if (warp == L::kSWarp) {
     // ---------------------------------------------------------------- S issuer
     const uint32_t leader = elect_one();
@@ -576,40 +576,54 @@ constexpr int kDkThreads = 256;
 // dK of one key head and block: the shares of its lists (a unit each), of the
 // CTAs that met them, in order, rounded to bf16 once.  Four values a thread.
 __global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constant__ SelBwdArgs a) {
+  constexpr int kUnits = 32;
+  __shared__ long long first_of[kUnits];  // a unit's first share
+  __shared__ int shares_of[kUnits];
   const SelPlan& p = a.p;
   const int j = blockIdx.x, hk = blockIdx.y % a.HK, b = blockIdx.y / a.HK;
   const int units = p.HU / a.HK, per = p.HU / p.HS;
-  const int bs = p.bs, quads = a.dg / 4;
+  const int bs = p.bs, quads = a.dg / 4, rows = min(bs, p.NK - j * bs);
   const int x = blockIdx.z * kDkThreads + threadIdx.x;
   const int key = x / quads, c = (x - key * quads) * 4;
-  if (key >= min(bs, p.NK - j * bs)) return;
   float4 sum{0.f, 0.f, 0.f, 0.f};
-  for (int u = hk * units; u < (hk + 1) * units; ++u) {
-    const int s = b * p.HS + u / per, sub = u % per, i = __ldg(p.place + size_t(s) * p.blocks + j);
-    if (i < 0) continue;
-    // the list's place among its group's costs, and the CTAs whose parts hold its tiles (see find_cut)
-    const int g = s / p.group;
-    long long total = 0, at = 0;
-    for (int k = g * p.group; k < min(p.B * p.HS, (g + 1) * p.group); ++k) {
-      if (k == s) at = total;
-      const int2 size = __ldg(p.sizes + k);
-      total += (long long)(size.x + size.y) * per;
+  for (int u0 = 0; u0 < units; u0 += kUnits) {
+    // a warp finds what a unit's list left: its place among its group's costs, and the CTAs whose parts hold its tiles
+    __syncthreads();
+    for (int u = u0 + (threadIdx.x >> 5); u < min(units, u0 + kUnits); u += kDkThreads / 32) {
+      const int unit = hk * units + u, s = b * p.HS + unit / per, sub = unit % per;
+      const int i = __ldg(p.place + size_t(s) * p.blocks + j);
+      long long first = 0;
+      int n = 0;
+      if (i >= 0) {
+        const int g = s / p.group;
+        long long total;
+        const int4 l = __ldg(p.lists + size_t(s) * p.cap + i);
+        const int tiles = (l.z + p.queries_per_tile - 1) / p.queries_per_tile;
+        const long long at = group_cost(p, g, s, total) + (long long)(l.w + i) * per + (long long)sub * (tiles + 1) + 1;
+        const long long parts = sel_parts(p, total), c0 = ((at + 1) * parts - 1) / total;
+        n = int(((at + tiles) * parts - 1) / total - c0) + 1;
+        first = ((long long)s * p.cap + i) * per + sub + (long long)g * p.ctas + c0;
+      }
+      if ((threadIdx.x & 31) == 0) {
+        first_of[u - u0] = first;
+        shares_of[u - u0] = n;
+      }
     }
-    const int4 l = __ldg(p.lists + size_t(s) * p.cap + i);
-    const int n = (l.z + p.queries_per_tile - 1) / p.queries_per_tile;
-    at += (long long)(l.w + i) * per + (long long)sub * (n + 1) + 1;  // of its first tile
-    const int c0 = int(((at + 1) * p.ctas - 1) / total), c1 = int(((at + n) * p.ctas - 1) / total);
-    const float* part = a.dk_part + ((((size_t(s) * p.cap + i) * per + sub + size_t(g) * p.ctas + c0) * bs) + key) * a.dg + c;
+    __syncthreads();
+    if (key >= rows) continue;
+    for (int u = 0; u < min(units - u0, kUnits); ++u) {
+      const float* part = a.dk_part + (size_t(first_of[u]) * bs + key) * a.dg + c;
 #pragma unroll 4
-    for (int k = c0; k <= c1; ++k, part += size_t(bs) * a.dg) {
-      if (total < p.ctas && k * total / p.ctas == (k + 1) * total / p.ctas) continue;  // a part without a tile
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(part));
-      sum.x += v.x;
-      sum.y += v.y;
-      sum.z += v.z;
-      sum.w += v.w;
+      for (int k = 0; k < shares_of[u]; ++k, part += size_t(bs) * a.dg) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(part));
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+      }
     }
   }
+  if (key >= rows) return;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dk) + b * a.dk_sb + hk * a.dk_sh + (j * bs + key) * a.dk_sn + c;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
 }
@@ -619,13 +633,10 @@ int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, cudaStream_t st) 
   using L = SelBwdLayout<D1, D2>;
   SelBwdArgs a = args;
   const int bs = a.p.bs;
-  // Two tiles' slots; then a fifth one first where lists are long (their change costs a load of K), else a second K.
+  // Two tiles' slots, then a second K, then more slots.
   auto fits = [&](int slots, int bufs) { return L::bytes(slots, bufs, bs) <= L::kMost; };
   a.k_bufs = 1;
   a.slots = fits(4, 1) ? 4 : 3;
-  const double listed = double(a.p.NQ) * a.p.T / a.p.queries_per_tile;  // tiles of a selection head's lists
-  const bool longer = listed >= 16.0 * (a.p.cap + double(a.p.ctas) * a.p.HS / a.p.HU);
-  if (longer && fits(5, 1)) a.slots = 5;
   if (fits(a.slots, 2)) a.k_bufs = 2;
   while (a.slots < L::kMaxRing && fits(a.slots + 1, a.k_bufs)) ++a.slots;
   if (!fits(a.slots, a.k_bufs)) return cudaErrorInvalidValue;

@@ -25,6 +25,7 @@ namespace skl {
 constexpr int kMaxSlots = 128;    // blocks of one query
 constexpr int kMaxSelBlocks = 4096;
 constexpr int kSlotBits = 7;
+constexpr int kPlanShared = 160 * 1024;  // counters of a plan made by one kernel
 
 struct SelPlan {
   int B, H, NQ, NK, HS, T;
@@ -37,7 +38,7 @@ struct SelPlan {
   const int* doc_q;      // [B][NQ] or null
   const int* selected;   // [B][HS][NQ][T]
   int chunk, chunks;     // queries whose entries one warp counts, and their number
-  unsigned* counts;      // [B HS][chunks][blocks]: entries of a chunk; then where they start
+  unsigned* counts;      // [B HS][chunks][blocks]: entries of a chunk; then where they start (null: made by one kernel)
   unsigned* entries;     // [B HS][NQ T]: query << kSlotBits | slot
   unsigned* slots;       // [B HS][NQ][words]: the slots that count
   int words;             // (T + 31) / 32
@@ -49,77 +50,144 @@ struct SelPlan {
   int* place;            // [B HS][blocks]: a block's list, or -1 (null: not needed)
   int group, groups;     // selection heads at a time, and how many times
   int ctas;
-  int4* starts;          // [groups][ctas]: (selection head, unit), list, its tile, tiles of the part
 };
 
+// Where a group's tiles are cut.  What a list takes counts as a tile more than
+// it has (its K, its start in the pipeline, its dK): CTA c begins at the tile of
+// cost c total / ctas.
+__device__ __forceinline__ long long sel_cost(const SelPlan& p, int s) {  // of a selection head's lists, all units
+  const int2 n = __ldg(p.sizes + s);
+  return (long long)(n.x + n.y) * (p.HU / p.HS);
+}
+// Sum over a group's heads before `s`, and over all of them.  By a whole warp.
+__device__ __forceinline__ long long group_cost(const SelPlan& p, int g, int s, long long& total) {
+  const int s0 = g * p.group, s1 = min(p.B * p.HS, s0 + p.group), lane = threadIdx.x & 31;
+  long long all = 0, before = 0;
+  for (int k = s0 + lane; k < s1; k += 32) {
+    const long long x = sel_cost(p, k);
+    all += x;
+    if (k < s) before += x;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  total = all;
+  return before;
+}
+// (as many parts as there are CTAs, or less where that leaves nothing for one)
+__device__ __forceinline__ long long sel_parts(const SelPlan& p, long long total) { return min((long long)p.ctas, total); }
+struct SelCut {
+  int s, sub, i, t;  // selection head, unit of it, list, its tile
+};
+// The tile at cost `at` of a group (below its total).  By a whole warp: 32
+// places of the table at a time.
+__device__ __forceinline__ SelCut find_cut(const SelPlan& p, int g, long long at) {
+  const int lane = threadIdx.x & 31, per = p.HU / p.HS, s1 = min(p.B * p.HS, (g + 1) * p.group);
+  SelCut k{g * p.group, 0, 0, 0};
+  while (true) {  // the head: 32 at a time
+    const long long mine = k.s + lane < s1 ? sel_cost(p, k.s + lane) : 0;
+    long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, at < sum);
+    if (past != 0u) {
+      const int l = __ffs(past) - 1;
+      at -= __shfl_sync(0xffffffffu, sum - mine, l);
+      k.s += l;
+      break;
+    }
+    at -= __shfl_sync(0xffffffffu, sum, 31);
+    k.s += 32;
+  }
+  // the last list that starts at or before it
+  const int4* lists = p.lists + size_t(k.s) * p.cap;
+  int lo = 0, n = __ldg(p.sizes + k.s).x;  // among [lo, lo + n)
+  while (n > 1) {
+    const int stride = (n + 31) / 32, mid = lo + lane * stride;
+    const bool in = lane * stride < n && (long long)(__ldg(lists + min(mid, lo + n - 1)).w + mid) * per <= at;
+    const int l = 31 - __clz(__ballot_sync(0xffffffffu, in));  // (lane 0's starts before it)
+    n = min(stride, n - l * stride);
+    lo += l * stride;
+  }
+  const int4 l = __ldg(lists + lo);
+  const int tiles = (l.z + p.queries_per_tile - 1) / p.queries_per_tile, in = int(at - (long long)(l.w + lo) * per);
+  k.i = lo;
+  k.sub = in / (tiles + 1);
+  k.t = max(in - k.sub * (tiles + 1) - 1, 0);
+  return k;
+}
+
 // A CTA's shares of lists, in order: `count` entries from `first` on.  What
-// comes next is read ahead.
+// comes next is read ahead.  By a whole warp.
 struct SelWalk {
   int first, count;
-  int g, left;        // group, tiles of the part from the current list on
-  int s, sub, i, n;   // selection head, unit of it, list, the head's lists
-  int tile, tiles;    // the current list's first tile and number of tiles here
-  int4 cur, next, start;
+  int g;              // group
+  SelCut k, end;      // where it is, and where this CTA's part of the group ends
+  int n;              // the head's lists
+  int4 cur, next;
+  bool on;
 
-  __device__ __forceinline__ explicit SelWalk(const SelPlan& p) : g(-1) {
-    start = part(p, 0);
-    enter(p);
-  }
-  __device__ __forceinline__ int4 part(const SelPlan& p, int at) const {
-    return at < p.groups ? __ldg(p.starts + size_t(at) * p.ctas + blockIdx.x) : int4{0, 0, 0, 0};
-  }
-  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ explicit SelWalk(const SelPlan& p) : g(-1) { enter(p); }
+  __device__ __forceinline__ bool more() const { return on; }
   __device__ __forceinline__ void list(const SelPlan& p, int4 now) {
     cur = now;
-    next = i + 1 < n ? __ldg(p.lists + size_t(s) * p.cap + i + 1) : int4{0, 0, 0, 0};
+    next = k.i + 1 < n ? __ldg(p.lists + size_t(k.s) * p.cap + k.i + 1) : int4{0, 0, 0, 0};
   }
   __device__ __forceinline__ void here(const SelPlan& p) {  // the current list's share
-    const int per = p.queries_per_tile;
-    tiles = min((cur.z + per - 1) / per - tile, left);
-    first = cur.y + tile * per;
-    count = min(cur.z - tile * per, tiles * per);
+    const bool last = k.s == end.s && k.i == end.i && k.sub == end.sub;
+    const int per = p.queries_per_tile, to = last ? end.t * per : cur.z;
+    first = cur.y + k.t * per;
+    count = min(to, cur.z) - k.t * per;
+    on = count > 0;
   }
   __device__ __forceinline__ void enter(const SelPlan& p) {  // the next group's part
-    left = 0;
-    count = first = tiles = tile = 0;
-    while (left == 0 && ++g < p.groups) {
-      const int4 v = start;
-      start = part(p, g + 1);
-      left = v.w;
-      if (left == 0) continue;
-      const int per = p.HU / p.HS;
-      s = v.x / per;
-      sub = v.x - s * per;
-      i = v.y;
-      tile = v.z;
-      n = __ldg(p.sizes + s).x;
-      list(p, __ldg(p.lists + size_t(s) * p.cap + i));
+    on = false;
+    count = first = 0;
+    while (!on && ++g < p.groups) {
+      long long total;
+      group_cost(p, g, 0, total);
+      const long long parts = sel_parts(p, total), a = blockIdx.x * total / max(parts, 1ll);
+      if (blockIdx.x >= parts) continue;
+      const long long b = (blockIdx.x + 1) * total / parts;
+      k = find_cut(p, g, a);
+      end = b < total ? find_cut(p, g, b) : SelCut{-1, 0, 0, 0};  // (nothing behind the last list)
+      n = __ldg(p.sizes + k.s).x;
+      list(p, __ldg(p.lists + size_t(k.s) * p.cap + k.i));
       here(p);
     }
   }
   __device__ __forceinline__ void advance(const SelPlan& p) {
-    left -= tiles;
-    if (left <= 0) return enter(p);
-    tile = 0;
-    if (++sub == p.HU / p.HS) {
-      sub = 0;
-      if (++i < n) {
+    if (k.s == end.s && k.i == end.i && k.sub == end.sub) return enter(p);
+    k.t = 0;
+    if (++k.sub == p.HU / p.HS) {
+      k.sub = 0;
+      if (++k.i < n) {
         list(p, next);
       } else {
-        i = 0;
-        do n = __ldg(p.sizes + ++s).x;  // (tiles are left, so lists are)
-        while (n == 0);
-        list(p, __ldg(p.lists + size_t(s) * p.cap));
+        k.i = 0;
+        const int s1 = min(p.B * p.HS, (g + 1) * p.group);
+        do {
+          if (++k.s >= s1) return enter(p);
+          n = __ldg(p.sizes + k.s).x;
+        } while (n == 0);
+        list(p, __ldg(p.lists + size_t(k.s) * p.cap));
       }
     }
     here(p);
+    if (!on) enter(p);  // (the part ends where this list begins)
   }
   // A number of its own for every (list, CTA) that meet: along the parts one or
   // the other goes up.
   __device__ __forceinline__ long long meeting(const SelPlan& p) const {
-    return ((long long)s * p.cap + i) * (p.HU / p.HS) + sub + (long long)g * p.ctas + blockIdx.x;
+    return ((long long)k.s * p.cap + k.i) * (p.HU / p.HS) + k.sub + (long long)g * p.ctas + blockIdx.x;
   }
 };
+
 // What the other warps of a CTA are told about a share; count 0: there are no more.
 struct alignas(16) SelShare {
   int first, count, b, head0;
@@ -136,21 +204,23 @@ __device__ __forceinline__ void tell_shares(const SelPlan& p, SelShare* shares, 
   SelWalk walk(p);
   for (int q = 0;; ++q) {
     const int at = q % kShares;
-    if (!mbar_wait_polled(bars + 8u * (kShares + at), ((q / kShares) & 1) ^ 1, ctl)) return;
-    SelShare x{0, 0, 0, 0, 0, 0, 0ull};
+    if (!mbar_wait_warp(bars + 8u * (kShares + at), ((q / kShares) & 1) ^ 1, ctl)) return;
     const bool more = walk.more();
-    if (more) {
-      const int unit = walk.s * (p.HU / p.HS) + walk.sub;
-      x.first = walk.first;
-      x.count = walk.count;
-      x.b = unit / p.HU;
-      x.unit = unit - x.b * p.HU;
-      x.head0 = x.unit * p.G;
-      x.block = walk.cur.x;
-      x.meeting = walk.meeting(p);
+    if ((threadIdx.x & 31) == 0) {
+      SelShare x{0, 0, 0, 0, 0, 0, 0ull};
+      if (more) {
+        const int unit = walk.k.s * (p.HU / p.HS) + walk.k.sub;
+        x.first = walk.first;
+        x.count = walk.count;
+        x.b = unit / p.HU;
+        x.unit = unit - x.b * p.HU;
+        x.head0 = x.unit * p.G;
+        x.block = walk.cur.x;
+        x.meeting = walk.meeting(p);
+      }
+      shares[at] = x;
+      mbar_arrive(bars + 8u * at);
     }
-    shares[at] = x;
-    mbar_arrive(bars + 8u * at);
     if (!more) return;
     walk.advance(p);
   }

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
     cp_async_wait_all();
   } else if (warp >= L::kMmaWarp) {
     if (warp == L::kWalkWarp) {
-      if (lane == 0) tell_shares(a.p, shares, told, ctl);
+      tell_shares(a.p, shares, told, ctl);
     } else if (warp == L::kLoadWarp) {
       // -------------------------------------------------------------- K
       int kept = 0;
@@ -324,13 +324,28 @@ __global__ void __launch_bounds__(kMergeThreads) sel_merge_kernel(const __grid_c
   const int sel = b * a.p.HS + h / (a.p.H / a.p.HS);
   const unsigned* slots = a.p.slots + (size_t(sel) * a.p.NQ + i) * a.p.words;
   ModStats st{0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int t = part; t < a.p.T; t += kMergeLanes) {
-    if (!((slots[t >> 5] >> (t & 31)) & 1u)) continue;
-    const float4 v = __ldcs(a.rec + row * a.p.T + t);
-    const ModStats o{v.x, v.y, v.z, v.w, __ldcs(a.acc + row * a.p.T + t)};
-    if (o.l1 == 0.f) continue;
-    if (st.l1 == 0.f) st = o;
-    else merge_stats(st, o);
+  constexpr int kAhead = 4;
+  for (int t0 = part; t0 < a.p.T; t0 += kAhead * kMergeLanes) {
+    // (slots that do not count were not written: read, but not looked at)
+    float4 v[kAhead];
+    float acc[kAhead];
+    bool on[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int t = t0 + x * kMergeLanes;
+      on[x] = t < a.p.T && ((slots[t >> 5] >> (t & 31)) & 1u);
+      if (t < a.p.T) {
+        v[x] = __ldcs(a.rec + row * a.p.T + t);
+        acc[x] = __ldcs(a.acc + row * a.p.T + t);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const ModStats o{v[x].x, v[x].y, v[x].z, v[x].w, acc[x]};
+      if (!on[x] || o.l1 == 0.f) continue;
+      if (st.l1 == 0.f) st = o;
+      else merge_stats(st, o);
+    }
   }
 #pragma unroll
   for (int d = 1; d < kMergeLanes; d *= 2) {

@@ -5,9 +5,10 @@
 // shared memory; it takes 32 slots at a time, and lanes with the same block find
 // one another by a warp match, so no order of atomics enters: count; then one
 // CTA for each selection head turns counts into places and lists; then the same
-// walk again writes the entries, while other blocks of that launch find where
-// every CTA's part starts.  A block that a query names twice counts once, and
-// one that it cannot see, or that does not exist, does not count.
+// walk again writes the entries.  With few queries one CTA does all three, its
+// warps' counters in shared memory throughout.  A block that a query names twice
+// counts once, and one that it cannot see, or that does not exist, does not
+// count.
 #include <algorithm>
 
 #include "sel_common.cuh"
@@ -20,8 +21,9 @@ constexpr int kPlanWarps = 4;
 constexpr int kScanThreads = 1024;
 
 // Walks the slots of a chunk's queries.  counters: of this warp, by block.
-// kFill: counters hold where the chunk's next entry of each block goes.
-template <bool kFill>
+// kFill: counters hold where the chunk's next entry of each block goes.  kWide:
+// there may be more than 32 slots.
+template <bool kFill, bool kWide>
 __device__ __forceinline__ void walk(const SelPlan& p, int sel, int q0, int q1, unsigned* counters) {
   const int lane = threadIdx.x & 31;
   const int b = sel / p.HS;
@@ -54,7 +56,7 @@ __device__ __forceinline__ void walk(const SelPlan& p, int sel, int q0, int q1, 
   auto counts = [&](int i, int j) {
     return j >= 0 && j < p.blocks && (!p.causal || j * p.bs <= i + off || j * p.bs < prefix);
   };
-  if (p.words == 1) {
+  if (!kWide || p.words == 1) {
     constexpr int kAhead = 8;  // loads in flight
     for (int i0 = q0; i0 < q1; i0 += kAhead * per) {
       int j[kAhead];
@@ -91,68 +93,18 @@ __device__ __forceinline__ void walk(const SelPlan& p, int sel, int q0, int q1, 
   }
 }
 
-// Where a group's tiles are cut.  What a list takes counts as a tile more than
-// it has (its K, its start in the pipeline, its dK): CTA c begins at the tile of
-// cost c total / ctas.
-struct SelCut {
-  int s, i, sub, t;  // t: the list's tile
-  long long tile;    // among the group's
-};
-__device__ __forceinline__ SelCut find_cut(const SelPlan& p, int s0, long long at) {
-  const int per = p.HU / p.HS;
-  SelCut k{s0, 0, 0, 0, 0};
-  for (; at >= (long long)(p.sizes[k.s].x + p.sizes[k.s].y) * per; ++k.s) {
-    at -= (long long)(p.sizes[k.s].x + p.sizes[k.s].y) * per;
-    k.tile += (long long)p.sizes[k.s].y * per;
-  }
-  const int4* lists = p.lists + size_t(k.s) * p.cap;
-  int hi = p.sizes[k.s].x - 1;  // the last list that starts at or before it
-  while (k.i < hi) {
-    const int mid = (k.i + hi + 1) / 2;
-    if ((long long)(lists[mid].w + mid) * per <= at) k.i = mid;
-    else hi = mid - 1;
-  }
-  const int4 l = lists[k.i];
-  const int in = int(at - (long long)(l.w + k.i) * per), n = (l.z + p.queries_per_tile - 1) / p.queries_per_tile;
-  k.sub = in / (n + 1);
-  k.t = max(in % (n + 1) - 1, 0);
-  k.tile += (long long)l.w * per + (long long)k.sub * n + k.t;
-  return k;
-}
-__device__ __forceinline__ void find_start(const SelPlan& p, int u) {
-  const int g = u / p.ctas, c = u - g * p.ctas, per = p.HU / p.HS;
-  const int s0 = g * p.group, s1 = min(p.B * p.HS, s0 + p.group);
-  long long total = 0, tiles = 0;
-  for (int s = s0; s < s1; ++s) {
-    total += (long long)(p.sizes[s].x + p.sizes[s].y) * per;
-    tiles += (long long)p.sizes[s].y * per;
-  }
-  int4 out{0, 0, 0, 0};
-  if (total > 0) {
-    const SelCut k = find_cut(p, s0, c * total / p.ctas);
-    const long long end = c + 1 == p.ctas ? tiles : find_cut(p, s0, (c + 1) * total / p.ctas).tile;
-    out = make_int4(k.s * per + k.sub, k.i, k.t, int(end - k.tile));
-  }
-  p.starts[u] = out;
-}
-
 template <bool kFill>
 __global__ void __launch_bounds__(32 * kPlanWarps) sel_walk_kernel(const __grid_constant__ SelPlan p) {
   extern __shared__ unsigned shared_counters[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int walkers = (p.chunks + kPlanWarps - 1) / kPlanWarps;
   const int sel = blockIdx.x / walkers, c = (blockIdx.x - sel * walkers) * kPlanWarps + warp;
-  if (sel >= p.B * p.HS) {  // (kFill only)
-    const int u = (blockIdx.x - p.B * p.HS * walkers) * 32 * kPlanWarps + threadIdx.x;
-    if (u < p.groups * p.ctas) find_start(p, u);
-    return;
-  }
   if (c >= p.chunks) return;
   unsigned* counters = shared_counters + warp * p.blocks;
   unsigned* mine = p.counts + (size_t(sel) * p.chunks + c) * p.blocks;
   for (int j = lane; j < p.blocks; j += 32) counters[j] = kFill ? mine[j] : 0u;
   __syncwarp();
-  walk<kFill>(p, sel, c * p.chunk, min(p.NQ, (c + 1) * p.chunk), counters);
+  walk<kFill, true>(p, sel, c * p.chunk, min(p.NQ, (c + 1) * p.chunk), counters);
   if (!kFill)
     for (int j = lane; j < p.blocks; j += 32) mine[j] = counters[j];
 }
@@ -186,17 +138,71 @@ __device__ __forceinline__ uint3 scan3(uint3 v, uint3& sum) {
   return make_uint3(before.x + x.x - v.x, before.y + x.y - v.y, before.z + x.z - v.z);
 }
 
+// A block's chunks are shared by as many threads as there are for it: `parts`,
+// a power of two, neighbours of a block in threads `width` apart.
 __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(const __grid_constant__ SelPlan p) {
+  __shared__ unsigned share[kScanThreads];
   const int sel = blockIdx.x;
   unsigned* counts = p.counts + size_t(sel) * p.chunks * p.blocks;
   const unsigned per = p.queries_per_tile, base = unsigned(sel) * unsigned(p.NQ) * p.T;
+  int width = 32;
+  while (width < p.blocks && width < kScanThreads) width *= 2;
+  const int parts = kScanThreads / width, part = threadIdx.x / width, len = (p.chunks + parts - 1) / parts;
+  const int c0 = min(p.chunks, part * len), c1 = min(p.chunks, c0 + len);
+  uint3 before{0, 0, 0};  // entries, lists, tiles
+  for (int j0 = 0; j0 < p.blocks; j0 += width) {
+    const int j = j0 + (threadIdx.x & (width - 1));
+    unsigned mine = 0;
+    if (j < p.blocks)
+#pragma unroll 16
+      for (int c = c0; c < c1; ++c) mine += counts[size_t(c) * p.blocks + j];
+    share[threadIdx.x] = mine;
+    __syncthreads();
+    unsigned n = 0, to = 0;  // of the block; of the parts before this one
+    for (int x = 0; x < parts; ++x) {
+      const unsigned k = share[x * width + (threadIdx.x & (width - 1))];
+      if (x < part) to += k;
+      n += k;
+    }
+    const bool first = part == 0 && j < p.blocks;
+    uint3 sum;
+    uint3 at = scan3(first ? make_uint3(n, n != 0u ? 1u : 0u, (n + per - 1) / per) : make_uint3(0, 0, 0), sum);
+    at = make_uint3(at.x + before.x, at.y + before.y, at.z + before.z);
+    before = make_uint3(before.x + sum.x, before.y + sum.y, before.z + sum.z);
+    if (part == 0) share[threadIdx.x] = at.x;
+    __syncthreads();
+    to += share[threadIdx.x & (width - 1)];
+    if (first) {
+      if (n != 0u) p.lists[size_t(sel) * p.cap + at.y] = make_int4(j, int(base + at.x), int(n), int(at.z));
+      if (p.place != nullptr) p.place[size_t(sel) * p.blocks + j] = n != 0u ? int(at.y) : -1;
+    }
+    if (j < p.blocks)
+#pragma unroll 16
+      for (int c = c0; c < c1; ++c) {
+        const unsigned k = counts[size_t(c) * p.blocks + j];
+        counts[size_t(c) * p.blocks + j] = to;
+        to += k;
+      }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) p.sizes[sel] = make_int2(int(before.y), int(before.z));
+}
+
+// All of it for one selection head, of up to 32 slots: `chunks` warps (32 at most) with a chunk each.
+__global__ void __launch_bounds__(kScanThreads) sel_plan_kernel(const __grid_constant__ SelPlan p) {
+  extern __shared__ unsigned counters[];  // [chunks][blocks]
+  const int sel = blockIdx.x, warp = threadIdx.x >> 5;
+  const unsigned per = p.queries_per_tile, base = unsigned(sel) * unsigned(p.NQ) * p.T;
+  for (int x = threadIdx.x; x < p.chunks * p.blocks; x += kScanThreads) counters[x] = 0u;
+  __syncthreads();
+  if (warp < p.chunks) walk<false, false>(p, sel, warp * p.chunk, min(p.NQ, (warp + 1) * p.chunk), counters + warp * p.blocks);
+  __syncthreads();
   uint3 before{0, 0, 0};  // entries, lists, tiles
   for (int j0 = 0; j0 < p.blocks; j0 += kScanThreads) {
     const int j = j0 + threadIdx.x;
     unsigned n = 0;
     if (j < p.blocks)
-#pragma unroll 16
-      for (int c = 0; c < p.chunks; ++c) n += counts[size_t(c) * p.blocks + j];
+      for (int c = 0; c < p.chunks; ++c) n += counters[c * p.blocks + j];
     uint3 sum;
     uint3 at = scan3(make_uint3(n, n != 0u ? 1u : 0u, (n + per - 1) / per), sum);
     at = make_uint3(at.x + before.x, at.y + before.y, at.z + before.z);
@@ -205,31 +211,37 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(const __grid_con
     if (n != 0u) p.lists[size_t(sel) * p.cap + at.y] = make_int4(j, int(base + at.x), int(n), int(at.z));
     if (p.place != nullptr) p.place[size_t(sel) * p.blocks + j] = n != 0u ? int(at.y) : -1;
     unsigned to = at.x;
-#pragma unroll 16
     for (int c = 0; c < p.chunks; ++c) {
-      const unsigned k = counts[size_t(c) * p.blocks + j];
-      counts[size_t(c) * p.blocks + j] = to;
+      const unsigned k = counters[c * p.blocks + j];
+      counters[c * p.blocks + j] = to;
       to += k;
     }
   }
   if (threadIdx.x == 0) p.sizes[sel] = make_int2(int(before.y), int(before.z));
+  __syncthreads();
+  if (warp < p.chunks) walk<true, false>(p, sel, warp * p.chunk, min(p.NQ, (warp + 1) * p.chunk), counters + warp * p.blocks);
 }
 
 }  // namespace
 
 int launch_sel_plan(const SelPlan& p, cudaStream_t st) {
+  // (always the most shared memory: threads that launch at once would set each other's size)
+  if (p.counts == nullptr) {
+    const cudaError_t e = cudaFuncSetAttribute(sel_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanShared);
+    if (e != cudaSuccess) return e;
+    sel_plan_kernel<<<p.B * p.HS, kScanThreads, p.chunks * p.blocks * int(sizeof(unsigned)), st>>>(p);
+    return cudaGetLastError();
+  }
   const unsigned walkers = unsigned((p.chunks + kPlanWarps - 1) / kPlanWarps * p.B * p.HS);
-  const unsigned finders = unsigned((p.groups * p.ctas + 32 * kPlanWarps - 1) / (32 * kPlanWarps));
   const int smem = kPlanWarps * p.blocks * int(sizeof(unsigned));
   for (auto kern : {sel_walk_kernel<false>, sel_walk_kernel<true>}) {
-    // (always the most: threads that launch at once would set each other's size)
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kPlanWarps * kMaxSelBlocks * int(sizeof(unsigned)));
     if (e != cudaSuccess) return e;
   }
   sel_walk_kernel<false><<<walkers, 32 * kPlanWarps, smem, st>>>(p);
   sel_scan_kernel<<<p.B * p.HS, kScanThreads, 0, st>>>(p);
-  sel_walk_kernel<true><<<walkers + finders, 32 * kPlanWarps, smem, st>>>(p);
+  sel_walk_kernel<true><<<walkers, 32 * kPlanWarps, smem, st>>>(p);
   return cudaGetLastError();
 }
 
