@@ -571,10 +571,10 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
   }
 }
 
-constexpr int kDkThreads = 256;
+constexpr int kDkThreads = 256, kDkQuads = 4;  // (four values each, of a thread)
 
 // dK of one key head and block: the shares of its lists (a unit each), of the
-// CTAs that met them, in order, rounded to bf16 once.  Four values a thread.
+// CTAs that met them, in order, rounded to bf16 once.
 __global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constant__ SelBwdArgs a) {
   constexpr int kUnits = 32;
   __shared__ long long first_of[kUnits];  // a unit's first share
@@ -583,9 +583,8 @@ __global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constan
   const int j = blockIdx.x, hk = blockIdx.y % a.HK, b = blockIdx.y / a.HK;
   const int units = p.HU / a.HK, per = p.HU / p.HS;
   const int bs = p.bs, quads = a.dg / 4, rows = min(bs, p.NK - j * bs);
-  const int x = blockIdx.z * kDkThreads + threadIdx.x;
-  const int key = x / quads, c = (x - key * quads) * 4;
-  float4 sum{0.f, 0.f, 0.f, 0.f};
+  const int x0 = blockIdx.z * (kDkThreads * kDkQuads) + threadIdx.x;
+  float4 sum[kDkQuads] = {};
   for (int u0 = 0; u0 < units; u0 += kUnits) {
     // a warp finds what a unit's list left: its place among its group's costs, and the CTAs whose parts hold its tiles
     __syncthreads();
@@ -610,22 +609,33 @@ __global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constan
       }
     }
     __syncthreads();
-    if (key >= rows) continue;
     for (int u = 0; u < min(units - u0, kUnits); ++u) {
-      const float* part = a.dk_part + (size_t(first_of[u]) * bs + key) * a.dg + c;
-#pragma unroll 4
+      const float* part = a.dk_part + size_t(first_of[u]) * bs * a.dg + 4 * x0;  // (a share is [bs][quads])
+#pragma unroll 2
       for (int k = 0; k < shares_of[u]; ++k, part += size_t(bs) * a.dg) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(part));
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
+        float4 v[kDkQuads];
+#pragma unroll
+        for (int e = 0; e < kDkQuads; ++e)
+          if (x0 + e * kDkThreads < rows * quads) v[e] = __ldcs(reinterpret_cast<const float4*>(part + 4 * e * kDkThreads));
+#pragma unroll
+        for (int e = 0; e < kDkQuads; ++e)
+          if (x0 + e * kDkThreads < rows * quads) {
+            sum[e].x += v[e].x;
+            sum[e].y += v[e].y;
+            sum[e].z += v[e].z;
+            sum[e].w += v[e].w;
+          }
       }
     }
   }
-  if (key >= rows) return;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dk) + b * a.dk_sb + hk * a.dk_sh + (j * bs + key) * a.dk_sn + c;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+#pragma unroll
+  for (int e = 0; e < kDkQuads; ++e) {
+    const int x = x0 + e * kDkThreads;
+    if (x >= rows * quads) return;
+    const int key = x / quads, c = (x - key * quads) * 4;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dk) + b * a.dk_sb + hk * a.dk_sh + (j * bs + key) * a.dk_sn + c;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(sum[e].x, sum[e].y), pack_bf16(sum[e].z, sum[e].w));
+  }
 }
 
 template <int D1, int D2, int MODE>
@@ -664,7 +674,8 @@ int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs&
 }
 
 int launch_sel_dk(const SelBwdArgs& a, cudaStream_t st) {
-  const unsigned parts = unsigned((a.p.bs * (a.dg / 4) + kDkThreads - 1) / kDkThreads);
+  constexpr int kEach = kDkThreads * kDkQuads;
+  const unsigned parts = unsigned((a.p.bs * (a.dg / 4) + kEach - 1) / kEach);
   sel_dk_kernel<<<dim3(unsigned(a.p.blocks), unsigned(a.p.B * a.HK), parts), kDkThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
