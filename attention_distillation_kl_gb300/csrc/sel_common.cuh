@@ -277,8 +277,8 @@ __device__ __forceinline__ void cp_async16_size(uint32_t dst, const void* src, u
 }
 // This thread's arrival on `bar` once its copies so far have landed.  The one
 // that waits for them and hands them to the tensor core puts the proxy fence
-// between the two: a fence of each copying warp held up its next copies (731
-// us instead of @@ for the forward at 16384 queries x 32 heads).
+// between the two: a fence of each copying warp held up its next copies (763
+// us instead of 686, at the time, for 16384 queries x 32 heads).
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }

@@ -120,10 +120,12 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
   const int sel = tile / a.tiles_q, q0 = (tile - sel * a.tiles_q) * kTile;
   const int b = sel / a.HS, hs = sel - b * a.HS;
   const int j0 = blockIdx.y * kN;
-  if (a.causal) {  // no query of the tile may see a block from j0 on
-    const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
-    const bool hidden = (long long)j0 * a.bs > min(q0 + kTile, a.NQ) - 1 + a.NK - a.NQ && (long long)j0 * a.bs >= prefix;
-    if (hidden && blockIdx.y != 0) return;  // (the first ones find |q|)
+  int columns = min(kN, a.pitch - j0);  // that some query of the tile may look at
+  if (a.causal) {
+    const int prefix = a.prefix != nullptr ? min(max(a.prefix[b], 0), a.NK) : 0;
+    const int keys = max(min(q0 + kTile, a.NQ) + a.NK - a.NQ, prefix);
+    columns = min(columns, (max(keys, 0) + a.bs - 1) / a.bs - j0);
+    if (columns <= 0 && blockIdx.y != 0) return;  // (the first ones find |q|)
   }
   const int steps = a.heads * parts;
 
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     }
   } else if (warp == 5) {
     const uint32_t leader = elect_one();
-    constexpr uint32_t idesc = idesc_bf16(128, kN, 0, 0);
+    const uint32_t idesc = idesc_bf16(128, max(columns + 15, 16) / 16 * 16, 0, 0);
     bool ok = mbar_wait_warp(bar(0), 0, ctl);
     for (int s = 0; ok && s < steps; ++s) {
       const int i = s % kScoreSlots, c = s % parts;
@@ -212,14 +214,13 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     if (ok) {
       tc_fence_after();
       float* dst = a.scores + at * a.pitch + j0;
-      const int n = min(kN, a.pitch - j0);
 #pragma unroll 1
-      for (int c = 0; c < n; c += 32) {
+      for (int c = 0; c < columns; c += 32) {
         uint32_t v[32];
         tmem_ld32(tmem + (uint32_t(warp * 32) << 16) + c, v);
 #pragma unroll
         for (int e = 0; e < 32; e += 8)
-          if (c + e < n && q0 + row < a.NQ) st_global_v8(dst + c + e, v + e);
+          if (c + e < columns && q0 + row < a.NQ) st_global_v8(dst + c + e, v + e);
       }
     }
   }
@@ -234,6 +235,14 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
 // ---------------------------------------------------------------- the best of a row
 
 constexpr int kTopThreads = 256;
+
+// Floats in order as integers, and back.
+__device__ __forceinline__ int float_key(float x) {
+  const int f = __float_as_int(x);
+  return f >= 0 ? f : -(f & 0x7fffffff);
+}
+__device__ __forceinline__ float key_float(int k) { return k >= 0 ? __int_as_float(k) : -__int_as_float(-k); }
+__device__ __forceinline__ float warp_min(float x) { return key_float(__reduce_min_sync(0xffffffffu, float_key(x))); }
 
 struct Wide {  // hi + lo
   float hi, lo;
@@ -273,18 +282,21 @@ __device__ __forceinline__ double exact_score(const SelectArgs& a, int b, int hs
   return d == d ? fmin(fmax(d, -DBL_MAX), DBL_MAX) : -DBL_MAX;
 }
 
-// K values a lane (block 32 k + lane): in registers for K > 0; K = 0: any
-// number of blocks, read from memory each time.
-template <int K>
-__global__ void __launch_bounds__(kTopThreads) select_top_kernel(const __grid_constant__ SelectArgs a) {
-  const int unit = (blockIdx.x * kTopThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+// A warp a row, its scores in shared memory (block 32 k + lane at a time).
+// (Scores in registers, a loop unrolled for each, took 29 us instead of 21 for
+// the latency alone with 1024 blocks, most of it code fetched.)
+__global__ void __launch_bounds__(kTopThreads, 6) select_top_kernel(const __grid_constant__ SelectArgs a) {
+  extern __shared__ float held[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int unit = blockIdx.x * (blockDim.x >> 5) + warp;
   const unsigned below = (1u << lane) - 1u;
   if (unit >= a.tiles * kTile) return;
+  float* mine = held + warp * ((a.blocks + 31) / 32 * 32) + lane;
   const int tile = a.tile0 + unit / kTile;
   const int sel = tile / a.tiles_q, i = (tile - sel * a.tiles_q) * kTile + unit % kTile;
   if (i >= a.NQ) return;
   const int b = sel / a.HS, hs = sel - b * a.HS;
-  float* row = a.scores + size_t(unit) * a.pitch;
+  const float* row = a.scores + size_t(unit) * a.pitch;
   int* out = a.selected + (size_t(sel) * a.NQ + i) * a.T;
   const int id = a.doc_q != nullptr ? a.doc_q[(long long)b * a.NQ + i] : 0;
   // blocks that may be candidates: the first `most`
@@ -308,53 +320,55 @@ __global__ void __launch_bounds__(kTopThreads) select_top_kernel(const __grid_co
     total = 0;
     for (int k = 0; k < rounds; ++k) total += __popc(__ballot_sync(0xffffffffu, candidate(32 * k + lane)));
   }
+  if (ranges == nullptr && total <= a.T) {  // all of them
+    for (int t = lane; t < a.T; t += 32) out[t] = t < total ? t : -1;
+    return;
+  }
   // Scores as they compete: the first `sink` and last `local` candidates at the
   // top, what is no candidate below everything.
-  constexpr int kRegs = K > 0 ? K : 1;
-  float v[kRegs];
   float least = FLT_MAX, best = -FLT_MAX;
   int seen = 0;
+  constexpr int kAhead = 4;
+  for (int k0 = 0; k0 < rounds; k0 += kAhead) {
+    float x[kAhead];
 #pragma unroll
-  for (int k = 0; k < (K > 0 ? K : kMaxSelBlocks / 32); ++k) {
-    if (K > 0) v[k % kRegs] = -INFINITY;
-    if (k >= rounds) {
-      if (K == 0) break;
-      continue;
+    for (int k = 0; k < kAhead; ++k) {
+      const int j = 32 * (k0 + k) + lane;
+      x[k] = j < most ? __ldcg(row + j) : -INFINITY;
     }
-    const int j = 32 * k + lane;
-    const bool can = candidate(j);
-    const unsigned who = __ballot_sync(0xffffffffu, can);
-    const int rank = seen + __popc(who & below);
-    seen += __popc(who);
-    float x = -INFINITY;
-    if (can) {
-      if (rank < a.sink || rank >= total - a.local) {
-        x = INFINITY;
-      } else {
-        x = __ldcg(row + j);
-        x = x == x ? fminf(fmaxf(x, -FLT_MAX), FLT_MAX) : -FLT_MAX;
-        least = fminf(least, x);
-        best = fmaxf(best, x);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (k0 + k >= rounds) break;
+      const int j = 32 * (k0 + k) + lane;
+      bool can = j < most;
+      int rank = j;
+      if (ranges != nullptr) {
+        can = candidate(j);
+        const unsigned who = __ballot_sync(0xffffffffu, can);
+        rank = seen + __popc(who & below);
+        seen += __popc(who);
       }
+      const bool forced = rank < a.sink || rank >= total - a.local;
+      float y = x[k] == x[k] ? fminf(fmaxf(x[k], -FLT_MAX), FLT_MAX) : -FLT_MAX;
+      if (can && !forced) {
+        least = fminf(least, y);
+        best = fmaxf(best, y);
+      }
+      y = !can ? -INFINITY : (forced ? INFINITY : y);
+      mine[32 * (k0 + k)] = y;
     }
-    if (K > 0) v[k % kRegs] = x;
-    else if (j < a.pitch) row[j] = x;
   }
-  auto value = [&](int k) { return K > 0 ? v[k % kRegs] : (32 * k + lane < a.pitch ? row[32 * k + lane] : -INFINITY); };
+  __syncwarp();
   auto each = [&](auto f) {
-    if (K > 0) {
-#pragma unroll
-      for (int k = 0; k < kRegs; ++k) f(k, v[k]);
-    } else {
-      for (int k = 0; k < rounds; ++k) f(k, value(k));
-    }
+#pragma unroll 4
+    for (int k = 0; k < rounds; ++k) f(k, mine[32 * k]);
   };
   // The T-th best score, and how those next to it are told apart.
   enum { kEvery, kForced, kAbove, kFirst, kChosen, kDeep };
   int how = kEvery, need = 0;
   float cut = 0.f, window = 0.f;
   unsigned chosen = 0;
-  double deep[K == 0 ? kMaxSelBlocks / 32 : kRegs];
+  double deep[kMaxSelBlocks / 32];  // (of kDeep)
   auto sum_over = [&](auto f) {
     int n = 0;
     each([&](int, float x) { n += f(x) ? 1 : 0; });
@@ -363,42 +377,36 @@ __global__ void __launch_bounds__(kTopThreads) select_top_kernel(const __grid_co
   auto sure = [&](float x) { return x > cut + window || x == INFINITY; };
   auto near = [&](float x) { return !sure(x) && x >= cut - window && x > -INFINITY; };
   if (total > a.T) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-    }
-    // Bisection: at least T scores are lo or above; fewer are hi or above (or lo is the best).  First by distance, then
-    // by the number of floats between the two, which ends.
+    least = warp_min(least);
+    best = -warp_min(-best);
+    // At least T scores are lo or above; fewer are hi or above (or lo is the best).  The next guess is where the count's
+    // logarithm, taken as straight between the two, passes T; every fourth halves the distance, and from the 24th on the
+    // number of floats between the two, which ends.
     float lo = least, hi = best;
-    int n_lo = total;
-    const int n_hi = sum_over([&](float x) { return x >= hi; });
+    int n_lo = total, n_hi = sum_over([&](float x) { return x >= hi; });
     if (n_hi >= a.T) lo = hi, n_lo = n_hi;
+    const float wanted = __log2f(float(a.T) + 0.5f);
+    float up = __log2f(float(n_lo)), down = __log2f(n_hi > 0 ? float(n_hi) : 0.5f);
     for (int step = 0; n_lo != a.T && lo < hi; ++step) {
-      float mid = 0.5f * lo + 0.5f * hi;
+      const float f = (step & 3) == 3 ? 0.5f : fminf(fmaxf(__fdividef(up - wanted, up - down), 0.02f), 0.98f);
+      float mid = fmaf(f, hi - lo, lo);
       if (step >= 24 || !(mid > lo && mid < hi)) {
-        auto key = [](float x) {
-          const int f = __float_as_int(x);
-          return f >= 0 ? (long long)f : -(long long)(f & 0x7fffffff);
-        };
-        const long long m = (key(lo) + key(hi)) >> 1;
-        mid = m >= 0 ? __int_as_float(int(m)) : -__int_as_float(int(-m));
+        const long long m = (float_key(lo) + (long long)float_key(hi)) >> 1;
+        mid = key_float(int(m));
         if (!(mid > lo && mid < hi)) break;  // neighbours
       }
       const int n = sum_over([&](float x) { return x >= mid; });
-      if (n >= a.T) lo = mid, n_lo = n;
-      else hi = mid;
+      const float log_n = __log2f(n > 0 ? float(n) : 0.5f);
+      if (n >= a.T) lo = mid, n_lo = n, up = log_n;
+      else hi = mid, down = log_n;
     }
     float a_min = INFINITY, b_max = -INFINITY;  // the T-th best, the best behind it
     each([&](int, float x) {
       if (x >= lo) a_min = fminf(a_min, x);
       else b_max = fmaxf(b_max, x);
     });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a_min = fminf(a_min, __shfl_xor_sync(0xffffffffu, a_min, o));
-      b_max = fmaxf(b_max, __shfl_xor_sync(0xffffffffu, b_max, o));
-    }
+    a_min = warp_min(a_min);
+    b_max = -warp_min(-b_max);
     const float eps = float(a.heads * a.d + 64) * 1.1920929e-7f * a.norms[unit] * __uint_as_float(a.kb_norm[b * a.HS + hs]);
     cut = a_min;
     if (a_min == INFINITY) {
@@ -493,11 +501,8 @@ int launch_select(const CUtensorMap& tq, const CUtensorMap& tkb, SelectArgs a, i
   for (a.tile0 = 0; a.tile0 < all; a.tile0 += strip) {
     a.tiles = std::min(strip, all - a.tile0);
     select_score_kernel<<<dim3(unsigned(a.tiles), unsigned((a.blocks + kN - 1) / kN)), kScoreThreads, smem, st>>>(tq, tkb, a);
-    const unsigned grid = unsigned(a.tiles) * kTile / (kTopThreads / 32);
-    if (a.blocks <= 256) select_top_kernel<8><<<grid, kTopThreads, 0, st>>>(a);
-    else if (a.blocks <= 512) select_top_kernel<16><<<grid, kTopThreads, 0, st>>>(a);
-    else if (a.blocks <= 1024) select_top_kernel<32><<<grid, kTopThreads, 0, st>>>(a);
-    else select_top_kernel<0><<<grid, kTopThreads, 0, st>>>(a);
+    const int bytes = (a.blocks + 31) / 32 * 32 * 4, warps = std::max(1, std::min(kTopThreads / 32, 32768 / bytes));
+    select_top_kernel<<<unsigned((a.tiles * kTile + warps - 1) / warps), 32 * warps, warps * bytes, st>>>(a);
   }
   return cudaGetLastError();
 }
@@ -554,9 +559,9 @@ SelectPlan select_plan(const streamkl_visible& vis, int B, int H, int heads, int
   a.prefix = vis.prefix;
   a.doc_q = vis.doc_q;
   a.doc_k = vis.doc_k;
-  // strips of 64 MB of scores: about half of L2
+  // strips of at most 128 MB of scores: L2's size (with causal about half of them are written)
   const long long all = (long long)B * heads * a.tiles_q;
-  f.strip = int(std::max(1ll, std::min(all, (64ll << 20) / (4ll * kTile * a.pitch))));
+  f.strip = int(std::max(1ll, std::min(all, (128ll << 20) / (4ll * kTile * a.pitch))));
   Carver c{static_cast<uint8_t*>(ws)};
   const size_t pad = (32 - (reinterpret_cast<uintptr_t>(ws) & 31u)) & 31u;  // score rows start at 32 bytes
   c.used = pad;
