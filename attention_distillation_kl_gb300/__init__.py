@@ -504,12 +504,17 @@ class AttnSide:
     of 8 with a dense last dimension, a transposed [B, N, H, d] for one),
     scale, an optional softcap, and either slopes [H] or a learned table
     [H, num_buckets] (fp32, contiguous) with max_distance and bidirectional.
+    rotary_q, rotary_k: a Rotary each for q and k that come without their
+    positions; the side then holds turned copies of them, made here on the
+    current stream, and the backward calls give the gradients of the unturned
+    ones (rounded to bf16 once more).
 
-    Holds references to its tensors, no copies; may be used for any number of
-    calls while they keep their memory.
+    Holds references to its tensors, no copies but those; may be used for any
+    number of calls while they keep their memory.
     """
 
-    def __init__(self, q, k, scale, softcap=0.0, slopes=None, table=None, max_distance=128, bidirectional=False):
+    def __init__(self, q, k, scale, softcap=0.0, slopes=None, table=None, max_distance=128, bidirectional=False,
+                 rotary_q=None, rotary_k=None):
         for t in (q, k):
             if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
                 raise TypeError("q and k must be CUDA bf16 tensors")
@@ -531,12 +536,34 @@ class AttnSide:
                 raise ValueError(f"slopes must have one value for each of the {H} heads")
             if table is not None and (table.dim() != 2 or table.shape[0] != H):
                 raise ValueError(f"table must have one row for each of the {H} heads")
+        if rotary_q is not None:
+            q = streamkl_rotate(q, rotary_q)
+        if rotary_k is not None:
+            k = streamkl_rotate(k, rotary_k)
+        self.rotary_q, self.rotary_k = rotary_q, rotary_k
         self.q, self.k, self.slopes, self.table = q, k, slopes, table
         self.device, self.rows, self.keys = device, (B, H, NQ), NK
         self.num_buckets = 0 if table is None else table.shape[1]
         self._c = _Side(_view(q), _view(k), d, HK, float(scale), float(softcap),
                         None if slopes is None else slopes.data_ptr(), None if table is None else table.data_ptr(),
                         self.num_buckets, int(max_distance), int(bool(bidirectional)))
+
+
+def _turned(p1, p2, stream):
+    """Sides used on another stream: the copies they made are not reused before it is done."""
+    for p in (p1, p2):
+        if p.rotary_q is not None:
+            p.q.record_stream(stream)
+        if p.rotary_k is not None:
+            p.k.record_stream(stream)
+
+
+def _turn_back(g, dq, dk, stream):
+    """Gradients of a side's q and k as it was given them."""
+    if g.rotary_q is not None:
+        streamkl_rotate(dq, g.rotary_q, inverse=True, out=dq, stream=stream)
+    if g.rotary_k is not None:
+        streamkl_rotate(dk, g.rotary_k, inverse=True, out=dk, stream=stream)
 
 
 def _mod_call(p1, p2, causal, prefix, doc_q, doc_k):
@@ -635,6 +662,7 @@ def streamkl_fwd_mod(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, 
     dev, num_splits, c = p1.device, int(num_splits), lib()
     if stream is not None:
         _check_stream(stream, dev)
+        _turned(p1, p2, stream)
     need = c.streamkl_fwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, num_splits)
     ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
     kl, lse1, lse2 = _mod_rows((kl, lse1, lse2), ("kl", "lse1", "lse2"), (B, H, NQ), dev, stream)
@@ -667,6 +695,7 @@ def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=
     dev, c = g.device, lib()
     if stream is not None:
         _check_stream(stream, dev)
+        _turned(p1, p2, stream)
     for name, t in (("kl", kl), ("lse1", lse1), ("lse2", lse2), ("dkl", dkl)):
         if t is None:
             raise ValueError(f"{name} is missing")
@@ -688,6 +717,7 @@ def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=
                               dkl.data_ptr(), int(mode), det, _view(dq), _view(dk),
                               dtable.data_ptr() if want_table else None, ws, ws_bytes, _mod_stream(stream, dev)),
            "streamkl_bwd_mod")
+    _turn_back(g, dq, dk, stream)
     return dq, dk, dtable if want_table else None
 
 
@@ -871,6 +901,7 @@ def streamkl_fwd_sel(p1, p2, blocks, block, causal=False, prefix=None, doc_q=Non
     sel, dev, c = _sel_call(blocks, block, p1), p1.device, lib()
     if stream is not None:
         _check_stream(stream, dev)
+        _turned(p1, p2, stream)
     need = c.streamkl_fwd_sel_workspace_bytes(p1._c, p2._c, vis, sel, B, H, NQ, NK)
     ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
     kl, lse1, lse2 = _mod_rows((kl, lse1, lse2), ("kl", "lse1", "lse2"), (B, H, NQ), dev, stream)
@@ -898,6 +929,7 @@ def streamkl_bwd_sel(p1, p2, blocks, block, kl, lse1, lse2, dkl, mode=STREAMKL_G
     sel, dev, c = _sel_call(blocks, block, p1), g.device, lib()
     if stream is not None:
         _check_stream(stream, dev)
+        _turned(p1, p2, stream)
     for name, t in (("kl", kl), ("lse1", lse1), ("lse2", lse2), ("dkl", dkl)):
         if t is None:
             raise ValueError(f"{name} is missing")
@@ -912,6 +944,7 @@ def streamkl_bwd_sel(p1, p2, blocks, block, kl, lse1, lse2, dkl, mode=STREAMKL_G
     _check(c.streamkl_bwd_sel(p1._c, p2._c, vis, sel, B, H, NQ, NK, kl.data_ptr(), lse1.data_ptr(), lse2.data_ptr(),
                               dkl.data_ptr(), int(mode), _view(dq), _view(dk), ws, ws_bytes, _mod_stream(stream, dev)),
            "streamkl_bwd_sel")
+    _turn_back(g, dq, dk, stream)
     return dq, dk
 
 

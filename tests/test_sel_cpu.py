@@ -4,6 +4,7 @@ fails validation before any CUDA call), empty problems, structures."""
 import os
 import re
 
+import numpy as np
 import pytest
 
 import attention_distillation_kl_gb300 as skl
@@ -17,6 +18,12 @@ def blocks(selected=A, heads=1, count=4, block=32):
 def fwd(L, s1=None, s2=None, vis=None, sel=None, B=1, H=2, NQ=128, NK=128, ws=A, ws_bytes=1 << 40, out=(A, A, A)):
     return L.streamkl_fwd_sel(s1 or side(), s2 or side(), vis or seen(), sel or blocks(), B, H, NQ, NK, ws, ws_bytes,
                               *out, None)
+
+
+def bwd(L, s1=None, s2=None, vis=None, sel=None, B=1, H=2, NQ=128, NK=128, ws=A, ws_bytes=1 << 40, rows=(A, A, A, A),
+        mode=0, dq=None, dk=None):
+    return L.streamkl_bwd_sel(s1 or side(), s2 or side(), vis or seen(), sel or blocks(), B, H, NQ, NK, *rows, mode,
+                              dq or view(), dk or view(), ws, ws_bytes, None)
 
 
 BAD = [
@@ -41,6 +48,45 @@ BAD = [
 @pytest.mark.parametrize("kw,status", BAD)
 def test_bad_calls_are_refused(L, kw, status):  # noqa: F811
     assert fwd(L, **kw) == status
+    assert bwd(L, **kw) == status
+
+
+def test_backward_refusals(L):  # noqa: F811
+    assert bwd(L, mode=2) == skl.STREAMKL_INVALID_ARG
+    assert bwd(L, rows=(A, 0, A, A)) == skl.STREAMKL_INVALID_ARG
+    assert bwd(L, rows=(A, A, A, A + 4)) == skl.STREAMKL_INVALID_ARG
+    assert bwd(L, dq=view(0)) == skl.STREAMKL_INVALID_ARG
+    assert bwd(L, dk=view(A + 2)) == skl.STREAMKL_INVALID_ARG
+    need = L.streamkl_bwd_sel_workspace_bytes(side(), side(), seen(), blocks(), 1, 2, 128, 128, 0)
+    assert need >= 2 * 128 * 64 * 4 and bwd(L, ws_bytes=need - 1) == skl.STREAMKL_INVALID_ARG
+    assert L.streamkl_bwd_sel_workspace_bytes(side(), side(), seen(), blocks(), 1, 2, 128, 128, 2) == 0
+
+
+@pytest.mark.parametrize("mode", ["1", "2"])
+def test_reference_gradients_by_differences(mode):
+    """The float64 definitions that the GPU tests compare with: forward and backward fit together."""
+    import sel_reference as ref
+    g = np.random.default_rng(4)
+    H, NQ, NK, d = 2, 7, 11, 3
+    p = {n: g.standard_normal((1, h, n_, d)) for n, h, n_ in (("q1", H, NQ), ("k1", 1, NK), ("q2", H, NQ), ("k2", H, NK))}
+    for t in "12":
+        p.update({"scale" + t: 0.7, "cap" + t: 0.0, "slopes" + t: None, "table" + t: None})
+    p.update(blocks=g.integers(-1, 4, (1, 2, NQ, 2)), bs=4, causal=True, prefix=None, doc_q=None, doc_k=None)
+    w = g.standard_normal((1, H, NQ))
+    rows = ref.forward(p)[:3]
+    grads = dict(zip(("q", "k"), ref.backward(p, *rows, w, mode)[:2]))
+    h = 1e-5
+    for name, grad in grads.items():
+        x = p[name + mode]
+        for at in list(np.ndindex(x.shape))[::5]:
+            old = x[at]
+            x[at] = old + h
+            up = (w * ref.forward(p)[0]).sum()
+            x[at] = old - h
+            down = (w * ref.forward(p)[0]).sum()
+            x[at] = old
+            # central differences: an error of h^2 / 6 times a third derivative (of order 10 here), and 2^-53 / h
+            assert abs((up - down) / (2 * h) - grad[at]) <= 1e-7
 
 
 def test_forward_outputs_are_checked(L):  # noqa: F811
@@ -52,6 +98,7 @@ def test_empty_problems_do_nothing(L):  # noqa: F811
     none = side(q=view(0), k=view(0))
     for kw in (dict(NQ=0), dict(B=0)):
         assert fwd(L, none, none, sel=blocks(selected=0), ws=0, out=(0, 0, 0), **kw) == skl.STREAMKL_OK
+    assert bwd(L, none, none, sel=blocks(selected=0), ws=0, rows=(0, 0, 0, 0), B=0) == skl.STREAMKL_OK
 
 
 def test_workspace_bytes(L):  # noqa: F811
