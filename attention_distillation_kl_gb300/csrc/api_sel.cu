@@ -210,7 +210,7 @@ int streamkl_fwd_sel(const streamkl_side* p1, const streamkl_side* p2, const str
   a.lse1 = lse1;
   a.lse2 = lse2;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_mod_prep(f.prep, cs) != 0 || launch_sel_plan(a.p, cs) != 0) return STREAMKL_CUDA_ERROR;
+  if (launch_mod_prep(f.prep, cs) != 0 || launch_sel_plan(a.p, nullptr, cs) != 0) return STREAMKL_CUDA_ERROR;
   if (launch_sel_fwd(m, tile_width(p1->d), tile_width(p2->d), a, cs) != 0) return STREAMKL_CUDA_ERROR;
   return as_status(launch_sel_merge(a, cs));
 }
@@ -276,16 +276,18 @@ int streamkl_bwd_sel(const streamkl_side* p1, const streamkl_side* p2, const str
   a.dk_sh = g.HK > 1 ? dk->stride_h : 0;
   a.dk_sn = NK > 1 ? dk->stride_n : 0;
   a.HK = g.HK;
-  if (launch_mod_prep(f.prep, cs) != 0 || launch_sel_plan(a.p, cs) != 0) return STREAMKL_CUDA_ERROR;
-  if (launch_kmax_strided(g.k.data, B, g.HK, NK, g.d, B > 1 ? g.k.stride_b : 0, g.HK > 1 ? g.k.stride_h : 0,
-                          NK > 1 ? g.k.stride_n : 0, f.prep.ids_k, f.kmax, cs) != 0)
+  a.mode = mode;
+  a.k = g.k.data;
+  a.k_sb = B > 1 ? g.k.stride_b : 0;
+  a.k_sh = g.HK > 1 ? g.k.stride_h : 0;
+  a.k_sn = NK > 1 ? g.k.stride_n : 0;
+  a.doc_k = vis->doc_k;
+  const ModFinishArgs::Rows rows{f.dq32, B * H, H, NQ, g.d, f.pitch, static_cast<__nv_bfloat16*>(dq->data),
+                                 B > 1 ? dq->stride_b : 0, H > 1 ? dq->stride_h : 0, NQ > 1 ? dq->stride_n : 0};
+  if (launch_mod_prep(f.prep, cs) != 0 || launch_sel_plan(a.p, &a, cs) != 0 ||
+      launch_sel_bwd(m, tile_width(p1->d), tile_width(p2->d), a, cs) != 0)
     return STREAMKL_CUDA_ERROR;
-  if (launch_sel_bwd(m, tile_width(p1->d), tile_width(p2->d), mode, a, cs) != 0 || launch_sel_dk(a, cs) != 0)
-    return STREAMKL_CUDA_ERROR;
-  ModFinishArgs fin{};
-  fin.rows[0] = {f.dq32, B * H, H, NQ, g.d, f.pitch, static_cast<__nv_bfloat16*>(dq->data), B > 1 ? dq->stride_b : 0,
-                 H > 1 ? dq->stride_h : 0, NQ > 1 ? dq->stride_n : 0};
-  return as_status(launch_mod_finish(fin, cs));
+  return as_status(launch_sel_finish(a, rows, cs));
 }
 
 }  // extern "C"

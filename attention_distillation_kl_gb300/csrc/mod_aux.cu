@@ -103,8 +103,7 @@ struct FinishBlocks {
   int rows[2];
 };
 
-// Eight values a thread; the blocks of a part run over all its heads' rows.
-// The table: one block per head; thread (g, k) adds every 4th of the head's
+// Rows by finish_rows.  The table: one block per head; thread (g, k) adds every 4th of the head's
 // warp sums of bucket k in order, then the four shares are added.
 __global__ void __launch_bounds__(kAuxThreads) mod_finish_kernel(const __grid_constant__ ModFinishArgs a,
                                                                  const __grid_constant__ FinishBlocks fb) {
@@ -113,26 +112,7 @@ __global__ void __launch_bounds__(kAuxThreads) mod_finish_kernel(const __grid_co
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if (blk < fb.rows[s]) {
-      const ModFinishArgs::Rows& r = a.rows[s];
-      const int per_row = r.d / 8;
-      const long long total = (long long)r.heads * r.n * per_row;
-      for (long long u = (long long)blk * kAuxThreads + threadIdx.x; u < total; u += (long long)fb.rows[s] * kAuxThreads) {
-        const long long row = u / per_row;
-        const int c = int(u - row * per_row) * 8, hd = int(row / r.n), i = int(row - (long long)hd * r.n);
-        const int b = hd / r.per_batch, h = hd - b * r.per_batch;
-        float4 x{0.f, 0.f, 0.f, 0.f}, y = x;
-        if (r.src != nullptr) {
-          const float4* p = reinterpret_cast<const float4*>(r.src + row * r.pitch + c);
-          x = __ldcs(p);
-          y = __ldcs(p + 1);
-        }
-        uint4 o;
-        o.x = pack_bf16(x.x, x.y);
-        o.y = pack_bf16(x.z, x.w);
-        o.z = pack_bf16(y.x, y.y);
-        o.w = pack_bf16(y.z, y.w);
-        *reinterpret_cast<uint4*>(r.dst + b * r.sb + h * r.sh + i * r.sn + c) = o;
-      }
+      finish_rows(a.rows[s], blk, fb.rows[s]);
       return;
     }
     blk -= fb.rows[s];
@@ -156,28 +136,14 @@ __global__ void __launch_bounds__(256) mod_kmax_kernel(const __nv_bfloat16* __re
                                                        long long sb, long long sh, long long sn, const int* ids, int ids_stride,
                                                        unsigned* kmax) {
   const int b = blockIdx.y / per_batch, h = blockIdx.y - b * per_batch;
-  const __nv_bfloat16* p = k + b * sb + h * sh;
-  const int per_row = d / 8;
-  const long long total = (long long)n * per_row;
-  uint32_t m = 0;
-  for (long long u = blockIdx.x * 256ll + threadIdx.x; u < total; u += gridDim.x * 256ll) {
-    const long long i = u / per_row;
-    if (ids != nullptr && ids[size_t(b) * ids_stride + i] < 0) continue;
-    const uint4 w = *reinterpret_cast<const uint4*>(p + i * sn + (u - i * per_row) * 8);
-    const uint32_t x = max(max(w.x & 0x7fffu, (w.x >> 16) & 0x7fffu), max(w.y & 0x7fffu, (w.y >> 16) & 0x7fffu));
-    const uint32_t y = max(max(w.z & 0x7fffu, (w.z >> 16) & 0x7fffu), max(w.w & 0x7fffu, (w.w >> 16) & 0x7fffu));
-    m = max(m, max(x, y));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) atomicMax(kmax + blockIdx.y, m);
+  kmax_share(k + b * sb + h * sh, n, d, sn, ids != nullptr ? ids + size_t(b) * ids_stride : nullptr, blockIdx.x, gridDim.x,
+             kmax + blockIdx.y);
 }
 
-// Blocks for `total` units of work, 256 a block: at most 16 blocks per SM of
-// a full GPU, each then loops.
-int loop_blocks(long long total) { return int(std::max(1ll, std::min((total + kAuxThreads - 1) / kAuxThreads, 2432ll))); }
-
 }  // namespace
+
+// At most 16 blocks per SM of a full GPU.
+int loop_blocks(long long total) { return int(std::max(1ll, std::min((total + kAuxThreads - 1) / kAuxThreads, 2432ll))); }
 
 int launch_mod_prep(const ModPrepArgs& a, cudaStream_t st) {
   PrepBlocks pb{};

@@ -10,6 +10,7 @@
 
 #include <cuda_bf16.h>
 
+#include "bwd_common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -151,10 +152,65 @@ int launch_bwd_mod_p2(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cud
 int launch_bwd_mod_p1(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cudaStream_t st);
 int launch_mod_finish(const ModFinishArgs& a, cudaStream_t st);
 // ids: of the keys, padded to whole tiles (ModVis::ids_k), or null
+int loop_blocks(long long total);  // blocks of 256 threads for that many units of work, which then loop
 int launch_kmax_strided(const void* k, int B, int per_batch, int n, int d, long long sb, long long sh, long long sn,
                         const int* ids, unsigned* kmax, cudaStream_t st);
 
 // ------------------------------------------------------------------ device
+
+// A block's share of rounding rows to bf16: eight values a thread; the blocks
+// of a part run over all its heads' rows.
+__device__ __forceinline__ void finish_rows(const ModFinishArgs::Rows& r, int blk, int blocks) {
+  const int per_row = r.d / 8;
+  const long long total = (long long)r.heads * r.n * per_row;
+  for (long long u = (long long)blk * blockDim.x + threadIdx.x; u < total; u += (long long)blocks * blockDim.x) {
+    const long long row = u / per_row;
+    const int c = int(u - row * per_row) * 8, hd = int(row / r.n), i = int(row - (long long)hd * r.n);
+    const int b = hd / r.per_batch, h = hd - b * r.per_batch;
+    float4 x{0.f, 0.f, 0.f, 0.f}, y = x;
+    if (r.src != nullptr) {
+      const float4* p = reinterpret_cast<const float4*>(r.src + row * r.pitch + c);
+      x = __ldcs(p);
+      y = __ldcs(p + 1);
+    }
+    uint4 o;
+    o.x = pack_bf16(x.x, x.y);
+    o.y = pack_bf16(x.z, x.w);
+    o.z = pack_bf16(y.x, y.y);
+    o.w = pack_bf16(y.z, y.w);
+    *reinterpret_cast<uint4*>(r.dst + b * r.sb + h * r.sh + i * r.sn + c) = o;
+  }
+}
+
+// A block's share of max |k| of one head, as bf16 bits; ids: negative where a
+// key does not count.
+__device__ __forceinline__ void kmax_share(const __nv_bfloat16* k, int n, int d, long long sn, const int* ids, int blk,
+                                           int blocks, unsigned* kmax) {
+  const int per_row = d / 8;
+  const long long total = (long long)n * per_row;
+  const long long step = (long long)blocks * blockDim.x;
+  uint32_t m = 0;
+  constexpr int kAhead = 4;  // loads in flight
+  for (long long u = (long long)blk * blockDim.x + threadIdx.x; u < total; u += kAhead * step) {
+    uint4 w[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const long long v = u + e * step, i = v / per_row;
+      w[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (v < total && (ids == nullptr || ids[i] >= 0))
+        w[e] = *reinterpret_cast<const uint4*>(k + i * sn + (v - i * per_row) * 8);
+    }
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const uint32_t x = max(max(w[e].x & 0x7fffu, (w[e].x >> 16) & 0x7fffu), max(w[e].y & 0x7fffu, (w[e].y >> 16) & 0x7fffu));
+      const uint32_t y = max(max(w[e].z & 0x7fffu, (w[e].z >> 16) & 0x7fffu), max(w[e].w & 0x7fffu, (w[e].w >> 16) & 0x7fffu));
+      m = max(m, max(x, y));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) atomicMax(kmax, m);
+}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y,
                                             int z, int w) {

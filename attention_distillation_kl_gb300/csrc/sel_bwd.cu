@@ -5,7 +5,7 @@
 //
 // Persistent CTAs walk their lists.  dK of a list's block accumulates in TMEM
 // and leaves as one fp32 tile for each CTA that had a share of the list, which
-// sel_dk_kernel adds in order.
+// sel_finish_kernel adds in order.
 // A row of dQ gets a contribution from each of its blocks, out of different
 // CTAs: fp32 vector reductions, each value rounded to its row's grid first
 // (dq_fixed_exp), so that the sums are exact in any order and the result is
@@ -15,7 +15,7 @@
 //               shared memory, 8 rows x 32 values at a time, so that 8 lanes
 //               reduce a whole line of 128 bytes; after a list, dK alike
 //   warps 16-19 gather 32 rows each of both sides, and the rows' parameters
-//               (sel_rows_kernel)
+//               (row_params)
 //   warp 20     S1, S2      warp 21     dK, dQ      warp 22     K by TMA
 //   warp 23     tells the others what to take (SelShare)
 // TMEM: S1, S2 of bs columns (two buffers with blocks up to 64), dK [256, 384),
@@ -107,27 +107,6 @@ __device__ __forceinline__ void ds_columns(const uint32_t (&x1)[16], const uint3
     f2_split(D, a, b);
     out[k / 2] = pack_bf16(a, b);
   }
-}
-
-constexpr int kRowThreads = 256;
-
-// What dS and dQ need of every row: na, nb, ws as in ds_chunk_row, and the
-// exponent of its grid.  A row that saw nothing has na = -inf.
-__global__ void __launch_bounds__(kRowThreads) sel_rows_kernel(const __grid_constant__ SelBwdArgs a, int mode) {
-  const long long row = (long long)blockIdx.x * kRowThreads + threadIdx.x;
-  if (row >= (long long)a.p.B * a.p.H * a.p.NQ) return;
-  const bool p2 = mode == STREAMKL_GRAD_P2;
-  const float l1 = a.lse1[row], l2 = a.lse2[row], kl = a.kl[row], dkl = a.dkl[row], sg = p2 ? a.scale2 : a.scale1;
-  float4 par{-INFINITY, p2 ? -INFINITY : 0.f, 0.f, 0.f};
-  if (l1 != -INFINITY) {
-    const int bh = int(row / a.p.NQ), b = bh / a.p.H, h = bh - b * a.p.H;
-    const float kmax = __uint_as_float(a.kmax[b * a.HK + h / (a.p.H / a.HK)] << 16);
-    par.x = -l1 * kLog2e;
-    par.y = p2 ? -l2 * kLog2e : -(l1 - l2 + kl);
-    par.z = sg * dkl;
-    par.w = float(dq_fixed_exp(mode, sg, dkl, kl, kmax));
-  }
-  a.rows[row] = par;
 }
 
 template <int D1, int D2, int MODE>
@@ -574,16 +553,17 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
 constexpr int kDkThreads = 256, kDkQuads = 4;  // (four values each, of a thread)
 
 // dK of one key head and block: the shares of its lists (a unit each), of the
-// CTAs that met them, in order, rounded to bf16 once.
-__global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constant__ SelBwdArgs a) {
+// CTAs that met them, in order, rounded to bf16 once.  part_of: which of the
+// block's values.
+__device__ __forceinline__ void dk_of_block(const SelBwdArgs& a, int j, int head, int part_of) {
   constexpr int kUnits = 32;
   __shared__ long long first_of[kUnits];  // a unit's first share
   __shared__ int shares_of[kUnits];
   const SelPlan& p = a.p;
-  const int j = blockIdx.x, hk = blockIdx.y % a.HK, b = blockIdx.y / a.HK;
+  const int hk = head % a.HK, b = head / a.HK;
   const int units = p.HU / a.HK, per = p.HU / p.HS;
   const int bs = p.bs, quads = a.dg / 4, rows = min(bs, p.NK - j * bs);
-  const int x0 = blockIdx.z * (kDkThreads * kDkQuads) + threadIdx.x;
+  const int x0 = part_of * (kDkThreads * kDkQuads) + threadIdx.x;
   float4 sum[kDkQuads] = {};
   for (int u0 = 0; u0 < units; u0 += kUnits) {
     // a warp finds what a unit's list left: its place among its group's costs, and the CTAs whose parts hold its tiles
@@ -638,6 +618,19 @@ __global__ void __launch_bounds__(kDkThreads) sel_dk_kernel(const __grid_constan
   }
 }
 
+// The blocks' dK by the first CTAs, dQ's rows by the others.
+__global__ void __launch_bounds__(kDkThreads, 4) sel_finish_kernel(const __grid_constant__ SelBwdArgs a,
+                                                                const __grid_constant__ ModFinishArgs::Rows dq, int dk,
+                                                                int rows) {
+  const int blk = blockIdx.x;
+  if (blk >= dk) {
+    finish_rows(dq, blk - dk, rows);
+    return;
+  }
+  const int heads = a.p.B * a.HK, x = blk / a.p.blocks;
+  dk_of_block(a, blk - x * a.p.blocks, x % heads, x / heads);
+}
+
 template <int D1, int D2, int MODE>
 int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, cudaStream_t st) {
   using L = SelBwdLayout<D1, D2>;
@@ -653,30 +646,29 @@ int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, cudaStream_t st) 
   auto kern = sel_bwd_kernel<D1, D2, MODE>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kMost);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)a.p.B * a.p.H * a.p.NQ;
-  sel_rows_kernel<<<unsigned((rows + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st>>>(a, MODE);
   kern<<<a.p.ctas, L::kThreads, L::bytes(a.slots, a.k_bufs, bs), st>>>(m.k1, m.k2, a);
   return cudaGetLastError();
 }
 
 template <int D1, int D2>
-int launch_sel_bwd_m(const SelMaps& m, int mode, const SelBwdArgs& a, cudaStream_t st) {
-  return mode == STREAMKL_GRAD_P2 ? launch_sel_bwd_t<D1, D2, STREAMKL_GRAD_P2>(m, a, st)
+int launch_sel_bwd_m(const SelMaps& m, const SelBwdArgs& a, cudaStream_t st) {
+  return a.mode == STREAMKL_GRAD_P2 ? launch_sel_bwd_t<D1, D2, STREAMKL_GRAD_P2>(m, a, st)
                                   : launch_sel_bwd_t<D1, D2, STREAMKL_GRAD_P1>(m, a, st);
 }
 
 }  // namespace
 
-int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs& a, cudaStream_t st) {
+int launch_sel_bwd(const SelMaps& m, int d1, int d2, const SelBwdArgs& a, cudaStream_t st) {
   if (d1 == 64)
-    return d2 == 64 ? launch_sel_bwd_m<64, 64>(m, mode, a, st) : launch_sel_bwd_m<64, 128>(m, mode, a, st);
-  return d2 == 64 ? launch_sel_bwd_m<128, 64>(m, mode, a, st) : launch_sel_bwd_m<128, 128>(m, mode, a, st);
+    return d2 == 64 ? launch_sel_bwd_m<64, 64>(m, a, st) : launch_sel_bwd_m<64, 128>(m, a, st);
+  return d2 == 64 ? launch_sel_bwd_m<128, 64>(m, a, st) : launch_sel_bwd_m<128, 128>(m, a, st);
 }
 
-int launch_sel_dk(const SelBwdArgs& a, cudaStream_t st) {
+int launch_sel_finish(const SelBwdArgs& a, const ModFinishArgs::Rows& dq, cudaStream_t st) {
   constexpr int kEach = kDkThreads * kDkQuads;
-  const unsigned parts = unsigned((a.p.bs * (a.dg / 4) + kEach - 1) / kEach);
-  sel_dk_kernel<<<dim3(unsigned(a.p.blocks), unsigned(a.p.B * a.HK), parts), kDkThreads, 0, st>>>(a);
+  const int parts = (a.p.bs * (a.dg / 4) + kEach - 1) / kEach;
+  const int dk = a.p.blocks * a.p.B * a.HK * parts, rows = loop_blocks((long long)dq.heads * dq.n * (dq.d / 8));
+  sel_finish_kernel<<<unsigned(dk + rows), kDkThreads, 0, st>>>(a, dq, dk, rows);
   return cudaGetLastError();
 }
 

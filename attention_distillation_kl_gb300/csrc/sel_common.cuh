@@ -359,18 +359,42 @@ struct SelBwdArgs {
   int dg, pitch;          // head dim of the gradient side; row length of dq32
   float* dq32;            // [B H NQ][pitch], zeroed: dQ contributions, on their rows' grids
   float* dk_part;         // [meetings][bs][dg]: a CTA's dK of a list
-  const unsigned* kmax;   // per key head of the gradient side (launch_kmax_strided)
+  unsigned* kmax;         // per key head of the gradient side, zeroed: max |K|, as bf16 bits
   void* dk;               // bf16 [B][HK][NK][dg]
   long long dk_sb, dk_sh, dk_sn;
   int HK;                 // of the gradient side
   int* status;
-  float4* rows;           // [B H NQ], of sel_rows_kernel
+  float4* rows;           // [B H NQ], of row_params
+  int mode;
+  const void* k;          // K of the gradient side
+  long long k_sb, k_sh, k_sn;
+  const int* doc_k;
   int slots, k_bufs;
 };
 
-int launch_sel_bwd(const SelMaps& m, int d1, int d2, int mode, const SelBwdArgs& a, cudaStream_t st);
-int launch_sel_dk(const SelBwdArgs& a, cudaStream_t st);
-int launch_sel_plan(const SelPlan& p, cudaStream_t st);
+// What dS and dQ need of a row: na, nb, ws as in the dense kernels, and the
+// exponent of its grid.  A row that saw nothing has na = -inf.
+__device__ __forceinline__ void row_params(const SelBwdArgs& a, long long row) {
+  if (row >= (long long)a.p.B * a.p.H * a.p.NQ) return;
+  const bool p2 = a.mode == STREAMKL_GRAD_P2;
+  const float l1 = a.lse1[row], l2 = a.lse2[row], kl = a.kl[row], dkl = a.dkl[row], sg = p2 ? a.scale2 : a.scale1;
+  float4 par{-INFINITY, p2 ? -INFINITY : 0.f, 0.f, 0.f};
+  if (l1 != -INFINITY) {
+    const int bh = int(row / a.p.NQ), b = bh / a.p.H, h = bh - b * a.p.H;
+    const float kmax = __uint_as_float(__ldcg(a.kmax + b * a.HK + h / (a.p.H / a.HK)) << 16);
+    par.x = -l1 * kLog2e;
+    par.y = p2 ? -l2 * kLog2e : -(l1 - l2 + kl);
+    par.z = sg * dkl;
+    par.w = float(dq_fixed_exp(a.mode, sg, dkl, kl, kmax));
+  }
+  a.rows[row] = par;
+}
+
+// The plan; of a backward (else null) max |K| and the rows' parameters too.
+int launch_sel_plan(const SelPlan& p, const SelBwdArgs* bwd, cudaStream_t st);
+int launch_sel_bwd(const SelMaps& m, int d1, int d2, const SelBwdArgs& a, cudaStream_t st);
+// dK from its shares, and dq32 to bf16
+int launch_sel_finish(const SelBwdArgs& a, const ModFinishArgs::Rows& dq, cudaStream_t st);
 int launch_sel_fwd(const SelMaps& m, int d1, int d2, const SelFwdArgs& a, cudaStream_t st);
 int launch_sel_merge(const SelFwdArgs& a, cudaStream_t st);
 

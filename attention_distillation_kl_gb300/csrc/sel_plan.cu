@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kPlanWarps = 4;
 constexpr int kScanThreads = 1024;
+constexpr int kRowThreads = 256;
 
 // Walks the slots of a chunk's queries.  counters: of this warp, by block.
 // kFill: counters hold where the chunk's next entry of each block goes.  kWide:
@@ -74,28 +75,52 @@ __device__ __forceinline__ void walk(const SelPlan& p, int sel, int q0, int q1, 
     }
     return;
   }
-  for (int i = q0; i < q1; ++i) {
-    const bool row = ids == nullptr || ids[i] >= 0;
-    int before[kMaxSlots / 32];
+  if constexpr (kWide) {
+    for (int i = q0; i < q1; ++i) {
+      const bool row = ids == nullptr || ids[i] >= 0;
+      int before[kMaxSlots / 32];
 #pragma unroll
-    for (int w = 0; w < kMaxSlots / 32; ++w) {
-      if (w >= p.words) break;
-      const int t = 32 * w + t0;
-      const int j = row && t < p.T ? sel_rows[size_t(i) * p.T + t] : -1;
-      bool on = counts(i, j);
-      before[w] = on ? j : -1;
+      for (int w = 0; w < kMaxSlots / 32; ++w) {
+        if (w >= p.words) break;
+        const int t = 32 * w + t0;
+        const int j = row && t < p.T ? sel_rows[size_t(i) * p.T + t] : -1;
+        bool on = counts(i, j);
+        before[w] = on ? j : -1;
 #pragma unroll
-      for (int v = 0; v < w; ++v)  // named in the words before?
-        for (int s = 0; s < 32; ++s)
-          if (__shfl_sync(0xffffffffu, before[v], s) == j) on = false;
-      step(i, j, on, w, t);
+        for (int v = 0; v < w; ++v)  // named in the words before?
+          for (int s = 0; s < 32; ++s)
+            if (__shfl_sync(0xffffffffu, before[v], s) == j) on = false;
+        step(i, j, on, w, t);
+      }
     }
   }
 }
 
+// CTAs of a plan's launches that a backward has beside the plan: with what
+// counts, those for max |K| of each key head; with what fills, those for the
+// rows' parameters.
+struct Beside {
+  int plan;   // CTAs of the plan itself
+  int each;   // a head's CTAs for max |K|
+};
+
+__device__ __forceinline__ void kmax_beside(const SelBwdArgs& a, const Beside& by) {
+  const int x = blockIdx.x - by.plan, head = x / by.each, b = head / a.HK;
+  kmax_share(static_cast<const __nv_bfloat16*>(a.k) + b * a.k_sb + (head - b * a.HK) * a.k_sh, a.p.NK, a.dg, a.k_sn,
+             a.doc_k != nullptr ? a.doc_k + size_t(b) * a.p.NK : nullptr, x - head * by.each, by.each, a.kmax + head);
+}
+
 template <bool kFill>
-__global__ void __launch_bounds__(32 * kPlanWarps) sel_walk_kernel(const __grid_constant__ SelPlan p) {
+__global__ void __launch_bounds__(32 * kPlanWarps)
+    sel_walk_kernel(const __grid_constant__ SelPlan p, const __grid_constant__ SelBwdArgs bwd, const __grid_constant__ Beside by) {
   extern __shared__ unsigned shared_counters[];
+  if (blockIdx.x >= by.plan) {
+    if (kFill)
+      row_params(bwd, (long long)(blockIdx.x - by.plan) * blockDim.x + threadIdx.x);
+    else
+      kmax_beside(bwd, by);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int walkers = (p.chunks + kPlanWarps - 1) / kPlanWarps;
   const int sel = blockIdx.x / walkers, c = (blockIdx.x - sel * walkers) * kPlanWarps + warp;
@@ -189,8 +214,13 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(const __grid_con
 }
 
 // All of it for one selection head, of up to 32 slots: `chunks` warps (32 at most) with a chunk each.
-__global__ void __launch_bounds__(kScanThreads) sel_plan_kernel(const __grid_constant__ SelPlan p) {
+__global__ void __launch_bounds__(kScanThreads)
+    sel_plan_kernel(const __grid_constant__ SelPlan p, const __grid_constant__ SelBwdArgs bwd, const __grid_constant__ Beside by) {
   extern __shared__ unsigned counters[];  // [chunks][blocks]
+  if (blockIdx.x >= by.plan) {
+    kmax_beside(bwd, by);
+    return;
+  }
   const int sel = blockIdx.x, warp = threadIdx.x >> 5;
   const unsigned per = p.queries_per_tile, base = unsigned(sel) * unsigned(p.NQ) * p.T;
   for (int x = threadIdx.x; x < p.chunks * p.blocks; x += kScanThreads) counters[x] = 0u;
@@ -222,14 +252,28 @@ __global__ void __launch_bounds__(kScanThreads) sel_plan_kernel(const __grid_con
   if (warp < p.chunks) walk<true, false>(p, sel, warp * p.chunk, min(p.NQ, (warp + 1) * p.chunk), counters + warp * p.blocks);
 }
 
+__global__ void __launch_bounds__(kRowThreads) sel_rows_kernel(const __grid_constant__ SelBwdArgs a) {
+  row_params(a, (long long)blockIdx.x * kRowThreads + threadIdx.x);
+}
+
 }  // namespace
 
-int launch_sel_plan(const SelPlan& p, cudaStream_t st) {
+int launch_sel_plan(const SelPlan& p, const SelBwdArgs* bwd, cudaStream_t st) {
+  static const SelBwdArgs kNone{};
+  const SelBwdArgs& a = bwd != nullptr ? *bwd : kNone;
+  const long long rows = bwd != nullptr ? (long long)p.B * p.H * p.NQ : 0;
+  // CTAs of so many threads for max |K|, and so many heads' worth of them
+  auto beside = [&](unsigned plan, int threads) {
+    const long long blocks = loop_blocks((long long)p.NK * (a.dg / 8)) * 256ll / threads;
+    return Beside{int(plan), bwd != nullptr ? int(std::max(1ll, blocks / (p.B * a.HK))) : 0};
+  };
   // (always the most shared memory: threads that launch at once would set each other's size)
   if (p.counts == nullptr) {
     const cudaError_t e = cudaFuncSetAttribute(sel_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanShared);
     if (e != cudaSuccess) return e;
-    sel_plan_kernel<<<p.B * p.HS, kScanThreads, p.chunks * p.blocks * int(sizeof(unsigned)), st>>>(p);
+    const Beside by = beside(p.B * p.HS, kScanThreads);
+    sel_plan_kernel<<<by.plan + p.B * a.HK * by.each, kScanThreads, p.chunks * p.blocks * int(sizeof(unsigned)), st>>>(p, a, by);
+    if (rows > 0) sel_rows_kernel<<<unsigned((rows + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
   const unsigned walkers = unsigned((p.chunks + kPlanWarps - 1) / kPlanWarps * p.B * p.HS);
@@ -239,9 +283,11 @@ int launch_sel_plan(const SelPlan& p, cudaStream_t st) {
                                                kPlanWarps * kMaxSelBlocks * int(sizeof(unsigned)));
     if (e != cudaSuccess) return e;
   }
-  sel_walk_kernel<false><<<walkers, 32 * kPlanWarps, smem, st>>>(p);
+  constexpr int kThreads = 32 * kPlanWarps;
+  const Beside by = beside(walkers, kThreads);
+  sel_walk_kernel<false><<<walkers + unsigned(p.B * a.HK * by.each), kThreads, smem, st>>>(p, a, by);
   sel_scan_kernel<<<p.B * p.HS, kScanThreads, 0, st>>>(p);
-  sel_walk_kernel<true><<<walkers, 32 * kPlanWarps, smem, st>>>(p);
+  sel_walk_kernel<true><<<walkers + unsigned((rows + kThreads - 1) / kThreads), kThreads, smem, st>>>(p, a, by);
   return cudaGetLastError();
 }
 
