@@ -416,6 +416,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&a)[32]) {
       : "memory");
 }
 
+// The same back; visible to the thread's later loads.
+#define SKL_IN8(a, i) \
+  "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+__device__ __forceinline__ void tmem_st32(uint32_t ta, const uint32_t (&a)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::SKL_IN8(a, 0), SKL_IN8(a, 8), SKL_IN8(a, 16), SKL_IN8(a, 24), "r"(ta)
+      : "memory");
+}
+#undef SKL_IN8
+
 // Moves a whole warpgroup's per-thread register budget down or up (the
 // registers one warpgroup gives back are what another can take; an increase
 // waits until enough are free, so every decrease must run first or

@@ -228,3 +228,73 @@ def test_strips_streams_and_graphs():
     for i0 in range(0, 24000, 8000):
         part = skl.streamkl_select_blocks(q[:, :, i0:i0 + 8000], kb, 4, 32, 60000)
         assert torch.equal(part, whole[:, :, i0:i0 + 8000])
+
+
+# Many rows of up to 256 blocks: their lists come from where the scores are made.
+MANY = dict(B=19, H=32, HS=16, NQ=7, d=32)
+MANY_CASES = {
+    "one token": dict(NQ=1, NK=1, T=1, sink=0),
+    "grouped": dict(H=64, NQ=9, NK=1500, T=6, d=128),
+    "odd head dim": dict(H=16, NK=900, T=7, d=80, bs=64, bshd=True),
+    "not causal": dict(NK=8192, T=12, causal=False, sink=0, local=0),
+    "no forced": dict(NK=300, T=3, sink=0, local=0),
+    "all forced": dict(NK=300, T=4, sink=2, local=2),
+    "one place": dict(NK=3000, T=1, sink=0, local=0),
+    "fewer candidates than places": dict(NQ=40, NK=200, T=16),
+    "more queries than keys": dict(NQ=150, NK=40, T=3),
+    "prefix": dict(NQ=12, NK=1000, prefix=[0, 177, 400, 1000, 31, 32, 33] * 2 + [999, 1, 500, 64, 65], T=5),
+    "63 places": dict(NK=200 * 32, T=63),
+    "64 places": dict(NK=200 * 32, T=64),
+    "128 places": dict(NK=256 * 128 - 7, bs=128, T=128),
+    "tiles": dict(B=4, H=8, HS=8, NQ=1250, NK=2500, T=6, bs=128),
+}
+
+
+@gpu
+@pytest.mark.parametrize("name", MANY_CASES)
+def test_lists_of_many_rows(name):
+    run(**{**MANY, **MANY_CASES[name]})
+
+
+@gpu
+@pytest.mark.parametrize("make", [whole_numbers, equal_keys, zeros, near, cancelling])
+@pytest.mark.parametrize("shape", [dict(NK=2000, T=6), dict(NK=8000, T=40, causal=False, HS=16)])
+def test_ties_and_close_scores_of_many_rows(make, shape):
+    run(make=make, **{**MANY, **shape})
+
+
+@gpu
+def test_many_rows_whose_numbers_are_not_finite():
+    """Rows with such numbers stay in bounds, the others as they were; and so with those of a block."""
+    q, kb, kw, want = run(**MANY, NK=2000, T=6)
+    q[0, 0, 5] = float("nan")
+    q[3, 9, 2, 3] = float("inf")
+    got = skl.streamkl_select_blocks(q, kb, 6, 32, 2000, **kw)
+    assert got.min() >= -1 and got.max() < 63
+    same = torch.ones(want.shape[:3], dtype=torch.bool)
+    same[0, 0, 5] = same[3, 4, 2] = False
+    assert torch.equal(got[same], want[same])
+    kb[18, 15, 40] = float("nan")
+    got = skl.streamkl_select_blocks(q, kb, 6, 32, 2000, **kw)
+    assert got.min() >= -1 and got.max() < 63
+    same[18, 15] = False
+    assert torch.equal(got[same], want[same])
+
+
+@gpu
+def test_many_rows_or_few_are_the_same():
+    """A part of the batch, by the other way, has the same lists; replayed too, with other queries."""
+    q, kb, kw, want = run(**MANY, NK=3000, T=9, bshd=True)
+    assert torch.equal(skl.streamkl_select_blocks(q[:3], kb[:3], 9, 32, 3000, **kw), want[:3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = skl.streamkl_select_blocks(q, kb, 9, 32, 3000, **kw)
+    q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(3)))
+    graph.replay()
+    now = skl.streamkl_select_blocks(q[4:6], kb[4:6], 9, 32, 3000, **kw)
+    assert torch.equal(again[4:6], now) and not torch.equal(again, want)
+    need = skl.streamkl_select_blocks_workspace_bytes(19, 32, 16, 7, 3000, 32, 32, 9, causal=True)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(skl.streamkl_select_blocks(q, kb, 9, 32, 3000, **kw, workspace=ws), again)
+    with pytest.raises(skl.StreamKLError):
+        skl.streamkl_select_blocks(q, kb, 9, 32, 3000, **kw, workspace=ws[: need - 16])
