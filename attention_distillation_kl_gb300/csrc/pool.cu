@@ -1,7 +1,9 @@
 // One key for each block of keys: the mean of those whose id is not negative,
 // summed in fp32 and rounded to bf16 once.  A warp takes a block, its lanes 16
 // bytes of a row each, as many rows at a time as 32 lanes hold.  Bound by the
-// one read of K.
+// one read of K: 65536 keys x 8 heads x 128 take 22.6 us, 6.0 TB/s (24.4 without
+// the hint that they are read once; 31 with 16 loads of a lane in flight instead
+// of 8, and 27 with 8 warps a block).
 #include <cuda_bf16.h>
 
 #include "bwd_common.cuh"
@@ -50,7 +52,7 @@ __global__ void __launch_bounds__(32 * kPoolWarps) pool_kernel(const __grid_cons
       for (int e = 0; e < kAtOnce; ++e) {
         const int r = r0 + e * at_once;
         on[e] = r < rows && (ids == nullptr || ids[r] >= 0);
-        if (on[e]) w[e] = __ldg(reinterpret_cast<const uint4*>(src + r * a.kn));
+        if (on[e]) w[e] = __ldcs(reinterpret_cast<const uint4*>(src + r * a.kn));
       }
 #pragma unroll
       for (int e = 0; e < kAtOnce; ++e)

@@ -6,12 +6,15 @@
 // fp32's 24 bits (at position 10^6 an fp32 product is off by 0.03 radians).
 // inv_freq / 2 pi is taken once as a 64-bit fraction of a turn; position times
 // it, modulo 2^64, is the angle modulo a turn without any rounding, and its
-// high 32 bits go to sincospi.  What is left is the 53 bits of that fraction:
-// 2^-22 turns at position 2^31.
+// high 32 bits go to sincospi.  What is left is the error of that fraction: up to
+// inv_freq = 1 less than 2^-63, or 2^-32 turns at position 2^31 (beyond 1024 that of
+// fp64's 53 bits).
 //
 // The kernel reads and writes every value once and is bound by that; angles
 // depend on the token and pair alone, so a block computes those of its tokens
-// once, for all of its heads.  Measured: see kTokens.
+// once, for all of its heads.  32760 tokens x 32 heads x 128 take 85 us, 6.3 TB/s;
+// with 256 threads a block 101, with 4 vectors of a thread in flight instead of 2
+// 87, with twice or four times the tokens 85 and 86.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -23,7 +26,7 @@ namespace skl {
 
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 128;
 constexpr int kRotMaxPairs = 128;
 
 struct RotArgs {
@@ -67,6 +70,21 @@ __device__ __forceinline__ void turn4(uint4& u, const Turn* t) {
   }
 }
 
+// frac(f / 2 pi) 2^64.  f = m 2^-s: m times the first 64 bits of 1 / 2 pi, s bits
+// down; beyond 1024 (and below 0) in fp64, which is slow here (2.5 us of a small call).
+__device__ __forceinline__ unsigned long long turn_step(float f) {
+  const unsigned u = __float_as_uint(f), exponent = u >> 23;
+  if (exponent < 137u) {
+    constexpr unsigned long long kTurn = 0x28be60db9391054aull;  // 2^64 / 2 pi
+    const unsigned long long m = (u & 0x7fffffu) | (exponent != 0u ? 0x800000u : 0u);
+    const int s = 150 - max(int(exponent), 1);  // 14 to 149
+    const unsigned long long hi = __umul64hi(m, kTurn), lo = m * kTurn;
+    return s < 64 ? (hi << (64 - s)) | (lo >> s) : (s < 128 ? hi >> (s - 64) : 0ull);
+  }
+  const double x = double(f) * 0.15915494309189535;
+  return __double2ull_rn((x - floor(x)) * 18446744073709551616.0);
+}
+
 enum { kHalves = 0, kNeighbours = 1, kSingle = 2 };
 
 // kHalves: pairs (p, p + R), 8 at a time, R a multiple of 8; kNeighbours: pairs
@@ -80,9 +98,7 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_consta
     const int t = u / a.pairs, p = u - t * a.pairs;
     const int axis = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);
     const long long pos = a.positions[axis * a.pos_axis + b * a.pos_b + n0 + t];
-    const double f = double(a.inv_freq[p]) * 0.15915494309189535;  // turns per position
-    const unsigned long long step = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
-    const int part = int((unsigned long long)pos * step >> 32);  // of 2^32, signed
+    const int part = int((unsigned long long)pos * turn_step(a.inv_freq[p]) >> 32);  // of 2^32, signed
     Turn r;
     sincospif(float(part) * 4.656612873077393e-10f, &r.si, &r.co);  // 2^-31: half turns
     if (a.inverse) r.si = -r.si;
@@ -119,7 +135,7 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_consta
     }
     return;
   }
-  constexpr int kAtOnce = 4;
+  constexpr int kAtOnce = 2;
   for (int u0 = threadIdx.x; u0 < total; u0 += kAtOnce * kRotThreads) {
     uint4 lo[kAtOnce], hi[kAtOnce];
     __nv_bfloat16* y[kAtOnce];
