@@ -24,7 +24,7 @@ int check_blocks(const streamkl_blocks* s, int B, int H, int NQ, int NK, bool da
   if (s->block != 32 && s->block != 64 && s->block != 128) return STREAMKL_INVALID_ARG;
   if (s->count < 1 || s->count > kMaxSlots) return STREAMKL_INVALID_ARG;
   if (s->heads < 1 || s->heads > std::max(H, 1) || H % s->heads != 0) return STREAMKL_INVALID_ARG;
-  if ((NK + s->block - 1) / s->block > kMaxSelBlocks) return STREAMKL_UNSUPPORTED;
+  if (((long long)NK + s->block - 1) / s->block > kMaxSelBlocks) return STREAMKL_UNSUPPORTED;
   if (data && (s->selected == nullptr || !aligned4(s->selected))) return STREAMKL_INVALID_ARG;
   if (NQ >= 1 << (32 - kSlotBits) || (long long)B * s->heads * NQ * s->count > (1ll << 31) - 1) return STREAMKL_INVALID_ARG;
   return STREAMKL_OK;

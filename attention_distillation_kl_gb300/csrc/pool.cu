@@ -90,7 +90,7 @@ extern "C" int streamkl_pool_blocks(const streamkl_view* k, const int* doc_k, in
   if (d < 16 || d > 128 || d % 16 != 0) return STREAMKL_UNSUPPORTED;
   if (!aligned4(doc_k)) return STREAMKL_INVALID_ARG;
   if (B == 0 || HK == 0 || NK == 0) return STREAMKL_OK;
-  const int blocks = (NK + block - 1) / block;
+  const int blocks = int(((long long)NK + block - 1) / block);
   if (!view_ok(*k, B, HK, NK) || !view_ok(*kb, B, HK, blocks)) return STREAMKL_INVALID_ARG;
   if ((long long)B * HK > 65535 || (long long)B * HK * NK > (1ll << 31) - 1) return STREAMKL_INVALID_ARG;
   const int s = check_device();

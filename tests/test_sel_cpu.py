@@ -27,6 +27,7 @@ def bwd(L, s1=None, s2=None, vis=None, sel=None, B=1, H=2, NQ=128, NK=128, ws=A,
 
 
 BAD = [
+    (dict(s1=side(HK=1), s2=side(HK=1), sel=blocks(heads=1), H=1, NQ=1, NK=2 ** 31 - 1), skl.STREAMKL_INVALID_ARG),
     (dict(sel=blocks(selected=0)), skl.STREAMKL_INVALID_ARG), (dict(sel=blocks(selected=A + 2)), skl.STREAMKL_INVALID_ARG),
     (dict(sel=blocks(heads=0)), skl.STREAMKL_INVALID_ARG), (dict(sel=blocks(heads=3)), skl.STREAMKL_INVALID_ARG),
     (dict(sel=blocks(heads=4)), skl.STREAMKL_INVALID_ARG), (dict(sel=blocks(count=0)), skl.STREAMKL_INVALID_ARG),

@@ -127,3 +127,102 @@ def test_captured_steps_in_turn():
     torch.cuda.synchronize()
     for out, (alone, *_) in zip(outs, data):
         assert [torch.equal(a, b) for a, b in zip(out, alone)] == [True] * 3
+
+
+def far(t, at):
+    """t with its heads 2^31 values and more apart (and the whole of `at` behind)."""
+    B, H, N, d = t.shape
+    y = FAR.as_strided((B, H, N, d), (H * 2 ** 31, 2 ** 31 + 64, d, 1), at)
+    y.copy_(t)
+    return y
+
+
+def test_strides_beyond_32_bits():
+    """Heads further apart than 32 bits count: the results of dense tensors."""
+    global FAR
+    FAR = torch.empty(2 ** 31 + 2 ** 20, dtype=torch.bfloat16, device="cuda")
+    x, pos, sections, freq = setting(H=2, HK=2, N=200)
+    rot = skl.Rotary(freq, pos[..., :200], sections)
+    results = []
+    for place in (lambda t, n: t, lambda t, n: far(t, n * 2 ** 16)):
+        q1, k1, q2, k2 = (place(x[n], at) for at, n in enumerate(("q1", "k1", "q2", "k2")))
+
+        def empty(at, n=200):
+            return place(torch.zeros_like(x["q1"][:, :, :n]), at)
+
+        turned = [skl.streamkl_rotate(t, rot, out=empty(4 + at)) for at, t in enumerate((q1, k1, q2, k2))]
+        kb = skl.streamkl_pool_blocks(turned[3], 32, out=empty(8, 7))
+        blocks = skl.streamkl_select_blocks(turned[2], kb, 3, 32, 200, causal=True)
+        p1, p2 = skl.AttnSide(turned[0], turned[1], 0.125), skl.AttnSide(turned[2], turned[3], 0.125)
+        rows = skl.streamkl_fwd_sel(p1, p2, blocks, 32, causal=True)
+        grads = skl.streamkl_bwd_sel(p1, p2, blocks, 32, *rows, torch.ones_like(rows[0]), causal=True,
+                                     dq=empty(9), dk=empty(10))
+        results.append([t.clone() for t in (*turned, kb, blocks, *rows, *grads)])
+    assert [torch.equal(a, b) for a, b in zip(*results)] == [True] * len(results[0])
+    del FAR
+
+
+def test_threads_with_streams_of_their_own():
+    """Calls at once from several threads, each on its stream, give what they give alone."""
+    import threading
+    work = []
+    for seed in range(3):
+        x, pos, sections, freq = setting(N=300 + 100 * seed, seed=seed)
+        rot = skl.Rotary(freq, pos, sections)
+
+        def step(x=x, rot=rot, N=300 + 100 * seed):
+            p1, p2 = (skl.AttnSide(x["q" + t], x["k" + t], 0.125, rotary_q=rot, rotary_k=rot) for t in "12")
+            blocks = skl.streamkl_select_blocks(p2.q, skl.streamkl_pool_blocks(p2.k, 32), 4, 32, N, causal=True)
+            rows = skl.streamkl_fwd_sel(p1, p2, blocks, 32, causal=True)
+            return *rows, *skl.streamkl_bwd_sel(p1, p2, blocks, 32, *rows, torch.ones_like(rows[0]), causal=True)
+
+        work.append((step, [t.clone() for t in step()]))
+    torch.cuda.synchronize()
+    wrong, rounds = [], 20
+
+    def loop(step, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(rounds):
+                    got = step()
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        wrong.append("another result")
+        except Exception as e:
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=loop, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and skl.streamkl_get_device_status() == skl.STREAMKL_OK
+
+
+def test_gradients_by_differences():
+    """A step along a gradient, forward and back, moves the KL as the gradient says (the blocks held fixed)."""
+    x, pos, sections, freq = setting(H=4, N=300, d=64, seed=5)
+    rot = skl.Rotary(freq, pos, sections)
+    w = torch.rand((1, 4, 300), generator=torch.Generator().manual_seed(6)).cuda()
+
+    def sides(**other):
+        y = {**x, **other}
+        return [skl.AttnSide(y["q" + t], y["k" + t], 0.125, rotary_q=rot, rotary_k=rot) for t in "12"]
+
+    p1, p2 = sides()
+    blocks = skl.streamkl_select_blocks(p2.q, skl.streamkl_pool_blocks(p2.k, 32), 4, 32, 300, causal=True)
+    rows = skl.streamkl_fwd_sel(p1, p2, blocks, 32, causal=True)
+    for t, mode in (("1", skl.STREAMKL_GRAD_P1), ("2", skl.STREAMKL_GRAD_P2)):
+        grads = skl.streamkl_bwd_sel(p1, p2, blocks, 32, *rows, w, mode, causal=True)
+        for name, g in zip("qk", grads):
+            at = x[name + t]
+            # Steps of 0.5 % of the values, as far as bf16 takes them: what is counted is the step after rounding.  Scores
+            # then move by 0.04 in the mean and some 0.1 where the gradient is large, and the third derivative's share is
+            # a sixth of that squared, times a few: 0.5 %.  Rounding the turned q and k moves the difference by
+            # 2^-9 |g x| against 0.01 |g| |x|, of 76800 or 19200 independent values: below 0.2 %.
+            step = 0.005 * at.float().norm() / g.float().norm() * g.float()
+            up, down = (at.float() + step).bfloat16(), (at.float() - step).bfloat16()
+            ends = [(skl.streamkl_fwd_sel(*sides(**{name + t: y}), blocks, 32, causal=True)[0].double() * w).sum()
+                    for y in (up, down)]
+            says = (g.double() * (up.double() - down.double())).sum()
+            assert abs((ends[0] - ends[1]) - says) <= 0.02 * abs(says), (name, t)
