@@ -51,31 +51,35 @@ constexpr int kPrepThreads = 256;
 // vanished); 0 for nothing but zeros.
 __device__ __forceinline__ float norm_above(float sum, bool some) { return some ? sqrtf(sum) * 1.0001f + 1.0e-17f : 0.f; }
 
-// A warp a block: |kb| of every head, and with ids the range of its keys' ids.
+// A warp a block and head: max |kb|; the first head's warps find with ids the
+// range of the block's keys' ids too.
 __global__ void __launch_bounds__(kPrepThreads) select_prep_kernel(const __grid_constant__ SelectArgs a) {
-  const int unit = (blockIdx.x * kPrepThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (unit >= a.B * a.blocks) return;
-  const int b = unit / a.blocks, j = unit - b * a.blocks;
-  for (int h = 0; h < a.HS; ++h) {
-    float s = 0.f;
-    uint32_t any = 0;
-    if (lane < a.kb.chunks) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.kb.at(b, h, j)) + lane);
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  __shared__ unsigned most[kPrepThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = blockIdx.x * (kPrepThreads / 32) + warp;
+  const int b = blockIdx.y / a.HS, h = blockIdx.y - b * a.HS;
+  float s = 0.f;
+  uint32_t any = 0;
+  if (j < a.blocks && lane < a.kb.chunks) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.kb.at(b, h, j)) + lane);
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = __uint_as_float(v[e] << 16), y = __uint_as_float(v[e] & 0xffff0000u);
-        s = fmaf(x, x, fmaf(y, y, s));
-        any |= v[e] & 0x7fff7fffu;
-      }
+    for (int e = 0; e < 4; ++e) {
+      const float x = __uint_as_float(v[e] << 16), y = __uint_as_float(v[e] & 0xffff0000u);
+      s = fmaf(x, x, fmaf(y, y, s));
+      any |= v[e] & 0x7fff7fffu;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const bool some = __any_sync(0xffffffffu, any != 0u);
-    // (a NaN compares above every number, as bits do)
-    if (lane == 0) atomicMax(a.kb_norm + b * a.HS + h, __float_as_uint(norm_above(s, some)) & 0x7fffffffu);
   }
-  if (a.doc_k == nullptr) return;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const bool some = __any_sync(0xffffffffu, any != 0u);
+  // (a NaN compares above every number, as bits do)
+  if (lane == 0) most[warp] = __float_as_uint(norm_above(s, some)) & 0x7fffffffu;
+  __syncthreads();
+  if (warp == 0) {
+    const unsigned m = __reduce_max_sync(0xffffffffu, lane < kPrepThreads / 32 ? most[lane] : 0u);
+    if (lane == 0) atomicMax(a.kb_norm + b * a.HS + h, m);
+  }
+  if (a.doc_k == nullptr || h != 0 || j >= a.blocks) return;
   int lo = INT_MAX, hi = -1;
   for (int e = lane; e < a.bs; e += 32) {
     const int k = j * a.bs + e;
@@ -87,7 +91,7 @@ __global__ void __launch_bounds__(kPrepThreads) select_prep_kernel(const __grid_
     lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
-  if (lane == 0) a.ranges[unit] = make_int2(lo, hi);
+  if (lane == 0) a.ranges[b * a.blocks + j] = make_int2(lo, hi);
 }
 
 constexpr int kN = 256;  // blocks of a tile's part
@@ -731,7 +735,8 @@ int launch_select(const CUtensorMap& tq, const CUtensorMap& tkb, SelectArgs a, i
   const int all = a.B * a.HS * a.tiles_q;
   cudaError_t e = cudaMemsetAsync(a.kb_norm, 0, size_t(a.B) * a.HS * 4, st);
   if (e != cudaSuccess) return e;
-  select_prep_kernel<<<unsigned((a.B * a.blocks + kPrepThreads / 32 - 1) / (kPrepThreads / 32)), kPrepThreads, 0, st>>>(a);
+  select_prep_kernel<<<dim3(unsigned((a.blocks + kPrepThreads / 32 - 1) / (kPrepThreads / 32)), unsigned(a.B * a.HS)),
+                       kPrepThreads, 0, st>>>(a);
   const int parts = (a.d + 63) / 64;
   const bool lists = lists_at_once(a);
   const int smem = 1024 + parts * kN * 128 + kScoreSlots * int(kQBytes) + 64;

@@ -461,6 +461,10 @@ int streamkl_fwd_sel(const streamkl_side* p1, const streamkl_side* p2, const str
  * keys must hold finite values.  The results are bitwise repeatable: dK is
  * added in a fixed order, and what a block adds to row i of dq is rounded to
  * the grid that streamkl_bwd's deterministic mode describes.
+ * workspace: device memory as for the forward, of at least
+ * streamkl_bwd_sel_workspace_bytes bytes: about 4 d + 4 count for each row, and
+ * 4 d for each key and each unit of query heads that share keys on both sides
+ * and a selection.
  */
 size_t streamkl_bwd_sel_workspace_bytes(const streamkl_side* p1, const streamkl_side* p2, const streamkl_visible* vis,
                                         const streamkl_blocks* sel, int B, int H, int NQ, int NK, int mode);
