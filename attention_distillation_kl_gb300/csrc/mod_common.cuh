@@ -151,8 +151,8 @@ int launch_mod_reduce(const ModFwdArgs& a, cudaStream_t st);
 int launch_bwd_mod_p2(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cudaStream_t st);
 int launch_bwd_mod_p1(const ModMaps& m, int d1, int d2, const ModBwdArgs& a, cudaStream_t st);
 int launch_mod_finish(const ModFinishArgs& a, cudaStream_t st);
-// ids: of the keys, padded to whole tiles (ModVis::ids_k), or null
 int loop_blocks(long long total);  // blocks of 256 threads for that many units of work, which then loop
+// ids: of the keys, padded to whole tiles (ModVis::ids_k), or null
 int launch_kmax_strided(const void* k, int B, int per_batch, int n, int d, long long sb, long long sh, long long sn,
                         const int* ids, unsigned* kmax, cudaStream_t st);
 
