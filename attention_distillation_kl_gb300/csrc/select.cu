@@ -694,8 +694,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     }
     const size_t at = size_t(blockIdx.x) * kTile + row;
     if (!LISTS && ok && blockIdx.y == 0) a.norms[at] = norm_above(sum, any != 0u);
+    if (LISTS) named_bar_sync(1, kTile);  // all four warps have read the last slots for |q| (on an abort too)
     ok = ok && mbar_wait_warp(bar(5), 0, ctl);
-    if (ok && LISTS) {  // (the operands have been read: their memory is free)
+    if (ok && LISTS) {  // (the products have read the operands too: their memory is free)
       tc_fence_after();
       const bool staged = kTile * (a.T | 1) * int(sizeof(int)) <= kScoreSlots * int(kQBytes);
       select_rows(a, tmem + (uint32_t(warp * 32) << 16), b, hs, q0, norm_above(sum, any != 0u),

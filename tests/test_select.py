@@ -298,3 +298,30 @@ def test_many_rows_or_few_are_the_same():
     assert torch.equal(skl.streamkl_select_blocks(q, kb, 9, 32, 3000, **kw, workspace=ws), again)
     with pytest.raises(skl.StreamKLError):
         skl.streamkl_select_blocks(q, kb, 9, 32, 3000, **kw, workspace=ws[: need - 16])
+
+
+def best_blocks(q, kb, T, bs, NK):
+    """Lists of causal queries from scores in float64 on the GPU, the first and last candidate forced."""
+    B, H, NQ, d = q.shape
+    nb = kb.shape[2]
+    s = q.double().reshape(B, kb.shape[1], -1, NQ, d).sum(2) @ kb.double().transpose(2, 3)
+    at = torch.arange(nb, device=q.device)
+    last = (torch.arange(NQ, device=q.device) + NK - NQ)[:, None].clamp(max=NK - 1) // bs
+    s = torch.where((at == 0) | (at == last), float("inf"), torch.where(at <= last, s, -float("inf")))
+    top, idx = torch.sort(s, dim=3, descending=True, stable=True)
+    idx = torch.where(top[..., :T] > -float("inf"), idx[..., :T], nb).sort(3)[0]
+    return torch.where(idx < nb, idx, -1).int()
+
+
+@gpu
+@pytest.mark.parametrize("T", [3, 16, 40, 63])
+def test_lists_of_full_tiles_keep_their_error_bound(T):
+    """All four warps of a tile hold rows: their lists go where the last queries were, from which |q| is found.  Keys one
+    rounding apart, so that a |q| of anything else gives other lists."""
+    g = torch.Generator().manual_seed(T)
+    q, kb = near(torch.randn((5, 32, 500, 32), generator=g), torch.randn((5, 16, 64, 32), generator=g))
+    q, kb = q.to(torch.bfloat16).cuda(), kb.to(torch.bfloat16).cuda()
+    want = best_blocks(q, kb, T, 32, 2048)
+    for _ in range(3):
+        assert torch.equal(skl.streamkl_select_blocks(q, kb, T, 32, 2048, causal=True), want)
+    assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
