@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(SelBwdLayout<D1, D2>::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  // columns past the head dim (K's are zeros, and no product may meet a NaN there)
+  // columns past the head dim (K's are zeros, and no product may meet a NaN there; slots_of_sides keeps them so)
   if (a.r1.chunks < D1 / 8 || a.r2.chunks < D2 / 8)
     for (uint32_t o = threadIdx.x * 16; o < a.slots * L::kSlot; o += L::kThreads * 16) st_shared_v4(sb + oQ + o, 0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
@@ -636,13 +636,14 @@ int launch_sel_bwd_t(const SelMaps& m, const SelBwdArgs& args, cudaStream_t st) 
   using L = SelBwdLayout<D1, D2>;
   SelBwdArgs a = args;
   const int bs = a.p.bs;
-  // Two tiles' slots, then a second K, then more slots.
+  // Two tiles' slots, then a second K, then more slots.  (Two slots are enough for the walk: a tile at a time.)
   auto fits = [&](int slots, int bufs) { return L::bytes(slots, bufs, bs) <= L::kMost; };
   a.k_bufs = 1;
   a.slots = fits(4, 1) ? 4 : 3;
   if (fits(a.slots, 2)) a.k_bufs = 2;
   while (a.slots < L::kMaxRing && fits(a.slots + 1, a.k_bufs)) ++a.slots;
   if (!fits(a.slots, a.k_bufs)) return cudaErrorInvalidValue;
+  a.slots = slots_of_sides(a.slots, a.r1, D1, a.r2, D2);
   auto kern = sel_bwd_kernel<D1, D2, MODE>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kMost);
   if (e != cudaSuccess) return e;

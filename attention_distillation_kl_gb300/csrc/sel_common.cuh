@@ -287,6 +287,17 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // Step kk of 16 along d of a K-major operand of `rows` rows.
 __device__ __forceinline__ uint32_t step_off(int kk, int rows) { return (kk >> 2) * (rows * 128) + (kk & 3) * 32; }
 
+// Slots of a ring that the sides' tiles (D1 and D2 columns) take in turn.  Columns past a head dim are zeros from the
+// start on, but with an odd number of slots each holds tiles of both sides, and a side that is narrower than the other
+// would find that one's values there: a NaN among them reaches products of rows that have nothing to do with it.  An
+// even number keeps a slot with its side.  (Zeros written with each tile instead: the forward of 8192 tokens x 32 heads,
+// 16 blocks of 64, took 272 us instead of 262 whatever the head dims; the backward of d 128 and 96 over blocks of 128,
+// which is left 2 slots, 437 instead of 513.)
+inline int slots_of_sides(int slots, const SelRows& r1, int d1, const SelRows& r2, int d2) {
+  const bool mixed = (r1.chunks < d1 / 8 && r2.chunks > r1.chunks) || (r2.chunks < d2 / 8 && r1.chunks > r2.chunks);
+  return mixed ? slots / 2 * 2 : slots;
+}
+
 // Copies 32 rows (lane r holds the address of row r; 0: not copied, or with
 // ZERO zeros) into rows [first, first + 32) of a [128][D] operand tile,
 // swizzled as TMA would: 64 bytes of 8 rows at a time, so that all but four

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(SelFwdLayout::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  // columns past the head dim (K's are zeros, and no product may meet a NaN there)
+  // columns past the head dim (K's are zeros, and no product may meet a NaN there; slots_of_sides keeps them so)
   if (a.r1.chunks < D1 / 8 || a.r2.chunks < D2 / 8)
     for (uint32_t o = threadIdx.x * 16; o < a.slots * kSlot; o += L::kThreads * 16) st_shared_v4(sb + oQ + o, 0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
@@ -375,6 +375,7 @@ int launch_sel_fwd_t(const SelMaps& m, const SelFwdArgs& args, cudaStream_t st) 
   a.k_bufs = L::bytes(5, 2, D1, D2, a.p.bs) <= L::kMost ? 2 : 1;
   a.slots = 5;
   while (a.slots < L::kMaxSlots && L::bytes(a.slots + 1, a.k_bufs, D1, D2, a.p.bs) <= L::kMost) ++a.slots;
+  a.slots = slots_of_sides(a.slots, a.r1, D1, a.r2, D2);
   auto kern = sel_fwd_kernel<D1, D2>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kMost);
   if (e != cudaSuccess) return e;

@@ -252,3 +252,33 @@ def test_outputs_workspace_streams_and_graphs():
     torch.cuda.synchronize()
     for g, w in zip(again, skl.streamkl_fwd_sel(p1, p2, idx, 32, **where)):
         assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("bs", [32, 64, 128])
+@pytest.mark.parametrize("d1,d2", [(96, 128), (128, 96), (48, 128), (128, 48), (80, 112)])
+def test_nan_queries_stay_with_their_rows_beside_a_narrower_side(d1, d2, bs):
+    """The sides' tiles take turns in the same memory, where the narrower one leaves columns of the other: many tiles a
+    CTA, so that each place is used by both."""
+    dev, idx, where, p = problem(H=16, HK1=2, HK2=2, HS=2, NQ=2000, NK=2000, T=6, bs=bs, d1=d1, d2=d2)
+    bad = torch.arange(11, 2000, 97, device="cuda")
+    idx[:, :, bad] = -1
+    idx[:, :, bad, 0] = 0  # what these rows reach: block 0
+    want = skl.streamkl_fwd_sel(*sides(dev), idx, bs, **where)
+    dkl = torch.ones_like(want[0])
+    grads = {m: skl.streamkl_bwd_sel(*sides(dev), idx, bs, *want, dkl, m, **where)
+             for m in (skl.STREAMKL_GRAD_P1, skl.STREAMKL_GRAD_P2)}
+    others = torch.ones(2000, dtype=torch.bool, device="cuda")
+    others[bad] = False
+    for side in "12":
+        q = dev["q" + side].clone()
+        dev["q" + side][:, :, bad] = float("nan")
+        got = skl.streamkl_fwd_sel(*sides(dev), idx, bs, **where)
+        for g, w in zip(got, want):
+            assert torch.equal(g[:, :, others], w[:, :, others])
+        assert torch.isnan(got[0][:, :, bad]).all()
+        for m, (dq, dk) in grads.items():
+            a, b = skl.streamkl_bwd_sel(*sides(dev), idx, bs, *got, dkl, m, **where)
+            assert torch.equal(a[:, :, others], dq[:, :, others])
+            assert torch.equal(b[:, :, bs:], dk[:, :, bs:])
+        dev["q" + side].copy_(q)
+    assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
