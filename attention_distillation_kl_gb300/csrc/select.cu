@@ -10,8 +10,11 @@
 //
 // The list has to be that of the exact scores, ties to the lowest block, while
 // the tensor core's are fp32 sums.  Their error is at most
-//   eps = (heads d + 64) 2^-23 |q| max |kb|   (|q|: over all heads of hs),
-// the bound for heads d additions in any order, each off by a unit at most.  Where a block
+//   eps = x (1 + 2 x) sum_h |q_h| max |kb|,  x = (heads d + 64) 2^-23:
+// heads d additions in any order, each off by a unit of the sum so far at most (the
+// tensor core cuts off what does not fit), which stays below (1 + x) of the terms'
+// sizes, and these below sum_h |q_h| |kb|.  (The root of all heads' squares would be
+// short by up to the root of heads: 65535 equal heads then gave wrong lists.)  Where a block
 // lies within 2 eps of the border, those that do are scored again, with
 // products that are exact in fp32 and a sum kept in two floats (an error of
 // 2^-45 of the terms), and the border is drawn by these.
@@ -38,7 +41,7 @@ struct SelectArgs {
   const int* doc_k;
   SelRows q, kb;
   float* scores;       // [tiles * 128][pitch]
-  float* norms;        // [tiles * 128]: |q|
+  float* norms;        // [tiles * 128]: the heads' |q|, summed
   unsigned* kb_norm;   // [B HS], zeroed: max |kb|, as bits
   int2* ranges;        // [B][blocks]: smallest and largest id of a block, with ids
   int* selected;
@@ -185,9 +188,10 @@ __device__ __forceinline__ bool guess(int step, float lo, float hi, float up, fl
   return true;
 }
 
-// What fp32 sums of a row's products may be off by.
+// What fp32 sums of a row's products may be off by.  (The other half of 2 x is more than the norms' own sum loses.)
 __device__ __forceinline__ float error_of(const SelectArgs& a, int b, int hs, float norm) {
-  return float(a.heads * a.d + 64) * 1.1920929e-7f * norm * __uint_as_float(a.kb_norm[b * a.HS + hs]);
+  const float x = float(a.heads * a.d + 64) * 1.1920929e-7f;
+  return x * fmaf(2.f, x, 1.f) * norm * __uint_as_float(a.kb_norm[b * a.HS + hs]);
 }
 
 // The list of row i from its scores as they compete, in shared memory (block 32 k
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(kTopThreads, 6) select_top_kernel(const __grid
 // ---------------------------------------------------------------- scores
 
 // Scores of one tile: 128 queries x kN blocks, which with LISTS are all there are.
-// Warps 0-3: |q| of a row a thread while the products run, then the accumulator
+// Warps 0-3: the heads' |q| of a row a thread while the products run, then the accumulator
 // to memory, or with LISTS the rows' lists from it; warp 4 TMA; warp 5 MMA.  The K
 // loop runs over heads and 64 values of d at a time.  Two CTAs share an SM.
 constexpr int kScoreThreads = 192, kScoreSlots = 2;
@@ -668,8 +672,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     mbar_drain(bar(5), 0, 1000000000ull);
   } else {
     const int row = warp * 32 + lane;
-    float sum = 0.f;
+    float sum = 0.f, norm = 0.f;  // of a head; of those before it
     uint32_t any = 0;
+    int left = parts;  // of the head
     bool ok = true;
     for (int s = 0; ok && s < steps; ++s) {
       const int i = s % kScoreSlots;
@@ -688,18 +693,24 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
             any |= v[e] & 0x7fff7fffu;
           }
         }
+        if (--left == 0) {
+          norm += norm_above(sum, any != 0u);
+          sum = 0.f;
+          any = 0;
+          left = parts;
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(3 + i));
     }
     const size_t at = size_t(blockIdx.x) * kTile + row;
-    if (!LISTS && ok && blockIdx.y == 0) a.norms[at] = norm_above(sum, any != 0u);
+    if (!LISTS && ok && blockIdx.y == 0) a.norms[at] = norm;
     if (LISTS) named_bar_sync(1, kTile);  // all four warps have read the last slots for |q| (on an abort too)
     ok = ok && mbar_wait_warp(bar(5), 0, ctl);
     if (ok && LISTS) {  // (the products have read the operands too: their memory is free)
       tc_fence_after();
       const bool staged = kTile * (a.T | 1) * int(sizeof(int)) <= kScoreSlots * int(kQBytes);
-      select_rows(a, tmem + (uint32_t(warp * 32) << 16), b, hs, q0, norm_above(sum, any != 0u),
+      select_rows(a, tmem + (uint32_t(warp * 32) << 16), b, hs, q0, norm,
                   smem + warp * kSelectBuffer, staged ? reinterpret_cast<int*>(smem + oQ) : nullptr);
     } else if (ok) {
       tc_fence_after();

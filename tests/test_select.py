@@ -325,3 +325,35 @@ def test_lists_of_full_tiles_keep_their_error_bound(T):
     for _ in range(3):
         assert torch.equal(skl.streamkl_select_blocks(q, kb, T, 32, 2048, causal=True), want)
     assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
+
+
+def many_heads(H, d, bump, early):
+    """Equal heads on one list, whose fp32 sums grow to 2^19 and more: there they lose what block 1 has ahead of block 0,
+    a little for each head; block 2 is ahead by a gain of the first heads, which they keep."""
+    q, kb = torch.ones((1, H, 1, d)), torch.ones((1, 1, 4, d))
+    q[:, :H // 2 + 200, :, 0] = 0.0
+    q[:, early:, :, 1] = 0.0
+    kb[:, :, 1, 0] += bump * 2.0 ** -7
+    kb[:, :, 2, 1] += 2.0 ** -3
+    return q.to(torch.bfloat16).cuda(), kb.to(torch.bfloat16).cuda()
+
+
+@gpu
+@pytest.mark.parametrize("H,d,bump,early", [(65535, 16, 6, 8800), (65535, 16, 6, 12000), (65535, 16, 7, 12000),
+                                            (65535, 32, 14, 10400), (4096, 128, 3, 700)])
+def test_many_equal_heads_on_one_list(H, d, bump, early):
+    q, kb = many_heads(H, d, bump, early)
+    score = (q.double().sum(1) @ kb[0].double().transpose(1, 2)).flatten()
+    got = skl.streamkl_select_blocks(q, kb, 1, 32, 128, sink=0, local=0)
+    assert got.item() == score.argmax().item()
+
+
+@gpu
+@pytest.mark.parametrize("shape", [dict(H=64, HS=1, NQ=60, NK=2000, T=6), dict(B=19, H=64, HS=16, NQ=7, NK=2000, T=6, d=32)])
+@pytest.mark.parametrize("make", [near, cancelling, whole_numbers])
+def test_close_scores_of_many_heads(make, shape):
+    """Heads that point the same way: their terms add up to the root of their number times the norm of all of them."""
+    def alike(q, kb):
+        q[:] = q[:, :1]
+        return make(q, kb)
+    run(make=alike, **shape)
