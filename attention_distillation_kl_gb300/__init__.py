@@ -541,6 +541,7 @@ class AttnSide:
         if rotary_k is not None:
             k = streamkl_rotate(k, rotary_k)
         self.rotary_q, self.rotary_k = rotary_q, rotary_k
+        self.made_on = None if rotary_q is rotary_k is None else torch.cuda.current_stream(device).cuda_stream
         self.q, self.k, self.slopes, self.table = q, k, slopes, table
         self.device, self.rows, self.keys = device, (B, H, NQ), NK
         self.num_buckets = 0 if table is None else table.shape[1]
@@ -550,12 +551,18 @@ class AttnSide:
 
 
 def _turned(p1, p2, stream):
-    """Sides used on another stream: the copies they made are not reused before it is done."""
+    """Sides used on another stream than they were made on (stream, or the current one): the copies they made are not
+    reused before it is done, even where the side goes first."""
     for p in (p1, p2):
+        if p.made_on is None:
+            continue
+        on = torch.cuda.current_stream(p.device) if stream is None else stream
+        if on.cuda_stream == p.made_on:
+            continue
         if p.rotary_q is not None:
-            p.q.record_stream(stream)
+            p.q.record_stream(on)
         if p.rotary_k is not None:
-            p.k.record_stream(stream)
+            p.k.record_stream(on)
 
 
 def _turn_back(g, dq, dk, stream):
@@ -662,7 +669,7 @@ def streamkl_fwd_mod(p1, p2, causal=False, prefix=None, doc_q=None, doc_k=None, 
     dev, num_splits, c = p1.device, int(num_splits), lib()
     if stream is not None:
         _check_stream(stream, dev)
-        _turned(p1, p2, stream)
+    _turned(p1, p2, stream)
     need = c.streamkl_fwd_mod_workspace_bytes(p1._c, p2._c, vis, B, H, NQ, NK, num_splits)
     ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
     kl, lse1, lse2 = _mod_rows((kl, lse1, lse2), ("kl", "lse1", "lse2"), (B, H, NQ), dev, stream)
@@ -695,7 +702,7 @@ def streamkl_bwd_mod(p1, p2, kl, lse1, lse2, dkl, mode=STREAMKL_GRAD_P2, causal=
     dev, c = g.device, lib()
     if stream is not None:
         _check_stream(stream, dev)
-        _turned(p1, p2, stream)
+    _turned(p1, p2, stream)
     for name, t in (("kl", kl), ("lse1", lse1), ("lse2", lse2), ("dkl", dkl)):
         if t is None:
             raise ValueError(f"{name} is missing")
@@ -901,7 +908,7 @@ def streamkl_fwd_sel(p1, p2, blocks, block, causal=False, prefix=None, doc_q=Non
     sel, dev, c = _sel_call(blocks, block, p1), p1.device, lib()
     if stream is not None:
         _check_stream(stream, dev)
-        _turned(p1, p2, stream)
+    _turned(p1, p2, stream)
     need = c.streamkl_fwd_sel_workspace_bytes(p1._c, p2._c, vis, sel, B, H, NQ, NK)
     ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
     kl, lse1, lse2 = _mod_rows((kl, lse1, lse2), ("kl", "lse1", "lse2"), (B, H, NQ), dev, stream)
@@ -929,7 +936,7 @@ def streamkl_bwd_sel(p1, p2, blocks, block, kl, lse1, lse2, dkl, mode=STREAMKL_G
     sel, dev, c = _sel_call(blocks, block, p1), g.device, lib()
     if stream is not None:
         _check_stream(stream, dev)
-        _turned(p1, p2, stream)
+    _turned(p1, p2, stream)
     for name, t in (("kl", kl), ("lse1", lse1), ("lse2", lse2), ("dkl", dkl)):
         if t is None:
             raise ValueError(f"{name} is missing")

@@ -124,3 +124,83 @@ def test_work_pending_on_the_current_stream_does_not_reach_the_plain_results(spl
         got = calls(stream=s)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def turned_side(made_on, q=True, k=True):
+    t = [torch.zeros(1), torch.zeros(1)]
+    return types.SimpleNamespace(device=torch.device("cuda:0"), q=t[0], k=t[1], made_on=made_on,
+                                 rotary_q="r" if q else None, rotary_k="r" if k else None)
+
+
+def test_turned_copies_are_kept_for_the_stream_that_uses_them(monkeypatch):
+    marked = []
+    here, other = types.SimpleNamespace(cuda_stream=1), types.SimpleNamespace(cuda_stream=2)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: here)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: marked.append((t, s)))
+    plain, same, away = turned_side(None, False, False), turned_side(1), turned_side(2, q=False)
+
+    def marks(p1, p2, stream):
+        marked.clear()
+        skl._turned(p1, p2, stream)
+        return [(id(t), s.cuda_stream) for t, s in marked]
+
+    assert marks(plain, same, None) == []  # used where it was made
+    assert marks(plain, away, None) == [(id(away.k), 1)]
+    assert marks(same, plain, other) == [(id(same.q), 2), (id(same.k), 2)]
+    assert marks(away, same, other) == [(id(same.q), 2), (id(same.k), 2)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("calls", ["mod", "sel"])
+def test_a_side_dropped_while_another_stream_reads_its_copies(calls):
+    """The current stream, not the one that the side was made on: its memory is not handed out before that is done."""
+    n = torch.arange(256, dtype=torch.int32, device="cuda")[None]
+    x = [torch.randn((1, 4, 256, 64), generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in range(4)]
+    rot = skl.Rotary((100.0 ** (-torch.arange(32, device="cuda") / 32)).float(), n)
+    blocks = torch.arange(8, dtype=torch.int32, device="cuda").expand(1, 4, 256, 8).contiguous()
+
+    def use(p1, p2):
+        if calls == "mod":
+            rows = skl.streamkl_fwd_mod(p1, p2, causal=True)
+            return (*rows, *skl.streamkl_bwd_mod(p1, p2, *rows, torch.ones_like(rows[0]), causal=True, deterministic=True)[:2])
+        rows = skl.streamkl_fwd_sel(p1, p2, blocks, 32, causal=True)
+        return (*rows, *skl.streamkl_bwd_sel(p1, p2, blocks, 32, *rows, torch.ones_like(rows[0]), causal=True))
+
+    def sides():
+        return [skl.AttnSide(x[i], x[i + 1], 0.125, rotary_q=rot, rotary_k=rot) for i in (0, 2)]
+
+    want = [t.clone() for t in use(*sides())]
+    b = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        p1, p2 = sides()
+        held = {t.data_ptr() for p in (p1, p2) for t in (p.q, p.k)}
+        b.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(b):
+            torch.cuda._sleep(100_000_000)  # some 50 ms before they are read
+            got = use(p1, p2)
+        del p1, p2
+        new = [torch.empty_like(x[0]).fill_(float("nan")) for _ in range(8)]
+        assert not held & {t.data_ptr() for t in new}
+        torch.cuda.current_stream().wait_stream(b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_sides_made_before_a_capture():
+    n = torch.arange(256, dtype=torch.int32, device="cuda")[None]
+    x = [torch.randn((1, 4, 256, 64), generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in range(4)]
+    rot = skl.Rotary((100.0 ** (-torch.arange(32, device="cuda") / 32)).float(), n)
+    p1, p2 = (skl.AttnSide(x[i], x[i + 1], 0.125, rotary_q=rot, rotary_k=rot) for i in (0, 2))
+    want = skl.streamkl_fwd_mod(p1, p2, causal=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = skl.streamkl_fwd_mod(p1, p2, causal=True)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(got, want))
+    del p1, p2
+    torch.cuda.synchronize()
+    torch.empty_like(x[0])
