@@ -752,12 +752,15 @@ def _like_new(shape, device, stream, given, name, dtype=torch.bfloat16):
 
 def _at_device(fn):
     """Runs fn with its first tensor's device current (the library launches there)."""
+    first = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def wrapped(x, *a, **k):
+    def wrapped(*args, **kw):
+        x = args[0] if args else kw.get(first)
         if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device.index == torch.cuda.current_device():
-            return fn(x, *a, **k)
+            return fn(*args, **kw)
         with torch.cuda.device(x.device):
-            return fn(x, *a, **k)
+            return fn(*args, **kw)
     return wrapped
 
 

@@ -124,3 +124,27 @@ def test_structures_match_the_header():
                 if m:
                     fields.append(m.group(1))
         assert fields == [f for f, _ in struct._fields_], name
+
+
+def test_calls_take_their_arguments_by_name():
+    import torch
+    x = torch.zeros((1, 1, 8, 16), dtype=torch.bfloat16)  # not on a GPU: refused for that, behind the wrappers
+    with pytest.raises(TypeError, match="x must be a CUDA"):
+        skl.streamkl_rotate(rotary=None, x=x)
+    with pytest.raises(TypeError, match="k must be a CUDA"):
+        skl.streamkl_pool_blocks(k=x, block=32)
+    with pytest.raises(TypeError, match="q must be a CUDA"):
+        skl.streamkl_select_blocks(q=x, kb=x, count=4, block=32, NK=100)
+    with pytest.raises(TypeError, match="missing"):
+        skl.streamkl_pool_blocks()
+
+
+@pytest.mark.gpu
+def test_results_of_arguments_by_name():
+    import torch
+    q = torch.randn((1, 4, 100, 32), device="cuda").to(torch.bfloat16)
+    k = torch.randn((1, 2, 100, 32), device="cuda").to(torch.bfloat16)
+    kb = skl.streamkl_pool_blocks(k=k, block=32)
+    assert torch.equal(kb, skl.streamkl_pool_blocks(k, 32))
+    assert torch.equal(skl.streamkl_select_blocks(q=q, kb=kb, count=3, block=32, NK=100),
+                       skl.streamkl_select_blocks(q, kb, 3, 32, 100))
