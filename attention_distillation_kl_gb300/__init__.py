@@ -846,38 +846,49 @@ def _visible(B, NQ, NK, device, causal, prefix, doc_q, doc_k):
     return _Visible(1 if causal else 0, *(None if t is None else t.data_ptr() for t in (prefix, doc_q, doc_k)))
 
 
-def streamkl_select_blocks_workspace_bytes(B, H, heads, NQ, NK, d, block, count, causal=False, ids=False, sink=1, local=1):
+def _ends(count, sink, local):
+    """How many of the first and last candidates are always taken: one each where nothing is said and `count` leaves
+    room for it, the last before the first."""
+    local = max(0, min(1, count - (0 if sink is None else int(sink)))) if local is None else int(local)
+    return max(0, min(1, count - local)) if sink is None else int(sink), local
+
+
+def streamkl_select_blocks_workspace_bytes(B, H, heads, NQ, NK, d, block, count, causal=False, ids=False, sink=None,
+                                           local=None):
     """Workspace bytes streamkl_select_blocks needs (ids: whether doc_q, doc_k are given)."""
+    sink, local = _ends(count, sink, local)
     vis = _Visible(1 if causal else 0, None, 16 if ids else None, 16 if ids else None)  # (which are null is all it asks)
     return int(lib().streamkl_select_blocks_workspace_bytes(vis, B, H, heads, NQ, NK, d, block, count, sink, local))
 
 
 @_at_device
-def streamkl_select_blocks(q, kb, count, block, NK, causal=False, prefix=None, doc_q=None, doc_k=None, sink=1, local=1,
-                           out=None, workspace=None, stream=None):
+def streamkl_select_blocks(q, kb, count, block, NK, causal=False, prefix=None, doc_q=None, doc_k=None, sink=None,
+                           local=None, out=None, workspace=None, stream=None):
     """The `count` blocks of `block` keys that score best for each query, int32
     [B, heads, NQ, count], ascending, -1 behind them: kb [B, heads,
     ceil(NK / block), d] holds a key for each block (streamkl_pool_blocks),
     and a block's score is the sum of q_h . kb over the H // heads query heads
     that share a head of kb.  Candidates hold a key that causal, prefix, doc_q
     and doc_k leave visible; the first `sink` and last `local` of them are
-    always taken.  Ties go to the lowest block."""
+    always taken (sink + local <= count; one each by default, with count = 1
+    the last alone).  Ties go to the lowest block."""
     _strided(q, "q")
     _strided(kb, "kb")
     B, H, NQ, d = q.shape
     heads, dev, c = kb.shape[1], q.device, lib()
     count, block, NK = int(count), int(block), int(NK)
+    sink, local = _ends(count, sink, local)
     if kb.device != dev or kb.shape[0] != B or kb.shape[3] != d or block < 1 or kb.shape[2] != -(-NK // block):
         raise ValueError(f"kb must be [{B}, heads, {-(-NK // max(block, 1))}, {d}] on {dev}")
     vis = _visible(B, NQ, NK, dev, causal, prefix, doc_q, doc_k)
     if stream is not None:
         _check_stream(stream, dev)
-    need = c.streamkl_select_blocks_workspace_bytes(vis, B, H, heads, NQ, NK, d, block, count, int(sink), int(local))
+    need = c.streamkl_select_blocks_workspace_bytes(vis, B, H, heads, NQ, NK, d, block, count, sink, local)
     ws, ws_bytes, keep = _mod_workspace(workspace, need, dev, stream)
     sel = _like_new((B, heads, NQ, max(count, 1)), dev, stream, out, "out", torch.int32)
     if not sel.is_contiguous():
         raise ValueError("out must be contiguous")
-    _check(c.streamkl_select_blocks(_view(q), _view(kb), vis, B, H, heads, NQ, NK, d, block, count, int(sink), int(local),
+    _check(c.streamkl_select_blocks(_view(q), _view(kb), vis, B, H, heads, NQ, NK, d, block, count, sink, local,
                                     sel.data_ptr(), ws, ws_bytes, _mod_stream(stream, dev)), "streamkl_select_blocks")
     return sel
 

@@ -357,3 +357,22 @@ def test_close_scores_of_many_heads(make, shape):
         q[:] = q[:, :1]
         return make(q, kb)
     run(make=alike, **shape)
+
+
+def test_ends_taken_by_default(L):
+    assert skl._ends(4, None, None) == (1, 1) and skl._ends(2, None, None) == (1, 1)
+    assert skl._ends(1, None, None) == (0, 1)
+    assert skl._ends(4, 4, None) == (4, 0) and skl._ends(4, None, 4) == (0, 4) and skl._ends(3, 2, None) == (2, 1)
+    assert skl._ends(4, 3, 2) == (3, 2)  # refused by the library
+    f = skl.streamkl_select_blocks_workspace_bytes
+    assert f(1, 4, 2, 100, 300, 64, 32, 1) > 0
+    assert f(1, 4, 2, 100, 300, 64, 32, 1, sink=1, local=1) == 0
+
+
+@gpu
+def test_one_place_by_default():
+    """The last candidate, as the defaults say; the best with none forced."""
+    q, kb, kw, _ = run(NQ=100, NK=300, T=1, sink=0, local=0)
+    del kw["sink"], kw["local"]
+    got = skl.streamkl_select_blocks(q, kb, 1, 32, 300, **kw)
+    assert torch.equal(got.flatten(0, 1).squeeze(2).cpu(), ((torch.arange(100) + 200) // 32).int().expand(2, 100))
