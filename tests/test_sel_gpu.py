@@ -282,3 +282,75 @@ def test_nan_queries_stay_with_their_rows_beside_a_narrower_side(d1, d2, bs):
             assert torch.equal(b[:, :, bs:], dk[:, :, bs:])
         dev["q" + side].copy_(q)
     assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
+
+
+ANYTHING = {
+    "packed": dict(B=2, H=4, HK1=2, HK2=2, HS=2, NQ=300, NK=300, docs="packed", T=5),
+    "shuffled ids, large blocks": dict(B=2, H=4, HK1=1, HK2=4, HS=1, NQ=200, NK=333, docs="shuffled", T=2, bs=128, d1=128, d2=96),
+    "shuffled ids, blocks of 64": dict(B=2, H=6, HK1=2, HK2=3, HS=2, NQ=260, NK=400, docs="shuffled", T=3, bs=64, d1=48, d2=64),
+    "more queries than keys": dict(H=2, NQ=300, NK=100, T=3),
+    "few lists": dict(H=4, HK1=2, HK2=2, NQ=400, NK=400, T=2, d1=80, d2=128),
+}
+
+
+@pytest.mark.parametrize("mode", ["1", "2"])
+@pytest.mark.parametrize("name", ANYTHING)
+def test_what_nobody_sees_may_hold_anything(name, mode):
+    """Rows that see nothing (padded, before the first key, without a list, or whose blocks hold no key of theirs): q and
+    dkl; keys with a negative id: k.  The results are those of zeros there, and theirs are zeros."""
+    dev, idx, where, p = problem(**ANYTHING[name])
+    bs, flag = p["bs"], skl.STREAMKL_GRAD_P1 if mode == "1" else skl.STREAMKL_GRAD_P2
+    rows = skl.streamkl_fwd_sel(*sides(dev), idx, bs, **where)
+    blind = torch.isinf(rows[1])  # [B, H, NQ]
+    assert blind.any() and torch.equal(blind, torch.isinf(rows[2])) and not blind.all()
+    hidden = where["doc_k"] < 0 if where["doc_k"] is not None else torch.zeros_like(dev["k1"][:, 0, :, 0], dtype=torch.bool)
+    dkl = torch.rand(rows[0].shape, generator=torch.Generator().manual_seed(2)).cuda() + 0.5
+    results = []
+    for junk in (0.0, float("nan"), float("inf"), -3.0e38):
+        x = {n: t.clone() for n, t in dev.items()}
+        w = dkl.clone()
+        for t in "12":
+            x["q" + t][blind] = junk
+            k = x["k" + t]
+            k[hidden[:, None].expand(k.shape[:3])] = junk
+        w[blind] = junk
+        got = skl.streamkl_fwd_sel(*sides(x), idx, bs, **where)
+        for g, v in zip(got, rows):
+            assert torch.equal(g, v)
+        results.append(skl.streamkl_bwd_sel(*sides(x), idx, bs, *got, w, flag, **where))
+    for dq, dk in results:
+        assert torch.equal(dq, results[0][0]) and torch.equal(dk, results[0][1])
+        assert not dq[blind].any() and not dk[hidden[:, None].expand(dk.shape[:3])].any()
+        assert dq.isfinite().all() and dk.isfinite().all() and dq.any() and dk.any()
+    assert skl.streamkl_get_device_status() == skl.STREAMKL_OK
+
+
+@pytest.mark.parametrize("mode", ["1", "2"])
+def test_backward_workspace_streams_and_graphs(mode):
+    dev, idx, where, p = problem(H=4, HK1=2, HK2=2, NQ=200, NK=200, T=4)
+    p1, p2 = sides(dev)
+    flag = skl.STREAMKL_GRAD_P1 if mode == "1" else skl.STREAMKL_GRAD_P2
+    rows = skl.streamkl_fwd_sel(p1, p2, idx, 32, **where)
+    dkl = torch.ones_like(rows[0])
+    want = skl.streamkl_bwd_sel(p1, p2, idx, 32, *rows, dkl, flag, **where)
+    need = skl.streamkl_bwd_sel_workspace_bytes(p1, p2, idx, 32, flag, **where)
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    out = [torch.full_like(w, float("nan")) for w in want]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    got = skl.streamkl_bwd_sel(p1, p2, idx, 32, *rows, dkl, flag, **where, dq=out[0], dk=out[1], workspace=ws[:need], stream=st)
+    torch.cuda.current_stream().wait_stream(st)
+    assert all(g is o for g, o in zip(got, out)) and (ws[need:] == 255).all()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    for less in (need - 1, need - 16, 16):
+        with pytest.raises(skl.StreamKLError):
+            skl.streamkl_bwd_sel(p1, p2, idx, 32, *rows, dkl, flag, **where, workspace=ws[:less])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = skl.streamkl_bwd_sel(p1, p2, idx, 32, *rows, dkl, flag, **where)
+    idx.copy_(idx.roll(1, 2))
+    dkl.copy_(torch.rand_like(dkl))
+    graph.replay()
+    torch.cuda.synchronize()
+    for g, w in zip(again, skl.streamkl_bwd_sel(p1, p2, idx, 32, *rows, dkl, flag, **where)):
+        assert torch.equal(g, w)
