@@ -868,10 +868,12 @@ def streamkl_select_blocks(q, kb, count, block, NK, causal=False, prefix=None, d
     [B, heads, NQ, count], ascending, -1 behind them: kb [B, heads,
     ceil(NK / block), d] holds a key for each block (streamkl_pool_blocks),
     and a block's score is the sum of q_h . kb over the H // heads query heads
-    that share a head of kb.  Candidates hold a key that causal, prefix, doc_q
-    and doc_k leave visible; the first `sink` and last `local` of them are
-    always taken (sink + local <= count; one each by default, with count = 1
-    the last alone).  Ties go to the lowest block."""
+    that share a head of kb.  Candidates are the blocks that begin at or before
+    the query (causal) or in the prefix, and whose keys' ids, the negative ones
+    aside, enclose the query's (doc_q, doc_k); the first `sink` and last `local`
+    of them are always taken (sink + local <= count; one each by default, with
+    count = 1 the last alone).  Ties go to the lowest block (see the header for
+    what scores are told apart)."""
     _strided(q, "q")
     _strided(kb, "kb")
     B, H, NQ, d = q.shape

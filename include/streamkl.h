@@ -426,9 +426,15 @@ typedef struct streamkl_blocks {
  * and largest id (negative ones aside) enclose the query's.  selected
  * [B][heads][NQ][count] gets the `count` best candidates in ascending order and
  * -1 behind them; the first `sink` and the last `local` candidates always are
- * among them (sink + local <= count).  The order is that of the exact scores,
- * ties go to the lowest block; differences below 1e-30 are not resolved, and
- * what a query whose q is not finite selects is not specified.  q is bf16
+ * among them (sink + local <= count).  (A candidate may hold no key that the
+ * query sees: its ids enclose the query's, and need not be in order.)
+ *
+ * The order is that of the exact scores, ties go to the lowest block; what is
+ * not resolved are differences below 1e-30, or below (n / 32 + 18)^2 2^-48 of
+ * the sizes of a score's n = d H / heads terms, added up (2^-37 for 512 terms,
+ * 2^-29 for 16384).  What a query whose q is not finite selects is not
+ * specified, nor is the place of a block whose kb is not, or the sizes of whose
+ * terms add up to more than 3e38.  q is bf16
  * [B][H][NQ][d], kb [B][heads][blocks][d] (streamkl_pool_blocks, or any other).
  * workspace: as above, with streamkl_select_blocks_workspace_bytes.
  */

@@ -376,3 +376,14 @@ def test_one_place_by_default():
     del kw["sink"], kw["local"]
     got = skl.streamkl_select_blocks(q, kb, 1, 32, 300, **kw)
     assert torch.equal(got.flatten(0, 1).squeeze(2).cpu(), ((torch.arange(100) + 200) // 32).int().expand(2, 100))
+
+
+@gpu
+def test_a_candidate_may_hold_no_key_of_the_query():
+    """Ids out of order: a block whose smallest and largest enclose the query's is a candidate, one beside them is not."""
+    ids = torch.tensor([[0] * 16 + [2] * 16 + [1] * 32 + [3] * 32 + [-1] * 16 + [1] * 16], dtype=torch.int32, device="cuda")
+    doc_q = torch.tensor([[1, 0, 3, -1, 2]], dtype=torch.int32, device="cuda")
+    q = torch.ones((1, 1, 5, 16), dtype=torch.bfloat16, device="cuda")
+    kb = torch.ones((1, 1, 4, 16), dtype=torch.bfloat16, device="cuda")
+    got = skl.streamkl_select_blocks(q, kb, 4, 32, 128, doc_q=doc_q, doc_k=ids)
+    assert got[0, 0].tolist() == [[0, 1, 3, -1], [0, -1, -1, -1], [2, -1, -1, -1], [-1] * 4, [0, -1, -1, -1]]
