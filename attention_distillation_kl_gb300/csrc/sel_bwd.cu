@@ -25,7 +25,7 @@
 // some 6.4 TB/s of them (measured alone, rows of 512 bytes over 32 MB: 6.4 with 8
 // or 32 lanes to a line, 3.8 with lanes to sectors of several lines, 3.1 with a
 // row a lane; as bulk reductions 5.4 in pieces of 256 bytes and 2.8 in 128),
-// where rows that are read come at 14.
+// where rows that are read come at 19.5.
 #include "sel_common.cuh"
 
 namespace skl {

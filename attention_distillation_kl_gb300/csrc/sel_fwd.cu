@@ -7,7 +7,8 @@
 //   warps 12-15 gather 32 rows each, 16 bytes a lane (cp.async).  TMA takes
 //               some 50 clocks for a copy of few rows, whatever its form: at
 //               rows of 256 bytes out of L2 its gather of four reached 2.5
-//               TB/s, cp.async of 4 and 8 warps 11.6 and 14.3.
+//               TB/s, cp.async 19.5 (64 bytes of 8 rows at a time, as here;
+//               20.5 with whole rows; of 4 and 8 warps alike).
 //   warp 16     S1 = Q1 K1^T, S2 = Q2 K2^T into one of 4 TMEM buffers (2 for blocks of 128)
 //   warp 17     K by TMA
 //   warp 18     tells the others what to take (SelShare)

@@ -736,13 +736,14 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
 }
 
 // Whether the lists are found where the scores are.  A row a thread takes fewer
-// instructions and longer: 41 us for one tile of 256 blocks, where a warp a row
-// takes 29 with the scores through L2.  16384 causal queries x 8 selection heads
-// x 256 blocks (1024 tiles): 130 and 233 us; 512 tiles of 64 blocks: 58 and 103; 64 tiles
-// of 256: 64 and 46.  So from a wave of CTAs on, two for each of 152 SMs.  (Of 512
-// blocks, with a CTA an SM, it was 222 and 238.)  Rows whose border needs the exact
-// scores of many blocks go the other way: 4096 queries x 16 selection heads x 128
-// blocks take 85 and 143 us, with equal keys in all of them 4.0 and 2.4 ms.
+// instructions and longer: 45 us for one tile of 256 blocks, where a warp a row
+// takes 26 with the scores through L2.  16384 causal queries x 8 selection heads
+// x 256 blocks (1024 tiles): 143 and 239 us; 512 tiles of 64 blocks: 65 and 103; 64 tiles
+// of 256: 76 and 47.  So from a wave of CTAs on, two for each of 152 SMs.  (Of 512
+// blocks, with a CTA an SM, there was no gain to speak of.)  Rows whose border needs the
+// exact scores of many blocks go the other way: 4096 queries x 16 selection heads x 128
+// blocks take 88 and 128 us, with equal keys in half of them 0.78 and 0.29 ms, in all 4.0
+// and 2.3.  A key that is not finite does the same to every row of its head.
 bool lists_at_once(const SelectArgs& a) {
   return a.doc_q == nullptr && a.blocks <= kN && (long long)a.B * a.HS * a.tiles_q >= 304;
 }
